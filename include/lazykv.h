@@ -219,8 +219,70 @@ int lazy_attn_prefill(const void* q, const int32_t* cu_q, const int32_t* q_start
                       const lazy_pos_cfg* cfg, void* out, float* lse, void* ws,
                       size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 4-bit caches.  The same paged, position-free cache (one copy of a document, keys rotated by
+ * their local positions) in 4.5 bits per value instead of 16: every 16 consecutive dimensions
+ * of a row form a group with one e4m3 scale s, and a value is an e2m1 code (sign, then 0, 0.5,
+ * 1, 1.5, 2, 3, 4 or 6) times s times the cache's factor (k_scale / v_scale, a power of two in
+ * [2^-32, 2^32]; 0 selects 1).  s = e4m3(max |y| / (6 factor)), at most 448; the code is the
+ * nearest of y / factor / s, ties to even, saturating at 6.  A group with an infinity or a NaN
+ * gets the scale NaN and reads back as NaN.  Choose a factor other than 1 only if a group's
+ * maximum can leave [0.1, 2688]: smaller ones lose accuracy in s, larger ones saturate.  All
+ * calls on a cache take the same factors.
+ *
+ * kv_cache (device) uint8 [num_pages][Hkv][18 D], 16-byte aligned: one block of 18 D bytes per
+ * page and KV head.  For row r (0..15) and dimension d of a block:
+ *   K code   r D/2 + d/2 (low half of the byte: even d)
+ *   K scale  8 D + ((r % 8) 4 + d / (D/4)) D/32 + (r / 8) D/64 + (d % (D/4)) / 16
+ *   V code   9 D + (r / 8) A + (d / (D/8) 4 + (r % 8) / 2) 16 + (r % 2) D/16 + (d % (D/8)) / 2,
+ *            A = 512 for D = 128 and 8 for D = 64 (low half of the byte: even d)
+ *   V scale  17 D + (d / 16) 16 + ((r % 8) / 2) 4 + (r / 8) 2 + r % 2
+ * Rows that hold no visible key may hold anything.  Slots, block words, query and workspace
+ * conventions are those of the bf16 entry points above; so are the head shapes they accept, the
+ * status bits and the return codes.  Arguments are checked before the device is.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * lazy_kv_write_q4 -- lazy_kv_write into a 4-bit cache: quantises bf16_RNE(R_j k) and v.  With a
+ * cos/sin table in cfg the rotation is fl(fl(x1 c) - fl(x2 s)), fl(fl(x1 s) + fl(x2 c)) in fp32.
+ * Only the bytes of the written rows change.  The slots of one call must be distinct: a row
+ * that two tokens share ends as a mix of both.
+ */
+int lazy_kv_write_q4(const void* k, const void* v, const int32_t* slot, const int32_t* local_pos,
+                     int T, int Hkv, int D, void* kv_cache, int num_pages,
+                     const lazy_pos_cfg* cfg, float k_scale, float v_scale, void* stream);
+
+/*
+ * lazy_kv_read_q4 -- the values held in T cache rows, exactly, in bf16 (keys as stored: rotated
+ * by their local positions).
+ *   slot  (device) int32 [T];  k, v  (device, written) bf16 [T][Hkv][D]
+ * A slot outside [0, num_pages * 16) sets LAZY_STATUS_BAD_SLOT and its output rows are left as
+ * they were.
+ */
+int lazy_kv_read_q4(const int32_t* slot, int T, int Hkv, int D, const void* kv_cache,
+                    int num_pages, float k_scale, float v_scale, void* k, void* v, void* stream);
+
+/*
+ * lazy_attn_decode_q4 / lazy_attn_prefill_q4 -- lazy_attn_decode / lazy_attn_prefill over a
+ * 4-bit cache.  Workspace: lazy_workspace_size with LAZY_PHASE_DECODE_Q4 / LAZY_PHASE_PREFILL_Q4.
+ * A row without a visible key gets out = 0 and lse = -inf.
+ */
+int lazy_attn_decode_q4(const void* q, const int32_t* seq_len, const int32_t* q_start,
+                        const int32_t* doc_blocks, const uint64_t* meta, int B, int max_blocks,
+                        const void* kv_cache, int num_pages, int Hq, int Hkv, int D, float scale,
+                        float k_scale, float v_scale, const lazy_pos_cfg* cfg, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream);
+int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const int32_t* q_start,
+                         const int32_t* doc_blocks, const uint64_t* meta, int B, int max_blocks,
+                         int total_q, int max_q, const void* kv_cache, int num_pages, int Hq,
+                         int Hkv, int D, float scale, float k_scale, float v_scale,
+                         const lazy_pos_cfg* cfg, void* out, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+
 #define LAZY_PHASE_DECODE 0
 #define LAZY_PHASE_PREFILL 1
+#define LAZY_PHASE_DECODE_Q4 2
+#define LAZY_PHASE_PREFILL_Q4 3
 
 /*
  * lazy_workspace_size -- bytes of workspace the given call needs (0 if none).

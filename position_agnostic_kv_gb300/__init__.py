@@ -7,7 +7,8 @@ current CUDA stream.  There is no fallback of any kind: if the library is missin
 this package raises.
 
 Functions mirror the C entry points: ``build_doc_meta`` (host), ``build_rope_table``,
-``kv_write``, ``attn_decode``, ``attn_prefill``, ``workspace_size``, ``device_status``.
+``kv_write``, ``attn_decode``, ``attn_prefill``, ``workspace_size``, ``device_status``; over a
+4-bit cache ``kv_write_q4``, ``kv_read_q4``, ``attn_decode_q4``, ``attn_prefill_q4``.
 """
 from __future__ import annotations
 
@@ -19,16 +20,18 @@ import numpy as np
 __all__ = ["LIB_PATH", "lib", "PosCfg", "LazyError", "DocCache", "POS_ROPE", "POS_YARN", "POS_ALIBI",
            "POS_NONE", "PHASE_DECODE", "PHASE_PREFILL", "EXPORTED_SYMBOLS", "build_doc_meta",
            "build_rope_table", "kv_write", "attn_decode", "attn_decode_noalloc", "attn_prefill", "workspace_size",
-           "device_status", "pos_cfg_from"]
+           "device_status", "pos_cfg_from", "PHASE_DECODE_Q4", "PHASE_PREFILL_Q4", "q4_cache_shape", "kv_write_q4",
+           "kv_read_q4", "attn_decode_q4", "attn_prefill_q4"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblazykv.so")
 POS_ROPE, POS_YARN, POS_ALIBI, POS_NONE = 0, 1, 2, 3
-PHASE_DECODE, PHASE_PREFILL = 0, 1
+PHASE_DECODE, PHASE_PREFILL, PHASE_DECODE_Q4, PHASE_PREFILL_Q4 = 0, 1, 2, 3
 EXPORTED_SYMBOLS = ("lazy_build_doc_meta", "lazy_build_rope_table", "lazy_kv_write",
                     "lazy_attn_decode", "lazy_attn_decode_noalloc", "lazy_attn_prefill", "lazy_workspace_size",
                     "lazy_device_status", "lazy_last_error", "lazy_version", "lazy_doc_cache_create",
                     "lazy_doc_cache_destroy", "lazy_doc_cache_lookup", "lazy_doc_cache_acquire",
-                    "lazy_doc_cache_release", "lazy_doc_cache_stats")
+                    "lazy_doc_cache_release", "lazy_doc_cache_stats", "lazy_kv_write_q4", "lazy_kv_read_q4",
+                    "lazy_attn_decode_q4", "lazy_attn_prefill_q4")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -63,6 +66,13 @@ _sig = {
                                  ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P],
     "lazy_attn_prefill": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _I,
                           ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
+    "lazy_kv_write_q4": [_P, _P, _P, _P, _I, _I, _I, _P, _I, ctypes.POINTER(PosCfg), ctypes.c_float,
+                         ctypes.c_float, _P],
+    "lazy_kv_read_q4": [_P, _I, _I, _I, _P, _I, ctypes.c_float, ctypes.c_float, _P, _P, _P],
+    "lazy_attn_decode_q4": [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float,
+                            ctypes.c_float, ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
+    "lazy_attn_prefill_q4": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float,
+                             ctypes.c_float, ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
     "lazy_workspace_size": [_I, _I, _I, _I, _I, _I, _I],
     "lazy_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],
     "lazy_last_error": [],
@@ -266,6 +276,120 @@ def attn_prefill(q, cu_q, q_start, doc_blocks, meta, k_cache, v_cache, cfg: PosC
                                  _dev_ptr(out, torch.bfloat16, "out"),
                                  _dev_ptr(lse, torch.float32, "lse"), wsp, wsb, _stream(stream)),
            "lazy_attn_prefill")
+
+
+# ------------------------------------------------------------------ 4-bit caches
+def q4_cache_shape(num_pages: int, Hkv: int, D: int) -> tuple:
+    """Shape of a 4-bit cache (uint8): keys and values together, 18 D bytes per page and head."""
+    if D not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {D}")
+    return (num_pages, Hkv, 18 * D)
+
+
+def _q4_call(fn, what, stream, *args):
+    """Check the tensors among ``args`` -- (name, tensor, dtype, shape), None allowed as the tensor --
+    and call ``fn`` with the other arguments as they are, on the tensors' device and its current
+    stream (or ``stream``, which must be of that device)."""
+    import torch
+    dev, ptrs = None, []
+    for x in args:
+        if type(x) is not tuple:
+            ptrs.append(x)
+            continue
+        name, t, dtype, shape = x
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: {name} must be a torch.Tensor")
+        if t.dtype is not dtype and not (dtype is torch.int64 and t.dtype is torch.uint64):
+            raise TypeError(f"{what}: {name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on another device than the tensors before it")
+        ptrs.append(t.data_ptr())
+    if dev < 0:
+        raise ValueError(f"{what}: the tensors must be on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{what}: the stream is of another device than the tensors")
+    if dev == torch.cuda.current_device():
+        rc = fn(*ptrs, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*ptrs, stream.cuda_stream)
+    if rc:
+        _check(rc, fn.__name__)
+
+
+def _q4_dims(what, kv_cache, Hkv, D):
+    if kv_cache.dim() != 3 or kv_cache.shape[1] != Hkv or kv_cache.shape[2] != 18 * D:
+        raise ValueError(f"{what}: kv_cache must be [num_pages, {Hkv}, {18 * D}], got {tuple(kv_cache.shape)}")
+    return kv_cache.shape[0]
+
+
+def kv_write_q4(k, v, slot, local_pos, kv_cache, cfg: PosCfg, k_scale: float = 1.0, v_scale: float = 1.0,
+                stream=None):
+    """Write raw k/v [T, Hkv, D] (bf16) into a 4-bit cache of shape ``q4_cache_shape``: the keys
+    rotated by their local positions as ``kv_write`` does, then both quantised.  ``k_scale`` and
+    ``v_scale`` are the cache's power-of-two factors.  The slots must be distinct; only the rows
+    they name change."""
+    import torch
+    T, Hkv, D = k.shape
+    P = _q4_dims("kv_write_q4", kv_cache, Hkv, D)
+    _q4_call(lib.lazy_kv_write_q4, "kv_write_q4", stream, ("k", k, torch.bfloat16, k.shape),
+             ("v", v, torch.bfloat16, k.shape), ("slot", slot, torch.int32, (T,)),
+             ("local_pos", local_pos, torch.int32, (T,)), T, Hkv, D, ("kv_cache", kv_cache, torch.uint8, kv_cache.shape),
+             P, ctypes.byref(cfg), k_scale, v_scale)
+
+
+def kv_read_q4(slot, kv_cache, k, v, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Read cache rows back: writes the values held in ``slot`` [T] to k/v [T, Hkv, D] (bf16, exact;
+    keys as stored, rotated by their local positions)."""
+    import torch
+    T, Hkv, D = k.shape
+    P = _q4_dims("kv_read_q4", kv_cache, Hkv, D)
+    _q4_call(lib.lazy_kv_read_q4, "kv_read_q4", stream, ("slot", slot, torch.int32, (T,)), T, Hkv, D,
+             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, k_scale, v_scale,
+             ("k", k, torch.bfloat16, k.shape), ("v", v, torch.bfloat16, k.shape))
+
+
+def attn_decode_q4(q, seq_len, q_start, doc_blocks, meta, kv_cache, cfg: PosCfg, out, lse=None, ws=None,
+                   scale: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """``attn_decode`` over a 4-bit cache: q [B, Hq, D] raw at m = seq_len - 1; writes out [B, Hq, D]
+    (bf16).  ``ws`` holds at least ``workspace_size(PHASE_DECODE_Q4, ...)`` bytes."""
+    import torch
+    B, Hq, D = q.shape
+    Hkv, mb = kv_cache.shape[1], meta.shape[1]
+    P = _q4_dims("attn_decode_q4", kv_cache, Hkv, D)
+    _q4_call(lib.lazy_attn_decode_q4, "attn_decode_q4", stream, ("q", q, torch.bfloat16, q.shape),
+             ("seq_len", seq_len, torch.int32, (B,)), ("q_start", q_start, torch.int32, (B,)),
+             ("doc_blocks", doc_blocks, torch.int32, (B,)), ("meta", meta, torch.int64, (B, mb)), B, mb,
+             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, Hq, Hkv, D, scale, k_scale, v_scale,
+             ctypes.byref(cfg), ("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (B, Hq)),
+             ("ws", ws, torch.uint8, ws.shape if ws is not None else None), ws.numel() if ws is not None else 0)
+
+
+def attn_prefill_q4(q, cu_q, q_start, doc_blocks, meta, kv_cache, cfg: PosCfg, out, max_q: int, lse=None,
+                    ws=None, scale: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """``attn_prefill`` over a 4-bit cache: q [sum Lq, Hq, D] raw; writes out [sum Lq, Hq, D] (bf16).
+    ``ws`` holds at least ``workspace_size(PHASE_PREFILL_Q4, ...)`` bytes."""
+    import torch
+    n, Hq, D = q.shape
+    B, Hkv, mb = cu_q.shape[0] - 1, kv_cache.shape[1], meta.shape[1]
+    P = _q4_dims("attn_prefill_q4", kv_cache, Hkv, D)
+    _q4_call(lib.lazy_attn_prefill_q4, "attn_prefill_q4", stream, ("q", q, torch.bfloat16, q.shape),
+             ("cu_q", cu_q, torch.int32, (B + 1,)), ("q_start", q_start, torch.int32, (B,)),
+             ("doc_blocks", doc_blocks, torch.int32, (B,)), ("meta", meta, torch.int64, (B, mb)), B, mb, n, max_q,
+             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, Hq, Hkv, D, scale, k_scale, v_scale,
+             ctypes.byref(cfg), ("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (n, Hq)),
+             ("ws", ws, torch.uint8, ws.shape if ws is not None else None), ws.numel() if ws is not None else 0)
 
 
 def device_status(stream=None) -> int:

@@ -1,5 +1,6 @@
 // extern "C" entry points of the attention kernels: argument checks and dispatch.
 #include "decode.cuh"
+#include "q4_attn.cuh"
 
 using namespace lazykv;
 
@@ -98,6 +99,8 @@ extern "C" size_t lazy_workspace_size(int phase, int rows, int B, int max_blocks
   (void)B;
   if (rows <= 0 || max_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return 0;
   if (phase == LAZY_PHASE_DECODE) return decode_ws_bytes(rows, Hq, Hkv, D, max_blocks);
+  if (phase == LAZY_PHASE_DECODE_Q4) return q4_ws_bytes(rows, Hq, Hkv, D, max_blocks, false);
+  if (phase == LAZY_PHASE_PREFILL_Q4) return q4_ws_bytes(rows, Hq, Hkv, D, max_blocks, true);
   if (phase != LAZY_PHASE_PREFILL) return 0;
   const int G = Hq / Hkv;
   if (G <= 128 && 128 % G == 0) return 0;  // the tensor-core prefill needs no workspace

@@ -1,0 +1,61 @@
+// Arguments of the attention kernels over the 4-bit cache.
+#pragma once
+
+#include "q4.cuh"
+
+namespace lazykv {
+
+struct Q4Args {
+  const __nv_bfloat16* q;
+  const int32_t* seq_len;     // decode: [B]; null for prefill
+  const int32_t* cu_q;        // prefill: [B + 1]; null for decode
+  const int32_t* q_start;
+  const int32_t* doc_blocks;
+  const uint64_t* meta;
+  const uint8_t* cache;       // [num_pages][Hkv][18 D]
+  int num_pages, B, max_blocks, Hq, Hkv, rows;
+  float qk_log2;              // softmax scale * log2(e) * k factor: scores in base-2 units
+  float v_factor;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;              // [rows][Hq][S][D] unnormalised partial outputs (S > 1)
+  float* part_ml;             // [rows][Hq][S][2] their base-2 maximum and sum
+  int S;                      // key splits
+  uint32_t* status;
+  PosParams pos;
+};
+
+// Query row -> request b and absolute position m; number of blocks nb that m can see.
+struct Q4Row {
+  int b, m, nb;
+};
+template <bool ROWS>
+__device__ __forceinline__ Q4Row q4_row(const Q4Args& a, int r) {
+  Q4Row w;
+  if constexpr (ROWS) {
+    int lo = 0, hi = a.B;  // last b with cu_q[b] <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu_q[mid] <= r) lo = mid; else hi = mid;
+    }
+    w.b = lo;
+    w.m = a.q_start[lo] + (r - a.cu_q[lo]);
+  } else {
+    w.b = r;
+    w.m = a.seq_len[r] - 1;
+  }
+  const int rel = w.m - a.q_start[w.b];  // negative: the request has no token of its own yet
+  w.nb = max(0, a.doc_blocks[w.b]) + (rel >= 0 ? rel / kPage + 1 : 0);
+  return w;
+}
+
+// Rows of a block that hold a key visible to position m (a prefix of the page).
+__device__ __forceinline__ int q4_rows(uint64_t w, int m) {
+  const int start = int(word_delta(w) + kPage * word_pg(w));
+  return max(0, min(min(int(word_nvalid(w)), kPage), m - start + 1));
+}
+
+int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st);
+size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_mode);
+
+}  // namespace lazykv

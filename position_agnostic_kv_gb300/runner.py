@@ -13,8 +13,9 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (PHASE_DECODE, PHASE_PREFILL, attn_decode, attn_prefill, build_doc_meta,
-               build_rope_table, kv_write, pos_cfg_from, workspace_size)
+from . import (PHASE_DECODE, PHASE_DECODE_Q4, PHASE_PREFILL, PHASE_PREFILL_Q4, attn_decode,
+               attn_decode_q4, attn_prefill, attn_prefill_q4, build_doc_meta, build_rope_table, kv_write,
+               kv_write_q4, pos_cfg_from, q4_cache_shape, workspace_size)
 
 PAGE = 16
 
@@ -30,9 +31,16 @@ def i32(x, device) -> torch.Tensor:
 
 
 class PagedBatch:
-    """Caches, block words and per-request metadata of one batch, resident on one GPU."""
+    """Caches, block words and per-request metadata of one batch, resident on one GPU.
 
-    def __init__(self, w, device="cuda", use_table: bool = False, pos_kind: str | None = None):
+    ``kv_bits=4`` keeps keys and values in one 4-bit cache (``kv_cache``, with the power-of-two
+    factors ``k_scale`` / ``v_scale``) instead of the bf16 ``k_cache`` and ``v_cache``."""
+
+    def __init__(self, w, device="cuda", use_table: bool = False, pos_kind: str | None = None,
+                 kv_bits: int = 16, k_scale: float = 1.0, v_scale: float = 1.0):
+        if kv_bits not in (4, 16):
+            raise ValueError(f"kv_bits must be 16 or 4, got {kv_bits}")
+        self.kv_bits, self.factors = kv_bits, dict(k_scale=k_scale, v_scale=v_scale)
         self.w = w
         self.device = torch.device(device)
         self.B, self.Hq, self.Hkv, self.D = w.B, w.Hq, w.Hkv, w.D
@@ -49,8 +57,12 @@ class PagedBatch:
         self.max_q = int(np.max(w.q_len)) if len(w.q_len) else 0
         self.total_q = int(np.sum(w.q_len))
         shape = (w.num_pages, w.Hkv, PAGE, w.D)
-        self.k_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
-        self.v_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        self.k_cache = self.v_cache = self.kv_cache = None
+        if kv_bits == 4:
+            self.kv_cache = torch.zeros(q4_cache_shape(w.num_pages, w.Hkv, w.D), dtype=torch.uint8, device=dev)
+        else:
+            self.k_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+            self.v_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
         p = w.pos
         kind = pos_kind or p.kind
         self.slopes = None
@@ -73,11 +85,18 @@ class PagedBatch:
                                     yarn_beta_slow=p.yarn_beta_slow, alibi_slopes=self.slopes,
                                     cos_sin=self.table, rotary_dim=rd, interleaved=inter)
         self.max_blocks = w.max_blocks
-        ws_dec = workspace_size(PHASE_DECODE, self.B, self.B, self.max_blocks, self.Hq, self.Hkv,
+        ph_dec, ph_pre = (PHASE_DECODE, PHASE_PREFILL) if kv_bits == 16 else (PHASE_DECODE_Q4, PHASE_PREFILL_Q4)
+        ws_dec = workspace_size(ph_dec, self.B, self.B, self.max_blocks, self.Hq, self.Hkv,
                                 self.D)
-        ws_pre = workspace_size(PHASE_PREFILL, max(self.total_q, 1), self.B, self.max_blocks,
+        ws_pre = workspace_size(ph_pre, max(self.total_q, 1), self.B, self.max_blocks,
                                 self.Hq, self.Hkv, self.D)
         self.ws = torch.empty(max(ws_dec, ws_pre, 256), dtype=torch.uint8, device=dev)
+
+    def _write(self, k, v, slot, lp):
+        if self.kv_bits == 4:
+            kv_write_q4(k, v, slot, lp, self.kv_cache, self.cfg, **self.factors)
+        else:
+            kv_write(k, v, slot, lp, self.k_cache, self.v_cache, self.cfg)
 
     # ---------------------------------------------------------------- cache fill
     def fill_documents(self):
@@ -91,8 +110,7 @@ class PagedBatch:
             kt, vt = bits_to_tensor(k, self.device), bits_to_tensor(v, self.device)
             for i in insts:
                 slot, lp = w.inst_slots(i)
-                kv_write(kt, vt, i32(slot, self.device), i32(lp, self.device), self.k_cache,
-                         self.v_cache, self.cfg)
+                self._write(kt, vt, i32(slot, self.device), i32(lp, self.device))
 
     # ---------------------------------------------------------------- prefill
     def upload_prefill(self):
@@ -108,9 +126,13 @@ class PagedBatch:
                               device=self.device)
         if self.total_q == 0:
             return out
-        kv_write(inp["k"], inp["v"], inp["slot"], inp["lp"], self.k_cache, self.v_cache, self.cfg)
-        attn_prefill(inp["q"], self.cu_q, self.q_start, self.doc_blocks, self.meta, self.k_cache,
-                     self.v_cache, self.cfg, out, self.max_q, lse=lse, ws=self.ws)
+        self._write(inp["k"], inp["v"], inp["slot"], inp["lp"])
+        if self.kv_bits == 4:
+            attn_prefill_q4(inp["q"], self.cu_q, self.q_start, self.doc_blocks, self.meta, self.kv_cache, self.cfg,
+                            out, self.max_q, lse=lse, ws=self.ws, **self.factors)
+        else:
+            attn_prefill(inp["q"], self.cu_q, self.q_start, self.doc_blocks, self.meta, self.k_cache,
+                         self.v_cache, self.cfg, out, self.max_q, lse=lse, ws=self.ws)
         return out
 
     # ---------------------------------------------------------------- decode
@@ -125,14 +147,18 @@ class PagedBatch:
         """Write step t's token (at p = m) then attend from it."""
         if out is None:
             out = torch.empty((self.B, self.Hq, self.D), dtype=torch.bfloat16, device=self.device)
-        kv_write(inp["k"], inp["v"], inp["slot"], inp["lp"], self.k_cache, self.v_cache, self.cfg)
-        attn_decode(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta,
-                    self.k_cache, self.v_cache, self.cfg, out, lse=lse, ws=self.ws)
+        self._write(inp["k"], inp["v"], inp["slot"], inp["lp"])
+        if self.kv_bits == 4:
+            attn_decode_q4(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta, self.kv_cache,
+                           self.cfg, out, lse=lse, ws=self.ws, **self.factors)
+        else:
+            attn_decode(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta,
+                        self.k_cache, self.v_cache, self.cfg, out, lse=lse, ws=self.ws)
         return out
 
 
 # -------------------------------------------------------------------- cold documents
-def encode_document(q, k, v, pages, k_cache, v_cache, cfg, ws=None, out=None):
+def encode_document(q, k, v, pages, k_cache, v_cache, cfg, ws=None, out=None, **factors):
     """Cold-document processing: the first time a document is seen it is encoded alone, from
     local position 0 ([NOTE] 整体框架: each document's cache is built independently, indexed
     from 0).  Its keys (rotated by their local positions) and values are written into
@@ -141,14 +167,21 @@ def encode_document(q, k, v, pages, k_cache, v_cache, cfg, ws=None, out=None):
 
     q, k, v: bf16 [L, Hq | Hkv, D] raw projections of the document's tokens; pages: int list
     of ceil(L / 16) physical page ids.  Returns the attention output [L, Hq, D] (bf16); the
-    cached pages can then be reused by any later request at any document offset."""
+    cached pages can then be reused by any later request at any document offset.
+
+    With ``v_cache=None``, ``k_cache`` is a 4-bit cache that holds both (``factors``: its
+    ``k_scale`` and ``v_scale``); the document then attends to its keys and values as stored."""
     L, Hq, D = q.shape
     dev = q.device
     pages = np.asarray(pages, dtype=np.int32)
     if len(pages) * PAGE < L:
         raise ValueError("encode_document: fewer pages than the document needs")
     t = np.arange(L, dtype=np.int32)
-    kv_write(k, v, i32(pages[t // PAGE] * PAGE + t % PAGE, dev), i32(t, dev), k_cache, v_cache, cfg)
+    slot, lp = i32(pages[t // PAGE] * PAGE + t % PAGE, dev), i32(t, dev)
+    if v_cache is None:
+        kv_write_q4(k, v, slot, lp, k_cache, cfg, **factors)
+    else:
+        kv_write(k, v, slot, lp, k_cache, v_cache, cfg, **factors)
     max_blocks = len(pages)
     _, meta_h, _, q_start_h, doc_blocks_h = build_doc_meta(
         [0, 0], [], [], [0], [], [L], [0, len(pages)], pages, max_blocks)
@@ -157,8 +190,12 @@ def encode_document(q, k, v, pages, k_cache, v_cache, cfg, ws=None, out=None):
         out = torch.empty((L, Hq, D), dtype=torch.bfloat16, device=dev)
     Hkv = k_cache.shape[1]
     if ws is None:
-        n = workspace_size(PHASE_PREFILL, L, 1, max_blocks, Hq, Hkv, D)
+        n = workspace_size(PHASE_PREFILL_Q4 if v_cache is None else PHASE_PREFILL, L, 1, max_blocks, Hq, Hkv, D)
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    if v_cache is None:
+        attn_prefill_q4(q, i32([0, L], dev), i32(q_start_h, dev), i32(doc_blocks_h, dev), meta, k_cache, cfg, out, L,
+                        ws=ws, **factors)
+        return out
     attn_prefill(q, i32([0, L], dev), i32(q_start_h, dev), i32(doc_blocks_h, dev), meta, k_cache,
                  v_cache, cfg, out, L, ws=ws)
     return out
