@@ -1,191 +1,570 @@
-// Attention of single query rows over the 4-bit cache: the decode step, and prefill rows.
+// Attention of single query rows over the 4-bit cache: the decode step, and prefill rows of head
+// groups that do not fit the tensor-core prefill.
 //
-// One CTA per (query row, KV head, up to 8 query heads of its group), tiles of 128 keys, one key
-// per thread: the thread dequantises its key row, rotates it by its document's Delta and takes the
-// dot products with the query heads (rotated by the absolute position m); an online softmax in
-// base 2 over the tile; then one dimension per thread accumulates P V.
+// Mathematics.  For one KV head and the (up to 8) query heads that share it, per page of 16 keys:
+//   S^T [16 keys x 8] = K [16 x D] (R_{m - Delta} q)^T,   O^T [D x 8] += V^T [D x 16] P^T [16 x 8]
+// with an online softmax in base 2 between them.  Both products run on 16x8x16 f16 matrix
+// instructions whose 16-row operand (K rows, V columns) is dequantised into registers: a tile of a
+// decode step has 8 rows of queries, so the 128-row tcgen05 tiles would be nearly empty, and their
+// operands would cross shared memory once more (2 x 2 bytes per value against 0.56 loaded).
+//  * The cache block is laid out in fragment order (q4.cuh), so a page is four 16-byte shared loads
+//    per lane plus two scale words, all without bank conflicts.
+//  * A code times its e4m3 scale is exact in f16.  q is normalised per head by a power of two and
+//    split in two f16 (hi + lo), so the scores carry fp32 accuracy.  Groups of at most 4 heads put hi
+//    in columns 0-3 and lo in columns 4-7 of one instruction; groups of 8 use two instructions.
+//  * q is rotated by R_{m - Delta} only when a page's Delta differs from the one before: the warp
+//    computes the D/2 angles together (two per lane), then each lane its fragment.
+//  * P is f16 (2^-11 relative), held as 2^(s - max + 7): the lazy maximum (moved only when a score
+//    beats it by more than 8) keeps it below 2^15, and small weights stay normal numbers longer.
+//  * P^T comes out of the S^T fragment by one 8x8 transpose per 8 keys.
+//
+// What bounds it: HBM for long contexts (18 D bytes per page and head).  Per page a warp issues ~240
+// instructions; at the measured HBM rate an SM gets one page-head per 99 cycles = 396 issue slots.
+//
+// Work: a CTA = (query row, KV head, head group, key split), 4 warps, each with its own run of pages
+// and a ring of stages of two page blocks, one bulk copy per block; the warps' partial (O, max, sum)
+// are merged in shared memory, those of the splits by a second kernel.
 #include <cfloat>
 
 #include "q4_attn.cuh"
 
 namespace lazykv {
 
-constexpr int kHeads = 8;  // query heads per CTA at most
+namespace {
+
+constexpr float kTau = 8.0f;   // the running maximum moves when a score beats it by more (base 2)
+constexpr float kPOff = 7.0f;  // weights are held times 2^7
+constexpr int kWarps = 4;
+constexpr int kStages = 2;
+constexpr int kPair = 2;       // pages per stage
 
 template <int D>
-__device__ __forceinline__ float q4_v_value(const uint8_t* blk, int r, int d) {
-  using Q = Q4<D>;
-  const uint32_t c = blk[Q::v_code(r, d)] >> (4 * (d & 1));
-  return h2_to_f2(e2m1x2_to_h2(c & 15u)).x * e4m3_to_f(blk[Q::v_scale(r, d / 16)]);
+struct DecL {
+  static constexpr int DL = D / 4;                    // dimensions of a lane's K fragment
+  static constexpr int QROW = 4 * (DL + 4);           // padded: 4 t-chunks fall on different banks
+  static constexpr int STAGE = kPair * Q4<D>::BYTES;
+  static constexpr int QS = kWarps * kStages * STAGE;          // float [8][QROW]
+  static constexpr int CS = QS + 8 * QROW * 4;                 // float2 [warp][D/2]
+  static constexpr int SC = CS + kWarps * (D / 2) * 8;         // float [8] score factor of each head
+  static constexpr int SLOT = SC + 32;                         // {u64 word, i32 rows, pad} [warp][stage][2]
+  static constexpr int BAR = SLOT + kWarps * kStages * kPair * 16;
+  static constexpr int SMEM = BAR + kWarps * kStages * 8;
+  static_assert(kWarps * 8 * (D + 2) * 4 <= QS, "the merge buffer reuses the stages");
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-template <int D, bool ROWS>
-__global__ void __launch_bounds__(128) q4_rows_kernel(const Q4Args a, int heads, int ngrp) {
+// H8: eight heads (columns = heads, hi and lo by two instructions); else up to four.
+template <int D, bool H8, int POS>
+__global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(const Q4Args a, int heads, int ngrp) {
+  using L = DecL<D>;
   using Q = Q4<D>;
-  constexpr int NK = 128;          // keys per tile
-  constexpr int KH = 128 / D;      // threads per dimension in the PV step
-  __shared__ float qs[kHeads][D], ps[kHeads][NK], red[kHeads][4], mrun[kHeads], lrun[kHeads], alpha[kHeads];
-  __shared__ float osum[KH > 1 ? kHeads : 1][D];
-  __shared__ const uint8_t* vblk[NK / kPage];
-  __shared__ int vrows[NK / kPage];
+  constexpr int NKS = D / 16;   // k-steps of S, and m-tiles of O^T
+  constexpr int NW_ = D / 32;   // words of a K row per lane
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
+  const int split = int(blockIdx.x) % a.S;
+  int u = int(blockIdx.x) / a.S;
+  const int grp = u % ngrp;
+  u /= ngrp;
+  const int kvh = u % a.Hkv, r = u / a.Hkv;
+  const int h0 = kvh * (a.Hq / a.Hkv) + grp * heads;
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int grp = int(blockIdx.x % ngrp), g = int(blockIdx.x / ngrp) % a.Hkv, r = int(blockIdx.x / ngrp) / a.Hkv;
-  const Q4Row w = q4_row<ROWS>(a, r);
-  const int b = w.b, m = w.m;
-  int nb = w.nb;
+  const Q4Row row = a.cu_q ? q4_row<true>(a, r) : q4_row<false>(a, r);
+  const int m = row.m;
+  int nb = row.nb;
   if (nb > a.max_blocks) {
-    if (tid == 0) set_status(a.status, LAZY_STATUS_BAD_ROW);
+    if (threadIdx.x == 0) set_status(a.status, LAZY_STATUS_BAD_ROW);
     nb = a.max_blocks;
   }
-  const int h0 = g * (a.Hq / a.Hkv) + grp * heads;
-  const bool rotary = a.pos.kind == kRope || a.pos.kind == kYarn;
-  const int rd = rotary ? a.pos.rotary_dim : 0, hr = rd / 2;
-  // queries, rotated by m
-  for (int i = tid; i < heads * D; i += 128) {
-    const int h = i / D, d = i % D;
-    const __nv_bfloat16* qr = a.q + ((size_t)r * a.Hq + h0 + h) * D;
-    float x = __bfloat162float(qr[d]);
-    if (d < rd) {
-      const int f = a.pos.interleaved ? d / 2 : d % hr;
-      const bool first = a.pos.interleaved ? (d & 1) == 0 : d < hr;
-      const float p = __bfloat162float(qr[a.pos.interleaved ? d ^ 1 : (first ? d + hr : d - hr)]);
-      float s, c;
-      turn_sincos(uint32_t(max(m, 0)), a.pos.turns[f], s, c);
-      x = first ? x * c - p * s : p * s + x * c;
+  const int chunk = (nb + a.S - 1) / a.S;
+  const int beg = min(nb, split * chunk), len = min(nb, beg + chunk) - beg;
+  const int wb = beg + warp * len / kWarps;
+  const int n = beg + (warp + 1) * len / kWarps - wb;
+  const int ns = (n + kPair - 1) / kPair;
+
+  float* qs = reinterpret_cast<float*>(smem + L::QS);
+  float* scs = reinterpret_cast<float*>(smem + L::SC);
+  float2* cs = reinterpret_cast<float2*>(smem + L::CS) + warp * (D / 2);
+  uint8_t* slots = smem + L::SLOT + warp * kStages * kPair * 16;
+  const uint32_t bar0 = smem_u32(smem + L::BAR + warp * kStages * 8);
+  uint8_t* stages = smem + warp * kStages * L::STAGE;
+
+  const uint64_t* mrow = a.meta + (size_t)row.b * a.max_blocks + wb;
+  uint64_t mcur = lane < n ? ldg_u64(mrow + lane) : 0;
+  uint64_t mnxt = 32 + lane < n ? ldg_u64(mrow + 32 + lane) : 0;
+  int mbase = 0;
+  if (lane == 0)
+    for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+  fence_mbar_init();
+  __syncwarp();
+
+  auto issue = [&](int i) {  // stage i: pages 2i and 2i + 1, one per lane
+    if (kPair * i >= mbase + 32) {
+      mcur = mnxt;
+      mbase += 32;
+      mnxt = mbase + 32 + lane < n ? ldg_u64(mrow + mbase + 32 + lane) : 0;
     }
-    qs[h][d] = x * a.qk_log2;
-  }
-  if (tid < kHeads) {
-    mrun[tid] = -INFINITY;
-    lrun[tid] = 0.f;
-  }
-  float o[kHeads];
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) o[h] = 0.f;
-  const uint64_t* mrow = a.meta + (size_t)b * a.max_blocks;
-  for (int j0 = 0; j0 < nb; j0 += NK / kPage) {
-    __syncthreads();
-    const int jb = j0 + tid / kPage, t = tid % kPage;
-    int rows = 0, start = 0;
-    uint32_t delta = 0;
-    const uint8_t* blk = nullptr;
-    if (jb < nb) {
-      const uint64_t mw = ldg_u64(mrow + jb);
-      rows = q4_rows(mw, m);
-      delta = word_delta(mw);
-      start = int(delta + kPage * word_pg(mw));
-      if (word_page(mw) >= uint32_t(a.num_pages)) {
-        if (t == 0) set_status(a.status, LAZY_STATUS_BAD_PAGE);
+    const int st = i % kStages, j = kPair * i + (lane & 1);
+    const uint64_t w = __shfl_sync(0xffffffffu, mcur, (j - mbase) & 31);
+    int rows = 0;
+    if (lane < kPair && j < n) {
+      rows = q4_rows(w, m);
+      if (word_page(w) >= uint32_t(a.num_pages)) {
+        set_status(a.status, LAZY_STATUS_BAD_PAGE);
         rows = 0;
-      } else {
-        blk = a.cache + ((size_t)word_page(mw) * a.Hkv + g) * Q::BYTES;
       }
     }
-    if (t == 0) {
-      vblk[tid / kPage] = blk;
-      vrows[tid / kPage] = rows;
+    const uint32_t bar = bar0 + 8 * st;
+    if (lane < kPair) {
+      *reinterpret_cast<uint64_t*>(slots + (st * kPair + lane) * 16) = w;
+      *reinterpret_cast<int*>(slots + (st * kPair + lane) * 16 + 8) = rows;
     }
-    float s[kHeads];
+    const int loads = __popc(__ballot_sync(0xffffffffu, rows > 0));
+    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(loads) * Q::BYTES);
+    __syncwarp();
+    if (rows > 0)
+      bulk_g2s(smem_u32(stages + st * L::STAGE + lane * Q::BYTES),
+               a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES, Q::BYTES, bar);
+  };
+  for (int i = 0; i < min(kStages, ns); ++i) issue(i);
+
+  // ---- queries: one warp per head, normalised by a power of two, in fp32
+  for (int h = warp; h < 8; h += kWarps) {
+    float x[D / 32];
+    float top = 0.f;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) s[h] = -INFINITY;
-    if (t < rows) {
-      float x[D];
-#pragma unroll
-      for (int q = 0; q < Q::GROUPS; ++q) {
-        const uint2 c = *reinterpret_cast<const uint2*>(blk + Q::k_code(t, q));
-        const float sc = e4m3_to_f(blk[Q::k_scale(t, q)]);
-        uint32_t hh[8];
-        e2m1x8_to_h2(c.x, *reinterpret_cast<uint32_t(*)[4]>(hh));
-        e2m1x8_to_h2(c.y, *reinterpret_cast<uint32_t(*)[4]>(hh + 4));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 f = h2_to_f2(hh[e]);
-          x[16 * q + 2 * e] = f.x * sc;
-          x[16 * q + 2 * e + 1] = f.y * sc;
-        }
-      }
-      for (int f = 0; f < hr; ++f) {
-        const int d1 = a.pos.interleaved ? 2 * f : f, d2 = a.pos.interleaved ? 2 * f + 1 : f + hr;
-        float sn, co;
-        turn_sincos(delta, a.pos.turns[f], sn, co);
-        const float x1 = x[d1], x2 = x[d2];
-        x[d1] = x1 * co - x2 * sn;
-        x[d2] = x1 * sn + x2 * co;
-      }
-      for (int h = 0; h < heads; ++h) {
-        float acc = 0.f;
-        for (int d = 0; d < D; ++d) acc = fmaf(qs[h][d], x[d], acc);
-        if (a.pos.kind == kAlibi) acc -= a.pos.slopes[h0 + h] * 1.4426950408889634f * float(m - start - t);
-        s[h] = acc;
-      }
-    }
-    // tile maxima, then the weights
-    for (int h = 0; h < heads; ++h) {
-      float x = s[h];
-      for (int off = 16; off; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-      // fmaxf drops a NaN score: carry it to the weights instead
-      if (lane == 0) red[h][warp] = x;
-    }
-    __syncthreads();
-    for (int h = 0; h < heads; ++h) {
-      const float mx = fmaxf(fmaxf(red[h][0], red[h][1]), fmaxf(red[h][2], red[h][3]));
-      const float mn = fmaxf(mrun[h], mx);
-      ps[h][tid] = mn == -INFINITY ? (s[h] != s[h] ? s[h] : 0.f) : exp2f(s[h] - mn);
-      if (tid == 0) alpha[h] = mn == -INFINITY ? 1.f : exp2f(mrun[h] - mn);
-    }
-    __syncthreads();
-    if (tid < heads) {
-      const float mx = fmaxf(fmaxf(red[tid][0], red[tid][1]), fmaxf(red[tid][2], red[tid][3]));
-      mrun[tid] = fmaxf(mrun[tid], mx);
-      float l = lrun[tid] * alpha[tid];
-      for (int i = 0; i < NK; ++i) l += ps[tid][i];
-      lrun[tid] = l;
+    for (int e = 0; e < D / 32; ++e) {
+      x[e] = h < heads ? __bfloat162float(a.q[((size_t)r * a.Hq + h0 + h) * D + e * 32 + lane]) : 0.f;
+      top = fmaxf(top, fabsf(x[e]));
     }
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-      if (h < heads) o[h] *= alpha[h];
-    const int d = tid % D, part = tid / D;
-    for (int pg = part; pg < NK / kPage; pg += KH)
-      for (int rr = 0; rr < vrows[pg]; ++rr) {
-        const float v = q4_v_value<D>(vblk[pg], rr, d);
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    // 2^ex >= top, within the normal numbers (a zero, infinite or NaN head takes ex = 0)
+    int ex = int(__float_as_uint(top) >> 23) - 126;
+    if (ex < -100 || ex > 100) ex = 0;
+    const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-          if (h < heads) o[h] = fmaf(ps[h][pg * kPage + rr], v, o[h]);
-      }
+    for (int e = 0; e < D / 32; ++e) {
+      const int d = e * 32 + lane;
+      qs[h * L::QROW + (d / L::DL) * (L::DL + 4) + d % L::DL] = x[e] * inv;
+    }
+    if (lane == 0) scs[h] = a.qk_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
   }
   __syncthreads();
-  pdl_trigger();
-  if constexpr (KH > 1) {
-    if (tid >= D)
-      for (int h = 0; h < heads; ++h) osum[h][tid - D] = o[h];
-    __syncthreads();
-    if (tid >= D) return;
-    for (int h = 0; h < heads; ++h) o[h] += osum[h][tid];
+
+  // columns 2t and 2t + 1 of the score fragment: their heads, factors and slopes
+  const int c0 = H8 ? 2 * t : (2 * t) & 3, c1 = c0 + 1;
+  const float sc0 = scs[c0], sc1 = scs[c1];
+  float sl0 = 0.f, sl1 = 0.f;
+  if constexpr (POS == kAlibi) {
+    if (a.pos.slopes) {
+      sl0 = c0 < heads ? a.pos.slopes[h0 + c0] * 1.4426950408889634f : 0.f;
+      sl1 = c1 < heads ? a.pos.slopes[h0 + c1] * 1.4426950408889634f : 0.f;
+    }
   }
-  for (int h = 0; h < heads; ++h) {
-    const float l = lrun[h];
-    const float inv = l != 0.f ? a.v_factor / l : 0.f;
-    const size_t row = (size_t)r * a.Hq + h0 + h;
-    a.out[row * D + tid] = __float2bfloat16_rn(o[h] * inv);
-    if (a.lse && tid == 0) a.lse[row] = (mrun[h] + log2f(l)) * 0.6931471805599453f;
+
+  // ---- this lane's query fragment: column gr, dimensions DL t .. DL t + DL - 1
+  uint32_t qhi[NKS][2], qlo[H8 ? NKS : 1][2];
+  const float* qh = qs + (H8 ? gr : (gr & 3)) * L::QROW;
+  const bool low_half = !H8 && gr >= 4;  // this lane holds the lo parts
+  auto put = [&](int e, float y0, float y1) {  // dimensions e, e + 1 of the lane's run
+    const uint32_t hi = pack_h2(y0, y1);
+    const float2 f = h2_to_f2(hi);
+    const uint32_t lo = pack_h2(y0 - f.x, y1 - f.y);
+    if constexpr (H8) {
+      qhi[e / 4][(e / 2) & 1] = hi;
+      qlo[e / 4][(e / 2) & 1] = lo;
+    } else {
+      qhi[e / 4][(e / 2) & 1] = low_half ? lo : hi;
+    }
+  };
+  if constexpr (POS == kAlibi) {
+#pragma unroll
+    for (int e = 0; e < L::DL; e += 2) put(e, qh[t * (L::DL + 4) + e], qh[t * (L::DL + 4) + e + 1]);
+  }
+  auto rotate_q = [&](uint32_t delta) {
+    const uint32_t dp = uint32_t(m) - delta;
+    const int rd = POS == kRope ? D : a.pos.rotary_dim, hr = rd / 2;
+    const bool tab = a.pos.table != nullptr && dp < uint32_t(a.pos.max_pos);
+    __syncwarp();
+    for (int f = lane; f < hr; f += 32) {
+      float s, c;
+      if (tab) {
+        c = a.pos.table[(size_t)dp * rd + f];
+        s = a.pos.table[(size_t)dp * rd + hr + f];
+      } else {
+        turn_sincos_fast(dp, a.pos.turns[f], s, c);
+      }
+      cs[f] = make_float2(c, s);
+    }
+    __syncwarp();
+    if constexpr (POS == kRope) {
+      const bool first = t < 2;  // this run lies in the first half; its partner two chunks on
+      const float* x1 = qh + (t & 1) * (L::DL + 4);
+      const float* x2 = x1 + 2 * (L::DL + 4);
+      const float4* cp = reinterpret_cast<const float4*>(cs + (t & 1) * L::DL);
+#pragma unroll
+      for (int e = 0; e < L::DL; e += 2) {
+        const float4 w = cp[e / 2];  // cos, sin of two frequencies
+        const float2 p1 = *reinterpret_cast<const float2*>(x1 + e), p2 = *reinterpret_cast<const float2*>(x2 + e);
+        put(e, first ? p1.x * w.x - p2.x * w.y : p1.x * w.y + p2.x * w.x,
+            first ? p1.y * w.z - p2.y * w.w : p1.y * w.w + p2.y * w.z);
+      }
+    } else {
+      const bool inter = a.pos.interleaved != 0;
+#pragma unroll
+      for (int e = 0; e < L::DL; e += 2) {
+        const int d = t * L::DL + e;
+        auto at = [&](int i) { return qh[(i / L::DL) * (L::DL + 4) + i % L::DL]; };
+        float y0 = at(d), y1 = at(d + 1);
+        if (d < rd) {
+          if (inter) {
+            const float2 w = cs[d / 2];
+            const float x0 = y0, x1 = y1;
+            y0 = x0 * w.x - x1 * w.y;
+            y1 = x0 * w.y + x1 * w.x;
+          } else {  // hr is a multiple of 8: both dimensions lie in the same half
+            const bool first = d < hr;
+            const int f = first ? d : d - hr, o = first ? d + hr : d - hr;
+            const float2 w0 = cs[f], w1 = cs[f + 1];
+            const float p0 = at(o), p1 = at(o + 1);
+            y0 = first ? y0 * w0.x - p0 * w0.y : p0 * w0.y + y0 * w0.x;
+            y1 = first ? y1 * w1.x - p1 * w1.y : p1 * w1.y + y1 * w1.x;
+          }
+        }
+        put(e, y0, y1);
+      }
+    }
+  };
+
+  float o[NKS][4];
+#pragma unroll
+  for (int i = 0; i < NKS; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
+  uint32_t cur_delta = 0xFFFFFFFFu;
+  bool first = true;
+
+  for (int i = 0; i < ns; ++i) {
+    const int st = i % kStages;
+    if (!mbar_wait(bar0 + 8 * st, uint32_t((i / kStages) & 1))) {
+      if (lane == 0) set_status(a.status, LAZY_STATUS_TIMEOUT);
+      for (int j = i + 1; j < min(ns, i + kStages); ++j)
+        mbar_wait(bar0 + 8 * (j % kStages), uint32_t((j / kStages) & 1));
+      break;
+    }
+    const uint8_t* blk0 = stages + st * L::STAGE;
+    int rows[kPair];
+    float s[kPair][4];
+#pragma unroll
+    for (int pp = 0; pp < kPair; ++pp) {
+      const uint64_t w = *reinterpret_cast<const uint64_t*>(slots + (st * kPair + pp) * 16);
+      rows[pp] = *reinterpret_cast<const int*>(slots + (st * kPair + pp) * 16 + 8);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[pp][e] = -INFINITY;
+      if (rows[pp] > 0) {
+        const uint8_t* blk = blk0 + pp * Q::BYTES;
+        if constexpr (POS != kAlibi) {
+          if (word_delta(w) != cur_delta) {
+            cur_delta = word_delta(w);
+            rotate_q(cur_delta);
+          }
+        }
+        // ---- S^T = K q^T
+        uint32_t kw[2][NW_], ksc[2][NW_ / 2];
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(blk + lane * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
+          kw[0][0] = x.x; kw[0][1] = x.y; kw[0][2] = x.z; kw[0][3] = x.w;
+          kw[1][0] = y.x; kw[1][1] = y.y; kw[1][2] = y.z; kw[1][3] = y.w;
+          const uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::KS + lane * 4);
+          const uint32_t sa = e4m3x2_to_h2(sw & 0xFFFFu), sb = e4m3x2_to_h2(sw >> 16);
+          ksc[0][0] = __byte_perm(sa, 0, 0x1010);
+          ksc[0][1] = __byte_perm(sa, 0, 0x3232);
+          ksc[1][0] = __byte_perm(sb, 0, 0x1010);
+          ksc[1][1] = __byte_perm(sb, 0, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(blk + lane * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(blk + 256 + lane * 8);
+          kw[0][0] = x.x; kw[0][1] = x.y;
+          kw[1][0] = y.x; kw[1][1] = y.y;
+          const uint32_t sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(blk + Q::KS + lane * 2));
+          ksc[0][0] = __byte_perm(sa, 0, 0x1010);
+          ksc[1][0] = __byte_perm(sa, 0, 0x3232);
+        }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NW_; ++x) {
+          uint32_t ra[4], rb[4];
+          e2m1x8_to_h2(kw[0][x], ra);
+          e2m1x8_to_h2(kw[1][x], rb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ra[e] = hmul2(ra[e], ksc[0][x / 2]);
+            rb[e] = hmul2(rb[e], ksc[1][x / 2]);
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            mma16816(acc, ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
+            if constexpr (H8)
+              mma16816(acc, ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
+          }
+        }
+        if constexpr (!H8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 2);  // hi + lo
+        }
+        s[pp][0] = acc[0] * sc0;
+        s[pp][1] = acc[1] * sc1;
+        s[pp][2] = acc[2] * sc0;
+        s[pp][3] = acc[3] * sc1;
+        if constexpr (POS == kAlibi) {
+          const float dist = float(int(word_delta(w) + kPage * word_pg(w)) + gr - m);
+          s[pp][0] += sl0 * dist;
+          s[pp][1] += sl1 * dist;
+          s[pp][2] += sl0 * (dist + 8.f);
+          s[pp][3] += sl1 * (dist + 8.f);
+        }
+        if (rows[pp] < kPage) {
+          if (gr >= rows[pp]) s[pp][0] = s[pp][1] = -INFINITY;
+          if (gr + 8 >= rows[pp]) s[pp][2] = s[pp][3] = -INFINITY;
+        }
+      }
+    }
+    // ---- lazy running maximum of each column
+    float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+    float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+    if (__any_sync(0xffffffffu, first || x0 > m0 + kTau || x1 > m1 + kTau)) {
+      first = false;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+      }
+      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+      const float a0 = exp2f(m0 - n0), a1 = exp2f(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int x = 0; x < NKS; ++x) {
+        o[x][0] *= a0;
+        o[x][1] *= a1;
+        o[x][2] *= a0;
+        o[x][3] *= a1;
+      }
+    }
+    const float f0 = kPOff - m0, f1 = kPOff - m1;
+#pragma unroll
+    for (int pp = 0; pp < kPair; ++pp) {
+      if (rows[pp] == 0) continue;
+      const float p0 = ex2_approx(s[pp][0] + f0), p1 = ex2_approx(s[pp][1] + f1);
+      const float p2 = ex2_approx(s[pp][2] + f0), p3 = ex2_approx(s[pp][3] + f1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      const uint32_t b0 = transpose8(pack_h2(p0, p1)), b1 = transpose8(pack_h2(p2, p3));
+      // ---- O^T += V^T P^T
+      const uint8_t* blk = blk0 + pp * Q::BYTES;
+      const int vg = D == 128 ? lane : (gr >> 1) * 4 + t;
+      uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::VS + vg * 4);
+      if (rows[pp] < kPage) {  // rows without a key: scale 0, so that what they hold cannot matter
+        const int rr = rows[pp] - 2 * t;  // bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
+                              (rr > 9 ? 0xFF000000u : 0u);
+        sw &= keep;
+      }
+      const uint32_t vs0 = e4m3x2_to_h2(sw & 0xFFFFu), vs1 = e4m3x2_to_h2(sw >> 16);
+      uint32_t va[2][D / 64], vb[2][D / 64];  // [row half][word]: codes of the even and the odd row
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(blk + Q::VC + 512 + lane * 16);
+        va[0][0] = x.x; va[0][1] = x.y; vb[0][0] = x.z; vb[0][1] = x.w;
+        va[1][0] = y.x; va[1][1] = y.y; vb[1][0] = y.z; vb[1][1] = y.w;
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
+        va[0][0] = x.x; vb[0][0] = x.y; va[1][0] = x.z; vb[1][0] = x.w;
+      }
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {
+        uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd dimensions of the word, both row halves
+        const uint32_t A0 = va[0][w], B0 = vb[0][w], A1 = va[1][w], B1 = vb[1][w];
+        // two rows' codes of one dimension side by side in a byte
+        e2m1x8_to_h2((A0 & 0x0F0F0F0Fu) | ((B0 << 4) & 0xF0F0F0F0u), e0);
+        e2m1x8_to_h2(((A0 >> 4) & 0x0F0F0F0Fu) | (B0 & 0xF0F0F0F0u), o0);
+        e2m1x8_to_h2((A1 & 0x0F0F0F0Fu) | ((B1 << 4) & 0xF0F0F0F0u), e1);
+        e2m1x8_to_h2(((A1 >> 4) & 0x0F0F0F0Fu) | (B1 & 0xF0F0F0F0u), o1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mma16816(o[4 * w + x], hmul2(e0[x], vs0), hmul2(o0[x], vs0), hmul2(e1[x], vs1), hmul2(o1[x], vs1), b0, b1);
+      }
+    }
+    __syncwarp();
+    if (i + kStages < ns) issue(i + kStages);
+  }
+  pdl_trigger();
+
+  // ---- merge the warps: O^T fragments hold dimensions D/8 gr + 2x (+1), columns 2t, 2t + 1
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+  }
+  __syncthreads();  // every stage is consumed
+  float* mo = reinterpret_cast<float*>(smem);   // [warp][8][D]
+  float* mml = mo + kWarps * 8 * D;             // [warp][8][2]
+  if (H8 || t < 2) {
+#pragma unroll
+    for (int x = 0; x < NKS; ++x) {
+      const int d = (D / 8) * gr + 2 * x;
+      *reinterpret_cast<float2*>(mo + (warp * 8 + c0) * D + d) = make_float2(o[x][0], o[x][2]);
+      *reinterpret_cast<float2*>(mo + (warp * 8 + c1) * D + d) = make_float2(o[x][1], o[x][3]);
+    }
+    if (gr == 0) {
+      mml[(warp * 8 + c0) * 2] = l0 != 0.f ? m0 : -INFINITY;
+      mml[(warp * 8 + c0) * 2 + 1] = l0;
+      mml[(warp * 8 + c1) * 2] = l1 != 0.f ? m1 : -INFINITY;
+      mml[(warp * 8 + c1) * 2 + 1] = l1;
+    }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < heads * D; x += kWarps * 32) {
+    const int h = x / D, d = x % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mml[(w * 8 + h) * 2]);
+    float O = 0.f, l = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(mml[(w * 8 + h) * 2] - M);
+        O += f * mo[(w * 8 + h) * D + d];
+        l += f * mml[(w * 8 + h) * 2 + 1];
+      }
+    }
+    const size_t rh = (size_t)r * a.Hq + h0 + h;
+    if (a.S == 1) {
+      a.out[rh * D + d] = __float2bfloat16_rn(l != 0.f ? O * (a.v_factor / l) : 0.f);
+      if (a.lse && d == 0) a.lse[rh] = (M + log2f(l) - kPOff) * 0.6931471805599453f;
+    } else {
+      a.part_o[(rh * a.S + split) * D + d] = O * a.v_factor;
+      if (d == 0) {
+        a.part_ml[(rh * a.S + split) * 2] = M - kPOff;
+        a.part_ml[(rh * a.S + split) * 2 + 1] = l;
+      }
+    }
   }
 }
 
+// Merge the splits' partial (O, max, sum) of one (row, head) by their log-sum-exp.
+template <int D>
+__global__ void __launch_bounds__(D) q4_merge_kernel(const float* __restrict__ po, const float* __restrict__ pml, int S,
+                                                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t rh = blockIdx.x;
+  const int d = threadIdx.x;
+  const float2* ml = reinterpret_cast<const float2*>(pml) + rh * S;
+  float M = -INFINITY;
+  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
+  float O = 0.f, l = 0.f;
+  if (M != -INFINITY)
+    for (int s = 0; s < S; ++s) {
+      const float2 x = ml[s];
+      const float f = exp2f(x.x - M);
+      O += f * po[(rh * S + s) * D + d];
+      l += f * x.y;
+    }
+  out[rh * D + d] = __float2bfloat16_rn(l != 0.f ? O / l : 0.f);
+  if (lse && d == 0) lse[rh] = (M + log2f(l)) * 0.6931471805599453f;
+}
+
+// Heads per CTA, and key splits: about four waves of resident CTAs, at least 8 pages per warp.
+int q4_heads(int Hq, int Hkv) { return min(Hq / Hkv, 8); }
+
+int q4_splits(int rows, int Hq, int Hkv, int max_blocks) {
+  const long long units = (long long)rows * (Hq / q4_heads(Hq, Hkv));
+  const long long want = ((long long)sm_count() * 16 + units - 1) / units;
+  const long long by_len = (max_blocks + kWarps * 8 - 1) / (kWarps * 8);
+  return int(max(1ll, min(min(want, by_len), 64ll)));
+}
+
+template <int D, bool H8, int POS>
+int launch_q4(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
+  auto kern = q4_decode_kernel<D, H8, POS>;
+  LAZY_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecL<D>::SMEM));
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, a, heads, a.Hq / a.Hkv / heads));
+  return LAZY_OK;
+}
+
+template <int D, bool H8>
+int launch_q4_pos(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
+  if (a.pos.kind == kAlibi || a.pos.kind == kNone) return launch_q4<D, H8, kAlibi>(a, heads, grid, st);
+  if (a.pos.rotary_dim != D || a.pos.interleaved) return launch_q4<D, H8, kRopeX>(a, heads, grid, st);
+  return launch_q4<D, H8, kRope>(a, heads, grid, st);
+}
+
+}  // namespace
+
 size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_mode) {
-  (void)rows; (void)Hq; (void)Hkv; (void)D; (void)max_blocks; (void)rows_mode;
-  return 0;
+  (void)rows_mode;
+  const size_t S = size_t(q4_splits(rows, Hq, Hkv, max_blocks));
+  if (S <= 1) return 0;
+  const size_t po = (size_t)rows * Hq * S * D * 4;
+  return (po + 255) / 256 * 256 + (size_t)rows * Hq * S * 8;
 }
 
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {
-  (void)ws;
-  (void)ws_bytes;
-  const int G = a.Hq / a.Hkv, heads = G < kHeads ? G : kHeads, ngrp = G / heads;
-  const long long ctas = (long long)a.rows * a.Hkv * ngrp;
-  if (ctas > 0x7FFFFFFFll) return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
-  auto kern = D == 128 ? (rows_mode ? q4_rows_kernel<128, true> : q4_rows_kernel<128, false>)
-                       : (rows_mode ? q4_rows_kernel<64, true> : q4_rows_kernel<64, false>);
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(unsigned(ctas)), dim3(128), 0, st, a, heads, ngrp));
+  const int heads = q4_heads(a.Hq, a.Hkv);
+  a.S = q4_splits(a.rows, a.Hq, a.Hkv, a.max_blocks);
+  if (a.S > 1) {
+    const size_t need = q4_ws_bytes(a.rows, a.Hq, a.Hkv, D, a.max_blocks, rows_mode);
+    if (!ws || ws_bytes < need)
+      return fail(LAZY_EINVAL, "workspace too small: need %zu bytes, got %zu", need, ws ? ws_bytes : 0);
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(LAZY_EINVAL, "workspace must be 256-byte aligned");
+    const size_t po = (size_t)a.rows * a.Hq * a.S * D * 4;
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (po + 255) / 256 * 256);
+  }
+  const long long ctas = (long long)a.rows * (a.Hq / heads) * a.S;
+  if (ctas > 0x7FFFFFFFll || (long long)a.rows * a.Hq > 0x7FFFFFFFll)
+    return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
+  const unsigned grid = unsigned(ctas);
+  if (a.pos.kind == kNone) a.pos.slopes = nullptr;
+  int rc;
+  if (D == 128)
+    rc = heads == 8 ? launch_q4_pos<128, true>(a, heads, grid, st) : launch_q4_pos<128, false>(a, heads, grid, st);
+  else
+    rc = heads == 8 ? launch_q4_pos<64, true>(a, heads, grid, st) : launch_q4_pos<64, false>(a, heads, grid, st);
+  if (rc || a.S == 1) return rc;
+  const unsigned rh = unsigned((long long)a.rows * a.Hq);
+  if (D == 128)
+    LAZY_CUDA_TRY(launch_pdl(q4_merge_kernel<128>, dim3(rh), dim3(128), 0, st, (const float*)a.part_o,
+                             (const float*)a.part_ml, a.S, a.out, a.lse));
+  else
+    LAZY_CUDA_TRY(launch_pdl(q4_merge_kernel<64>, dim3(rh), dim3(64), 0, st, (const float*)a.part_o,
+                             (const float*)a.part_ml, a.S, a.out, a.lse));
   return LAZY_OK;
 }
 
