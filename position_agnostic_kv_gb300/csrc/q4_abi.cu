@@ -6,7 +6,7 @@ using namespace lazykv;
 
 static int check_q4(const char* what, int B, int max_blocks, int Hq, int Hkv, int D, int num_pages, const void* cache,
                     const void* q, const void* out, const void* meta, const void* q_start, const void* doc_blocks,
-                    float k_scale, float v_scale, float* kf, float* vf) {
+                    float scale, float k_scale, float v_scale, float* kf, float* vf) {
   if (B < 0 || max_blocks <= 0 || Hq <= 0 || Hkv <= 0 || num_pages <= 0)
     return fail(LAZY_EINVAL, "%s: bad sizes (B=%d max_blocks=%d Hq=%d Hkv=%d num_pages=%d)", what, B, max_blocks, Hq,
                 Hkv, num_pages);
@@ -16,6 +16,7 @@ static int check_q4(const char* what, int B, int max_blocks, int Hq, int Hkv, in
   if (G > 8 && G % 8) return fail(LAZY_EINVAL, "%s: Hq/Hkv = %d: above 8 it must be a multiple of 8", what, G);
   if (G < 8 && (G & (G - 1))) return fail(LAZY_EINVAL, "%s: Hq/Hkv = %d must be a power of two below 8", what, G);
   if (num_pages > (1 << 24)) return fail(LAZY_ERANGE, "%s: num_pages above 2^24", what);
+  if (!(scale >= 0.f && scale <= 3.0e38f)) return fail(LAZY_EINVAL, "%s: scale must be positive (or 0 for the default)", what);
   if (!q4_factor(k_scale, kf) || !q4_factor(v_scale, vf))
     return fail(LAZY_EINVAL, "%s: k_scale and v_scale must be powers of two in [2^-32, 2^32] (or 0 for 1)", what);
   if (B == 0) return LAZY_OK;
@@ -55,7 +56,7 @@ extern "C" int lazy_attn_decode_q4(const void* q, const int32_t* seq_len, const 
   Q4Args a = {};
   float kf, vf;
   int rc = check_q4("lazy_attn_decode_q4", B, max_blocks, Hq, Hkv, D, num_pages, kv_cache, q, out, meta, q_start,
-                    doc_blocks, k_scale, v_scale, &kf, &vf);
+                    doc_blocks, scale, k_scale, v_scale, &kf, &vf);
   if (rc) return rc;
   if (B > 0 && !seq_len) return fail(LAZY_EINVAL, "lazy_attn_decode_q4: seq_len is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
@@ -77,7 +78,7 @@ extern "C" int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const in
   float kf, vf;
   if (total_q < 0 || max_q < 0) return fail(LAZY_EINVAL, "lazy_attn_prefill_q4: bad total_q / max_q");
   int rc = check_q4("lazy_attn_prefill_q4", total_q == 0 ? 0 : B, max_blocks, Hq, Hkv, D, num_pages, kv_cache, q, out,
-                    meta, q_start, doc_blocks, k_scale, v_scale, &kf, &vf);
+                    meta, q_start, doc_blocks, scale, k_scale, v_scale, &kf, &vf);
   if (rc) return rc;
   if (B > 0 && total_q > 0 && !cu_q) return fail(LAZY_EINVAL, "lazy_attn_prefill_q4: cu_q is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
@@ -87,5 +88,6 @@ extern "C" int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const in
   fill_args(a, q, q_start, doc_blocks, meta, B, max_blocks, kv_cache, num_pages, Hq, Hkv, kf, vf, out, lse);
   a.cu_q = cu_q;
   a.rows = total_q;
+  if (q4_use_tc(Hq, Hkv)) return max_q > 0 ? run_q4_tc(a, D, max_q, static_cast<cudaStream_t>(stream)) : LAZY_OK;
   return run_q4_rows(a, D, true, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }

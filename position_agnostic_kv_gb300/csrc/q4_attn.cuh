@@ -55,6 +55,16 @@ __device__ __forceinline__ int q4_rows(uint64_t w, int m) {
   return max(0, min(min(int(word_nvalid(w)), kPage), m - start + 1));
 }
 
+// Exponent ex of the power of two that normalises a query row whose largest magnitude is `top`: the row
+// times 2^-ex lies in [-1, 1] (rows below 2^-60 keep ex = 0: their scores vanish; infinities and NaN too, and
+// pass through).
+__device__ __forceinline__ int q4_exponent(float top) {
+  const int ex = int(__float_as_uint(top) >> 23) - 126;
+  return ex < -60 || ex > 128 ? 0 : min(ex, 126);
+}
+
+bool q4_use_tc(int Hq, int Hkv);
+int run_q4_tc(Q4Args& a, int D, int max_q, cudaStream_t st);
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st);
 size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_mode);
 

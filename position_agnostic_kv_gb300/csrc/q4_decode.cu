@@ -155,13 +155,11 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
       x[e] = h < heads ? __bfloat162float(a.q[((size_t)r * a.Hq + h0 + h) * D + e * 32 + lane]) : 0.f;
-      top = fmaxf(top, fabsf(x[e]));
+      top = fmaxf(top, fabsf(x[e]));  // a NaN does not raise it, and passes through
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    // 2^ex >= top, within the normal numbers (a zero, infinite or NaN head takes ex = 0)
-    int ex = int(__float_as_uint(top) >> 23) - 126;
-    if (ex < -100 || ex > 100) ex = 0;
+    const int ex = q4_exponent(top);
     const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {

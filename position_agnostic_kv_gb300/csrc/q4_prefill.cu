@@ -1,0 +1,965 @@
+// Causal prefill over the 4-bit paged cache on the 5th-generation tensor cores.
+//
+// Mathematics: per KV head, S = (R_m q)(R_Delta k)^T for every query row (a query head of a token at
+// position m) and visible key, an online softmax in base 2 over 128-key tiles, O += P V.
+//
+// One CTA per (request, KV head, 256 query rows = two 128-row Q tiles, rows = (token, head) pairs), 512
+// threads, one CTA per SM.  Roles:
+//   warps 0-3 / 4-7  softmax of Q tile 0 / 1 (thread = TMEM lane = row): the Q operand (rotated by m,
+//              normalised by a power of two per row, f16, 128-byte swizzle), then per tile the scores from
+//              TMEM, mask, running maximum (moved only when beaten by more than 8), P back to TMEM over S
+//              as f16, held as 2^(s - max + 7); the epilogue.
+//   warps 8-11 dequantisation: each tile's packed pages (9 D bytes of keys, 9 D of values per page)
+//              become the f16 operands.  Keys: code times scale is exact in f16; the rotation by the page's
+//              Delta then rounds cos, sin, one product and the sum to f16 (2^-12 each: 2 instructions per
+//              value against 3.5 through fp32; the 4-bit codes themselves are off by up to 2^-3 of a
+//              group's maximum).  Values: exact in f16.  A thread owns 8 frequencies (two runs of 8
+//              dimensions) of 8 rows of a page; the packed pages lie 9 D + pad bytes apart, so that its
+//              word loads meet no bank conflicts, and values are stored even and odd rows first in turn for
+//              the same reason.
+//   warp 12    producer: block words one tile ahead, one bulk copy per page into a 2-stage ring of packed
+//              keys and a 1-stage ring of packed values.
+//   warp 13    TMEM owner and MMA issuer: QK0(j) QK1(j) | PV0(j) QK0(j+1) PV1(j) QK1(j+1) | ...
+// Both f16 rings have 2 stages.  The dequantisation runs a tile ahead: keys of tile j + 1, then values
+// of tile j.  TMEM: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P_i in the first half of S_i.
+// With one live Q tile S0 and S1 double-buffer its scores; in launches whose CTAs all have one (KH) the two
+// softmax warpgroups each take half of every tile's keys and merge in the epilogue.
+//
+// What bounds it: the softmax (one exponential and ~4 other instructions per score) beside the tensor
+// pipe; the packed cache is read at 18 D / 16 bytes per key and head.  Every wait is bounded.
+#include <cfloat>
+
+#include "q4_attn.cuh"
+#include "tcgen05.cuh"
+
+namespace lazykv {
+
+namespace tcq {
+
+using namespace tc;
+
+constexpr int kM = 128, kQT = 2, kN = 128;
+constexpr int kPagesPerTile = kN / kPage;
+constexpr int kSlots = 6;  // per-tile metadata: published up to 5 tiles ahead of the softmax's use
+constexpr int kThreads = 512;
+constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13;
+constexpr int kRegsLaunch = 128;
+// registers per thread after the re-split: softmax, dequantisation, producer + MMA; they add up to the launch's
+template <bool KH> struct Regs {
+  static constexpr int softmax = KH ? 176 : 184, deq = KH ? 72 : 64, issue = KH ? 88 : 80;
+  static_assert(2 * softmax + deq + issue == 4 * kRegsLaunch, "warpgroup register shares");
+};
+constexpr float kTau = 8.0f, kPOff = 7.0f;
+
+enum : int {
+  B_PK_FULL = 0,   // [2] packed keys landed (bytes)
+  B_PK_FREE = 2,   // [2] packed keys read (128 arrivals)
+  B_PV_FULL = 4,   // packed values landed
+  B_PV_FREE = 5,   // packed values read
+  B_K_READY = 6,   // [2] K operand written (128)
+  B_K_FREE = 8,    // [2] every QK^T of the stage done (commit)
+  B_V_READY = 10,  // [2] V operand written (128)
+  B_V_FREE = 12,   // [2] every PV of the stage done (commit)
+  B_S_FULL = 14,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
+  B_P_FULL = 16,   // [2] P in TMEM, O rescaled (128, KH 256)
+  B_Q_READY = 18,  // Q operands written (256)
+  B_FINAL = 19,    // all MMAs done (commit)
+  B_PV_DONE = 20,  // one live Q tile: a tile's PV done (commit)
+  NBAR = 21
+};
+
+template <int D>
+struct Layout {
+  static constexpr int BLK = kM * 128;
+  static constexpr int TILE = kN * D * 2;
+  static constexpr int QTILE = kM * D * 2;
+  static constexpr int PKS = D == 128 ? 1184 : 656;  // bytes between packed key pages (9 D + pad)
+  static constexpr int PVS = 9 * D;
+  static constexpr int K_OFF = kQT * QTILE;
+  static constexpr int V_OFF = K_OFF + 2 * TILE;
+  static constexpr int PK_OFF = V_OFF + 2 * TILE;
+  static constexpr int PV_OFF = PK_OFF + 2 * kPagesPerTile * PKS;
+  static constexpr int PSTART_OFF = PV_OFF + kPagesPerTile * PVS;              // int [slot][8] first key position
+  static constexpr int PINFO_OFF = PSTART_OFF + kSlots * kPagesPerTile * 4;    // int2 [slot][8] {Delta, rows}
+  static constexpr int FLAG_OFF = PINFO_OFF + kSlots * kPagesPerTile * 8;      // int [slot] every key visible
+  static constexpr int TURNS_OFF = FLAG_OFF + kSlots * 8;
+  static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+};
+static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, int POS, bool KH>
+__global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a, int nmp, int long_first) {
+  using L = Layout<D>;
+  using Q = Q4<D>;
+  constexpr bool kRotate = (POS == kRope || POS == kRopeX);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (sb - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // block order: (request, head) outermost, or (few of those) the longest query blocks first
+  const int split = int(blockIdx.x) % a.S;
+  int u = int(blockIdx.x) / a.S, mp, g, b;
+  if (long_first) {
+    const int bg = u % (a.B * a.Hkv);
+    mp = nmp - 1 - u / (a.B * a.Hkv);
+    g = bg % a.Hkv;
+    b = bg / a.Hkv;
+  } else {
+    mp = u % nmp;
+    u /= nmp;
+    g = u % a.Hkv;
+    b = u / a.Hkv;
+  }
+  pdl_wait();
+  const int G = a.Hq / a.Hkv;
+  const int tpt = kM / G;  // tokens per Q tile
+  const int qs = a.q_start[b];
+  const bool dec = a.seq_len != nullptr;
+  const int q0 = dec ? b : a.cu_q[b];
+  const int Lq = dec ? 1 : a.cu_q[b + 1] - q0;
+  const int mbase = dec ? a.seq_len[b] - 1 : qs;
+  const int tok0 = mp * kQT * tpt;
+  if (tok0 >= Lq) return;  // uniform for the CTA, before any barrier or TMEM use
+  const int nq = (tok0 + tpt < Lq) ? 2 : 1;
+  const int ntok = min(kQT * tpt, Lq - tok0);
+  const int m_min = mbase + tok0, m_max = mbase + tok0 + ntok - 1;
+  const int rel = m_max - qs;
+  int nb = max(0, a.doc_blocks[b]) + (rel >= 0 ? rel / kPage + 1 : 0);
+  if (nb > a.max_blocks) {
+    if (threadIdx.x == 0) set_status(a.status, LAZY_STATUS_BAD_ROW);
+    nb = a.max_blocks;
+  }
+  const int ntiles_all = (nb + kPagesPerTile - 1) / kPagesPerTile;
+  const int chunk = (ntiles_all + a.S - 1) / a.S;
+  const int t0 = split * chunk;
+  const int ntiles = min(ntiles_all, t0 + chunk) - t0;
+  if (ntiles <= 0) {  // nothing to see: a neutral partial, or (no split) an empty row
+    for (int i = threadIdx.x; i < ntok * G; i += blockDim.x) {
+      const size_t rh = (size_t)(q0 + tok0 + i / G) * a.Hq + g * G + i % G;
+      if (a.S > 1) {
+        a.part_ml[(rh * a.S + split) * 2] = -INFINITY;
+        a.part_ml[(rh * a.S + split) * 2 + 1] = 0.f;
+        for (int c = 0; c < D; ++c) a.part_o[(rh * a.S + split) * D + c] = 0.f;
+      } else {
+        for (int c = 0; c < D; ++c) a.out[rh * D + c] = __float2bfloat16_rn(0.f);
+        if (a.lse) a.lse[rh] = -INFINITY;
+      }
+    }
+    return;
+  }
+
+  const uint32_t sQ0 = sb, sK0 = sb + L::K_OFF, sV0 = sb + L::V_OFF;
+  const uint32_t sPK = sb + L::PK_OFF, sPV = sb + L::PV_OFF;
+  int* pstart = reinterpret_cast<int*>(sm + L::PSTART_OFF);
+  int2* pinfo = reinterpret_cast<int2*>(sm + L::PINFO_OFF);
+  int* flags = reinterpret_cast<int*>(sm + L::FLAG_OFF);
+  unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + L::TURNS_OFF);
+  const uint32_t bar0 = sb + L::BAR_OFF;
+  auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(BAR(B_PK_FULL + s), 1);
+      mbar_init(BAR(B_PK_FREE + s), 128);
+      mbar_init(BAR(B_K_READY + s), 128);
+      mbar_init(BAR(B_K_FREE + s), 1);
+      mbar_init(BAR(B_V_READY + s), 128);
+      mbar_init(BAR(B_V_FREE + s), 1);
+      mbar_init(BAR(B_S_FULL + s), 1);
+      mbar_init(BAR(B_P_FULL + s), KH ? 256 : 128);
+    }
+    mbar_init(BAR(B_PV_FULL), 1);
+    mbar_init(BAR(B_PV_FREE), 128);
+    mbar_init(BAR(B_Q_READY), 2 * 128);
+    mbar_init(BAR(B_FINAL), 1);
+    mbar_init(BAR(B_PV_DONE), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if constexpr (kRotate)
+    for (int i = threadIdx.x; i < D / 2; i += blockDim.x) turns[i] = a.pos.turns[i];
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    // ============================ Q operand, softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<KH>::softmax));
+    const int qt = warp >> 2;  // the warpgroup's Q tile, or (KH) its half of the keys
+    const int r = threadIdx.x & (kM - 1);
+    const int token = tok0 + (KH ? 0 : qt * tpt) + r / G;
+    const int h = g * G + r % G;
+    const bool valid = token < Lq && r < tpt * G;
+    const int m_row = valid ? mbase + token : -1;
+    float* rfac = reinterpret_cast<float*>(sm + L::QTILE + 4096);  // KH: row factors, in the unused second Q tile
+    float rf = 0.f;  // score -> base-2 logit
+    if (KH && qt == 1) {
+      mbar_arrive(BAR(B_Q_READY));
+    } else {
+      const uint32_t sQ = sQ0 + uint32_t(qt * L::QTILE);
+      auto qaddr = [&](int k) { return sQ + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)(q0 + token) * a.Hq + h) * D);
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint4 x = valid ? src[k] : make_uint4(0, 0, 0, 0);
+        st_shared_v4(qaddr(k), x);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(xs[e] & 0x7FFFu, (xs[e] >> 16) & 0x7FFFu));
+      }
+      const int ex = q4_exponent(__uint_as_float(top << 16));
+      rf = a.qk_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
+      const float sc = __uint_as_float(uint32_t(127 - ex) << 23);
+      if (KH) rfac[r] = rf;
+      auto pack = [&](const float (&y)[8]) {
+        return make_uint4(f2_to_h2(y[0] * sc, y[1] * sc), f2_to_h2(y[2] * sc, y[3] * sc),
+                          f2_to_h2(y[4] * sc, y[5] * sc), f2_to_h2(y[6] * sc, y[7] * sc));
+      };
+      auto unpack = [](uint4 x, float (&y)[8]) {
+        y[0] = bf_lo(x.x); y[1] = bf_hi(x.x); y[2] = bf_lo(x.y); y[3] = bf_hi(x.y);
+        y[4] = bf_lo(x.z); y[5] = bf_hi(x.z); y[6] = bf_lo(x.w); y[7] = bf_hi(x.w);
+      };
+      int done = 0;
+      if constexpr (kRotate) {
+        const uint32_t m = uint32_t(max(m_row, 0));
+        const int rd = a.pos.rotary_dim, hr = rd / 2;
+        const bool tab = a.pos.table != nullptr && m < uint32_t(a.pos.max_pos);
+        auto csf = [&](int i, float& sn, float& co) {
+          if (tab) {
+            co = a.pos.table[(size_t)m * rd + i];
+            sn = a.pos.table[(size_t)m * rd + hr + i];
+          } else {
+            turn_sincos_fast(m, turns[i], sn, co);
+          }
+        };
+        if (!a.pos.interleaved) {
+#pragma unroll 1
+          for (int c = 0; c < hr / 8; ++c) {
+            float x1[8], x2[8], y1[8], y2[8];
+            unpack(ld_shared_v4(qaddr(c)), x1);
+            unpack(ld_shared_v4(qaddr(c + hr / 8)), x2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float sn, co;
+              csf(c * 8 + e, sn, co);
+              y1[e] = x1[e] * co - x2[e] * sn;
+              y2[e] = x1[e] * sn + x2[e] * co;
+            }
+            st_shared_v4(qaddr(c), pack(y1));
+            st_shared_v4(qaddr(c + hr / 8), pack(y2));
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < rd / 8; ++k) {
+            float x[8], y[8];
+            unpack(ld_shared_v4(qaddr(k)), x);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float sn, co;
+              csf(k * 4 + w, sn, co);
+              y[2 * w] = x[2 * w] * co - x[2 * w + 1] * sn;
+              y[2 * w + 1] = x[2 * w] * sn + x[2 * w + 1] * co;
+            }
+            st_shared_v4(qaddr(k), pack(y));
+          }
+        }
+        done = rd / 8;
+      }
+#pragma unroll 1
+      for (int k = done; k < D / 8; ++k) {
+        float x[8];
+        unpack(ld_shared_v4(qaddr(k)), x);
+        st_shared_v4(qaddr(k), pack(x));
+      }
+      fence_async_smem();
+      mbar_arrive(BAR(B_Q_READY));
+    }
+    if (KH || qt < nq) {
+      bool ok = true;
+      if (KH && qt == 1) {
+        ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
+        rf = rfac[r];
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      const float2 rf2 = make_float2(rf, rf);
+      float slope = 0.f;
+      if constexpr (POS == kAlibi)
+        if (a.pos.slopes && valid) slope = a.pos.slopes[h] * 1.4426950408889634f;
+      const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+      const uint32_t tO = tl + uint32_t(2 * kN + qt * 128);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int slot = j % kSlots;
+        const int buf = nq == 2 ? qt : (j & 1);
+        const uint32_t tS = tl + uint32_t(buf * kN);
+        const bool got_s =
+            wait_bar(BAR(B_S_FULL + buf), uint32_t(nq == 2 ? (j & 1) : ((j >> 1) & 1)), abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
+        tc_fence_after();
+        const bool fast = flags[slot * 2] != 0;
+        constexpr int NK = KH ? kN / 2 : kN, NPG = NK / kPage;
+        const int pg0 = KH ? NPG * qt : 0;
+        uint32_t v[NK];
+#pragma unroll
+        for (int c = 0; c < NK / 32; ++c)
+          tmem_ld32(tS + uint32_t(pg0 * kPage + 32 * c), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+        tmem_wait_ld();
+        // ALiBi: the scores become logits here, the per-key part slope t of the bias added; its per-page
+        // part slope (pstart - m) goes onto the page's maximum and exponent offset
+        float bpg[NPG];
+        if constexpr (POS == kAlibi) {
+#pragma unroll
+          for (int pp = 0; pp < NPG; ++pp) {
+            bpg[pp] = slope * float(pstart[slot * kPagesPerTile + pg0 + pp] - m_row);
+#pragma unroll
+            for (int t = 0; t < kPage; t += 2) {
+              float2 x = make_float2(__uint_as_float(v[pp * kPage + t]), __uint_as_float(v[pp * kPage + t + 1]));
+              x = __ffma2_rn(x, rf2, make_float2(slope * float(t), slope * float(t + 1)));
+              v[pp * kPage + t] = __float_as_uint(x.x);
+              v[pp * kPage + t + 1] = __float_as_uint(x.y);
+            }
+          }
+        }
+        if (!fast) {  // row t of a page holds key p = pstart + t; visible iff t < rows and p <= m
+#pragma unroll
+          for (int pp = 0; pp < NPG; ++pp) {
+            const int hi = min(pinfo[slot * kPagesPerTile + pg0 + pp].y,
+                               m_row - pstart[slot * kPagesPerTile + pg0 + pp] + 1);
+#pragma unroll
+            for (int t = 0; t < kPage; ++t)
+              if (t >= hi) v[pp * kPage + t] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mq[NPG];
+#pragma unroll
+        for (int q = 0; q < NPG; ++q) {
+          const float* x = reinterpret_cast<const float*>(v + 16 * q);
+          float m = max3f(x[0], x[1], x[2]);
+#pragma unroll
+          for (int e = 3; e < 15; e += 2) m = max3f(m, x[e], x[e + 1]);
+          mq[q] = fmaxf(m, x[15]);
+          if constexpr (POS == kAlibi) mq[q] += bpg[q];
+        }
+        float mx;
+        if constexpr (KH)
+          mx = max3f(max3f(mq[0], mq[1], mq[2]), mq[3], mq[3]);
+        else
+          mx = max3f(max3f(mq[0], mq[1], mq[2]), max3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
+        if constexpr (POS != kAlibi) mx *= rf;  // rf > 0
+        const bool need = mx > m_run + kTau;
+        const float m_new = need ? mx : m_run;
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        float2 mneg[NPG];
+#pragma unroll
+        for (int pp = 0; pp < NPG; ++pp) {
+          const float o = POS == kAlibi ? bpg[pp] - m_use + kPOff : kPOff - m_use;
+          mneg[pp] = make_float2(o, o);
+        }
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                          make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int e = 0; e < NK / 2; ++e) {
+          float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          if constexpr (POS == kAlibi)
+            x = __fadd2_rn(x, mneg[e / (kPage / 2)]);
+          else
+            x = __ffma2_rn(x, rf2, mneg[e / (kPage / 2)]);
+          const float2 ev = make_float2(ex2(x.x), ex2(x.y));
+          sum4[e & 3] = __fadd2_rn(sum4[e & 3], ev);
+          v[e] = f2_to_h2(ev.x, ev.y);
+        }
+        const float2 s01 = __fadd2_rn(sum4[0], sum4[1]), s23 = __fadd2_rn(sum4[2], sum4[3]);
+        const float2 s03 = __fadd2_rn(s01, s23);
+        const float sum = s03.x + s03.y;
+        const float alpha = (j > 0 && need && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
+        l_run = (j == 0) ? sum : l_run * alpha + sum;
+        if (nq == 1 && j > 0) {  // S of tile j was issued before PV of tile j - 1: the rescale waits for it
+          const bool got_pv = wait_bar(BAR(B_PV_DONE), uint32_t((j - 1) & 1), abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, got_pv)) { ok = false; break; }
+          tc_fence_after();
+        }
+        if (__any_sync(0xffffffffu, j > 0 && alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + uint32_t(c * 32), o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + uint32_t(c * 32), o);
+          }
+        }
+        m_run = m_new;
+#pragma unroll
+        for (int c = 0; c < NK / 64; ++c)
+          tmem_st32(tS + uint32_t(pg0 * kPage + 32 * c), *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(B_P_FULL + buf));
+      }
+      const bool got_last = ok && wait_bar(BAR(B_FINAL), 0, abort_flag, a.status);
+      const size_t rh = (size_t)(q0 + token) * a.Hq + h;
+      const size_t pi = rh * a.S + split;
+      // 32 output columns of this row: scaled partials (S > 1) or the bf16 result
+      auto store = [&](int col, const float (&o)[32]) {
+        if (a.S > 1) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + pi * D + col);
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + rh * D + col);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+            dst[q4] = make_uint4(f2_to_bf2(o[8 * q4], o[8 * q4 + 1]), f2_to_bf2(o[8 * q4 + 2], o[8 * q4 + 3]),
+                                 f2_to_bf2(o[8 * q4 + 4], o[8 * q4 + 5]), f2_to_bf2(o[8 * q4 + 6], o[8 * q4 + 7]));
+        }
+      };
+      auto store_ml = [&](float M, float l) {
+        if (a.S > 1) {
+          a.part_ml[pi * 2] = l != 0.f ? M - kPOff : -INFINITY;
+          a.part_ml[pi * 2 + 1] = l;
+        } else if (a.lse) {
+          a.lse[rh] = (M + log2f(l) - kPOff) * 0.6931471805599453f;
+        }
+      };
+      if constexpr (KH) {
+        // the key halves' partial softmaxes, merged by their maxima and sums (exchanged in the unused
+        // second Q tile); each warpgroup writes half of the columns
+        float2* xml = reinterpret_cast<float2*>(sm + L::QTILE);
+        xml[qt * kM + r] = make_float2(l_run != 0.f ? m_run : -INFINITY, l_run);
+        named_sync(1, 2 * kM);
+        const float2 mine = xml[qt * kM + r], other = xml[(qt ^ 1) * kM + r];
+        const float2 hA = qt == 0 ? mine : other, hB = qt == 0 ? other : mine;
+        const float M = fmaxf(hA.x, hB.x);
+        const float wA = hA.y != 0.f ? ex2(hA.x - M) : 0.f, wB = hB.y != 0.f ? ex2(hB.x - M) : 0.f;
+        const float Lt = wA * hA.y + wB * hB.y;
+        if (__all_sync(0xffffffffu, got_last)) {
+          tc_fence_after();
+          const float inv = a.S > 1 ? a.v_factor : (Lt != 0.f ? a.v_factor / Lt : 0.f);
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            const int col = qt * (D / 2) + c * 32;
+            uint32_t oa[32], ob[32];
+            tmem_ld32(tl + uint32_t(2 * kN + col), oa);
+            tmem_ld32(tl + uint32_t(3 * kN + col), ob);
+            tmem_wait_ld();
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = (wA * __uint_as_float(oa[e]) + wB * __uint_as_float(ob[e])) * inv;
+            if (valid) store(col, o);
+          }
+          if (valid && qt == 0) store_ml(M, Lt);
+        }
+      } else if (__all_sync(0xffffffffu, got_last)) {
+        tc_fence_after();
+        const float inv = a.S > 1 ? a.v_factor : (l_run != 0.f ? a.v_factor / l_run : 0.f);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t oa[32];
+          tmem_ld32(tO + uint32_t(c * 32), oa);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(oa[e]) * inv;
+          if (valid) store(c * 32, o);
+        }
+        if (valid) store_ml(m_run, l_run);
+      }
+    }
+  } else if (warp < kProdWarp) {
+    // ============================ dequantisation
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<KH>::deq));
+    const int rt = threadIdx.x - kDeqWarp0 * 32;
+    const int ps = rt / kPage, l = rt % kPage;  // page slot, thread of the page
+    constexpr int NCP = D / 16;                 // runs of 8 dimensions in half a row
+    bool ok = true;  // once a wait gives up, the thread skips work but keeps arriving
+    uint32_t co[4], sn[4], nsn[4];  // f16 pairs
+    int cur_delta = -1;
+    int g_kind = 3, g_chunk = 0, g_part = 0, g_f0 = 0;
+    if constexpr (POS == kRopeX) {
+      // one task per thread, all 16 rows: a rotated chunk pair (kind 0), an interleaved chunk (1), or a
+      // chunk beyond rotary_dim (2)
+      const int rd = a.pos.rotary_dim;
+      const int nrot = a.pos.interleaved ? rd / 8 : rd / 16, ntail = (D - rd) / 8;
+      if (l < nrot) {
+        g_kind = a.pos.interleaved ? 1 : 0;
+        g_chunk = l;
+        g_part = l + rd / 16;
+        g_f0 = a.pos.interleaved ? 4 * l : 8 * l;
+      } else if (l < nrot + ntail) {
+        g_kind = 2;
+        g_chunk = rd / 8 + (l - nrot);
+      }
+    }
+    auto keys = [&](int j) {
+      const int s = j & 1, slot = j % kSlots;
+      if (ok) ok = wait_bar(BAR(B_PK_FULL + s), uint32_t((j >> 1) & 1), abort_flag, a.status);
+      if (ok && j >= 2) ok = wait_bar(BAR(B_K_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
+      const int2 pi = ok ? pinfo[slot * kPagesPerTile + ps] : make_int2(0, 0);
+      if (pi.y > 0) {  // rows past the page's keys are converted too (their scores are masked)
+        const uint32_t src = sPK + uint32_t((s * kPagesPerTile + ps) * L::PKS);
+        const uint32_t sK = sK0 + uint32_t(s * L::TILE);
+        if constexpr (POS != kRopeX) {
+          constexpr int HG = 16 / NCP;  // row groups
+          const int c = l % NCP, hg = l / NCP;
+          if constexpr (POS == kRope) {
+            if (pi.x != cur_delta) {
+              cur_delta = pi.x;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                float s0, c0, s1, c1;
+                turn_sincos_fast(uint32_t(pi.x), turns[8 * c + 2 * w], s0, c0);
+                turn_sincos_fast(uint32_t(pi.x), turns[8 * c + 2 * w + 1], s1, c1);
+                co[w] = f2_to_h2(c0, c1);
+                sn[w] = f2_to_h2(s0, s1);
+                nsn[w] = f2_to_h2(-s0, -s1);
+              }
+            }
+          }
+          const uint32_t sel = D == 128 ? ((c >> 1) & 1 ? 0x3232u : 0x1010u) : 0u;
+#pragma unroll
+          for (int i = 0; i < 8 / HG; ++i) {
+            const int r7 = hg + HG * i;
+            uint32_t sc1[2], sc2[2];  // scales of rows r7 and r7 + 8, first run and its partner
+            if constexpr (D == 128) {
+              const uint32_t w1 = ld_shared_u32(src + Q::KS + (r7 * 4 + (c >> 2)) * 4);
+              const uint32_t w2 = ld_shared_u32(src + Q::KS + (r7 * 4 + (c >> 2) + 2) * 4);
+              sc1[0] = __byte_perm(e4m3x2_to_h2(w1 & 0xFFFFu), 0, sel);
+              sc1[1] = __byte_perm(e4m3x2_to_h2(w1 >> 16), 0, sel);
+              sc2[0] = __byte_perm(e4m3x2_to_h2(w2 & 0xFFFFu), 0, sel);
+              sc2[1] = __byte_perm(e4m3x2_to_h2(w2 >> 16), 0, sel);
+            } else {
+              const uint32_t h1 = e4m3x2_to_h2(ld_shared_u16(src + Q::KS + (r7 * 4 + (c >> 1)) * 2));
+              const uint32_t h2 = e4m3x2_to_h2(ld_shared_u16(src + Q::KS + (r7 * 4 + (c >> 1) + 2) * 2));
+              sc1[0] = __byte_perm(h1, 0, 0x1010);
+              sc1[1] = __byte_perm(h1, 0, 0x3232);
+              sc2[0] = __byte_perm(h2, 0, 0x1010);
+              sc2[1] = __byte_perm(h2, 0, 0x3232);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const int t = r7 + 8 * hh, r = ps * kPage + t;
+              uint32_t x1[4], x2[4];
+              e2m1x8_to_h2(ld_shared_u32(src + t * (D / 2) + c * 4), x1);
+              e2m1x8_to_h2(ld_shared_u32(src + t * (D / 2) + D / 4 + c * 4), x2);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t p1 = hmul2(x1[w], sc1[hh]), p2 = hmul2(x2[w], sc2[hh]);
+                if constexpr (POS == kRope) {
+                  x1[w] = hfma2(p2, nsn[w], hmul2(p1, co[w]));  // x1 c - x2 s
+                  x2[w] = hfma2(p2, co[w], hmul2(p1, sn[w]));   // x1 s + x2 c
+                } else {
+                  x1[w] = p1;
+                  x2[w] = p2;
+                }
+              }
+              const uint32_t a1 = sK + swz(r, c);
+              const uint32_t a2 = (D == 128) ? sK + uint32_t(L::BLK) + swz(r, c) : sK + swz(r, c + 4);
+              st_shared_v4(a1, make_uint4(x1[0], x1[1], x1[2], x1[3]));
+              st_shared_v4(a2, make_uint4(x2[0], x2[1], x2[2], x2[3]));
+            }
+          }
+        } else {
+          auto chunk8 = [&](int t, int k, uint32_t (&x)[4]) {  // 8 scaled values: row t, dimensions 8k ..
+            e2m1x8_to_h2(ld_shared_u32(src + t * (D / 2) + k * 4), x);
+            const uint32_t sc = __byte_perm(e4m3x2_to_h2(ld_shared_u8(src + Q::k_scale(t, k >> 1))), 0, 0x1010);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[w] = hmul2(x[w], sc);
+          };
+          auto put = [&](int t, int k, const uint32_t (&x)[4]) {
+            st_shared_v4(sK + uint32_t((k >> 3) * L::BLK) + swz(ps * kPage + t, k & 7), make_uint4(x[0], x[1], x[2], x[3]));
+          };
+          if (g_kind < 2 && pi.x != cur_delta) {
+            cur_delta = pi.x;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float s0, c0, s1, c1;
+              if (g_kind == 0) {
+                turn_sincos_fast(uint32_t(pi.x), turns[g_f0 + 2 * w], s0, c0);
+                turn_sincos_fast(uint32_t(pi.x), turns[g_f0 + 2 * w + 1], s1, c1);
+                co[w] = f2_to_h2(c0, c1);
+                sn[w] = f2_to_h2(s0, s1);
+                nsn[w] = f2_to_h2(-s0, -s1);
+              } else {
+                turn_sincos_fast(uint32_t(pi.x), turns[g_f0 + w], s0, c0);
+                co[w] = f2_to_h2(c0, c0);
+                sn[w] = f2_to_h2(-s0, s0);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int t = 0; t < kPage && g_kind < 3; ++t) {
+            uint32_t x1[4], x2[4];
+            chunk8(t, g_chunk, x1);
+            if (g_kind == 0) {
+              chunk8(t, g_part, x2);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t p1 = x1[w], p2 = x2[w];
+                x1[w] = hfma2(p2, nsn[w], hmul2(p1, co[w]));
+                x2[w] = hfma2(p2, co[w], hmul2(p1, sn[w]));
+              }
+              put(t, g_part, x2);
+            } else if (g_kind == 1) {  // pairs inside a register: (x0 c - x1 s, x1 c + x0 s)
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                x1[w] = hfma2(__byte_perm(x1[w], 0, 0x1032), sn[w], hmul2(x1[w], co[w]));
+            }
+            put(t, g_chunk, x1);
+          }
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(BAR(B_PK_FREE + s));
+      mbar_arrive(BAR(B_K_READY + s));
+    };
+    auto values = [&](int j) {
+      const int s = j & 1, slot = j % kSlots;
+      if (ok) ok = wait_bar(BAR(B_PV_FULL), uint32_t(j & 1), abort_flag, a.status);
+      if (ok && j >= 2) ok = wait_bar(BAR(B_V_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
+      if (ok) {
+        // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
+        const int rows = pinfo[slot * kPagesPerTile + ps].y;
+        const uint32_t src = sPV + uint32_t(ps * L::PVS);
+        const uint32_t sV = sV0 + uint32_t(s * L::TILE);
+        const int t = l & 3;
+        const int rr = rows - 2 * t;  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
+                              (rr > 9 ? 0xFF000000u : 0u);
+        auto put = [&](int row, int cb, int ch, uint32_t codes, uint32_t scale) {
+          uint32_t x[4];
+          e2m1x8_to_h2(codes, x);
+          st_shared_v4(sV + uint32_t(cb * L::BLK) + swz(ps * kPage + row, ch),
+                       make_uint4(hmul2(x[0], scale), hmul2(x[1], scale), hmul2(x[2], scale), hmul2(x[3], scale)));
+        };
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int half = k & 1, q = (l >> 2) + 4 * (k >> 1);
+            const uint4 x = ld_shared_v4(src + half * 512 + (q * 4 + t) * 16);
+            const uint32_t sw = ld_shared_u32(src + 8 * D + q * 16 + t * 4) & keep;
+            const uint32_t hs = e4m3x2_to_h2(half ? sw >> 16 : sw & 0xFFFFu);
+            const int odd = q & 1;  // odd groups store their odd row first: no two lanes share a bank
+            const uint32_t a0 = odd ? x.z : x.x, a1 = odd ? x.w : x.y, b0 = odd ? x.x : x.z, b1 = odd ? x.y : x.w;
+            const uint32_t sa = __byte_perm(hs, 0, odd ? 0x3232 : 0x1010), sc = __byte_perm(hs, 0, odd ? 0x1010 : 0x3232);
+            const int ra = half * 8 + 2 * t + odd, rb = half * 8 + 2 * t + 1 - odd, ch = (2 * q) & 7;
+            put(ra, q >> 2, ch, a0, sa);
+            put(rb, q >> 2, ch, b0, sc);
+            put(ra, q >> 2, ch + 1, a1, sa);
+            put(rb, q >> 2, ch + 1, b1, sc);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int gd = (l >> 2) + 4 * k;  // run of 8 dimensions
+            const uint4 x = ld_shared_v4(src + (gd * 4 + t) * 16);
+            const uint32_t sw = ld_shared_u32(src + 8 * D + (gd >> 1) * 16 + t * 4) & keep;
+            const uint32_t h0 = e4m3x2_to_h2(sw & 0xFFFFu), h1 = e4m3x2_to_h2(sw >> 16);
+            put(2 * t, 0, gd, x.x, __byte_perm(h0, 0, 0x1010));
+            put(2 * t + 1, 0, gd, x.y, __byte_perm(h0, 0, 0x3232));
+            put(2 * t + 8, 0, gd, x.z, __byte_perm(h1, 0, 0x1010));
+            put(2 * t + 9, 0, gd, x.w, __byte_perm(h1, 0, 0x3232));
+          }
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(BAR(B_PV_FREE));
+      mbar_arrive(BAR(B_V_READY + s));
+    };
+    keys(0);
+    for (int j = 0; j < ntiles; ++j) {
+      if (j + 1 < ntiles) keys(j + 1);
+      values(j);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<KH>::issue));
+    if (warp == kProdWarp) {
+      // ============================ block words and bulk copies: K0 K1 V0 K2 V1 ...
+      const uint64_t* mrow = a.meta + (size_t)b * a.max_blocks;
+      // ALiBi visits the tiles newest first: the first tile then fixes each row's running maximum
+      auto tile_of = [&](int j) { return POS == kAlibi ? t0 + ntiles - 1 - j : t0 + j; };
+      auto fetch = [&](int j) -> uint64_t {
+        const int jb = tile_of(j) * kPagesPerTile + lane;
+        return (lane < kPagesPerTile && j < ntiles && jb < nb) ? ldg_u64(mrow + jb) : 0ull;
+      };
+      uint64_t w_next = fetch(0);
+      int issued_k = 0, issued_v = 0;
+      const uint8_t *v_cur = nullptr, *v_next = nullptr;  // this lane's blocks of tiles j and j + 1 (null: none)
+      auto issue_k = [&](int j) -> bool {
+        const int s = j & 1, slot = j % kSlots;
+        const uint64_t w = w_next;
+        w_next = fetch(j + 1);
+        int rows = 0, start = 0, delta = 0;
+        const int jb = tile_of(j) * kPagesPerTile + lane;
+        const uint8_t* blk = nullptr;
+        if (lane < kPagesPerTile && jb < nb) {
+          delta = int(word_delta(w));
+          start = delta + kPage * int(word_pg(w));
+          rows = q4_rows(w, m_max);
+          if (word_page(w) >= uint32_t(a.num_pages)) {
+            set_status(a.status, LAZY_STATUS_BAD_PAGE);
+            rows = 0;
+          }
+          if (rows > 0) blk = a.cache + ((size_t)word_page(w) * a.Hkv + g) * Q::BYTES;
+        }
+        if (j >= 2) {
+          const bool freed = wait_bar(BAR(B_PK_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, freed)) return false;
+        }
+        if (lane < kPagesPerTile) {
+          pinfo[slot * kPagesPerTile + lane] = make_int2(delta, rows);
+          pstart[slot * kPagesPerTile + lane] = start;
+        }
+        const int all16 = __all_sync(0xffffffffu, lane >= kPagesPerTile || rows == kPage);
+        // every key visible to every row: full pages that end at or before the first row's position
+        const int seen = __all_sync(0xffffffffu, lane >= kPagesPerTile || start + kPage - 1 <= m_min);
+        if (lane == 0) flags[slot * 2] = all16 && seen;
+        __syncwarp();
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, blk != nullptr));
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_PK_FULL + s), loads * uint32_t(Q::VC));
+        __syncwarp();
+        if (blk) bulk_g2s(sPK + uint32_t((s * kPagesPerTile + lane) * L::PKS), blk, Q::VC, BAR(B_PK_FULL + s));
+        v_next = blk;
+        __syncwarp();
+        issued_k = j + 1;
+        return true;
+      };
+      auto issue_v = [&](int j) -> bool {
+        if (j >= 1) {
+          const bool freed = wait_bar(BAR(B_PV_FREE), uint32_t((j - 1) & 1), abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, freed)) return false;
+        }
+        const uint8_t* blk = v_cur;
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, blk != nullptr));
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_PV_FULL), loads * uint32_t(Q::BYTES - Q::VC));
+        __syncwarp();
+        if (blk) bulk_g2s(sPV + uint32_t(lane * L::PVS), blk + Q::VC, Q::BYTES - Q::VC, BAR(B_PV_FULL));
+        __syncwarp();
+        issued_v = j + 1;
+        return true;
+      };
+      bool ok = issue_k(0);
+      for (int j = 0; j < ntiles && ok; ++j) {
+        v_cur = v_next;
+        if (j + 1 < ntiles) ok = issue_k(j + 1);
+        if (ok) ok = issue_v(j);
+      }
+      // never leave copies in flight: wait (bounded) for the last loads
+      if (lane == 0) {
+        for (int j = max(0, issued_k - 2); j < issued_k; ++j) {
+          WaitClock clk;
+          while (!mbar_test(BAR(B_PK_FULL + (j & 1)), uint32_t((j >> 1) & 1)) && !clk.expired()) {
+          }
+        }
+        if (issued_v > 0) {
+          WaitClock clk;
+          while (!mbar_test(BAR(B_PV_FULL), uint32_t((issued_v - 1) & 1)) && !clk.expired()) {
+          }
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ============================ MMA issue (one thread)
+      if (lane == 0) {
+        constexpr uint32_t IQK = idesc_mma(kM, kN, 0, 1);
+        constexpr uint32_t IPV = idesc_mma(kM, D, 1, 1);
+        bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
+        auto wait = [&](int bar, int phase) -> bool {
+          return wait_bar(BAR(bar), uint32_t(phase & 1), abort_flag, a.status);
+        };
+        auto qk = [&](int qt, int j, int buf) {  // S_buf = Q_qt K_j^T
+          const uint32_t sK = sK0 + uint32_t((j & 1) * L::TILE), sQ = sQ0 + uint32_t(qt * L::QTILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = uint32_t((kk >> 2) * L::BLK + (kk & 3) * 32);
+            mma_bf16(tmem + uint32_t(buf * kN), sdesc(sQ + off, 16, 1024), sdesc(sK + off, 16, 1024), IQK,
+                     kk > 0 ? 1u : 0u);
+          }
+          mma_commit(BAR(B_S_FULL + buf));
+        };
+        auto pv = [&](int qt, int jj) {  // O_qt += P_qt V_jj
+          const uint32_t sV = sV0 + uint32_t((jj & 1) * L::TILE);
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_ts(tmem + uint32_t(2 * kN + qt * 128), tmem + uint32_t(qt * kN + kk * 8),
+                   sdesc(sV + uint32_t(kk * 16 * 128), L::BLK, 1024), IPV, (jj > 0 || kk > 0) ? 1u : 0u);
+        };
+        if (nq == 1) {
+          // one live Q tile: QK(0) QK(1) | PV(0) QK(2) | PV(1) ...
+          auto qk1 = [&](int j) -> bool {
+            if (!wait(B_K_READY + (j & 1), j >> 1)) return false;
+            tc_fence_after();
+            qk(0, j, j & 1);
+            mma_commit(BAR(B_K_FREE + (j & 1)));
+            return true;
+          };
+          if (ok) ok = qk1(0);
+          if (ok && ntiles > 1) ok = qk1(1);
+          for (int j = 0; j < ntiles && ok; ++j) {
+            ok = wait(B_P_FULL + (j & 1), j >> 1) && wait(B_V_READY + (j & 1), j >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sV = sV0 + uint32_t((j & 1) * L::TILE);
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk) {
+              const int hk = KH ? kk / 4 : 0;
+              const uint32_t pcol = uint32_t((j & 1) * kN + (KH ? 64 * hk + (kk % 4) * 8 : kk * 8));
+              mma_ts(tmem + uint32_t((2 + hk) * kN), tmem + pcol, sdesc(sV + uint32_t(kk * 16 * 128), L::BLK, 1024),
+                     IPV, (j > 0 || kk > (KH ? 4 * hk : 0)) ? 1u : 0u);
+            }
+            mma_commit(BAR(B_PV_DONE));
+            mma_commit(BAR(B_V_FREE + (j & 1)));
+            if (j + 2 < ntiles) ok = qk1(j + 2);
+          }
+        } else {
+          if (ok) ok = wait(B_K_READY, 0);
+          if (ok) {
+            tc_fence_after();
+            qk(0, 0, 0);
+            qk(1, 0, 1);
+            mma_commit(BAR(B_K_FREE));
+          }
+          for (int j = 1; j < ntiles && ok; ++j) {
+            const int s = j & 1, sp = (j - 1) & 1;
+            ok = wait(B_P_FULL, j - 1) && wait(B_V_READY + sp, (j - 1) >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(0, j - 1);
+            ok = wait(B_K_READY + s, j >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            qk(0, j, 0);
+            ok = wait(B_P_FULL + 1, j - 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(1, j - 1);
+            mma_commit(BAR(B_V_FREE + sp));
+            qk(1, j, 1);
+            mma_commit(BAR(B_K_FREE + s));
+          }
+          if (ok) {
+            const int jl = ntiles - 1;
+            ok = wait(B_P_FULL, jl) && wait(B_V_READY + (jl & 1), jl >> 1);
+            if (ok) {
+              tc_fence_after();
+              pv(0, jl);
+              ok = wait(B_P_FULL + 1, jl);
+            }
+            if (ok) {
+              tc_fence_after();
+              pv(1, jl);
+              mma_commit(BAR(B_V_FREE + (jl & 1)));
+            }
+          }
+        }
+        // every MMA must be complete before TMEM is released (and before the epilogue reads O)
+        mma_commit(BAR(B_FINAL));
+        WaitClock clk;
+        while (!mbar_test(BAR(B_FINAL), 0) && !clk.expired()) {
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace tcq
+
+namespace {
+
+template <int D, int POS, bool KH>
+int launch_q4_tc(const Q4Args& a, int max_q, cudaStream_t st) {
+  using L = tcq::Layout<D>;
+  auto kern = tcq::q4_prefill_kernel<D, POS, KH>;
+  LAZY_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM));
+  // the setmaxnreg split is only valid for a launch with exactly kRegsLaunch registers per thread
+  cudaFuncAttributes fa;
+  LAZY_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+  if (fa.numRegs != tcq::kRegsLaunch)
+    return fail(LAZY_ECUDA, "4-bit prefill kernel built with %d registers per thread, expected %d", fa.numRegs,
+                tcq::kRegsLaunch);
+  const int rows_tok = tcq::kQT * (tcq::kM / (a.Hq / a.Hkv));
+  const int nmp = (max_q + rows_tok - 1) / rows_tok;
+  const long long pairs = (long long)a.B * a.Hkv;
+  const long long ctas = pairs * nmp * a.S;
+  if (ctas > 0x7FFFFFFFll) return fail(LAZY_ERANGE, "too many query rows (B=%d, max_q=%d)", a.B, max_q);
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(unsigned(ctas)), dim3(tcq::kThreads), L::SMEM, st, a, nmp,
+                           int(pairs < sm_count())));
+  return LAZY_OK;
+}
+
+template <bool KH>
+int dispatch_q4_tc(int D, int kind, const Q4Args& a, int max_q, cudaStream_t st) {
+  if (D == 128) {
+    if (kind == kRope) return launch_q4_tc<128, kRope, KH>(a, max_q, st);
+    if (kind == kRopeX) return launch_q4_tc<128, kRopeX, KH>(a, max_q, st);
+    return launch_q4_tc<128, kAlibi, KH>(a, max_q, st);
+  }
+  if (kind == kRope) return launch_q4_tc<64, kRope, KH>(a, max_q, st);
+  if (kind == kRopeX) return launch_q4_tc<64, kRopeX, KH>(a, max_q, st);
+  return launch_q4_tc<64, kAlibi, KH>(a, max_q, st);
+}
+
+}  // namespace
+
+// The tensor-core kernel holds whole tokens in 128-row tiles: head groups that divide 128.
+bool q4_use_tc(int Hq, int Hkv) { return 128 % (Hq / Hkv) == 0; }
+
+int run_q4_tc(Q4Args& a, int D, int max_q, cudaStream_t st) {
+  int kind = a.pos.kind == kYarn ? kRope : a.pos.kind;
+  if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
+  if (kind == kNone) {  // no rotation and no bias: the ALiBi kernel with slope 0
+    kind = kAlibi;
+    a.pos.slopes = nullptr;
+  }
+  // every CTA has one live Q tile: its keys are shared by the two softmax warpgroups
+  if (a.seq_len || max_q <= tcq::kM / (a.Hq / a.Hkv)) return dispatch_q4_tc<true>(D, kind, a, max_q, st);
+  return dispatch_q4_tc<false>(D, kind, a, max_q, st);
+}
+
+}  // namespace lazykv

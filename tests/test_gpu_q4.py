@@ -7,8 +7,10 @@ values that the cache holds.
 Tolerances of the attention, from the arithmetic that the kernels document.  With A = sum_j p_j |v_j|:
   * the output is rounded to bf16: at most 2^-8 of it;
   * the weights p are rounded to f16, 2^-11 of each, and sums run in fp32: 2^-10 A covers both;
-  * where rotated queries and keys are rounded to f16 (the tensor-core prefill), a score is off by
-    at most E = 2 * 2^-11 |q| |k| scale, a weight by 2 E of itself: 2 E A more;
+  * the tensor-core kernel (prefill; decode of head groups above 8) rounds queries to f16 (2^-11) and
+    rotates keys in f16: cos, sin, a product and the sum each 2^-11, so a key is off by at most
+    3 sqrt(2) 2^-11 |k|, a score by at most E = 6 * 2^-11 |q| |k| scale, a weight by 2 E of itself:
+    2 E A more;
   * a weight is held as 2^(s - max + 7), max a score that was met, so the sum of the weights is at
     least 2^7; weights below 2^-14 are subnormal f16 numbers, off by at most 2^-25, which is 2^-32 of
     the sum: 2^-32 max |v| more per key.  Inputs are N(0, 1): |v| < 8.
@@ -234,11 +236,11 @@ def _check_attention(got, want, absv, score_err, keys, what):
 
 
 def _score_err(w, q, kb):
-    """E of the module's docstring: rotated queries and keys rounded to f16."""
+    """E of the module's docstring."""
     kv = lo.bf16_bits_to_f64(kb)
     kmax = np.sqrt((np.nan_to_num(kv) ** 2).sum(-1).max())
     qmax = np.sqrt((lo.bf16_bits_to_f64(q) ** 2).sum(-1).max()) if len(q) else 0.0
-    return 2 * 2.0 ** -11 * qmax * kmax * lo.softmax_scale(w.pos.as_dict(), w.D)
+    return 6 * 2.0 ** -11 * qmax * kmax * lo.softmax_scale(w.pos.as_dict(), w.D)
 
 
 def _load(raw, D, kf=1.0, vf=1.0):
@@ -548,9 +550,9 @@ def test_one_large_key(lk):
     pos = PosCfg("rope", 1e4, D).as_dict()
     ref, _ = lo.prefill(q, [0, T], [0], [0], meta, kb, vb, pos)
     a, _ = lo.prefill(q, [0, T], [0], [0], meta, kb, _values(vb), pos)
-    # the large key has two components after its rotation: their f16 roundings move its logit by at most
-    # 2 * 2^-11 of it, which matters only where it is within reach of the others (below 16)
-    _check_attention(out, ref, a, 2 * 2.0 ** -11 * 16, T, "prefill")
+    # the large key's f16 roundings move its logit by at most 6 * 2^-11 of its two components' products,
+    # which matters only where it is within reach of the others (below 16)
+    _check_attention(out, ref, a, 6 * 2.0 ** -11 * 16, T, "prefill")
     _check_attention(out_d, ref[-1:], a[-1:], 0.0, T, "decode")
 
 

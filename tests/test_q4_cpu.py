@@ -78,7 +78,7 @@ class _Args:
         cfg = kw.pop("cfg", cfg)
         d = dict(B=2, max_blocks=4, total_q=3, max_q=2, cache=p, num_pages=8, Hq=8, Hkv=2, D=128, q=p, seq_len=p,
                  cu_q=p, q_start=p, doc_blocks=p, meta=p, out=p, k_scale=1.0, v_scale=1.0, ws=None, ws_bytes=0, T=3,
-                 k=p, v=p, slot=p, local_pos=p)
+                 k=p, v=p, slot=p, local_pos=p, scale=0.0)
         unknown = set(kw) - set(d)
         assert not unknown, unknown
         d.update(kw)
@@ -92,10 +92,10 @@ class _Args:
                                        None)
         if what == "decode":
             return lib.lazy_attn_decode_q4(*g("q", "seq_len", "q_start", "doc_blocks", "meta", "B", "max_blocks",
-                                              "cache", "num_pages", "Hq", "Hkv", "D"), 0.0,
+                                              "cache", "num_pages", "Hq", "Hkv", "D", "scale"),
                                            *g("k_scale", "v_scale"), c, *g("out"), None, *g("ws", "ws_bytes"), None)
         return lib.lazy_attn_prefill_q4(*g("q", "cu_q", "q_start", "doc_blocks", "meta", "B", "max_blocks", "total_q",
-                                           "max_q", "cache", "num_pages", "Hq", "Hkv", "D"), 0.0,
+                                           "max_q", "cache", "num_pages", "Hq", "Hkv", "D", "scale"),
                                         *g("k_scale", "v_scale"), c, *g("out"), None, *g("ws", "ws_bytes"), None)
 
 
@@ -124,6 +124,9 @@ REFUSED = [
     (("decode", "prefill"), dict(Hq=9), -1, "multiple of Hkv"),
     (("decode", "prefill"), dict(Hq=12), -1, "power of two below 8"),
     (("decode", "prefill"), dict(Hq=24), -1, "multiple of 8"),
+    (("decode", "prefill"), dict(scale=-0.1), -1, "scale must be positive"),
+    (("decode", "prefill"), dict(scale=float("nan")), -1, "scale must be positive"),
+    (("decode", "prefill"), dict(scale=float("inf")), -1, "scale must be positive"),
     (("decode", "prefill"), dict(q=None), -1, "NULL pointer"),
     (("decode", "prefill"), dict(out=None), -1, "NULL pointer"),
     (("decode", "prefill"), dict(meta=None), -1, "NULL pointer"),

@@ -1,0 +1,150 @@
+"""The 4-bit prefill's barrier protocol in the host-side model (no GPU).
+
+q4_prefill_kernel differs from prefill_tc_kernel in how operands reach the tensor cores: packed keys
+land in a 2-stage ring and packed values in a single stage; the dequantisation role turns them into
+the K and V operand rings (2 stages each), keys one tile ahead of values.  Softmax and MMA roles
+are the model's own.  Random interleavings must show no deadlock, no wait ahead of or two phases
+behind a barrier, and no stage or metadata slot reused too early; planted mistakes must be caught.
+"""
+import random
+
+import pytest
+
+from tests import prefill_protocol_model as pm
+
+
+class Q4Sim(pm.Sim):
+    def __init__(self, n, nq, seed=0, slots=6, kh=False):
+        super().__init__(n, nq, seed=seed, slots=slots, kst=2, kh=kh)
+        self.PK_FULL = [pm.Bar(f"PK_FULL{s}", 1) for s in range(2)]
+        self.PK_FREE = [pm.Bar(f"PK_FREE{s}", 1) for s in range(2)]
+        self.PV_FULL, self.PV_FREE = pm.Bar("PV_FULL", 1), pm.Bar("PV_FREE", 1)
+        self.V_READY = [pm.Bar(f"V_READY{s}", 1) for s in range(2)]
+        self.packed = {"K": [None, None], "V": [None]}   # landed tile of each packed stage
+        self.pending = {"K": [False, False], "V": [False]}  # landed and not read yet
+
+    # packed copies
+    def issue_tma(self, kind, j, bar):
+        st = j % len(self.packed[kind])
+        if self.pending[kind][st]:
+            raise pm.ProtocolError(f"packed {kind}({j}) issued into stage {st} before it was read")
+        self.pending[kind][st] = True
+        self.tma.append((kind, st, j, bar, self.now + self.rng.randint(0, self.max_latency)))
+
+    def step_tma(self):
+        i = self.rng.choice(self.tma_ready())
+        kind, st, j, bar, _ = self.tma.pop(i)
+        self.packed[kind][st] = j
+        bar.complete_tx(1)
+
+    def producer(self):
+        def issue_k(j):
+            s = j % 2
+            if j >= 2:
+                yield ("wait", self.PK_FREE[s], j // 2 - 1)
+            self.publish(j)
+            self.PK_FULL[s].arrive(expect_tx=1)
+            self.issue_tma("K", j, self.PK_FULL[s])
+            yield ("step",)
+
+        yield from issue_k(0)
+        for j in range(self.n):
+            if j + 1 < self.n:
+                yield from issue_k(j + 1)
+            if j >= 1:
+                yield ("wait", self.PV_FREE, j - 1)
+            self.PV_FULL.arrive(expect_tx=1)
+            self.issue_tma("V", j, self.PV_FULL)
+            yield ("step",)
+
+    def wait_free(self, bars, j):
+        if j >= 2:
+            yield ("wait", bars[j % 2], j // 2 - 1)
+
+    def rotation(self):  # the dequantisation role
+        def read(kind, j, users, stages, holder):
+            ring, st = self.packed[kind], j % len(self.packed[kind])
+            if ring[st] != j:
+                raise pm.ProtocolError(f"dequantisation of {kind}({j}) finds packed {ring[st]}")
+            self.read_slot(j, f"dequantise {kind}")
+            if users[j % 2]:
+                raise pm.ProtocolError(f"{kind}({j}) written into stage {j % 2} while {sorted(users[j % 2])} still use it")
+            holder[j % 2] = j
+            users[j % 2] = {stages + "0"} | ({stages + "1"} if self.nq == 2 else set())
+            self.pending[kind][st] = False
+
+        def keys(j):
+            yield ("wait", self.PK_FULL[j % 2], j // 2)
+            yield from self.wait_free(self.K_FREE, j)
+            read("K", j, self.kstage_users, "qk", self.kstage)
+            yield ("step",)
+            self.PK_FREE[j % 2].arrive()
+            self.K_READY[j % 2].arrive()
+
+        def values(j):
+            yield ("wait", self.PV_FULL, j)
+            yield from self.wait_free(self.V_FREE, j)
+            read("V", j, self.vstage_users, "pv", self.vstage)
+            yield ("step",)
+            self.PV_FREE.arrive()
+            self.V_READY[j % 2].arrive()
+
+        yield from keys(0)
+        for j in range(self.n):
+            if j + 1 < self.n:
+                yield from keys(j + 1)
+            yield from values(j)
+
+    def mma_wait_v(self, jj):
+        yield ("wait", self.V_READY[jj % 2], jj // 2)
+
+    def read_slot(self, j, who):
+        if not who.startswith("mma"):  # this kernel's MMA thread reads no metadata
+            super().read_slot(j, who)
+
+
+def _schedules(n_runs, seed0=0):
+    for seed in range(seed0, seed0 + n_runs):
+        rng = random.Random(seed)
+        yield seed, rng.choice([1, 2, 3, 4, 5, 8, 9, 16, 17]), rng.choice([1, 2])
+
+
+@pytest.mark.parametrize("part", range(4))
+def test_protocol_is_safe_under_random_interleavings(part):
+    for seed, n, nq in _schedules(400, seed0=400 * part):
+        for kh in (False, True):
+            try:
+                Q4Sim(n, nq, seed=seed, kh=kh).run()
+            except pm.ProtocolError as e:
+                pytest.fail(f"seed {seed}, {n} tiles, {nq} live Q tiles, key halves {kh}: {e}")
+
+
+def _caught(cls, **kw):
+    caught = 0
+    for seed, n, nq in _schedules(200):
+        try:
+            cls(n, nq, seed=seed, **kw).run()
+        except pm.ProtocolError:
+            caught += 1
+    return caught
+
+
+def test_model_catches_too_few_metadata_slots():
+    assert _caught(Q4Sim, slots=3) > 0
+
+
+def test_model_catches_operands_written_before_their_products_are_done():
+    class NoWait(Q4Sim):
+        def wait_free(self, bars, j):
+            yield ("step",)
+    assert _caught(NoWait) > 0
+
+
+def test_model_catches_packed_values_overwritten():
+    class Early(Q4Sim):
+        def producer(self):
+            for x in super().producer():
+                if x[0] == "wait" and x[1] is self.PV_FREE:
+                    continue
+                yield x
+    assert _caught(Early) > 0
