@@ -9,19 +9,18 @@
 //              normalised by a power of two per row, f16, 128-byte swizzle), then per tile the scores from
 //              TMEM, mask, running maximum (moved only when beaten by more than 8), P back to TMEM over S
 //              as f16, held as 2^(s - max + 7); the epilogue.
-//   warps 8-11 dequantisation: each tile's packed pages (9 D bytes of keys, 9 D of values per page)
-//              become the f16 operands.  Keys: code times scale is exact in f16; the rotation by the page's
-//              Delta then rounds cos, sin, one product and the sum to f16 (2^-12 each: 2 instructions per
-//              value against 3.5 through fp32; the 4-bit codes themselves are off by up to 2^-3 of a
-//              group's maximum).  Values: exact in f16.  A thread owns 8 frequencies (two runs of 8
-//              dimensions) of 8 rows of a page; the packed pages lie 9 D + pad bytes apart, so that its
-//              word loads meet no bank conflicts, and values are stored even and odd rows first in turn for
-//              the same reason.
+//   warps 8-11 keys: each tile's packed pages (9 D bytes of keys each) become the f16 operand.  Code
+//              times scale is exact in f16; the rotation by the page's Delta then rounds cos, sin, one
+//              product and the sum to f16 (2^-11 each: 2 instructions per value against 3.5 through
+//              fp32; the 4-bit codes themselves are off by up to 2^-3 of a group's maximum).  A thread owns
+//              8 frequencies (two runs of 8 dimensions) of 8 rows of a page; the packed pages lie 9 D + pad
+//              bytes apart, so that its word loads meet no bank conflicts.
+//   warps 14-15 values: the same, exact in f16; even and odd groups store their rows in opposite order,
+//              against bank conflicts.
 //   warp 12    producer: block words one tile ahead, one bulk copy per page into a 2-stage ring of packed
 //              keys and a 1-stage ring of packed values.
 //   warp 13    TMEM owner and MMA issuer: QK0(j) QK1(j) | PV0(j) QK0(j+1) PV1(j) QK1(j+1) | ...
-// Both f16 rings have 2 stages.  The dequantisation runs a tile ahead: keys of tile j + 1, then values
-// of tile j.  TMEM: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P_i in the first half of S_i.
+// Both f16 rings have 2 stages, filled a tile ahead.  TMEM: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P_i in the first half of S_i.
 // With one live Q tile S0 and S1 double-buffer its scores; in launches whose CTAs all have one (KH) the two
 // softmax warpgroups each take half of every tile's keys and merge in the epilogue.
 //
@@ -42,7 +41,7 @@ constexpr int kM = 128, kQT = 2, kN = 128;
 constexpr int kPagesPerTile = kN / kPage;
 constexpr int kSlots = 6;  // per-tile metadata: published up to 5 tiles ahead of the softmax's use
 constexpr int kThreads = 512;
-constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13;
+constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13, kValWarp0 = 14;
 constexpr int kRegsLaunch = 128;
 // registers per thread after the re-split: softmax, dequantisation, producer + MMA; they add up to the launch's
 template <bool KH> struct Regs {
@@ -55,10 +54,10 @@ enum : int {
   B_PK_FULL = 0,   // [2] packed keys landed (bytes)
   B_PK_FREE = 2,   // [2] packed keys read (128 arrivals)
   B_PV_FULL = 4,   // packed values landed
-  B_PV_FREE = 5,   // packed values read
+  B_PV_FREE = 5,   // packed values read (64)
   B_K_READY = 6,   // [2] K operand written (128)
   B_K_FREE = 8,    // [2] every QK^T of the stage done (commit)
-  B_V_READY = 10,  // [2] V operand written (128)
+  B_V_READY = 10,  // [2] V operand written (64)
   B_V_FREE = 12,   // [2] every PV of the stage done (commit)
   B_S_FULL = 14,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
   B_P_FULL = 16,   // [2] P in TMEM, O rescaled (128, KH 256)
@@ -194,13 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       mbar_init(BAR(B_PK_FREE + s), 128);
       mbar_init(BAR(B_K_READY + s), 128);
       mbar_init(BAR(B_K_FREE + s), 1);
-      mbar_init(BAR(B_V_READY + s), 128);
+      mbar_init(BAR(B_V_READY + s), 64);
       mbar_init(BAR(B_V_FREE + s), 1);
       mbar_init(BAR(B_S_FULL + s), 1);
       mbar_init(BAR(B_P_FULL + s), KH ? 256 : 128);
     }
     mbar_init(BAR(B_PV_FULL), 1);
-    mbar_init(BAR(B_PV_FREE), 128);
+    mbar_init(BAR(B_PV_FREE), 64);
     mbar_init(BAR(B_Q_READY), 2 * 128);
     mbar_init(BAR(B_FINAL), 1);
     mbar_init(BAR(B_PV_DONE), 1);
@@ -554,35 +553,46 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
               }
             }
           }
-          const uint32_t sel = D == 128 ? ((c >> 1) & 1 ? 0x3232u : 0x1010u) : 0u;
+          // Two rows (r7, r7 + 8) a time, the next ones' words loaded ahead.  The loop stays rolled: five
+          // roles run different code at once, and unrolled they miss the instruction cache (a third of
+          // all stalls).
+          constexpr int NI = 8 / HG;
+          const uint32_t wsrc = src + hg * (D / 2) + c * 4;
+          const uint32_t ssrc = src + Q::KS + (D == 128 ? (hg * 4 + (c >> 2)) * 4 : (hg * 4 + (c >> 1)) * 2);
+          auto load = [&](int i, uint32_t (&w)[6]) {  // codes of both rows, first run and its partner; scales
+            const uint32_t x = wsrc + i * HG * (D / 2);
+            w[0] = ld_shared_u32(x);
+            w[1] = ld_shared_u32(x + D / 4);
+            w[2] = ld_shared_u32(x + 4 * D);
+            w[3] = ld_shared_u32(x + 4 * D + D / 4);
+            const uint32_t y = ssrc + i * HG * (D == 128 ? 16 : 8);
+            w[4] = D == 128 ? ld_shared_u32(y) : ld_shared_u16(y);
+            w[5] = D == 128 ? ld_shared_u32(y + 8) : ld_shared_u16(y + 4);
+          };
+          // D = 128: a word holds two groups of row r7, then of r7 + 8; D = 64: one group of each
+          const uint32_t sel_a = D == 128 ? ((c >> 1) & 1 ? 0x3232u : 0x1010u) : 0x1010u;
+          const uint32_t sel_b = D == 128 ? sel_a : 0x3232u;
+          uint32_t nxt[6];
+          load(0, nxt);
+          // rows r7 + 8 lie 1024 bytes on, equally swizzled
+#pragma unroll 1
+          for (int i = 0; i < NI; ++i) {
+            uint32_t cur[6];
 #pragma unroll
-          for (int i = 0; i < 8 / HG; ++i) {
-            const int r7 = hg + HG * i;
-            uint32_t sc1[2], sc2[2];  // scales of rows r7 and r7 + 8, first run and its partner
-            if constexpr (D == 128) {
-              const uint32_t w1 = ld_shared_u32(src + Q::KS + (r7 * 4 + (c >> 2)) * 4);
-              const uint32_t w2 = ld_shared_u32(src + Q::KS + (r7 * 4 + (c >> 2) + 2) * 4);
-              sc1[0] = __byte_perm(e4m3x2_to_h2(w1 & 0xFFFFu), 0, sel);
-              sc1[1] = __byte_perm(e4m3x2_to_h2(w1 >> 16), 0, sel);
-              sc2[0] = __byte_perm(e4m3x2_to_h2(w2 & 0xFFFFu), 0, sel);
-              sc2[1] = __byte_perm(e4m3x2_to_h2(w2 >> 16), 0, sel);
-            } else {
-              const uint32_t h1 = e4m3x2_to_h2(ld_shared_u16(src + Q::KS + (r7 * 4 + (c >> 1)) * 2));
-              const uint32_t h2 = e4m3x2_to_h2(ld_shared_u16(src + Q::KS + (r7 * 4 + (c >> 1) + 2) * 2));
-              sc1[0] = __byte_perm(h1, 0, 0x1010);
-              sc1[1] = __byte_perm(h1, 0, 0x3232);
-              sc2[0] = __byte_perm(h2, 0, 0x1010);
-              sc2[1] = __byte_perm(h2, 0, 0x3232);
-            }
+            for (int e = 0; e < 6; ++e) cur[e] = nxt[e];
+            if (i + 1 < NI) load(i + 1, nxt);
+            const uint32_t a1 = sK + swz(ps * kPage + hg + HG * i, c);
+            const uint32_t a2 = (D == 128) ? a1 + uint32_t(L::BLK) : sK + swz(ps * kPage + hg + HG * i, c + 4);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const int t = r7 + 8 * hh, r = ps * kPage + t;
+              const uint32_t sc1 = __byte_perm(e4m3x2_to_h2(D == 128 && hh ? cur[4] >> 16 : cur[4] & 0xFFFFu), 0, hh ? sel_b : sel_a);
+              const uint32_t sc2 = __byte_perm(e4m3x2_to_h2(D == 128 && hh ? cur[5] >> 16 : cur[5] & 0xFFFFu), 0, hh ? sel_b : sel_a);
               uint32_t x1[4], x2[4];
-              e2m1x8_to_h2(ld_shared_u32(src + t * (D / 2) + c * 4), x1);
-              e2m1x8_to_h2(ld_shared_u32(src + t * (D / 2) + D / 4 + c * 4), x2);
+              e2m1x8_to_h2(cur[2 * hh], x1);
+              e2m1x8_to_h2(cur[2 * hh + 1], x2);
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
-                const uint32_t p1 = hmul2(x1[w], sc1[hh]), p2 = hmul2(x2[w], sc2[hh]);
+                const uint32_t p1 = hmul2(x1[w], sc1), p2 = hmul2(x2[w], sc2);
                 if constexpr (POS == kRope) {
                   x1[w] = hfma2(p2, nsn[w], hmul2(p1, co[w]));  // x1 c - x2 s
                   x2[w] = hfma2(p2, co[w], hmul2(p1, sn[w]));   // x1 s + x2 c
@@ -591,10 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
                   x2[w] = p2;
                 }
               }
-              const uint32_t a1 = sK + swz(r, c);
-              const uint32_t a2 = (D == 128) ? sK + uint32_t(L::BLK) + swz(r, c) : sK + swz(r, c + 4);
-              st_shared_v4(a1, make_uint4(x1[0], x1[1], x1[2], x1[3]));
-              st_shared_v4(a2, make_uint4(x2[0], x2[1], x2[2], x2[3]));
+              st_shared_v4(a1 + hh * 1024, make_uint4(x1[0], x1[1], x1[2], x1[3]));
+              st_shared_v4(a2 + hh * 1024, make_uint4(x2[0], x2[1], x2[2], x2[3]));
             }
           }
         } else {
@@ -651,64 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       mbar_arrive(BAR(B_PK_FREE + s));
       mbar_arrive(BAR(B_K_READY + s));
     };
-    auto values = [&](int j) {
-      const int s = j & 1, slot = j % kSlots;
-      if (ok) ok = wait_bar(BAR(B_PV_FULL), uint32_t(j & 1), abort_flag, a.status);
-      if (ok && j >= 2) ok = wait_bar(BAR(B_V_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
-      if (ok) {
-        // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
-        const int rows = pinfo[slot * kPagesPerTile + ps].y;
-        const uint32_t src = sPV + uint32_t(ps * L::PVS);
-        const uint32_t sV = sV0 + uint32_t(s * L::TILE);
-        const int t = l & 3;
-        const int rr = rows - 2 * t;  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
-                              (rr > 9 ? 0xFF000000u : 0u);
-        auto put = [&](int row, int cb, int ch, uint32_t codes, uint32_t scale) {
-          uint32_t x[4];
-          e2m1x8_to_h2(codes, x);
-          st_shared_v4(sV + uint32_t(cb * L::BLK) + swz(ps * kPage + row, ch),
-                       make_uint4(hmul2(x[0], scale), hmul2(x[1], scale), hmul2(x[2], scale), hmul2(x[3], scale)));
-        };
-        if constexpr (D == 128) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int half = k & 1, q = (l >> 2) + 4 * (k >> 1);
-            const uint4 x = ld_shared_v4(src + half * 512 + (q * 4 + t) * 16);
-            const uint32_t sw = ld_shared_u32(src + 8 * D + q * 16 + t * 4) & keep;
-            const uint32_t hs = e4m3x2_to_h2(half ? sw >> 16 : sw & 0xFFFFu);
-            const int odd = q & 1;  // odd groups store their odd row first: no two lanes share a bank
-            const uint32_t a0 = odd ? x.z : x.x, a1 = odd ? x.w : x.y, b0 = odd ? x.x : x.z, b1 = odd ? x.y : x.w;
-            const uint32_t sa = __byte_perm(hs, 0, odd ? 0x3232 : 0x1010), sc = __byte_perm(hs, 0, odd ? 0x1010 : 0x3232);
-            const int ra = half * 8 + 2 * t + odd, rb = half * 8 + 2 * t + 1 - odd, ch = (2 * q) & 7;
-            put(ra, q >> 2, ch, a0, sa);
-            put(rb, q >> 2, ch, b0, sc);
-            put(ra, q >> 2, ch + 1, a1, sa);
-            put(rb, q >> 2, ch + 1, b1, sc);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int gd = (l >> 2) + 4 * k;  // run of 8 dimensions
-            const uint4 x = ld_shared_v4(src + (gd * 4 + t) * 16);
-            const uint32_t sw = ld_shared_u32(src + 8 * D + (gd >> 1) * 16 + t * 4) & keep;
-            const uint32_t h0 = e4m3x2_to_h2(sw & 0xFFFFu), h1 = e4m3x2_to_h2(sw >> 16);
-            put(2 * t, 0, gd, x.x, __byte_perm(h0, 0, 0x1010));
-            put(2 * t + 1, 0, gd, x.y, __byte_perm(h0, 0, 0x3232));
-            put(2 * t + 8, 0, gd, x.z, __byte_perm(h1, 0, 0x1010));
-            put(2 * t + 9, 0, gd, x.w, __byte_perm(h1, 0, 0x3232));
-          }
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(BAR(B_PV_FREE));
-      mbar_arrive(BAR(B_V_READY + s));
-    };
-    keys(0);
-    for (int j = 0; j < ntiles; ++j) {
-      if (j + 1 < ntiles) keys(j + 1);
-      values(j);
-    }
+    for (int j = 0; j < ntiles; ++j) keys(j);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<KH>::issue));
     if (warp == kProdWarp) {
@@ -894,6 +845,84 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         WaitClock clk;
         while (!mbar_test(BAR(B_FINAL), 0) && !clk.expired()) {
         }
+      }
+      __syncwarp();
+    } else if (warp >= kValWarp0) {
+      // ============================ values: packed -> f16, 8 threads per page
+      const int rt = threadIdx.x - kValWarp0 * 32;
+      const int ps = rt >> 3, l = rt & 7, t = l & 3;
+      bool ok = true;
+      for (int j = 0; j < ntiles; ++j) {
+        const int s = j & 1, slot = j % kSlots;
+        if (ok) ok = wait_bar(BAR(B_PV_FULL), uint32_t(j & 1), abort_flag, a.status);
+        if (ok && j >= 2) ok = wait_bar(BAR(B_V_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
+        if (ok) {
+          // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
+          const int rows = pinfo[slot * kPagesPerTile + ps].y;
+          const uint32_t src = sPV + uint32_t(ps * L::PVS);
+          const uint32_t sV = sV0 + uint32_t(s * L::TILE);
+          const int rr = rows - 2 * t;  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
+          const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
+                                (rr > 9 ? 0xFF000000u : 0u);
+          auto put = [&](int row, int cb, int ch, uint32_t codes, uint32_t scale) {
+            uint32_t x[4];
+            e2m1x8_to_h2(codes, x);
+            st_shared_v4(sV + uint32_t(cb * L::BLK) + swz(ps * kPage + row, ch),
+                         make_uint4(hmul2(x[0], scale), hmul2(x[1], scale), hmul2(x[2], scale), hmul2(x[3], scale)));
+          };
+          const uint32_t csrc = src + (l >> 2) * 64 + t * 16, ssrc = src + 8 * D + (D == 128 ? l >> 2 : 0) * 16 + t * 4;
+          if constexpr (D == 128) {
+            // groups q = l / 4 + 2 k; odd ones store their odd row first: no two lanes share a bank
+            const int odd = l >> 2;
+            const uint32_t sela = odd ? 0x3232 : 0x1010, selb = odd ? 0x1010 : 0x3232;
+            uint4 n0 = ld_shared_v4(csrc), n1 = ld_shared_v4(csrc + 512);
+            uint32_t ns = ld_shared_u32(ssrc);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const uint4 x[2] = {n0, n1};
+              const uint32_t sw = ns & keep;
+              if (k < 3) {
+                n0 = ld_shared_v4(csrc + (k + 1) * 128);
+                n1 = ld_shared_v4(csrc + (k + 1) * 128 + 512);
+                ns = ld_shared_u32(ssrc + (k + 1) * 32);
+              }
+              const int q = odd + 2 * k, ch = (2 * q) & 7;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t hs = e4m3x2_to_h2(half ? sw >> 16 : sw & 0xFFFFu);
+                const uint32_t a0 = odd ? x[half].z : x[half].x, a1 = odd ? x[half].w : x[half].y;
+                const uint32_t b0 = odd ? x[half].x : x[half].z, b1 = odd ? x[half].y : x[half].w;
+                const uint32_t sa = __byte_perm(hs, 0, sela), sc = __byte_perm(hs, 0, selb);
+                const int ra = half * 8 + 2 * t + odd, rb = half * 8 + 2 * t + 1 - odd;
+                put(ra, q >> 2, ch, a0, sa);
+                put(rb, q >> 2, ch, b0, sc);
+                put(ra, q >> 2, ch + 1, a1, sa);
+                put(rb, q >> 2, ch + 1, b1, sc);
+              }
+            }
+          } else {
+            uint4 n0 = ld_shared_v4(csrc);
+            uint32_t ns = ld_shared_u32(ssrc);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {  // runs of 8 dimensions gd = l / 4 + 2 k
+              const uint4 x = n0;
+              const uint32_t sw = ns & keep;
+              if (k < 3) {
+                n0 = ld_shared_v4(csrc + (k + 1) * 128);
+                ns = ld_shared_u32(ssrc + (k + 1) * 16);
+              }
+              const int gd = (l >> 2) + 2 * k;
+              const uint32_t h0 = e4m3x2_to_h2(sw & 0xFFFFu), h1 = e4m3x2_to_h2(sw >> 16);
+              put(2 * t, 0, gd, x.x, __byte_perm(h0, 0, 0x1010));
+              put(2 * t + 1, 0, gd, x.y, __byte_perm(h0, 0, 0x3232));
+              put(2 * t + 8, 0, gd, x.z, __byte_perm(h1, 0, 0x1010));
+              put(2 * t + 9, 0, gd, x.w, __byte_perm(h1, 0, 0x3232));
+            }
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(BAR(B_PV_FREE));
+        mbar_arrive(BAR(B_V_READY + s));
       }
       __syncwarp();
     }

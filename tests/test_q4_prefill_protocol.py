@@ -1,9 +1,8 @@
 """The 4-bit prefill's barrier protocol in the host-side model (no GPU).
 
 q4_prefill_kernel differs from prefill_tc_kernel in how operands reach the tensor cores: packed keys
-land in a 2-stage ring and packed values in a single stage; the dequantisation role turns them into
-the K and V operand rings (2 stages each), keys one tile ahead of values.  Softmax and MMA roles
-are the model's own.  Random interleavings must show no deadlock, no wait ahead of or two phases
+land in a 2-stage ring and packed values in a single stage; one role turns the keys, another the
+values into operand rings of 2 stages each.  Softmax and MMA roles are the model's own.  Random interleavings must show no deadlock, no wait ahead of or two phases
 behind a barrier, and no stage or metadata slot reused too early; planted mistakes must be caught.
 """
 import random
@@ -61,39 +60,37 @@ class Q4Sim(pm.Sim):
         if j >= 2:
             yield ("wait", bars[j % 2], j // 2 - 1)
 
-    def rotation(self):  # the dequantisation role
-        def read(kind, j, users, stages, holder):
-            ring, st = self.packed[kind], j % len(self.packed[kind])
-            if ring[st] != j:
-                raise pm.ProtocolError(f"dequantisation of {kind}({j}) finds packed {ring[st]}")
-            self.read_slot(j, f"dequantise {kind}")
-            if users[j % 2]:
-                raise pm.ProtocolError(f"{kind}({j}) written into stage {j % 2} while {sorted(users[j % 2])} still use it")
-            holder[j % 2] = j
-            users[j % 2] = {stages + "0"} | ({stages + "1"} if self.nq == 2 else set())
-            self.pending[kind][st] = False
+    def dequantise(self, kind, j, users, stages, holder):
+        ring, st = self.packed[kind], j % len(self.packed[kind])
+        if ring[st] != j:
+            raise pm.ProtocolError(f"dequantisation of {kind}({j}) finds packed {ring[st]}")
+        self.read_slot(j, f"dequantise {kind}")
+        if users[j % 2]:
+            raise pm.ProtocolError(f"{kind}({j}) written into stage {j % 2} while {sorted(users[j % 2])} still use it")
+        holder[j % 2] = j
+        users[j % 2] = {stages + "0"} | ({stages + "1"} if self.nq == 2 else set())
+        self.pending[kind][st] = False
 
-        def keys(j):
+    def rotation(self):  # the keys' role
+        for j in range(self.n):
             yield ("wait", self.PK_FULL[j % 2], j // 2)
             yield from self.wait_free(self.K_FREE, j)
-            read("K", j, self.kstage_users, "qk", self.kstage)
+            self.dequantise("K", j, self.kstage_users, "qk", self.kstage)
             yield ("step",)
             self.PK_FREE[j % 2].arrive()
             self.K_READY[j % 2].arrive()
 
-        def values(j):
+    def values(self):
+        for j in range(self.n):
             yield ("wait", self.PV_FULL, j)
             yield from self.wait_free(self.V_FREE, j)
-            read("V", j, self.vstage_users, "pv", self.vstage)
+            self.dequantise("V", j, self.vstage_users, "pv", self.vstage)
             yield ("step",)
             self.PV_FREE.arrive()
             self.V_READY[j % 2].arrive()
 
-        yield from keys(0)
-        for j in range(self.n):
-            if j + 1 < self.n:
-                yield from keys(j + 1)
-            yield from values(j)
+    def actors(self):
+        return super().actors() | {"values": self.values()}
 
     def mma_wait_v(self, jj):
         yield ("wait", self.V_READY[jj % 2], jj // 2)
