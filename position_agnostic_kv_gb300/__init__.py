@@ -286,23 +286,27 @@ def q4_cache_shape(num_pages: int, Hkv: int, D: int) -> tuple:
     return (num_pages, Hkv, 18 * D)
 
 
-def _q4_call(fn, what, stream, *args):
-    """Check the tensors among ``args`` -- (name, tensor, dtype, shape), None allowed as the tensor --
-    and call ``fn`` with the other arguments as they are, on the tensors' device and its current
-    stream (or ``stream``, which must be of that device)."""
+_torch = None  # torch and what the 4-bit calls look up of it, bound by the first of them
+
+
+def _bind_torch():
+    global _torch, _BF16, _I32, _I64, _F32, _U8, _raw_stream, _device_index
     import torch
-    dev, ptrs = None, []
-    for x in args:
-        if type(x) is not tuple:
-            ptrs.append(x)
-            continue
-        name, t, dtype, shape = x
+    _torch = torch
+    _BF16, _I32, _I64, _F32, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8
+    _raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+
+def _q4_refuse(what, tensors):
+    """Raise what is wrong with one of ``tensors`` -- (name, tensor, dtype, shape); the calls below test
+    the same in one expression and come here when it fails."""
+    dev = None
+    for name, t, dtype, shape in tensors:
         if t is None:
-            ptrs.append(None)
             continue
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _torch.Tensor):
             raise TypeError(f"{what}: {name} must be a torch.Tensor")
-        if t.dtype is not dtype and not (dtype is torch.int64 and t.dtype is torch.uint64):
+        if t.dtype is not dtype and not (dtype is _I64 and t.dtype is _torch.uint64):
             raise TypeError(f"{what}: {name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -312,18 +316,23 @@ def _q4_call(fn, what, stream, *args):
             dev = t.get_device()
         elif t.get_device() != dev:
             raise ValueError(f"{what}: {name} is on another device than the tensors before it")
-        ptrs.append(t.data_ptr())
     if dev < 0:
         raise ValueError(f"{what}: the tensors must be on a CUDA device")
+
+
+def _q4_run(fn, what, dev, stream, *args):
+    """Call ``fn`` on device ``dev`` and its current stream (or ``stream``, which must be of that device)."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        raw = _raw_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"{what}: the stream is of another device than the tensors")
-    if dev == torch.cuda.current_device():
-        rc = fn(*ptrs, stream.cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*ptrs, stream.cuda_stream)
+        raw = stream.cuda_stream
+    if dev == _device_index():
+        rc = fn(*args, raw)
+    else:
+        with _torch.cuda.device(dev):
+            rc = fn(*args, raw)
     if rc:
         _check(rc, fn.__name__)
 
@@ -331,7 +340,6 @@ def _q4_call(fn, what, stream, *args):
 def _q4_dims(what, kv_cache, Hkv, D):
     if kv_cache.dim() != 3 or kv_cache.shape[1] != Hkv or kv_cache.shape[2] != 18 * D:
         raise ValueError(f"{what}: kv_cache must be [num_pages, {Hkv}, {18 * D}], got {tuple(kv_cache.shape)}")
-    return kv_cache.shape[0]
 
 
 def kv_write_q4(k, v, slot, local_pos, kv_cache, cfg: PosCfg, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -340,56 +348,92 @@ def kv_write_q4(k, v, slot, local_pos, kv_cache, cfg: PosCfg, k_scale: float = 1
     rotated by their local positions as ``kv_write`` does, then both quantised.  ``k_scale`` and
     ``v_scale`` are the cache's power-of-two factors.  The slots must be distinct; only the rows
     they name change."""
-    import torch
-    T, Hkv, D = k.shape
-    P = _q4_dims("kv_write_q4", kv_cache, Hkv, D)
-    _q4_call(lib.lazy_kv_write_q4, "kv_write_q4", stream, ("k", k, torch.bfloat16, k.shape),
-             ("v", v, torch.bfloat16, k.shape), ("slot", slot, torch.int32, (T,)),
-             ("local_pos", local_pos, torch.int32, (T,)), T, Hkv, D, ("kv_cache", kv_cache, torch.uint8, kv_cache.shape),
-             P, ctypes.byref(cfg), k_scale, v_scale)
+    if _torch is None:
+        _bind_torch()
+    shape, cache = k.shape, kv_cache.shape
+    T, Hkv, D = shape
+    rows, dev = (T,), k.get_device()
+    if not (dev >= 0 and k.dtype is _BF16 and v.dtype is _BF16 and slot.dtype is _I32 and local_pos.dtype is _I32
+            and kv_cache.dtype is _U8 and v.shape == shape and slot.shape == rows and local_pos.shape == rows
+            and cache[1:] == (Hkv, 18 * D) and k.is_contiguous() and v.is_contiguous() and slot.is_contiguous()
+            and local_pos.is_contiguous() and kv_cache.is_contiguous()
+            and dev == v.get_device() == slot.get_device() == local_pos.get_device() == kv_cache.get_device()):
+        _q4_dims("kv_write_q4", kv_cache, Hkv, D)
+        _q4_refuse("kv_write_q4", (("k", k, _BF16, shape), ("v", v, _BF16, shape), ("slot", slot, _I32, rows),
+                                   ("local_pos", local_pos, _I32, rows), ("kv_cache", kv_cache, _U8, cache)))
+    _q4_run(lib.lazy_kv_write_q4, "kv_write_q4", dev, stream, k.data_ptr(), v.data_ptr(), slot.data_ptr(),
+            local_pos.data_ptr(), T, Hkv, D, kv_cache.data_ptr(), cache[0], ctypes.byref(cfg), k_scale, v_scale)
 
 
 def kv_read_q4(slot, kv_cache, k, v, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
     """Read cache rows back: writes the values held in ``slot`` [T] to k/v [T, Hkv, D] (bf16, exact;
     keys as stored, rotated by their local positions)."""
-    import torch
-    T, Hkv, D = k.shape
-    P = _q4_dims("kv_read_q4", kv_cache, Hkv, D)
-    _q4_call(lib.lazy_kv_read_q4, "kv_read_q4", stream, ("slot", slot, torch.int32, (T,)), T, Hkv, D,
-             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, k_scale, v_scale,
-             ("k", k, torch.bfloat16, k.shape), ("v", v, torch.bfloat16, k.shape))
+    if _torch is None:
+        _bind_torch()
+    shape, cache = k.shape, kv_cache.shape
+    T, Hkv, D = shape
+    rows, dev = (T,), k.get_device()
+    if not (dev >= 0 and k.dtype is _BF16 and v.dtype is _BF16 and slot.dtype is _I32 and kv_cache.dtype is _U8
+            and v.shape == shape and slot.shape == rows and cache[1:] == (Hkv, 18 * D) and k.is_contiguous()
+            and v.is_contiguous() and slot.is_contiguous() and kv_cache.is_contiguous()
+            and dev == v.get_device() == slot.get_device() == kv_cache.get_device()):
+        _q4_dims("kv_read_q4", kv_cache, Hkv, D)
+        _q4_refuse("kv_read_q4", (("slot", slot, _I32, rows), ("kv_cache", kv_cache, _U8, cache), ("k", k, _BF16, shape),
+                                  ("v", v, _BF16, shape)))
+    _q4_run(lib.lazy_kv_read_q4, "kv_read_q4", dev, stream, slot.data_ptr(), T, Hkv, D, kv_cache.data_ptr(), cache[0],
+            k_scale, v_scale, k.data_ptr(), v.data_ptr())
+
+
+def _q4_attn(what, fn, q, per_row, n, q_start, doc_blocks, meta, kv_cache, cfg, out, lse, ws, sizes, scale, k_scale,
+             v_scale, stream):
+    """The checks and the call that decode and prefill share.  ``per_row`` is seq_len [B] or cu_q [B + 1] (``n``
+    entries), ``sizes`` the arguments between max_blocks and kv_cache."""
+    shape, words, cache = q.shape, meta.shape, kv_cache.shape
+    Hq, D = shape[1:]
+    B, dev = words[0], q.get_device()
+    if not (dev >= 0 and q.dtype is _BF16 and out.dtype is _BF16 and per_row.dtype is _I32 and q_start.dtype is _I32
+            and doc_blocks.dtype is _I32 and meta.dtype is _I64 and kv_cache.dtype is _U8 and out.shape == shape
+            and per_row.shape == (n,) and q_start.shape == (B,) and doc_blocks.shape == (B,) and len(cache) == 3
+            and cache[2] == 18 * D and q.is_contiguous() and out.is_contiguous() and per_row.is_contiguous()
+            and q_start.is_contiguous() and doc_blocks.is_contiguous() and meta.is_contiguous()
+            and kv_cache.is_contiguous()
+            and dev == out.get_device() == per_row.get_device() == q_start.get_device() == doc_blocks.get_device()
+            == meta.get_device() == kv_cache.get_device()) or lse is not None or len(words) != 2:
+        _q4_dims(what, kv_cache, cache[1], D)
+        _q4_refuse(what, (("q", q, _BF16, shape), ("seq_len" if n == B else "cu_q", per_row, _I32, (n,)),
+                          ("q_start", q_start, _I32, (B,)), ("doc_blocks", doc_blocks, _I32, (B,)),
+                          ("meta", meta, _I64, (B, words[1])), ("kv_cache", kv_cache, _U8, cache),
+                          ("out", out, _BF16, shape), ("lse", lse, _F32, shape[:2])))
+    wsp, wsb = None, 0
+    if ws is not None:
+        if ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+            _q4_refuse(what, (("q", q, _BF16, shape), ("ws", ws, _U8, ws.shape)))
+        wsp, wsb = ws.data_ptr(), ws.numel()
+    _q4_run(fn, what, dev, stream, q.data_ptr(), per_row.data_ptr(), q_start.data_ptr(), doc_blocks.data_ptr(),
+            meta.data_ptr(), B, words[1], *sizes, kv_cache.data_ptr(), cache[0], Hq, cache[1], D, scale, k_scale,
+            v_scale, ctypes.byref(cfg), out.data_ptr(), None if lse is None else lse.data_ptr(), wsp, wsb)
 
 
 def attn_decode_q4(q, seq_len, q_start, doc_blocks, meta, kv_cache, cfg: PosCfg, out, lse=None, ws=None,
                    scale: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
     """``attn_decode`` over a 4-bit cache: q [B, Hq, D] raw at m = seq_len - 1; writes out [B, Hq, D]
-    (bf16).  ``ws`` holds at least ``workspace_size(PHASE_DECODE_Q4, ...)`` bytes."""
-    import torch
-    B, Hq, D = q.shape
-    Hkv, mb = kv_cache.shape[1], meta.shape[1]
-    P = _q4_dims("attn_decode_q4", kv_cache, Hkv, D)
-    _q4_call(lib.lazy_attn_decode_q4, "attn_decode_q4", stream, ("q", q, torch.bfloat16, q.shape),
-             ("seq_len", seq_len, torch.int32, (B,)), ("q_start", q_start, torch.int32, (B,)),
-             ("doc_blocks", doc_blocks, torch.int32, (B,)), ("meta", meta, torch.int64, (B, mb)), B, mb,
-             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, Hq, Hkv, D, scale, k_scale, v_scale,
-             ctypes.byref(cfg), ("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (B, Hq)),
-             ("ws", ws, torch.uint8, ws.shape if ws is not None else None), ws.numel() if ws is not None else 0)
+    (bf16).  ``ws`` (uint8) holds at least ``workspace_size(PHASE_DECODE_Q4, ...)`` bytes."""
+    if _torch is None:
+        _bind_torch()
+    if meta.shape[0] != q.shape[0]:
+        raise ValueError(f"attn_decode_q4: meta must have shape [{q.shape[0]}, max_blocks], got {tuple(meta.shape)}")
+    _q4_attn("attn_decode_q4", lib.lazy_attn_decode_q4, q, seq_len, q.shape[0], q_start, doc_blocks, meta, kv_cache, cfg,
+             out, lse, ws, (), scale, k_scale, v_scale, stream)
 
 
 def attn_prefill_q4(q, cu_q, q_start, doc_blocks, meta, kv_cache, cfg: PosCfg, out, max_q: int, lse=None,
                     ws=None, scale: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
     """``attn_prefill`` over a 4-bit cache: q [sum Lq, Hq, D] raw; writes out [sum Lq, Hq, D] (bf16).
-    ``ws`` holds at least ``workspace_size(PHASE_PREFILL_Q4, ...)`` bytes."""
-    import torch
-    n, Hq, D = q.shape
-    B, Hkv, mb = cu_q.shape[0] - 1, kv_cache.shape[1], meta.shape[1]
-    P = _q4_dims("attn_prefill_q4", kv_cache, Hkv, D)
-    _q4_call(lib.lazy_attn_prefill_q4, "attn_prefill_q4", stream, ("q", q, torch.bfloat16, q.shape),
-             ("cu_q", cu_q, torch.int32, (B + 1,)), ("q_start", q_start, torch.int32, (B,)),
-             ("doc_blocks", doc_blocks, torch.int32, (B,)), ("meta", meta, torch.int64, (B, mb)), B, mb, n, max_q,
-             ("kv_cache", kv_cache, torch.uint8, kv_cache.shape), P, Hq, Hkv, D, scale, k_scale, v_scale,
-             ctypes.byref(cfg), ("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (n, Hq)),
-             ("ws", ws, torch.uint8, ws.shape if ws is not None else None), ws.numel() if ws is not None else 0)
+    ``ws`` (uint8) holds at least ``workspace_size(PHASE_PREFILL_Q4, ...)`` bytes."""
+    if _torch is None:
+        _bind_torch()
+    _q4_attn("attn_prefill_q4", lib.lazy_attn_prefill_q4, q, cu_q, meta.shape[0] + 1, q_start, doc_blocks, meta,
+             kv_cache, cfg, out, lse, ws, (q.shape[0], max_q), scale, k_scale, v_scale, stream)
 
 
 def device_status(stream=None) -> int:

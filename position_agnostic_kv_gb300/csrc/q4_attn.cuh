@@ -1,6 +1,8 @@
 // Arguments of the attention kernels over the 4-bit cache.
 #pragma once
 
+#include <atomic>
+
 #include "q4.cuh"
 
 namespace lazykv {
@@ -61,6 +63,19 @@ __device__ __forceinline__ int q4_rows(uint64_t w, int m) {
 __device__ __forceinline__ int q4_exponent(float top) {
   const int ex = int(__float_as_uint(top) >> 23) - 126;
   return ex < -60 || ex > 128 ? 0 : min(ex, 126);
+}
+
+// Set a kernel's dynamic shared memory limit, once per device (`done`: one bit per device, per kernel).
+template <typename F>
+inline cudaError_t q4_smem_limit(F kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 bool q4_use_tc(int Hq, int Hkv);

@@ -12,18 +12,23 @@
 //  * A code times its e4m3 scale is exact in f16.  q is normalised per head by a power of two and
 //    split in two f16 (hi + lo), so the scores carry fp32 accuracy.  Groups of at most 4 heads put hi
 //    in columns 0-3 and lo in columns 4-7 of one instruction; groups of 8 use two instructions.
+//  * With at most 4 heads the two pages of a step share one softmax: the hi and lo parts are added so that
+//    lanes t < 2 hold the even page's scores and lanes t >= 2 the odd page's, and the columns 0-3 and 4-7 of
+//    O^T accumulate even and odd pages (P's other columns are zeroed), merged in the epilogue.
 //  * q is rotated by R_{m - Delta} only when a page's Delta differs from the one before: the warp
 //    computes the D/2 angles together (two per lane), then each lane its fragment.
 //  * P is f16 (2^-11 relative), held as 2^(s - max + 7): the lazy maximum (moved only when a score
 //    beats it by more than 8) keeps it below 2^15, and small weights stay normal numbers longer.
 //  * P^T comes out of the S^T fragment by one 8x8 transpose per 8 keys.
 //
-// What bounds it: HBM for long contexts (18 D bytes per page and head).  Per page a warp issues ~240
-// instructions; at the measured HBM rate an SM gets one page-head per 99 cycles = 396 issue slots.
+// What bounds it: HBM and instruction issue together.  At the measured HBM rate an SM gets one page-head
+// (18 D bytes) per 99 cycles = 396 issue slots; a page costs about 250 warp instructions.
 //
 // Work: a CTA = (query row, KV head, head group, key split), 4 warps, each with its own run of pages
-// and a ring of stages of two page blocks, one bulk copy per block; the warps' partial (O, max, sum)
-// are merged in shared memory, those of the splits by a second kernel.
+// and a ring of stages of two page blocks, one bulk copy per block.  Block words are unpacked 32 at a time,
+// one per lane, which then issues its own copies.  The warps' partial (O, max, sum) are merged in shared
+// memory; up to 8 splits form a thread-block cluster and are merged through distributed shared memory,
+// more of them (few long rows) through the workspace and a second kernel.
 #include <cfloat>
 
 #include "q4_attn.cuh"
@@ -37,6 +42,7 @@ constexpr float kPOff = 7.0f;  // weights are held times 2^7
 constexpr int kWarps = 4;
 constexpr int kStages = 2;
 constexpr int kPair = 2;       // pages per stage
+constexpr int kMaxCluster = 8; // key splits merged inside a cluster
 
 template <int D>
 struct DecL {
@@ -46,10 +52,14 @@ struct DecL {
   static constexpr int QS = kWarps * kStages * STAGE;          // float [8][QROW]
   static constexpr int CS = QS + 8 * QROW * 4;                 // float2 [warp][D/2]
   static constexpr int SC = CS + kWarps * (D / 2) * 8;         // float [8] score factor of each head
-  static constexpr int SLOT = SC + 32;                         // {u64 word, i32 rows, pad} [warp][stage][2]
-  static constexpr int BAR = SLOT + kWarps * kStages * kPair * 16;
+  static constexpr int SLOT = SC + 32;                         // int4 {Delta, first position, rows} [warp][64]
+  static constexpr int BAR = SLOT + kWarps * 64 * 16;
   static constexpr int SMEM = BAR + kWarps * kStages * 8;
-  static_assert(kWarps * 8 * (D + 2) * 4 <= QS, "the merge buffer reuses the stages");
+  // the stages are reused to merge: the warps' partials, then (clusters) this CTA's
+  static constexpr int ML = kWarps * 8 * D * 4;
+  static constexpr int CO = ML + kWarps * 8 * 8;
+  static constexpr int CML = CO + 8 * D * 4;
+  static_assert(CML + 64 <= QS, "the merge buffers reuse the stages");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -71,6 +81,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {  // a float of CTA `rank`'s shared memory
+  float v;
+  asm volatile("{\n .reg .b32 x;\n mapa.shared::cluster.u32 x, %1, %2;\n ld.shared::cluster.f32 %0, [x];\n}\n"
+               : "=f"(v)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
 }
 
 // H8: eight heads (columns = heads, hi and lo by two instructions); else up to four.
@@ -105,46 +127,45 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   float* qs = reinterpret_cast<float*>(smem + L::QS);
   float* scs = reinterpret_cast<float*>(smem + L::SC);
   float2* cs = reinterpret_cast<float2*>(smem + L::CS) + warp * (D / 2);
-  uint8_t* slots = smem + L::SLOT + warp * kStages * kPair * 16;
+  int4* slots = reinterpret_cast<int4*>(smem + L::SLOT) + warp * 64;
   const uint32_t bar0 = smem_u32(smem + L::BAR + warp * kStages * 8);
-  uint8_t* stages = smem + warp * kStages * L::STAGE;
+  const uint32_t stage0 = smem_u32(smem + warp * kStages * L::STAGE);
 
+  // Block words, 32 pages at a time, one per lane: the lane unpacks its word, publishes what the compute
+  // needs of it (slots: two batches) and later issues its page's copy.
   const uint64_t* mrow = a.meta + (size_t)row.b * a.max_blocks + wb;
-  uint64_t mcur = lane < n ? ldg_u64(mrow + lane) : 0;
-  uint64_t mnxt = 32 + lane < n ? ldg_u64(mrow + 32 + lane) : 0;
-  int mbase = 0;
+  uint64_t mnxt = lane < n ? ldg_u64(mrow + lane) : 0;
+  int mbase = -32, my_rows = 0, my_loads = 0;
+  const uint8_t* my_src = nullptr;
+  auto next_batch = [&]() {
+    const uint64_t w = mnxt;
+    mbase += 32;
+    mnxt = mbase + 32 + lane < n ? ldg_u64(mrow + mbase + 32 + lane) : 0;
+    my_rows = 0;
+    if (mbase + lane < n) {
+      my_rows = q4_rows(w, m);
+      if (word_page(w) >= uint32_t(a.num_pages)) {
+        set_status(a.status, LAZY_STATUS_BAD_PAGE);
+        my_rows = 0;
+      }
+    }
+    slots[(mbase + lane) & 63] = make_int4(int(word_delta(w)), int(word_delta(w) + kPage * word_pg(w)), my_rows, 0);
+    my_src = a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES;
+    my_loads = (my_rows > 0) + (__shfl_xor_sync(0xffffffffu, my_rows, 1) > 0);
+  };
   if (lane == 0)
     for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
   fence_mbar_init();
   __syncwarp();
 
-  auto issue = [&](int i) {  // stage i: pages 2i and 2i + 1, one per lane
-    if (kPair * i >= mbase + 32) {
-      mcur = mnxt;
-      mbase += 32;
-      mnxt = mbase + 32 + lane < n ? ldg_u64(mrow + mbase + 32 + lane) : 0;
-    }
-    const int st = i % kStages, j = kPair * i + (lane & 1);
-    const uint64_t w = __shfl_sync(0xffffffffu, mcur, (j - mbase) & 31);
-    int rows = 0;
-    if (lane < kPair && j < n) {
-      rows = q4_rows(w, m);
-      if (word_page(w) >= uint32_t(a.num_pages)) {
-        set_status(a.status, LAZY_STATUS_BAD_PAGE);
-        rows = 0;
-      }
-    }
-    const uint32_t bar = bar0 + 8 * st;
-    if (lane < kPair) {
-      *reinterpret_cast<uint64_t*>(slots + (st * kPair + lane) * 16) = w;
-      *reinterpret_cast<int*>(slots + (st * kPair + lane) * 16 + 8) = rows;
-    }
-    const int loads = __popc(__ballot_sync(0xffffffffu, rows > 0));
-    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(loads) * Q::BYTES);
+  auto issue = [&](int i) {  // stage i: pages 2i and 2i + 1
+    if (kPair * i >= mbase + 32) next_batch();
+    const int x = kPair * i - mbase;  // the lanes that hold them: x and x + 1
+    const uint32_t bar = bar0 + 8 * (i % kStages);
+    if (lane == x) mbar_arrive_expect_tx(bar, uint32_t(my_loads) * Q::BYTES);
     __syncwarp();
-    if (rows > 0)
-      bulk_g2s(smem_u32(stages + st * L::STAGE + lane * Q::BYTES),
-               a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES, Q::BYTES, bar);
+    if ((lane & ~1) == x && my_rows > 0)
+      bulk_g2s(stage0 + (i % kStages) * L::STAGE + (lane & 1) * Q::BYTES, my_src, Q::BYTES, bar);
   };
   for (int i = 0; i < min(kStages, ns); ++i) issue(i);
 
@@ -263,6 +284,8 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
   uint32_t cur_delta = 0xFFFFFFFFu;
   bool first = true;
+  constexpr int NS = H8 ? kPair : 1;  // score sets of a lane: both pages', or its own page's
+  const bool mine1 = !H8 && t >= 2;   // this lane's page is the odd one
 
   for (int i = 0; i < ns; ++i) {
     const int st = i % kStages;
@@ -272,21 +295,21 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
         mbar_wait(bar0 + 8 * (j % kStages), uint32_t((j / kStages) & 1));
       break;
     }
-    const uint8_t* blk0 = stages + st * L::STAGE;
-    int rows[kPair];
-    float s[kPair][4];
+    const uint8_t* blk0 = smem + warp * kStages * L::STAGE + st * L::STAGE;
+    const int4 w0 = slots[(kPair * i) & 63], w1 = slots[(kPair * i + 1) & 63];
+    const int rows[kPair] = {w0.z, kPair * i + 1 < n ? w1.z : 0};
+    float acc[kPair][4];
 #pragma unroll
     for (int pp = 0; pp < kPair; ++pp) {
-      const uint64_t w = *reinterpret_cast<const uint64_t*>(slots + (st * kPair + pp) * 16);
-      rows[pp] = *reinterpret_cast<const int*>(slots + (st * kPair + pp) * 16 + 8);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[pp][e] = -INFINITY;
+      for (int e = 0; e < 4; ++e) acc[pp][e] = 0.f;
       if (rows[pp] > 0) {
         const uint8_t* blk = blk0 + pp * Q::BYTES;
         if constexpr (POS != kAlibi) {
-          if (word_delta(w) != cur_delta) {
-            cur_delta = word_delta(w);
-            rotate_q(cur_delta);
+          const uint32_t delta = uint32_t(pp ? w1.x : w0.x);
+          if (delta != cur_delta) {
+            cur_delta = delta;
+            rotate_q(delta);
           }
         }
         // ---- S^T = K q^T
@@ -311,7 +334,6 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
           ksc[0][0] = __byte_perm(sa, 0, 0x1010);
           ksc[1][0] = __byte_perm(sa, 0, 0x3232);
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < NW_; ++x) {
           uint32_t ra[4], rb[4];
@@ -324,35 +346,53 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            mma16816(acc, ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
+            mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
             if constexpr (H8)
-              mma16816(acc, ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
+              mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
           }
-        }
-        if constexpr (!H8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 2);  // hi + lo
-        }
-        s[pp][0] = acc[0] * sc0;
-        s[pp][1] = acc[1] * sc1;
-        s[pp][2] = acc[2] * sc0;
-        s[pp][3] = acc[3] * sc1;
-        if constexpr (POS == kAlibi) {
-          const float dist = float(int(word_delta(w) + kPage * word_pg(w)) + gr - m);
-          s[pp][0] += sl0 * dist;
-          s[pp][1] += sl1 * dist;
-          s[pp][2] += sl0 * (dist + 8.f);
-          s[pp][3] += sl1 * (dist + 8.f);
-        }
-        if (rows[pp] < kPage) {
-          if (gr >= rows[pp]) s[pp][0] = s[pp][1] = -INFINITY;
-          if (gr + 8 >= rows[pp]) s[pp][2] = s[pp][3] = -INFINITY;
         }
       }
     }
+    // ---- scores: [set][row gr | gr + 8][column 2t | 2t + 1], still without the factor sc (ALiBi: logits)
+    float s[NS][4];
+    if constexpr (H8) {
+#pragma unroll
+      for (int pp = 0; pp < kPair; ++pp)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[pp][e] = acc[pp][e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)  // hi + lo: each lane gives away its part of the other page
+        s[0][e] = (mine1 ? acc[1][e] : acc[0][e]) + __shfl_xor_sync(0xffffffffu, mine1 ? acc[0][e] : acc[1][e], 2);
+    }
+    if constexpr (POS == kAlibi) {
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        const float dist = float(((H8 ? x == 1 : mine1) ? w1.y : w0.y) + gr - m);
+        s[x][0] = fmaf(s[x][0], sc0, sl0 * dist);
+        s[x][1] = fmaf(s[x][1], sc1, sl1 * dist);
+        s[x][2] = fmaf(s[x][2], sc0, sl0 * (dist + 8.f));
+        s[x][3] = fmaf(s[x][3], sc1, sl1 * (dist + 8.f));
+      }
+    }
+    if (min(rows[0], rows[1]) < kPage) {
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        const int rr = (H8 ? x == 1 : mine1) ? rows[1] : rows[0];
+        if (gr >= rr) s[x][0] = s[x][1] = -INFINITY;
+        if (gr + 8 >= rr) s[x][2] = s[x][3] = -INFINITY;
+      }
+    }
     // ---- lazy running maximum of each column
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-    float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+    if constexpr (H8) {
+      x0 = fmaxf(x0, fmaxf(s[NS - 1][0], s[NS - 1][2]));
+      x1 = fmaxf(x1, fmaxf(s[NS - 1][1], s[NS - 1][3]));
+    }
+    if constexpr (POS != kAlibi) {
+      x0 *= sc0;
+      x1 *= sc1;
+    }
     if (__any_sync(0xffffffffu, first || x0 > m0 + kTau || x1 > m1 + kTau)) {
       first = false;
 #pragma unroll
@@ -375,14 +415,23 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
       }
     }
     const float f0 = kPOff - m0, f1 = kPOff - m1;
+    uint32_t pb[NS][2];  // P^T fragments: keys 0-7 and 8-15
+#pragma unroll
+    for (int x = 0; x < NS; ++x) {
+      const float k0 = POS == kAlibi ? 1.f : sc0, k1 = POS == kAlibi ? 1.f : sc1;
+      const float p0 = ex2_approx(fmaf(s[x][0], k0, f0)), p1 = ex2_approx(fmaf(s[x][1], k1, f1));
+      const float p2 = ex2_approx(fmaf(s[x][2], k0, f0)), p3 = ex2_approx(fmaf(s[x][3], k1, f1));
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      pb[x][0] = transpose8(pack_h2(p0, p1));
+      pb[x][1] = transpose8(pack_h2(p2, p3));
+    }
 #pragma unroll
     for (int pp = 0; pp < kPair; ++pp) {
       if (rows[pp] == 0) continue;
-      const float p0 = ex2_approx(s[pp][0] + f0), p1 = ex2_approx(s[pp][1] + f1);
-      const float p2 = ex2_approx(s[pp][2] + f0), p3 = ex2_approx(s[pp][3] + f1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      const uint32_t b0 = transpose8(pack_h2(p0, p1)), b1 = transpose8(pack_h2(p2, p3));
+      // columns of the other page take no part in this page's product
+      const bool use = H8 || (gr >= 4) == (pp == 1);
+      const uint32_t b0 = use ? pb[H8 ? pp : 0][0] : 0u, b1 = use ? pb[H8 ? pp : 0][1] : 0u;
       // ---- O^T += V^T P^T
       const uint8_t* blk = blk0 + pp * Q::BYTES;
       const int vg = D == 128 ? lane : (gr >> 1) * 4 + t;
@@ -423,48 +472,52 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   }
   pdl_trigger();
 
-  // ---- merge the warps: O^T fragments hold dimensions D/8 gr + 2x (+1), columns 2t, 2t + 1
+  // ---- merge the warps: O^T fragments hold dimensions D/8 gr + 2x (+1), columns 2t, 2t + 1.  With at most
+  // four heads the columns h and h + 4 are two partials of head h.
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, off);
     l1 += __shfl_xor_sync(0xffffffffu, l1, off);
   }
   __syncthreads();  // every stage is consumed
-  float* mo = reinterpret_cast<float*>(smem);   // [warp][8][D]
-  float* mml = mo + kWarps * 8 * D;             // [warp][8][2]
-  if (H8 || t < 2) {
+  float* mo = reinterpret_cast<float*>(smem);                  // [warp][column][D]
+  float2* mml = reinterpret_cast<float2*>(smem + L::ML);       // [warp][column]
 #pragma unroll
-    for (int x = 0; x < NKS; ++x) {
-      const int d = (D / 8) * gr + 2 * x;
-      *reinterpret_cast<float2*>(mo + (warp * 8 + c0) * D + d) = make_float2(o[x][0], o[x][2]);
-      *reinterpret_cast<float2*>(mo + (warp * 8 + c1) * D + d) = make_float2(o[x][1], o[x][3]);
-    }
-    if (gr == 0) {
-      mml[(warp * 8 + c0) * 2] = l0 != 0.f ? m0 : -INFINITY;
-      mml[(warp * 8 + c0) * 2 + 1] = l0;
-      mml[(warp * 8 + c1) * 2] = l1 != 0.f ? m1 : -INFINITY;
-      mml[(warp * 8 + c1) * 2 + 1] = l1;
-    }
+  for (int x = 0; x < NKS; ++x) {
+    const int d = (D / 8) * gr + 2 * x;
+    *reinterpret_cast<float2*>(mo + (warp * 8 + 2 * t) * D + d) = make_float2(o[x][0], o[x][2]);
+    *reinterpret_cast<float2*>(mo + (warp * 8 + 2 * t + 1) * D + d) = make_float2(o[x][1], o[x][3]);
+  }
+  if (gr == 0) {
+    mml[warp * 8 + 2 * t] = make_float2(l0 != 0.f ? m0 : -INFINITY, l0);
+    mml[warp * 8 + 2 * t + 1] = make_float2(l1 != 0.f ? m1 : -INFINITY, l1);
   }
   __syncthreads();
+  constexpr int PARTS = H8 ? kWarps : 2 * kWarps;
+  float* co = reinterpret_cast<float*>(smem + L::CO);          // [head][D] (clusters)
+  float2* cml = reinterpret_cast<float2*>(smem + L::CML);      // [head]
   for (int x = threadIdx.x; x < heads * D; x += kWarps * 32) {
     const int h = x / D, d = x % D;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mml[(w * 8 + h) * 2]);
+    for (int w = 0; w < PARTS; ++w) M = fmaxf(M, mml[H8 ? w * 8 + h : w * 4 + h].x);
     float O = 0.f, l = 0.f;
     if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(mml[(w * 8 + h) * 2] - M);
-        O += f * mo[(w * 8 + h) * D + d];
-        l += f * mml[(w * 8 + h) * 2 + 1];
+      for (int w = 0; w < PARTS; ++w) {
+        const int col = H8 ? w * 8 + h : w * 4 + h;
+        const float f = exp2f(mml[col].x - M);
+        O += f * mo[col * D + d];
+        l += f * mml[col].y;
       }
     }
     const size_t rh = (size_t)r * a.Hq + h0 + h;
     if (a.S == 1) {
       a.out[rh * D + d] = __float2bfloat16_rn(l != 0.f ? O * (a.v_factor / l) : 0.f);
       if (a.lse && d == 0) a.lse[rh] = (M + log2f(l) - kPOff) * 0.6931471805599453f;
+    } else if (a.S <= kMaxCluster) {
+      co[x] = O;
+      if (d == 0) cml[h] = make_float2(M, l);
     } else {
       a.part_o[(rh * a.S + split) * D + d] = O * a.v_factor;
       if (d == 0) {
@@ -472,6 +525,27 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
         a.part_ml[(rh * a.S + split) * 2 + 1] = l;
       }
     }
+  }
+  if (a.S > 1 && a.S <= kMaxCluster) {
+    // ---- merge the cluster: CTA `split` of it combines and writes its share of the elements
+    cluster_sync();
+    const int per = (heads * D + a.S - 1) / a.S;
+    for (int x = split * per + threadIdx.x; x < min(heads * D, (split + 1) * per); x += kWarps * 32) {
+      const int h = x / D, d = x % D;
+      float M = -INFINITY;
+      for (int c = 0; c < a.S; ++c) M = fmaxf(M, ld_cluster(smem_u32(&cml[h].x), c));
+      float O = 0.f, l = 0.f;
+      if (M != -INFINITY)
+        for (int c = 0; c < a.S; ++c) {
+          const float f = exp2f(ld_cluster(smem_u32(&cml[h].x), c) - M);
+          O += f * ld_cluster(smem_u32(co + x), c);
+          l += f * ld_cluster(smem_u32(&cml[h].y), c);
+        }
+      const size_t rh = (size_t)r * a.Hq + h0 + h;
+      a.out[rh * D + d] = __float2bfloat16_rn(l != 0.f ? O * (a.v_factor / l) : 0.f);
+      if (a.lse && d == 0) a.lse[rh] = (M + log2f(l) - kPOff) * 0.6931471805599453f;
+    }
+    cluster_sync();  // no CTA leaves while another still reads its partials
   }
 }
 
@@ -498,21 +572,36 @@ __global__ void __launch_bounds__(D) q4_merge_kernel(const float* __restrict__ p
   if (lse && d == 0) lse[rh] = (M + log2f(l)) * 0.6931471805599453f;
 }
 
-// Heads per CTA, and key splits: about four waves of resident CTAs, at least 8 pages per warp.
 int q4_heads(int Hq, int Hkv) { return min(Hq / Hkv, 8); }
 
+// Key splits of a unit (query row, KV head, head group): 1, 2, 4, 8 (one cluster) or 16, 32, 64 (workspace).
+// The slowest SM carries k = ceil(units S / SMs) CTAs of ceil(blocks / S) pages and a fixed part worth about
+// 10 pages each; it needs about four CTAs to run at full rate.
 int q4_splits(int rows, int Hq, int Hkv, int max_blocks) {
-  const long long units = (long long)rows * (Hq / q4_heads(Hq, Hkv));
-  const long long want = ((long long)sm_count() * 16 + units - 1) / units;
-  const long long by_len = (max_blocks + kWarps * 8 - 1) / (kWarps * 8);
-  return int(max(1ll, min(min(want, by_len), 64ll)));
+  const long long units = (long long)rows * (Hq / q4_heads(Hq, Hkv)), sms = sm_count();
+  int best = 1;
+  long long least = 0;
+  for (int S = 1; S <= 64 && S <= max(1, max_blocks / kWarps); S *= 2) {
+    const long long k = (units * S + sms - 1) / sms;
+    const long long cost = k * ((max_blocks + S - 1) / S + 10) * 4 / min(k, 4ll);
+    if (S == 1 || cost * 20 < least * 19) {  // a larger split has to gain 5 %
+      best = S;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <int D, bool H8, int POS>
 int launch_q4(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
   auto kern = q4_decode_kernel<D, H8, POS>;
-  LAZY_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecL<D>::SMEM));
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, a, heads, a.Hq / a.Hkv / heads));
+  static std::atomic<uint64_t> done{0};
+  LAZY_CUDA_TRY(q4_smem_limit(kern, DecL<D>::SMEM, done));
+  const int ngrp = a.Hq / a.Hkv / heads;
+  if (a.S > 1 && a.S <= kMaxCluster)
+    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, unsigned(a.S), a, heads, ngrp));
+  else
+    LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, a, heads, ngrp));
   return LAZY_OK;
 }
 
@@ -528,7 +617,7 @@ int launch_q4_pos(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
 size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_mode) {
   (void)rows_mode;
   const size_t S = size_t(q4_splits(rows, Hq, Hkv, max_blocks));
-  if (S <= 1) return 0;
+  if (S <= size_t(kMaxCluster)) return 0;
   const size_t po = (size_t)rows * Hq * S * D * 4;
   return (po + 255) / 256 * 256 + (size_t)rows * Hq * S * 8;
 }
@@ -536,7 +625,7 @@ size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_m
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {
   const int heads = q4_heads(a.Hq, a.Hkv);
   a.S = q4_splits(a.rows, a.Hq, a.Hkv, a.max_blocks);
-  if (a.S > 1) {
+  if (a.S > kMaxCluster) {
     const size_t need = q4_ws_bytes(a.rows, a.Hq, a.Hkv, D, a.max_blocks, rows_mode);
     if (!ws || ws_bytes < need)
       return fail(LAZY_EINVAL, "workspace too small: need %zu bytes, got %zu", need, ws ? ws_bytes : 0);
@@ -555,7 +644,7 @@ int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cud
     rc = heads == 8 ? launch_q4_pos<128, true>(a, heads, grid, st) : launch_q4_pos<128, false>(a, heads, grid, st);
   else
     rc = heads == 8 ? launch_q4_pos<64, true>(a, heads, grid, st) : launch_q4_pos<64, false>(a, heads, grid, st);
-  if (rc || a.S == 1) return rc;
+  if (rc || a.S <= kMaxCluster) return rc;
   const unsigned rh = unsigned((long long)a.rows * a.Hq);
   if (D == 128)
     LAZY_CUDA_TRY(launch_pdl(q4_merge_kernel<128>, dim3(rh), dim3(128), 0, st, (const float*)a.part_o,

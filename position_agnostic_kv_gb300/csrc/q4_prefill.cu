@@ -945,13 +945,18 @@ template <int D, int POS, bool KH>
 int launch_q4_tc(const Q4Args& a, int max_q, cudaStream_t st) {
   using L = tcq::Layout<D>;
   auto kern = tcq::q4_prefill_kernel<D, POS, KH>;
-  LAZY_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM));
   // the setmaxnreg split is only valid for a launch with exactly kRegsLaunch registers per thread
-  cudaFuncAttributes fa;
-  LAZY_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
-  if (fa.numRegs != tcq::kRegsLaunch)
-    return fail(LAZY_ECUDA, "4-bit prefill kernel built with %d registers per thread, expected %d", fa.numRegs,
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    LAZY_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != tcq::kRegsLaunch)
+    return fail(LAZY_ECUDA, "4-bit prefill kernel built with %d registers per thread, expected %d", regs.load(),
                 tcq::kRegsLaunch);
+  static std::atomic<uint64_t> done{0};
+  LAZY_CUDA_TRY(q4_smem_limit(kern, L::SMEM, done));
   const int rows_tok = tcq::kQT * (tcq::kM / (a.Hq / a.Hkv));
   const int nmp = (max_q + rows_tok - 1) / rows_tok;
   const long long pairs = (long long)a.B * a.Hkv;
