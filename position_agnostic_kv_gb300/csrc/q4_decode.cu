@@ -44,16 +44,16 @@ constexpr int kStages = 2;
 constexpr int kPair = 2;       // pages per stage
 constexpr int kMaxCluster = 8; // key splits merged inside a cluster
 
-template <int D>
+template <int D, bool H8>
 struct DecL {
   static constexpr int DL = D / 4;                    // dimensions of a lane's K fragment
   static constexpr int QROW = 4 * (DL + 4);           // padded: 4 t-chunks fall on different banks
   static constexpr int STAGE = kPair * Q4<D>::BYTES;
   static constexpr int QS = kWarps * kStages * STAGE;          // float [8][QROW]
-  static constexpr int CS = QS + 8 * QROW * 4;                 // float2 [warp][D/2]
+  static constexpr int CS = QS + (H8 ? 8 : 4) * QROW * 4;      // float2 [warp][D/2]
   static constexpr int SC = CS + kWarps * (D / 2) * 8;         // float [8] score factor of each head
-  static constexpr int SLOT = SC + 32;                         // int4 {Delta, first position, rows} [warp][64]
-  static constexpr int BAR = SLOT + kWarps * 64 * 16;
+  static constexpr int SLOT = SC + 32;                         // int2 {Delta | rows << 24, first position} [warp][64]
+  static constexpr int BAR = SLOT + kWarps * 64 * 8;
   static constexpr int SMEM = BAR + kWarps * kStages * 8;
   // the stages are reused to merge: the warps' partials, then (clusters) this CTA's
   static constexpr int ML = kWarps * 8 * D * 4;
@@ -98,7 +98,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {  // a flo
 // H8: eight heads (columns = heads, hi and lo by two instructions); else up to four.
 template <int D, bool H8, int POS>
 __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(const Q4Args a, int heads, int ngrp) {
-  using L = DecL<D>;
+  using L = DecL<D, H8>;
   using Q = Q4<D>;
   constexpr int NKS = D / 16;   // k-steps of S, and m-tiles of O^T
   constexpr int NW_ = D / 32;   // words of a K row per lane
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   float* qs = reinterpret_cast<float*>(smem + L::QS);
   float* scs = reinterpret_cast<float*>(smem + L::SC);
   float2* cs = reinterpret_cast<float2*>(smem + L::CS) + warp * (D / 2);
-  int4* slots = reinterpret_cast<int4*>(smem + L::SLOT) + warp * 64;
+  int2* slots = reinterpret_cast<int2*>(smem + L::SLOT) + warp * 64;
   const uint32_t bar0 = smem_u32(smem + L::BAR + warp * kStages * 8);
   const uint32_t stage0 = smem_u32(smem + warp * kStages * L::STAGE);
 
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
         my_rows = 0;
       }
     }
-    slots[(mbase + lane) & 63] = make_int4(int(word_delta(w)), int(word_delta(w) + kPage * word_pg(w)), my_rows, 0);
+    slots[(mbase + lane) & 63] =
+        make_int2(int(word_delta(w) | uint32_t(my_rows) << 24), int(word_delta(w) + kPage * word_pg(w)));
     my_src = a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES;
     my_loads = (my_rows > 0) + (__shfl_xor_sync(0xffffffffu, my_rows, 1) > 0);
   };
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   for (int i = 0; i < min(kStages, ns); ++i) issue(i);
 
   // ---- queries: one warp per head, normalised by a power of two, in fp32
-  for (int h = warp; h < 8; h += kWarps) {
+  for (int h = warp; h < (H8 ? 8 : 4); h += kWarps) {
     float x[D / 32];
     float top = 0.f;
 #pragma unroll
@@ -289,70 +290,77 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
 
   for (int i = 0; i < ns; ++i) {
     const int st = i % kStages;
-    if (!mbar_wait(bar0 + 8 * st, uint32_t((i / kStages) & 1))) {
+    if (!mbar_wait_quiet(bar0 + 8 * st, uint32_t((i / kStages) & 1))) {
       if (lane == 0) set_status(a.status, LAZY_STATUS_TIMEOUT);
       for (int j = i + 1; j < min(ns, i + kStages); ++j)
-        mbar_wait(bar0 + 8 * (j % kStages), uint32_t((j / kStages) & 1));
+        mbar_wait_quiet(bar0 + 8 * (j % kStages), uint32_t((j / kStages) & 1));
       break;
     }
     const uint8_t* blk0 = smem + warp * kStages * L::STAGE + st * L::STAGE;
-    const int4 w0 = slots[(kPair * i) & 63], w1 = slots[(kPair * i + 1) & 63];
-    const int rows[kPair] = {w0.z, kPair * i + 1 < n ? w1.z : 0};
-    float acc[kPair][4];
-#pragma unroll
-    for (int pp = 0; pp < kPair; ++pp) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[pp][e] = 0.f;
-      if (rows[pp] > 0) {
-        const uint8_t* blk = blk0 + pp * Q::BYTES;
-        if constexpr (POS != kAlibi) {
-          const uint32_t delta = uint32_t(pp ? w1.x : w0.x);
-          if (delta != cur_delta) {
-            cur_delta = delta;
-            rotate_q(delta);
-          }
-        }
-        // ---- S^T = K q^T
-        uint32_t kw[2][NW_], ksc[2][NW_ / 2];
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(blk + lane * 16);
-          const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
-          kw[0][0] = x.x; kw[0][1] = x.y; kw[0][2] = x.z; kw[0][3] = x.w;
-          kw[1][0] = y.x; kw[1][1] = y.y; kw[1][2] = y.z; kw[1][3] = y.w;
-          const uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::KS + lane * 4);
-          const uint32_t sa = e4m3x2_to_h2(sw & 0xFFFFu), sb = e4m3x2_to_h2(sw >> 16);
-          ksc[0][0] = __byte_perm(sa, 0, 0x1010);
-          ksc[0][1] = __byte_perm(sa, 0, 0x3232);
-          ksc[1][0] = __byte_perm(sb, 0, 0x1010);
-          ksc[1][1] = __byte_perm(sb, 0, 0x3232);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(blk + lane * 8);
-          const uint2 y = *reinterpret_cast<const uint2*>(blk + 256 + lane * 8);
-          kw[0][0] = x.x; kw[0][1] = x.y;
-          kw[1][0] = y.x; kw[1][1] = y.y;
-          const uint32_t sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(blk + Q::KS + lane * 2));
-          ksc[0][0] = __byte_perm(sa, 0, 0x1010);
-          ksc[1][0] = __byte_perm(sa, 0, 0x3232);
-        }
-#pragma unroll
-        for (int x = 0; x < NW_; ++x) {
-          uint32_t ra[4], rb[4];
-          e2m1x8_to_h2(kw[0][x], ra);
-          e2m1x8_to_h2(kw[1][x], rb);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ra[e] = hmul2(ra[e], ksc[0][x / 2]);
-            rb[e] = hmul2(rb[e], ksc[1][x / 2]);
-          }
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
-            if constexpr (H8)
-              mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
-          }
-        }
+    const int4 w = *reinterpret_cast<const int4*>(slots + ((kPair * i) & 63));  // both pages' slots
+    const int delta0 = w.x & 0xFFFFFF, delta1 = w.z & 0xFFFFFF, rows0 = w.x >> 24;
+    const int rows1 = kPair * i + 1 < n ? w.z >> 24 : 0;
+    // Both pages in one straight run of instructions, absent ones masked like absent rows.  Where the
+    // document changes between the two, they take a pass each.
+    const bool split_pair = POS != kAlibi && rows0 > 0 && rows1 > 0 && delta0 != delta1;
+#pragma unroll 1
+    for (int pass = 0; pass <= int(split_pair); ++pass) {
+    const int rows[kPair] = {split_pair && pass == 1 ? 0 : rows0, split_pair && pass == 0 ? 0 : rows1};
+    if constexpr (POS != kAlibi) {
+      const uint32_t delta = uint32_t(rows[0] > 0 ? delta0 : delta1);
+      if (delta != cur_delta && rows[0] + rows[1] > 0) {
+        cur_delta = delta;
+        rotate_q(delta);
       }
     }
+    // ---- S^T = K q^T
+    float acc[kPair][4];
+    uint32_t kw[kPair][2][NW_], ksc[kPair][2][NW_ / 2];
+#pragma unroll
+    for (int pp = 0; pp < kPair; ++pp) {
+      const uint8_t* blk = blk0 + pp * Q::BYTES;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[pp][e] = 0.f;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(blk + lane * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
+        kw[pp][0][0] = x.x; kw[pp][0][1] = x.y; kw[pp][0][2] = x.z; kw[pp][0][3] = x.w;
+        kw[pp][1][0] = y.x; kw[pp][1][1] = y.y; kw[pp][1][2] = y.z; kw[pp][1][3] = y.w;
+        const uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::KS + lane * 4);
+        const uint32_t sa = e4m3x2_to_h2(sw & 0xFFFFu), sb = e4m3x2_to_h2(sw >> 16);
+        ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
+        ksc[pp][0][1] = __byte_perm(sa, 0, 0x3232);
+        ksc[pp][1][0] = __byte_perm(sb, 0, 0x1010);
+        ksc[pp][1][1] = __byte_perm(sb, 0, 0x3232);
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(blk + lane * 8);
+        const uint2 y = *reinterpret_cast<const uint2*>(blk + 256 + lane * 8);
+        kw[pp][0][0] = x.x; kw[pp][0][1] = x.y;
+        kw[pp][1][0] = y.x; kw[pp][1][1] = y.y;
+        const uint32_t sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(blk + Q::KS + lane * 2));
+        ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
+        ksc[pp][1][0] = __byte_perm(sa, 0, 0x3232);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < NW_; ++x)
+#pragma unroll
+      for (int pp = 0; pp < kPair; ++pp) {
+        uint32_t ra[4], rb[4];
+        e2m1x8_to_h2(kw[pp][0][x], ra);
+        e2m1x8_to_h2(kw[pp][1][x], rb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ra[e] = hmul2(ra[e], ksc[pp][0][x / 2]);
+          rb[e] = hmul2(rb[e], ksc[pp][1][x / 2]);
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
+          if constexpr (H8)
+            mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
+        }
+      }
     // ---- scores: [set][row gr | gr + 8][column 2t | 2t + 1], still without the factor sc (ALiBi: logits)
     float s[NS][4];
     if constexpr (H8) {
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
     if constexpr (POS == kAlibi) {
 #pragma unroll
       for (int x = 0; x < NS; ++x) {
-        const float dist = float(((H8 ? x == 1 : mine1) ? w1.y : w0.y) + gr - m);
+        const float dist = float(((H8 ? x == 1 : mine1) ? w.w : w.y) + gr - m);
         s[x][0] = fmaf(s[x][0], sc0, sl0 * dist);
         s[x][1] = fmaf(s[x][1], sc1, sl1 * dist);
         s[x][2] = fmaf(s[x][2], sc0, sl0 * (dist + 8.f));
@@ -428,7 +436,6 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
     }
 #pragma unroll
     for (int pp = 0; pp < kPair; ++pp) {
-      if (rows[pp] == 0) continue;
       // columns of the other page take no part in this page's product
       const bool use = H8 || (gr >= 4) == (pp == 1);
       const uint32_t b0 = use ? pb[H8 ? pp : 0][0] : 0u, b1 = use ? pb[H8 ? pp : 0][1] : 0u;
@@ -466,6 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
         for (int x = 0; x < 4; ++x)
           mma16816(o[4 * w + x], hmul2(e0[x], vs0), hmul2(o0[x], vs0), hmul2(e1[x], vs1), hmul2(o1[x], vs1), b0, b1);
       }
+    }
     }
     __syncwarp();
     if (i + kStages < ns) issue(i + kStages);
@@ -596,12 +604,12 @@ template <int D, bool H8, int POS>
 int launch_q4(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
   auto kern = q4_decode_kernel<D, H8, POS>;
   static std::atomic<uint64_t> done{0};
-  LAZY_CUDA_TRY(q4_smem_limit(kern, DecL<D>::SMEM, done));
+  LAZY_CUDA_TRY(q4_smem_limit(kern, DecL<D, H8>::SMEM, done));
   const int ngrp = a.Hq / a.Hkv / heads;
   if (a.S > 1 && a.S <= kMaxCluster)
-    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, unsigned(a.S), a, heads, ngrp));
+    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3(grid), dim3(kWarps * 32), DecL<D, H8>::SMEM, st, unsigned(a.S), a, heads, ngrp));
   else
-    LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D>::SMEM, st, a, heads, ngrp));
+    LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D, H8>::SMEM, st, a, heads, ngrp));
   return LAZY_OK;
 }
 
