@@ -622,45 +622,66 @@ int launch_q4_pos(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
 
 }  // namespace
 
+// Key splits whose partials go through the workspace (1: none do).
+static int ws_splits(int rows, int Hq, int Hkv, int max_blocks, bool rows_mode) {
+  if (!rows_mode && q4_decode_on_tc(Hq, Hkv)) return q4_tc_splits(rows, Hkv, max_blocks);
+  if (rows_mode && q4_use_tc(Hq, Hkv)) return 1;
+  const int S = q4_splits(rows, Hq, Hkv, max_blocks);
+  return S <= kMaxCluster ? 1 : S;
+}
+
 size_t q4_ws_bytes(int rows, int Hq, int Hkv, int D, int max_blocks, bool rows_mode) {
-  (void)rows_mode;
-  const size_t S = size_t(q4_splits(rows, Hq, Hkv, max_blocks));
-  if (S <= size_t(kMaxCluster)) return 0;
+  const size_t S = size_t(ws_splits(rows, Hq, Hkv, max_blocks, rows_mode));
+  if (S == 1) return 0;
   const size_t po = (size_t)rows * Hq * S * D * 4;
   return (po + 255) / 256 * 256 + (size_t)rows * Hq * S * 8;
 }
 
+// Point the partials into the caller's workspace.
+static int take_ws(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes) {
+  const size_t need = q4_ws_bytes(a.rows, a.Hq, a.Hkv, D, a.max_blocks, rows_mode);
+  if (need == 0) return LAZY_OK;
+  if (!ws || ws_bytes < need)
+    return fail(LAZY_EINVAL, "workspace too small: need %zu bytes, got %zu", need, ws ? ws_bytes : 0);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(LAZY_EINVAL, "workspace must be 256-byte aligned");
+  const size_t po = (size_t)a.rows * a.Hq * a.S * D * 4;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (po + 255) / 256 * 256);
+  return LAZY_OK;
+}
+
+cudaError_t q4_merge(const Q4Args& a, int D, cudaStream_t st) {
+  const unsigned rh = unsigned((long long)a.rows * a.Hq);
+  return D == 128 ? launch_pdl(q4_merge_kernel<128>, dim3(rh), dim3(128), 0, st, (const float*)a.part_o,
+                               (const float*)a.part_ml, a.S, a.out, a.lse)
+                  : launch_pdl(q4_merge_kernel<64>, dim3(rh), dim3(64), 0, st, (const float*)a.part_o,
+                               (const float*)a.part_ml, a.S, a.out, a.lse);
+}
+
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if ((long long)a.rows * a.Hq > 0x7FFFFFFFll)
+    return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
+  if (!rows_mode && q4_decode_on_tc(a.Hq, a.Hkv)) {
+    a.S = q4_tc_splits(a.rows, a.Hkv, a.max_blocks);
+    int rc = take_ws(a, D, rows_mode, ws, ws_bytes);
+    if (rc == LAZY_OK) rc = run_q4_tc(a, D, 1, st);
+    if (rc == LAZY_OK && a.S > 1) LAZY_CUDA_TRY(q4_merge(a, D, st));
+    return rc;
+  }
   const int heads = q4_heads(a.Hq, a.Hkv);
   a.S = q4_splits(a.rows, a.Hq, a.Hkv, a.max_blocks);
-  if (a.S > kMaxCluster) {
-    const size_t need = q4_ws_bytes(a.rows, a.Hq, a.Hkv, D, a.max_blocks, rows_mode);
-    if (!ws || ws_bytes < need)
-      return fail(LAZY_EINVAL, "workspace too small: need %zu bytes, got %zu", need, ws ? ws_bytes : 0);
-    if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(LAZY_EINVAL, "workspace must be 256-byte aligned");
-    const size_t po = (size_t)a.rows * a.Hq * a.S * D * 4;
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (po + 255) / 256 * 256);
-  }
+  int rc = take_ws(a, D, rows_mode, ws, ws_bytes);
+  if (rc) return rc;
   const long long ctas = (long long)a.rows * (a.Hq / heads) * a.S;
-  if (ctas > 0x7FFFFFFFll || (long long)a.rows * a.Hq > 0x7FFFFFFFll)
-    return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
+  if (ctas > 0x7FFFFFFFll) return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
   const unsigned grid = unsigned(ctas);
   if (a.pos.kind == kNone) a.pos.slopes = nullptr;
-  int rc;
   if (D == 128)
     rc = heads == 8 ? launch_q4_pos<128, true>(a, heads, grid, st) : launch_q4_pos<128, false>(a, heads, grid, st);
   else
     rc = heads == 8 ? launch_q4_pos<64, true>(a, heads, grid, st) : launch_q4_pos<64, false>(a, heads, grid, st);
-  if (rc || a.S <= kMaxCluster) return rc;
-  const unsigned rh = unsigned((long long)a.rows * a.Hq);
-  if (D == 128)
-    LAZY_CUDA_TRY(launch_pdl(q4_merge_kernel<128>, dim3(rh), dim3(128), 0, st, (const float*)a.part_o,
-                             (const float*)a.part_ml, a.S, a.out, a.lse));
-  else
-    LAZY_CUDA_TRY(launch_pdl(q4_merge_kernel<64>, dim3(rh), dim3(64), 0, st, (const float*)a.part_o,
-                             (const float*)a.part_ml, a.S, a.out, a.lse));
-  return LAZY_OK;
+  if (rc == LAZY_OK && a.S > kMaxCluster) LAZY_CUDA_TRY(q4_merge(a, D, st));
+  return rc;
 }
 
 }  // namespace lazykv
