@@ -19,19 +19,21 @@
 //              against bank conflicts.
 //   warp 12    producer: block words one tile ahead, one bulk copy per page into a 2-stage ring of packed
 //              keys and a 1-stage ring of packed values.
-//   warp 13    TMEM owner and MMA issuer.
-// The operand rings have 2 stages, filled a tile ahead.  TMEM columns: S [0,256), O0 [256,384), O1 [384,512).
-// Two live Q tiles: a tile's keys are taken in halves of 64, with a score buffer for each Q tile and half
-// (S of tile i, half h at 128 i + 64 h, P over its first 32 columns), in the order
-//   PV0(x) QK0(x + 2) PV1(x) QK1(x + 2) | x + 1 ...   (x counts halves)
-// so each softmax warpgroup finds its next scores ready while its last weights are multiplied.  (With whole
-// tiles, one score buffer per Q tile, the warpgroups waited half of the time: a tile of a 10 300-key, two-
-// Q-tile CTA took 4300 cycles.)
-// One live Q tile (KH, chosen when every CTA has one): S0 and S1 double-buffer whole tiles, the two softmax
-// warpgroups take half of every tile's keys each, O_A and O_B are merged in the epilogue.
+//   warp 13    TMEM owner and MMA issuer: QK0(j) QK1(j) | PV0(j) QK0(j+1) PV1(j) QK1(j+1) | ...
+// Both f16 rings have 2 stages, filled a tile ahead.  TMEM: S0 [0,128), S1 [128,256), O0 [256,384),
+// O1 [384,512); P_i in the first half of S_i.
+// With one live Q tile S0 and S1 double-buffer its scores; in launches whose CTAs all have one (KH) the two
+// softmax warpgroups each take half of every tile's keys and merge in the epilogue.
 //
-// What bounds it: the softmax (one exponential and ~4 other instructions per score) beside the tensor
-// pipe; the packed cache is read at 18 D / 16 bytes per key and head.  Every wait is bounded.
+// What bounds it: the softmax, one exponential and ~4 other instructions per score: 128 scores of a row
+// take ~2100 of a tile's ~3800 cycles, the products of both Q tiles 2048, and the two overlap in part (the
+// scores of one Q tile are computed while the other's are waited for).  The packed cache, 18 D / 16 bytes
+// per key and head, comes out of the L2.  8 x 64 queries of 64 heads (8 KV heads) over 10 300 keys: 157 us,
+// 1100 TFLOP/s; 32 x 32 queries of 32 heads of one KV head over 12 000 keys, ALiBi: 216 us, 935 TFLOP/s; 32
+// heads, 4 requests of 100 queries over 2000 keys: 37.5 us.
+// Measured and left out: dequantisation of both operands by one warpgroup 232 us (first shape), scores in
+// halves of a tile with two buffers per Q tile 176 (second shape 200), values only in halves 171 (201), an
+// MMA thread per Q tile 229 (291).  Every wait is bounded.
 #include <cfloat>
 
 #include "q4_attn.cuh"
@@ -49,9 +51,10 @@ constexpr int kSlots = 6;  // per-tile metadata: published up to 5 tiles ahead o
 constexpr int kThreads = 512;
 constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13, kValWarp0 = 14;
 constexpr int kRegsLaunch = 128;
-// registers per thread after the re-split: softmax, dequantisation, producer + MMA; they add up to the launch's
+// Registers per thread after the re-split: softmax, keys, and the warpgroup of producer, MMA and values; they
+// add up to the launch's.  (176, 72, 88) takes 163 us for the first shape above, (168, 72, 104) 160.
 template <bool KH> struct Regs {
-  static constexpr int softmax = 176, deq = 72, issue = 88;
+  static constexpr int softmax = 176, deq = 56, issue = 104;
   static_assert(2 * softmax + deq + issue == 4 * kRegsLaunch, "warpgroup register shares");
 };
 constexpr float kTau = 8.0f, kPOff = 7.0f;
@@ -65,12 +68,12 @@ enum : int {
   B_K_FREE = 8,    // [2] every QK^T of the stage done (commit)
   B_V_READY = 10,  // [2] V operand written (64)
   B_V_FREE = 12,   // [2] every PV of the stage done (commit)
-  B_S_FULL = 14,   // [4] per score buffer (2 x Q tile + half; KH: per tile parity): S written (commit)
-  B_P_FULL = 18,   // [4] the same: P in TMEM, O rescaled (128, KH 256)
-  B_Q_READY = 22,  // Q operands written (256)
-  B_FINAL = 23,    // all MMAs done (commit)
-  B_PV_DONE = 24,  // [2] per Q tile (KH: the first): a step's PV done (commit)
-  NBAR = 26
+  B_S_FULL = 14,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
+  B_P_FULL = 16,   // [2] P in TMEM, O rescaled (128, KH 256)
+  B_Q_READY = 18,  // Q operands written (256)
+  B_FINAL = 19,    // all MMAs done (commit)
+  B_PV_DONE = 20,  // one live Q tile: a tile's PV done (commit)
+  NBAR = 21
 };
 
 template <int D>
@@ -210,9 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       mbar_init(BAR(B_K_FREE + s), 1);
       mbar_init(BAR(B_V_READY + s), 64);
       mbar_init(BAR(B_V_FREE + s), 1);
-      mbar_init(BAR(B_PV_DONE + s), 1);
-    }
-    for (int s = 0; s < 4; ++s) {
       mbar_init(BAR(B_S_FULL + s), 1);
       mbar_init(BAR(B_P_FULL + s), KH ? 256 : 128);
     }
@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
     mbar_init(BAR(B_PV_FREE), 64);
     mbar_init(BAR(B_Q_READY), 2 * 128);
     mbar_init(BAR(B_FINAL), 1);
+    mbar_init(BAR(B_PV_DONE), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -342,21 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
       const uint32_t tO = tl + uint32_t(2 * kN + qt * 128);
       float m_run = -INFINITY, l_run = 0.f;
-      constexpr int NK = kN / 2, NPG = NK / kPage;  // a step's keys and pages
-      const int steps = KH ? ntiles : 2 * ntiles;
-      for (int i = 0; i < steps && ok; ++i) {
-        // step i: tile j, half kh; ALiBi takes the newer half first, as it does tiles
-        const int j = KH ? i : i >> 1, kh = KH ? qt : (i & 1) ^ int(POS == kAlibi);
-        const int slot = j % kSlots, pg0 = NPG * kh;
-        const int buf = KH ? j & 1 : 2 * qt + kh;
-        const uint32_t tS = tl + uint32_t(KH ? (j & 1) * kN + kh * NK : buf * NK);
-        const bool got_s = wait_bar(BAR(B_S_FULL + buf), uint32_t((KH ? j >> 1 : j) & 1), abort_flag, a.status);
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int slot = j % kSlots;
+        const int buf = nq == 2 ? qt : (j & 1);
+        const uint32_t tS = tl + uint32_t(buf * kN);
+        const bool got_s =
+            wait_bar(BAR(B_S_FULL + buf), uint32_t(nq == 2 ? (j & 1) : ((j >> 1) & 1)), abort_flag, a.status);
         if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
         tc_fence_after();
         const bool fast = flags[slot * 2] != 0;
+        constexpr int NK = KH ? kN / 2 : kN, NPG = NK / kPage;
+        const int pg0 = KH ? NPG * qt : 0;
         uint32_t v[NK];
 #pragma unroll
-        for (int c = 0; c < NK / 32; ++c) tmem_ld32(tS + uint32_t(32 * c), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+        for (int c = 0; c < NK / 32; ++c)
+          tmem_ld32(tS + uint32_t(pg0 * kPage + 32 * c), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
         tmem_wait_ld();
         // ALiBi: the scores become logits here, the per-key part slope t of the bias added; its per-page
         // part slope (pstart - m) goes onto the page's maximum and exponent offset
@@ -394,7 +395,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           mq[q] = fmaxf(m, x[15]);
           if constexpr (POS == kAlibi) mq[q] += bpg[q];
         }
-        float mx = max3f(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
+        float mx;
+        if constexpr (KH)
+          mx = max3f(max3f(mq[0], mq[1], mq[2]), mq[3], mq[3]);
+        else
+          mx = max3f(max3f(mq[0], mq[1], mq[2]), max3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
         if constexpr (POS != kAlibi) mx *= rf;  // rf > 0
         const bool need = mx > m_run + kTau;
         const float m_new = need ? mx : m_run;
@@ -421,15 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         const float2 s01 = __fadd2_rn(sum4[0], sum4[1]), s23 = __fadd2_rn(sum4[2], sum4[3]);
         const float2 s03 = __fadd2_rn(s01, s23);
         const float sum = s03.x + s03.y;
-        const float alpha = (i > 0 && need && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
-        l_run = (i == 0) ? sum : l_run * alpha + sum;
-        if (__any_sync(0xffffffffu, i > 0 && alpha != 1.f)) {
-          // These scores were issued before the last step's PV: the rescale waits for it.  Most steps need none and
-          // leave that phase unwaited; the parity cannot be mistaken, since these scores' commit covers the PV of
-          // the step before the last, so at most one phase is open.
-          const bool got_pv = wait_bar(BAR(B_PV_DONE + (KH ? 0 : qt)), uint32_t((i - 1) & 1), abort_flag, a.status);
+        const float alpha = (j > 0 && need && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
+        l_run = (j == 0) ? sum : l_run * alpha + sum;
+        if (nq == 1 && j > 0) {  // S of tile j was issued before PV of tile j - 1: the rescale waits for it
+          const bool got_pv = wait_bar(BAR(B_PV_DONE), uint32_t((j - 1) & 1), abort_flag, a.status);
           if (!__all_sync(0xffffffffu, got_pv)) { ok = false; break; }
           tc_fence_after();
+        }
+        if (__any_sync(0xffffffffu, j > 0 && alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -441,7 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           }
         }
         m_run = m_new;
-        tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(v));  // P over the first half of these scores
+#pragma unroll
+        for (int c = 0; c < NK / 64; ++c)
+          tmem_st32(tS + uint32_t(pg0 * kPage + 32 * c), *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(BAR(B_P_FULL + buf));
@@ -764,24 +770,34 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       if (elect_one()) {
         const uint64_t dQ = sdesc(sQ0, 16, 1024), dK = sdesc(sK0, 16, 1024), dV = sdesc(sV0, L::BLK, 1024);
         auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };  // no carry: shared addresses end below 2^18
+        constexpr uint32_t IQK = idesc_mma(kM, kN, 0, 1);
         constexpr uint32_t IPV = idesc_mma(kM, D, 1, 1);
         bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
         auto wait = [&](int bar, int phase) -> bool {
           return wait_bar(BAR(bar), uint32_t(phase & 1), abort_flag, a.status);
         };
-        if constexpr (KH) {
-          // QK(0) QK(1) | PV(0) QK(2) | PV(1) ...
-          constexpr uint32_t IQK = idesc_mma(kM, kN, 0, 1);
+        auto qk = [&](int qt, int j, int buf) {  // S_buf = Q_qt K_j^T
+          const uint64_t d = at(dK, uint32_t((j & 1) * L::TILE)), e = at(dQ, uint32_t(qt * L::QTILE));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = uint32_t((kk >> 2) * L::BLK + (kk & 3) * 32);
+            mma_bf16(tm + uint32_t(buf * kN), at(e, off), at(d, off), IQK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(BAR(B_S_FULL + buf));
+        };
+        auto pv = [&](int qt, int jj) {  // O_qt += P_qt V_jj
+          const uint64_t d = at(dV, uint32_t((jj & 1) * L::TILE));
+#pragma unroll
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_ts(tm + uint32_t(2 * kN + qt * 128), tm + uint32_t(qt * kN + kk * 8),
+                   at(d, uint32_t(kk * 16 * 128)), IPV, (jj > 0 || kk > 0) ? 1u : 0u);
+        };
+        if (nq == 1) {
+          // one live Q tile: QK(0) QK(1) | PV(0) QK(2) | PV(1) ...
           auto qk1 = [&](int j) -> bool {
             if (!wait(B_K_READY + (j & 1), j >> 1)) return false;
             tc_fence_after();
-            const uint64_t d = at(dK, uint32_t((j & 1) * L::TILE));
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = uint32_t((kk >> 2) * L::BLK + (kk & 3) * 32);
-              mma_bf16(tm + uint32_t((j & 1) * kN), at(dQ, off), at(d, off), IQK, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(BAR(B_S_FULL + (j & 1)));
+            qk(0, j, j & 1);
             mma_commit(BAR(B_K_FREE + (j & 1)));
             return true;
           };
@@ -794,61 +810,53 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
             const uint64_t d = at(dV, uint32_t((j & 1) * L::TILE));
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk) {
-              const int hk = kk / 4;
-              mma_ts(tm + uint32_t((2 + hk) * kN), tm + uint32_t((j & 1) * kN + 64 * hk + (kk % 4) * 8),
-                     at(d, uint32_t(kk * 16 * 128)), IPV, (j > 0 || kk > 4 * hk) ? 1u : 0u);
+              const int hk = KH ? kk / 4 : 0;
+              const uint32_t pcol = uint32_t((j & 1) * kN + (KH ? 64 * hk + (kk % 4) * 8 : kk * 8));
+              mma_ts(tm + uint32_t((2 + hk) * kN), tm + pcol, at(d, uint32_t(kk * 16 * 128)),
+                     IPV, (j > 0 || kk > (KH ? 4 * hk : 0)) ? 1u : 0u);
             }
             mma_commit(BAR(B_PV_DONE));
             mma_commit(BAR(B_V_FREE + (j & 1)));
             if (j + 2 < ntiles) ok = qk1(j + 2);
           }
         } else {
-          constexpr uint32_t IQK = idesc_mma(kM, kN / 2, 0, 1);
-          auto qk = [&](int q, int j, int kh) {  // scores of half kh of tile j
-            const uint64_t d = at(dK, uint32_t((j & 1) * L::TILE + kh * 64 * 128)), e = at(dQ, uint32_t(q * L::QTILE));
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = uint32_t((kk >> 2) * L::BLK + (kk & 3) * 32);
-              mma_bf16(tm + uint32_t(q * kN + kh * 64), at(e, off), at(d, off), IQK, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(BAR(B_S_FULL + 2 * q + kh));
-          };
-          auto pv = [&](int q, int j, int kh, bool first) {
-            const uint64_t d = at(dV, uint32_t((j & 1) * L::TILE + kh * 64 * 128));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(tm + uint32_t(2 * kN + q * 128), tm + uint32_t(q * kN + kh * 64 + kk * 8),
-                     at(d, uint32_t(kk * 16 * 128)), IPV, (!first || kk > 0) ? 1u : 0u);
-            mma_commit(BAR(B_PV_DONE + q));
-          };
-          auto half = [](int i) { return (i & 1) ^ int(POS == kAlibi); };
-          const int steps = 2 * ntiles;
           if (ok) ok = wait(B_K_READY, 0);
           if (ok) {
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < 2 * nq; ++x) qk(nq == 2 ? x & 1 : 0, 0, half(nq == 2 ? x >> 1 : x));
+            qk(0, 0, 0);
+            qk(1, 0, 1);
             mma_commit(BAR(B_K_FREE));
           }
-          for (int i = 0; i < steps && ok; ++i) {
-            const int j = i >> 1, kh = half(i);
-            const bool more = j + 1 < ntiles;
-#pragma unroll 1
-            for (int q = 0; q < nq && ok; ++q) {
-              ok = wait(B_P_FULL + 2 * q + kh, j) && (q > 0 || (i & 1) || wait(B_V_READY + (j & 1), j >> 1));
-              if (!ok) break;
+          for (int j = 1; j < ntiles && ok; ++j) {
+            const int s = j & 1, sp = (j - 1) & 1;
+            ok = wait(B_P_FULL, j - 1) && wait(B_V_READY + sp, (j - 1) >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(0, j - 1);
+            ok = wait(B_K_READY + s, j >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            qk(0, j, 0);
+            ok = wait(B_P_FULL + 1, j - 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(1, j - 1);
+            mma_commit(BAR(B_V_FREE + sp));
+            qk(1, j, 1);
+            mma_commit(BAR(B_K_FREE + s));
+          }
+          if (ok) {
+            const int jl = ntiles - 1;
+            ok = wait(B_P_FULL, jl) && wait(B_V_READY + (jl & 1), jl >> 1);
+            if (ok) {
               tc_fence_after();
-              pv(q, j, kh, i == 0);
-              if (more) {
-                if (q == 0 && !(i & 1)) ok = wait(B_K_READY + ((j + 1) & 1), (j + 1) >> 1);
-                if (!ok) break;
-                tc_fence_after();
-                qk(q, j + 1, kh);
-              }
+              pv(0, jl);
+              ok = wait(B_P_FULL + 1, jl);
             }
-            if (ok && (i & 1)) {  // the tile's last half: its values, and the next tile's keys, are done with
-              mma_commit(BAR(B_V_FREE + (j & 1)));
-              if (more) mma_commit(BAR(B_K_FREE + ((j + 1) & 1)));
+            if (ok) {
+              tc_fence_after();
+              pv(1, jl);
+              mma_commit(BAR(B_V_FREE + (jl & 1)));
             }
           }
         }
