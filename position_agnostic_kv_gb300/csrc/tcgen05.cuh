@@ -1,4 +1,5 @@
-// tcgen05, TMEM and shared-memory wrappers of the tensor-core attention kernels (PTX ISA).
+// tcgen05, TMEM and shared-memory wrappers of the 4-bit tensor-core prefill (PTX ISA).  prefill_tc.cu keeps
+// its own: the traffic recorded for it is valid while that one file's code hashes to the recorded value.
 #pragma once
 
 #include "common.cuh"
