@@ -557,27 +557,53 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   }
 }
 
-// Merge the splits' partial (O, max, sum) of one (row, head) by their log-sum-exp.
+// Merge the splits' partial (O, max, sum) of a (row, head) by their log-sum-exp: a warp each, its lanes over
+// the splits' weights (at most 64) and then over the dimensions.
+constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(D) q4_merge_kernel(const float* __restrict__ po, const float* __restrict__ pml, int S,
-                                                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    q4_merge_kernel(const float* __restrict__ po, const float* __restrict__ pml, int S, long long n,
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   pdl_wait();
   pdl_trigger();
-  const size_t rh = blockIdx.x;
-  const int d = threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const long long rh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (rh >= n) return;
   const float2* ml = reinterpret_cast<const float2*>(pml) + rh * S;
-  float M = -INFINITY;
-  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
-  float O = 0.f, l = 0.f;
-  if (M != -INFINITY)
-    for (int s = 0; s < S; ++s) {
-      const float2 x = ml[s];
-      const float f = exp2f(x.x - M);
-      O += f * po[(rh * S + s) * D + d];
-      l += f * x.y;
-    }
-  out[rh * D + d] = __float2bfloat16_rn(l != 0.f ? O / l : 0.f);
-  if (lse && d == 0) lse[rh] = (M + log2f(l)) * 0.6931471805599453f;
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 x0 = lane < S ? ml[lane] : none, x1 = lane + 32 < S ? ml[lane + 32] : none;
+  constexpr int V = D / 32;  // a lane's dimensions: V lane ..
+  using Vec = std::conditional_t<V == 4, float4, float2>;
+  const float* p = po + rh * S * D + V * lane;
+  Vec ahead[4];  // the first partials, fetched beside the weights
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (s < S) ahead[s] = *reinterpret_cast<const Vec*>(p + s * D);
+  float M = fmaxf(x0.x, x1.x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.f : M;  // no key at all: every weight is 2^-inf
+  const float f0 = exp2f(x0.x - base), f1 = exp2f(x1.x - base);
+  float l = f0 * x0.y + f1 * x1.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float O[V] = {};
+  auto add = [&](int s, const Vec& x) {
+    const float f = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31);
+    const float* e = reinterpret_cast<const float*>(&x);
+#pragma unroll
+    for (int d = 0; d < V; ++d) O[d] += f * e[d];
+  };
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (s < S) add(s, ahead[s]);
+#pragma unroll 4
+  for (int s = 4; s < S; ++s) add(s, *reinterpret_cast<const Vec*>(p + s * D));
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + rh * D + V * lane);
+#pragma unroll
+  for (int d = 0; d < V; d += 2) dst[d / 2] = f2_to_bf2(O[d] * inv, O[d + 1] * inv);
+  if (lse && lane == 0) lse[rh] = (M + log2f(l)) * 0.6931471805599453f;
 }
 
 int q4_heads(int Hq, int Hkv) { return min(Hq / Hkv, 8); }
@@ -651,11 +677,10 @@ static int take_ws(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes) 
 }
 
 cudaError_t q4_merge(const Q4Args& a, int D, cudaStream_t st) {
-  const unsigned rh = unsigned((long long)a.rows * a.Hq);
-  return D == 128 ? launch_pdl(q4_merge_kernel<128>, dim3(rh), dim3(128), 0, st, (const float*)a.part_o,
-                               (const float*)a.part_ml, a.S, a.out, a.lse)
-                  : launch_pdl(q4_merge_kernel<64>, dim3(rh), dim3(64), 0, st, (const float*)a.part_o,
-                               (const float*)a.part_ml, a.S, a.out, a.lse);
+  const long long rh = (long long)a.rows * a.Hq;
+  const dim3 grid(unsigned((rh + kMergeWarps - 1) / kMergeWarps)), block(kMergeWarps * 32);
+  auto kern = D == 128 ? q4_merge_kernel<128> : q4_merge_kernel<64>;
+  return launch_pdl(kern, grid, block, 0, st, (const float*)a.part_o, (const float*)a.part_ml, a.S, rh, a.out, a.lse);
 }
 
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {

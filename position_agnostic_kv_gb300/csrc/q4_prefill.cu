@@ -62,18 +62,18 @@ constexpr float kTau = 8.0f, kPOff = 7.0f;
 enum : int {
   B_PK_FULL = 0,   // [2] packed keys landed (bytes)
   B_PK_FREE = 2,   // [2] packed keys read (128 arrivals)
-  B_PV_FULL = 4,   // packed values landed
-  B_PV_FREE = 5,   // packed values read (64)
-  B_K_READY = 6,   // [2] K operand written (128)
-  B_K_FREE = 8,    // [2] every QK^T of the stage done (commit)
-  B_V_READY = 10,  // [2] V operand written (64)
-  B_V_FREE = 12,   // [2] every PV of the stage done (commit)
-  B_S_FULL = 14,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
-  B_P_FULL = 16,   // [2] P in TMEM, O rescaled (128, KH 256)
-  B_Q_READY = 18,  // Q operands written (256)
-  B_FINAL = 19,    // all MMAs done (commit)
-  B_PV_DONE = 20,  // one live Q tile: a tile's PV done (commit)
-  NBAR = 21
+  B_PV_FULL = 4,   // [2] packed values landed
+  B_PV_FREE = 6,   // [2] packed values read (64)
+  B_K_READY = 8,   // [2] K operand written (128)
+  B_K_FREE = 10,   // [2] every QK^T of the stage done (commit)
+  B_V_READY = 12,  // [2] V operand written (64)
+  B_V_FREE = 14,   // [2] every PV of the stage done (commit)
+  B_S_FULL = 16,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
+  B_P_FULL = 18,   // [2] P in TMEM, O rescaled (32 per warp that holds rows)
+  B_Q_READY = 20,  // Q operands written (256)
+  B_FINAL = 21,    // all MMAs done (commit)
+  B_PV_DONE = 22,  // one live Q tile: a tile's PV done (commit)
+  NBAR = 23
 };
 
 template <int D>
@@ -94,6 +94,10 @@ struct Layout {
   static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  // in the second Q tile, unused where every CTA has one (KH): {max, sum} [2][128], packed values' stage 1
+  static constexpr int XML_OFF = QTILE;
+  static constexpr int PV1_OFF = QTILE + 4096;
+  static_assert(PV1_OFF + kPagesPerTile * PVS <= K_OFF, "stage 1 of the packed values");
 };
 static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
 
@@ -166,8 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   const int mbase = dec ? a.seq_len[b] - 1 : qs;
   const int tok0 = mp * kQT * tpt;
   if (tok0 >= Lq) return;  // uniform for the CTA, before any barrier or TMEM use
-  const int nq = (tok0 + tpt < Lq) ? 2 : 1;
-  const int ntok = min(kQT * tpt, Lq - tok0);
+  const int nq = (!KH && tok0 + tpt < Lq) ? 2 : 1;
+  const int ntok = min((KH ? 1 : kQT) * tpt, Lq - tok0);
+  // warps of each Q tile that hold rows (a short question leaves some without): the others only write Q
+  const int live0 = (min(ntok, tpt) * G + 31) / 32, live1 = (max(ntok - tpt, 0) * G + 31) / 32;
   const int m_min = mbase + tok0, m_max = mbase + tok0 + ntok - 1;
   const int rel = m_max - qs;
   int nb = max(0, a.doc_blocks[b]) + (rel >= 0 ? rel / kPage + 1 : 0);
@@ -195,13 +201,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   }
 
   const uint32_t sQ0 = sb, sK0 = sb + L::K_OFF, sV0 = sb + L::V_OFF;
-  const uint32_t sPK = sb + L::PK_OFF, sPV = sb + L::PV_OFF;
+  const uint32_t sPK = sb + L::PK_OFF;
   int* pstart = reinterpret_cast<int*>(sm + L::PSTART_OFF);
   int2* pinfo = reinterpret_cast<int2*>(sm + L::PINFO_OFF);
   int* flags = reinterpret_cast<int*>(sm + L::FLAG_OFF);
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + L::TURNS_OFF);
   const uint32_t bar0 = sb + L::BAR_OFF;
   auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  constexpr int kPV = KH ? 2 : 1;  // stages of packed values
+  auto PVS = [&](int j) { return KH && (j & 1) ? sb + uint32_t(L::PV1_OFF) : sb + uint32_t(L::PV_OFF); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
 
@@ -214,10 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       mbar_init(BAR(B_V_READY + s), 64);
       mbar_init(BAR(B_V_FREE + s), 1);
       mbar_init(BAR(B_S_FULL + s), 1);
-      mbar_init(BAR(B_P_FULL + s), KH ? 256 : 128);
+      mbar_init(BAR(B_P_FULL + s), 32 * (KH ? 2 * live0 : s == 1 && nq == 2 ? live1 : live0));
+      mbar_init(BAR(B_PV_FULL + s), 1);
+      mbar_init(BAR(B_PV_FREE + s), 64);
     }
-    mbar_init(BAR(B_PV_FULL), 1);
-    mbar_init(BAR(B_PV_FREE), 64);
     mbar_init(BAR(B_Q_READY), 2 * 128);
     mbar_init(BAR(B_FINAL), 1);
     mbar_init(BAR(B_PV_DONE), 1);
@@ -245,19 +253,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
     const int h = g * G + r % G;
     const bool valid = token < Lq && r < tpt * G;
     const int m_row = valid ? mbase + token : -1;
-    float* rfac = reinterpret_cast<float*>(sm + L::QTILE + 4096);  // KH: row factors, in the unused second Q tile
-    float rf = 0.f;  // score -> base-2 logit
-    if (KH && qt == 1) {
-      mbar_arrive(BAR(B_Q_READY));
-    } else {
-      const uint32_t sQ = sQ0 + uint32_t(qt * L::QTILE);
+    float rf;  // score -> base-2 logit
+    {
+      // KH: both warpgroups write the one Q tile, each the chunks (pairs) of one parity
+      const uint32_t sQ = sQ0 + uint32_t(KH ? 0 : qt * L::QTILE);
       auto qaddr = [&](int k) { return sQ + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
+      const int rd = kRotate ? a.pos.rotary_dim : 0, hr = rd / 2;
+      const int half = kRotate && !a.pos.interleaved ? hr / 8 : 0;  // chunk k is rotated with chunk k + half
+      auto mine = [&](int k) { return !KH || ((k >= half && k < 2 * half ? k - half : k) & 1) == qt; };
       const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)(q0 + token) * a.Hq + h) * D);
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = valid ? src[k] : make_uint4(0, 0, 0, 0);
-        st_shared_v4(qaddr(k), x);
+        if (mine(k)) st_shared_v4(qaddr(k), x);
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max(xs[e] & 0x7FFFu, (xs[e] >> 16) & 0x7FFFu));
@@ -265,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       const int ex = q4_exponent(__uint_as_float(top << 16));
       rf = a.qk_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
       const float sc = __uint_as_float(uint32_t(127 - ex) << 23);
-      if (KH) rfac[r] = rf;
       auto pack = [&](const float (&y)[8]) {
         return make_uint4(f2_to_h2(y[0] * sc, y[1] * sc), f2_to_h2(y[2] * sc, y[3] * sc),
                           f2_to_h2(y[4] * sc, y[5] * sc), f2_to_h2(y[6] * sc, y[7] * sc));
@@ -274,54 +282,53 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         y[0] = bf_lo(x.x); y[1] = bf_hi(x.x); y[2] = bf_lo(x.y); y[3] = bf_hi(x.y);
         y[4] = bf_lo(x.z); y[5] = bf_hi(x.z); y[6] = bf_lo(x.w); y[7] = bf_hi(x.w);
       };
-      int done = 0;
+      constexpr int step = KH ? 2 : 1;
+      const int first = KH ? qt : 0;
       if constexpr (kRotate) {
         const uint32_t m = uint32_t(max(m_row, 0));
-        const int rd = a.pos.rotary_dim, hr = rd / 2;
-        const bool tab = a.pos.table != nullptr && m < uint32_t(a.pos.max_pos);
-        auto csf = [&](int i, float& sn, float& co) {
+        const float* tab = a.pos.table != nullptr && m < uint32_t(a.pos.max_pos) ? a.pos.table + (size_t)m * rd : nullptr;
+        auto csf = [&](int i, float (&sn)[4], float (&co)[4]) {  // frequencies i .. i + 3
           if (tab) {
-            co = a.pos.table[(size_t)m * rd + i];
-            sn = a.pos.table[(size_t)m * rd + hr + i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) co[e] = tab[i + e], sn[e] = tab[hr + i + e];
           } else {
-            turn_sincos_fast(m, turns[i], sn, co);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) turn_sincos_fast(m, turns[i + e], sn[e], co[e]);
           }
         };
+        float sn[4], co[4];
         if (!a.pos.interleaved) {
 #pragma unroll 1
-          for (int c = 0; c < hr / 8; ++c) {
+          for (int c = first; c < half; c += step) {
             float x1[8], x2[8], y1[8], y2[8];
             unpack(ld_shared_v4(qaddr(c)), x1);
-            unpack(ld_shared_v4(qaddr(c + hr / 8)), x2);
+            unpack(ld_shared_v4(qaddr(c + half)), x2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float sn, co;
-              csf(c * 8 + e, sn, co);
-              y1[e] = x1[e] * co - x2[e] * sn;
-              y2[e] = x1[e] * sn + x2[e] * co;
+              if (e % 4 == 0) csf(c * 8 + e, sn, co);
+              y1[e] = x1[e] * co[e % 4] - x2[e] * sn[e % 4];
+              y2[e] = x1[e] * sn[e % 4] + x2[e] * co[e % 4];
             }
             st_shared_v4(qaddr(c), pack(y1));
-            st_shared_v4(qaddr(c + hr / 8), pack(y2));
+            st_shared_v4(qaddr(c + half), pack(y2));
           }
         } else {
 #pragma unroll 1
-          for (int k = 0; k < rd / 8; ++k) {
+          for (int k = first; k < rd / 8; k += step) {
             float x[8], y[8];
             unpack(ld_shared_v4(qaddr(k)), x);
+            csf(k * 4, sn, co);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              float sn, co;
-              csf(k * 4 + w, sn, co);
-              y[2 * w] = x[2 * w] * co - x[2 * w + 1] * sn;
-              y[2 * w + 1] = x[2 * w] * sn + x[2 * w + 1] * co;
+              y[2 * w] = x[2 * w] * co[w] - x[2 * w + 1] * sn[w];
+              y[2 * w + 1] = x[2 * w] * sn[w] + x[2 * w + 1] * co[w];
             }
             st_shared_v4(qaddr(k), pack(y));
           }
         }
-        done = rd / 8;
       }
 #pragma unroll 1
-      for (int k = done; k < D / 8; ++k) {
+      for (int k = rd / 8 + (KH ? (rd / 8 + qt) & 1 : 0); k < D / 8; k += step) {
         float x[8];
         unpack(ld_shared_v4(qaddr(k)), x);
         st_shared_v4(qaddr(k), pack(x));
@@ -329,13 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       fence_async_smem();
       mbar_arrive(BAR(B_Q_READY));
     }
-    if (KH || qt < nq) {
+    const int live = KH || qt == 0 ? live0 : live1;
+    float2* xml = reinterpret_cast<float2*>(sm + L::XML_OFF);
+    if ((warp & 3) < live) {
       bool ok = true;
-      if (KH && qt == 1) {
-        ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
-        rf = rfac[r];
-        ok = __all_sync(0xffffffffu, ok);
-      }
       const float2 rf2 = make_float2(rf, rf);
       float slope = 0.f;
       if constexpr (POS == kAlibi)
@@ -480,9 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       if constexpr (KH) {
         // the key halves' partial softmaxes, merged by their maxima and sums (exchanged in the unused
         // second Q tile); each warpgroup writes half of the columns
-        float2* xml = reinterpret_cast<float2*>(sm + L::QTILE);
         xml[qt * kM + r] = make_float2(l_run != 0.f ? m_run : -INFINITY, l_run);
-        named_sync(1, 2 * kM);
+        named_sync(1, 64 * live0);
         const float2 mine = xml[qt * kM + r], other = xml[(qt ^ 1) * kM + r];
         const float2 hA = qt == 0 ? mine : other, hB = qt == 0 ? other : mine;
         const float M = fmaxf(hA.x, hB.x);
@@ -732,15 +735,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         return true;
       };
       auto issue_v = [&](int j) -> bool {
-        if (j >= 1) {
-          const bool freed = wait_bar(BAR(B_PV_FREE), uint32_t((j - 1) & 1), abort_flag, a.status);
+        const uint32_t full = BAR(B_PV_FULL + j % kPV);
+        if (j >= kPV) {
+          const bool freed = wait_bar(BAR(B_PV_FREE + j % kPV), uint32_t((j / kPV - 1) & 1), abort_flag, a.status);
           if (!__all_sync(0xffffffffu, freed)) return false;
         }
         const uint8_t* blk = v_cur;
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, blk != nullptr));
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_PV_FULL), loads * uint32_t(Q::BYTES - Q::VC));
+        if (lane == 0) mbar_arrive_expect_tx(full, loads * uint32_t(Q::BYTES - Q::VC));
         __syncwarp();
-        if (blk) bulk_g2s(sPV + uint32_t(lane * L::PVS), blk + Q::VC, Q::BYTES - Q::VC, BAR(B_PV_FULL));
+        if (blk) bulk_g2s(PVS(j) + uint32_t(lane * L::PVS), blk + Q::VC, Q::BYTES - Q::VC, full);
         __syncwarp();
         issued_v = j + 1;
         return true;
@@ -758,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           while (!mbar_test(BAR(B_PK_FULL + (j & 1)), uint32_t((j >> 1) & 1)) && !clk.expired()) {
           }
         }
-        if (issued_v > 0) {
+        for (int j = max(0, issued_v - kPV); j < issued_v; ++j) {
           WaitClock clk;
-          while (!mbar_test(BAR(B_PV_FULL), uint32_t((issued_v - 1) & 1)) && !clk.expired()) {
+          while (!mbar_test(BAR(B_PV_FULL + j % kPV), uint32_t((j / kPV) & 1)) && !clk.expired()) {
           }
         }
       }
@@ -874,12 +878,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       bool ok = true;
       for (int j = 0; j < ntiles; ++j) {
         const int s = j & 1, slot = j % kSlots;
-        if (ok) ok = wait_bar(BAR(B_PV_FULL), uint32_t(j & 1), abort_flag, a.status);
+        if (ok) ok = wait_bar(BAR(B_PV_FULL + j % kPV), uint32_t((j / kPV) & 1), abort_flag, a.status);
         if (ok && j >= 2) ok = wait_bar(BAR(B_V_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
         if (ok) {
           // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
           const int rows = pinfo[slot * kPagesPerTile + ps].y;
-          const uint32_t src = sPV + uint32_t(ps * L::PVS);
+          const uint32_t src = PVS(j) + uint32_t(ps * L::PVS);
           const uint32_t sV = sV0 + uint32_t(s * L::TILE);
           const int rr = rows - 2 * t;  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
           const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
@@ -941,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           }
         }
         fence_async_smem();
-        mbar_arrive(BAR(B_PV_FREE));
+        mbar_arrive(BAR(B_PV_FREE + j % kPV));
         mbar_arrive(BAR(B_V_READY + s));
       }
       __syncwarp();

@@ -1,9 +1,11 @@
 """The 4-bit prefill's barrier protocol in the host-side model (no GPU).
 
 q4_prefill_kernel differs from prefill_tc_kernel in how operands reach the tensor cores: packed keys
-land in a 2-stage ring and packed values in a single stage; one role turns the keys, another the
-values into operand rings of 2 stages each.  Softmax and MMA roles are the model's own.  Random interleavings must show no deadlock, no wait ahead of or two phases
-behind a barrier, and no stage or metadata slot reused too early; planted mistakes must be caught.
+land in a 2-stage ring, packed values in a single stage (two where the softmax warpgroups share one Q
+tile by halves of its keys); one role turns the keys, another the values into operand rings of 2 stages
+each.  Softmax and MMA roles are the model's own.  Random interleavings must show no deadlock, no wait
+ahead of or two phases behind a barrier, and no stage or metadata slot reused too early; planted mistakes
+must be caught.
 """
 import random
 
@@ -17,10 +19,12 @@ class Q4Sim(pm.Sim):
         super().__init__(n, nq, seed=seed, slots=slots, kst=2, kh=kh)
         self.PK_FULL = [pm.Bar(f"PK_FULL{s}", 1) for s in range(2)]
         self.PK_FREE = [pm.Bar(f"PK_FREE{s}", 1) for s in range(2)]
-        self.PV_FULL, self.PV_FREE = pm.Bar("PV_FULL", 1), pm.Bar("PV_FREE", 1)
+        self.vst = pv = 2 if self.kh else 1
+        self.PV_FULL = [pm.Bar(f"PV_FULL{s}", 1) for s in range(pv)]
+        self.PV_FREE = [pm.Bar(f"PV_FREE{s}", 1) for s in range(pv)]
         self.V_READY = [pm.Bar(f"V_READY{s}", 1) for s in range(2)]
-        self.packed = {"K": [None, None], "V": [None]}   # landed tile of each packed stage
-        self.pending = {"K": [False, False], "V": [False]}  # landed and not read yet
+        self.packed = {"K": [None, None], "V": [None] * pv}   # landed tile of each packed stage
+        self.pending = {"K": [False, False], "V": [False] * pv}  # landed and not read yet
 
     # packed copies
     def issue_tma(self, kind, j, bar):
@@ -50,10 +54,11 @@ class Q4Sim(pm.Sim):
         for j in range(self.n):
             if j + 1 < self.n:
                 yield from issue_k(j + 1)
-            if j >= 1:
-                yield ("wait", self.PV_FREE, j - 1)
-            self.PV_FULL.arrive(expect_tx=1)
-            self.issue_tma("V", j, self.PV_FULL)
+            s, n = j % self.vst, j // self.vst
+            if n >= 1:
+                yield ("wait", self.PV_FREE[s], n - 1)
+            self.PV_FULL[s].arrive(expect_tx=1)
+            self.issue_tma("V", j, self.PV_FULL[s])
             yield ("step",)
 
     def wait_free(self, bars, j):
@@ -82,11 +87,11 @@ class Q4Sim(pm.Sim):
 
     def values(self):
         for j in range(self.n):
-            yield ("wait", self.PV_FULL, j)
+            yield ("wait", self.PV_FULL[j % self.vst], j // self.vst)
             yield from self.wait_free(self.V_FREE, j)
             self.dequantise("V", j, self.vstage_users, "pv", self.vstage)
             yield ("step",)
-            self.PV_FREE.arrive()
+            self.PV_FREE[j % self.vst].arrive()
             self.V_READY[j % 2].arrive()
 
     def actors(self):
@@ -141,7 +146,8 @@ def test_model_catches_packed_values_overwritten():
     class Early(Q4Sim):
         def producer(self):
             for x in super().producer():
-                if x[0] == "wait" and x[1] is self.PV_FREE:
+                if x[0] == "wait" and x[1] in self.PV_FREE:
                     continue
                 yield x
     assert _caught(Early) > 0
+    assert _caught(Early, kh=True) > 0
