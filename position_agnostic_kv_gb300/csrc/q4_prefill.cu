@@ -17,8 +17,8 @@
 //              bytes apart, so that its word loads meet no bank conflicts.
 //   warps 14-15 values: the same, exact in f16; even and odd groups store their rows in opposite order,
 //              against bank conflicts.
-//   warp 12    producer: block words one tile ahead, one bulk copy per page into a 2-stage ring of packed
-//              keys and a 1-stage ring of packed values.
+//   warp 12    producer: block words four tiles at a time, asynchronous 16-byte copies into a ring of packed
+//              keys (2 stages, KH 4) and one of packed values (1, KH 2).
 //   warp 13    TMEM owner and MMA issuer: QK0(j) QK1(j) | PV0(j) QK0(j+1) PV1(j) QK1(j+1) | ...
 // Both f16 rings have 2 stages, filled a tile ahead.  TMEM: S0 [0,128), S1 [128,256), O0 [256,384),
 // O1 [384,512); P_i in the first half of S_i.
@@ -47,7 +47,7 @@ using namespace tc;
 
 constexpr int kM = 128, kQT = 2, kN = 128;
 constexpr int kPagesPerTile = kN / kPage;
-constexpr int kSlots = 6;  // per-tile metadata: published up to 5 tiles ahead of the softmax's use
+constexpr int kSlots = 8;  // per-tile metadata: published up to 7 tiles ahead of the softmax's last use
 constexpr int kThreads = 512;
 constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13, kValWarp0 = 14;
 constexpr int kRegsLaunch = 128;
@@ -60,20 +60,20 @@ template <bool KH> struct Regs {
 constexpr float kTau = 8.0f, kPOff = 7.0f;
 
 enum : int {
-  B_PK_FULL = 0,   // [2] packed keys landed (bytes)
-  B_PK_FREE = 2,   // [2] packed keys read (128 arrivals)
-  B_PV_FULL = 4,   // [2] packed values landed
-  B_PV_FREE = 6,   // [2] packed values read (64)
-  B_K_READY = 8,   // [2] K operand written (128)
-  B_K_FREE = 10,   // [2] every QK^T of the stage done (commit)
-  B_V_READY = 12,  // [2] V operand written (64)
-  B_V_FREE = 14,   // [2] every PV of the stage done (commit)
-  B_S_FULL = 16,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
-  B_P_FULL = 18,   // [2] P in TMEM, O rescaled (32 per warp that holds rows)
-  B_Q_READY = 20,  // Q operands written (256)
-  B_FINAL = 21,    // all MMAs done (commit)
-  B_PV_DONE = 22,  // one live Q tile: a tile's PV done (commit)
-  NBAR = 23
+  B_PK_FULL = 0,   // [4] packed keys landed (the producer's 32 lanes, and its lane 0 for the metadata)
+  B_PK_FREE = 4,   // [4] packed keys read (128 arrivals)
+  B_PV_FULL = 8,   // [2] packed values landed
+  B_PV_FREE = 10,  // [2] packed values read (64)
+  B_K_READY = 12,  // [2] K operand written (128)
+  B_K_FREE = 14,   // [2] every QK^T of the stage done (commit)
+  B_V_READY = 16,  // [2] V operand written (64)
+  B_V_FREE = 18,   // [2] every PV of the stage done (commit)
+  B_S_FULL = 20,   // [2] per Q tile (one live tile: per S buffer): S written (commit)
+  B_P_FULL = 22,   // [2] P in TMEM, O rescaled (32 per warp that holds rows)
+  B_Q_READY = 24,  // Q operands written (256)
+  B_FINAL = 25,    // all MMAs done (commit)
+  B_PV_DONE = 26,  // one live Q tile: a tile's PV done (commit)
+  NBAR = 27
 };
 
 template <int D>
@@ -83,7 +83,12 @@ struct Layout {
   static constexpr int QTILE = kM * D * 2;
   static constexpr int PKS = D == 128 ? 1184 : 656;  // bytes between packed key pages (9 D + pad)
   static constexpr int PVS = 9 * D;
-  static constexpr int K_OFF = kQT * QTILE;
+  // in the second Q tile (KH): {max, sum} [2][128], stage 1 of the packed values, stages 2 and 3 of the keys
+  static constexpr int XML_OFF = QTILE;
+  static constexpr int PV1_OFF = XML_OFF + 2 * kM * 8;
+  static constexpr int PK2_OFF = PV1_OFF + kPagesPerTile * PVS;
+  static constexpr int Q_END = PK2_OFF + 2 * kPagesPerTile * PKS;
+  static constexpr int K_OFF = ((Q_END > kQT * QTILE ? Q_END : kQT * QTILE) + 1023) / 1024 * 1024;
   static constexpr int V_OFF = K_OFF + 2 * TILE;
   static constexpr int PK_OFF = V_OFF + 2 * TILE;
   static constexpr int PV_OFF = PK_OFF + 2 * kPagesPerTile * PKS;
@@ -94,10 +99,6 @@ struct Layout {
   static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
-  // in the second Q tile, unused where every CTA has one (KH): {max, sum} [2][128], packed values' stage 1
-  static constexpr int XML_OFF = QTILE;
-  static constexpr int PV1_OFF = QTILE + 4096;
-  static_assert(PV1_OFF + kPagesPerTile * PVS <= K_OFF, "stage 1 of the packed values");
 };
 static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
 
@@ -201,29 +202,36 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   }
 
   const uint32_t sQ0 = sb, sK0 = sb + L::K_OFF, sV0 = sb + L::V_OFF;
-  const uint32_t sPK = sb + L::PK_OFF;
   int* pstart = reinterpret_cast<int*>(sm + L::PSTART_OFF);
   int2* pinfo = reinterpret_cast<int2*>(sm + L::PINFO_OFF);
   int* flags = reinterpret_cast<int*>(sm + L::FLAG_OFF);
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + L::TURNS_OFF);
   const uint32_t bar0 = sb + L::BAR_OFF;
   auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
-  constexpr int kPV = KH ? 2 : 1;  // stages of packed values
+  // Stages of packed keys and values.  KH has room for more where the second Q tile would lie, and needs
+  // them: its tiles are half as long, and a stage's copy takes about as long as a tile.
+  constexpr int kPK = KH ? 4 : 2, kPV = KH ? 2 : 1;
+  auto PKS = [&](int j) {
+    const int s = j % kPK;
+    return sb + uint32_t(KH && s >= 2 ? L::PK2_OFF : L::PK_OFF) + uint32_t((s & 1) * kPagesPerTile * L::PKS);
+  };
   auto PVS = [&](int j) { return KH && (j & 1) ? sb + uint32_t(L::PV1_OFF) : sb + uint32_t(L::PV_OFF); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(B_PK_FULL + s), 1);
+    for (int s = 0; s < kPK; ++s) {
+      mbar_init(BAR(B_PK_FULL + s), 33);
       mbar_init(BAR(B_PK_FREE + s), 128);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(BAR(B_K_READY + s), 128);
       mbar_init(BAR(B_K_FREE + s), 1);
       mbar_init(BAR(B_V_READY + s), 64);
       mbar_init(BAR(B_V_FREE + s), 1);
       mbar_init(BAR(B_S_FULL + s), 1);
       mbar_init(BAR(B_P_FULL + s), 32 * (KH ? 2 * live0 : s == 1 && nq == 2 ? live1 : live0));
-      mbar_init(BAR(B_PV_FULL + s), 1);
+      mbar_init(BAR(B_PV_FULL + s), 33);
       mbar_init(BAR(B_PV_FREE + s), 64);
     }
     mbar_init(BAR(B_Q_READY), 2 * 128);
@@ -260,17 +268,35 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       auto qaddr = [&](int k) { return sQ + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
       const int rd = kRotate ? a.pos.rotary_dim : 0, hr = rd / 2;
       const int half = kRotate && !a.pos.interleaved ? hr / 8 : 0;  // chunk k is rotated with chunk k + half
-      auto mine = [&](int k) { return !KH || ((k >= half && k < 2 * half ? k - half : k) & 1) == qt; };
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)(q0 + token) * a.Hq + h) * D);
+      // whole rows by neighbouring lanes into place (a row per lane would touch 32 lines at once); KH: each
+      // warpgroup half of the rows
+      constexpr int CH = D / 8, RL = 32 / CH;  // chunks of a row, rows at a time
+      constexpr int NR = KH ? 16 : 32;
+      const int lg = __ffs(G) - 1;  // G divides 128
+      const int tbase = tok0 + (KH ? 0 : qt * tpt), lim = min(tpt, Lq - tbase) * G;
+      uint4 in[NR / RL];
+#pragma unroll
+      for (int i = 0; i < NR / RL; ++i) {
+        const int row = 32 * (warp & 3) + (KH ? 16 * qt : 0) + i * RL + lane / CH;
+        const size_t at = ((size_t)(q0 + tbase + (row >> lg)) * a.Hq + g * G + (row & (G - 1))) * D;
+        in[i] = row < lim ? *reinterpret_cast<const uint4*>(a.q + at + lane % CH * 8) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NR / RL; ++i) {
+        const int row = 32 * (warp & 3) + (KH ? 16 * qt : 0) + i * RL + lane / CH, k = lane % CH;
+        st_shared_v4(sQ + uint32_t((k >> 3) * L::BLK) + swz(row, k & 7), in[i]);
+      }
+      if (KH) named_sync(1, 2 * kM);
+      else __syncwarp();
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
-        const uint4 x = valid ? src[k] : make_uint4(0, 0, 0, 0);
-        if (mine(k)) st_shared_v4(qaddr(k), x);
+        const uint4 x = ld_shared_v4(qaddr(k));
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max(xs[e] & 0x7FFFu, (xs[e] >> 16) & 0x7FFFu));
       }
+      if (KH) named_sync(1, 2 * kM);  // both have read every row: it may be rotated in place
       const int ex = q4_exponent(__uint_as_float(top << 16));
       rf = a.qk_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
       const float sc = __uint_as_float(uint32_t(127 - ex) << 23);
@@ -551,11 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
     }
     auto keys = [&](int j) {
       const int s = j & 1, slot = j % kSlots;
-      if (ok) ok = wait_bar(BAR(B_PK_FULL + s), uint32_t((j >> 1) & 1), abort_flag, a.status);
+      if (ok) ok = wait_bar(BAR(B_PK_FULL + j % kPK), uint32_t((j / kPK) & 1), abort_flag, a.status);
       if (ok && j >= 2) ok = wait_bar(BAR(B_K_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
       const int2 pi = ok ? pinfo[slot * kPagesPerTile + ps] : make_int2(0, 0);
       if (pi.y > 0) {  // rows past the page's keys are converted too (their scores are masked)
-        const uint32_t src = sPK + uint32_t((s * kPagesPerTile + ps) * L::PKS);
+        const uint32_t src = PKS(j) + uint32_t(ps * L::PKS);
         const uint32_t sK = sK0 + uint32_t(s * L::TILE);
         if constexpr (POS != kRopeX) {
           constexpr int HG = 16 / NCP;  // row groups
@@ -677,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         }
       }
       fence_async_smem();
-      mbar_arrive(BAR(B_PK_FREE + s));
+      mbar_arrive(BAR(B_PK_FREE + j % kPK));
       mbar_arrive(BAR(B_K_READY + s));
     };
     for (int j = 0; j < ntiles; ++j) keys(j);
@@ -688,21 +714,42 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       const uint64_t* mrow = a.meta + (size_t)b * a.max_blocks;
       // ALiBi visits the tiles newest first: the first tile then fixes each row's running maximum
       auto tile_of = [&](int j) { return POS == kAlibi ? t0 + ntiles - 1 - j : t0 + j; };
+      // block words of four tiles at a time, one per lane, fetched four tiles before they are needed (a load
+      // takes about as long as a tile)
       auto fetch = [&](int j) -> uint64_t {
-        const int jb = tile_of(j) * kPagesPerTile + lane;
-        return (lane < kPagesPerTile && j < ntiles && jb < nb) ? ldg_u64(mrow + jb) : 0ull;
+        j += lane / kPagesPerTile;
+        const int jb = tile_of(j) * kPagesPerTile + lane % kPagesPerTile;
+        return (j < ntiles && jb < nb) ? ldg_u64(mrow + jb) : 0ull;
       };
-      uint64_t w_next = fetch(0);
-      int issued_k = 0, issued_v = 0;
-      const uint8_t *v_cur = nullptr, *v_next = nullptr;  // this lane's blocks of tiles j and j + 1 (null: none)
+      uint64_t words = 0, words_next = fetch(0);
+      const int page = lane >> 2;  // the lane's page of a tile
+      const uint8_t* ahead[kPK] = {};  // this lane's blocks of the tiles whose values are to come (null: none)
+      // Half a block (keys or values) by four lanes, 16 bytes a time: 9 D / 64 instructions per tile.  One bulk
+      // copy per page would be issued lane by lane, at 84 cycles each: 1340 of a tile's 2700.
+      auto copy = [&](uint32_t dst, const uint8_t* src, uint32_t full) {
+        if (src) {
+#pragma unroll
+          for (int i = 0; i < Q::VC / 64; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + uint32_t(64 * i + 16 * (lane & 3))),
+                         "l"(src + 64 * i + 16 * (lane & 3))
+                         : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);  // releases the tile's metadata too
+      };
       auto issue_k = [&](int j) -> bool {
-        const int s = j & 1, slot = j % kSlots;
-        const uint64_t w = w_next;
-        w_next = fetch(j + 1);
+        const int slot = j % kSlots;
+        const uint32_t full = BAR(B_PK_FULL + j % kPK);
+        if (j % 4 == 0) {
+          words = words_next;
+          words_next = fetch(j + 4);
+        }
+        const uint64_t w = __shfl_sync(0xffffffffu, words, j % 4 * kPagesPerTile + page);
         int rows = 0, start = 0, delta = 0;
-        const int jb = tile_of(j) * kPagesPerTile + lane;
+        const int jb = tile_of(j) * kPagesPerTile + page;
         const uint8_t* blk = nullptr;
-        if (lane < kPagesPerTile && jb < nb) {
+        if (jb < nb) {
           delta = int(word_delta(w));
           start = delta + kPage * int(word_pg(w));
           rows = q4_rows(w, m_max);
@@ -712,26 +759,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           }
           if (rows > 0) blk = a.cache + ((size_t)word_page(w) * a.Hkv + g) * Q::BYTES;
         }
-        if (j >= 2) {
-          const bool freed = wait_bar(BAR(B_PK_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
+        if (j >= kPK) {
+          const bool freed = wait_bar(BAR(B_PK_FREE + j % kPK), uint32_t((j / kPK - 1) & 1), abort_flag, a.status);
           if (!__all_sync(0xffffffffu, freed)) return false;
         }
-        if (lane < kPagesPerTile) {
-          pinfo[slot * kPagesPerTile + lane] = make_int2(delta, rows);
-          pstart[slot * kPagesPerTile + lane] = start;
+        if ((lane & 3) == 0) {
+          pinfo[slot * kPagesPerTile + page] = make_int2(delta, rows);
+          pstart[slot * kPagesPerTile + page] = start;
         }
-        const int all16 = __all_sync(0xffffffffu, lane >= kPagesPerTile || rows == kPage);
         // every key visible to every row: full pages that end at or before the first row's position
-        const int seen = __all_sync(0xffffffffu, lane >= kPagesPerTile || start + kPage - 1 <= m_min);
-        if (lane == 0) flags[slot * 2] = all16 && seen;
-        __syncwarp();
-        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, blk != nullptr));
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_PK_FULL + s), loads * uint32_t(Q::VC));
-        __syncwarp();
-        if (blk) bulk_g2s(sPK + uint32_t((s * kPagesPerTile + lane) * L::PKS), blk, Q::VC, BAR(B_PK_FULL + s));
-        v_next = blk;
-        __syncwarp();
-        issued_k = j + 1;
+        const int seen = __all_sync(0xffffffffu, rows == kPage && start + kPage - 1 <= m_min);
+        if (lane == 0) flags[slot * 2] = seen;
+        copy(PKS(j) + uint32_t(page * L::PKS), blk, full);
+        ahead[kPK - 1] = blk;
         return true;
       };
       auto issue_v = [&](int j) -> bool {
@@ -740,34 +780,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           const bool freed = wait_bar(BAR(B_PV_FREE + j % kPV), uint32_t((j / kPV - 1) & 1), abort_flag, a.status);
           if (!__all_sync(0xffffffffu, freed)) return false;
         }
-        const uint8_t* blk = v_cur;
-        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, blk != nullptr));
-        if (lane == 0) mbar_arrive_expect_tx(full, loads * uint32_t(Q::BYTES - Q::VC));
-        __syncwarp();
-        if (blk) bulk_g2s(PVS(j) + uint32_t(lane * L::PVS), blk + Q::VC, Q::BYTES - Q::VC, full);
-        __syncwarp();
-        issued_v = j + 1;
+        const uint8_t* blk = ahead[0];
+        copy(PVS(j) + uint32_t(page * L::PVS), blk ? blk + Q::VC : nullptr, full);
         return true;
       };
-      bool ok = issue_k(0);
-      for (int j = 0; j < ntiles && ok; ++j) {
-        v_cur = v_next;
-        if (j + 1 < ntiles) ok = issue_k(j + 1);
-        if (ok) ok = issue_v(j);
+      bool ok = true;
+      for (int i = 0; i < kPK - 1 + ntiles && ok; ++i) {  // keys of tile i, values of tile i - (kPK - 1)
+        const int j = i - (kPK - 1);
+#pragma unroll
+        for (int e = 0; e < kPK - 1; ++e) ahead[e] = ahead[e + 1];
+        if (KH && j >= 0) ok = issue_v(j);
+        if (ok && i < ntiles) ok = issue_k(i);
+        if (!KH && ok && j >= 0) ok = issue_v(j);
       }
-      // never leave copies in flight: wait (bounded) for the last loads
-      if (lane == 0) {
-        for (int j = max(0, issued_k - 2); j < issued_k; ++j) {
-          WaitClock clk;
-          while (!mbar_test(BAR(B_PK_FULL + (j & 1)), uint32_t((j >> 1) & 1)) && !clk.expired()) {
-          }
-        }
-        for (int j = max(0, issued_v - kPV); j < issued_v; ++j) {
-          WaitClock clk;
-          while (!mbar_test(BAR(B_PV_FULL + j % kPV), uint32_t((j / kPV) & 1)) && !clk.expired()) {
-          }
-        }
-      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // never leave copies in flight
     } else if (warp == kMmaWarp) {
       // ============================ MMA issue (one thread)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);

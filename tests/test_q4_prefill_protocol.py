@@ -1,8 +1,8 @@
 """The 4-bit prefill's barrier protocol in the host-side model (no GPU).
 
 q4_prefill_kernel differs from prefill_tc_kernel in how operands reach the tensor cores: packed keys
-land in a 2-stage ring, packed values in a single stage (two where the softmax warpgroups share one Q
-tile by halves of its keys); one role turns the keys, another the values into operand rings of 2 stages
+land in a 2-stage ring, packed values in a single stage (4 and 2 where the softmax warpgroups share one
+Q tile by halves of its keys); one role turns the keys, another the values into operand rings of 2 stages
 each.  Softmax and MMA roles are the model's own.  Random interleavings must show no deadlock, no wait
 ahead of or two phases behind a barrier, and no stage or metadata slot reused too early; planted mistakes
 must be caught.
@@ -15,16 +15,16 @@ from tests import prefill_protocol_model as pm
 
 
 class Q4Sim(pm.Sim):
-    def __init__(self, n, nq, seed=0, slots=6, kh=False):
+    def __init__(self, n, nq, seed=0, slots=8, kh=False):
         super().__init__(n, nq, seed=seed, slots=slots, kst=2, kh=kh)
-        self.PK_FULL = [pm.Bar(f"PK_FULL{s}", 1) for s in range(2)]
-        self.PK_FREE = [pm.Bar(f"PK_FREE{s}", 1) for s in range(2)]
-        self.vst = pv = 2 if self.kh else 1
+        self.pkst, self.vst = pk, pv = (4, 2) if self.kh else (2, 1)
+        self.PK_FULL = [pm.Bar(f"PK_FULL{s}", 1) for s in range(pk)]
+        self.PK_FREE = [pm.Bar(f"PK_FREE{s}", 1) for s in range(pk)]
         self.PV_FULL = [pm.Bar(f"PV_FULL{s}", 1) for s in range(pv)]
         self.PV_FREE = [pm.Bar(f"PV_FREE{s}", 1) for s in range(pv)]
         self.V_READY = [pm.Bar(f"V_READY{s}", 1) for s in range(2)]
-        self.packed = {"K": [None, None], "V": [None] * pv}   # landed tile of each packed stage
-        self.pending = {"K": [False, False], "V": [False] * pv}  # landed and not read yet
+        self.packed = {"K": [None] * pk, "V": [None] * pv}   # landed tile of each packed stage
+        self.pending = {"K": [False] * pk, "V": [False] * pv}  # landed and not read yet
 
     # packed copies
     def issue_tma(self, kind, j, bar):
@@ -42,24 +42,30 @@ class Q4Sim(pm.Sim):
 
     def producer(self):
         def issue_k(j):
-            s = j % 2
-            if j >= 2:
-                yield ("wait", self.PK_FREE[s], j // 2 - 1)
+            s, n = j % self.pkst, j // self.pkst
+            if n >= 1:
+                yield ("wait", self.PK_FREE[s], n - 1)
             self.publish(j)
             self.PK_FULL[s].arrive(expect_tx=1)
             self.issue_tma("K", j, self.PK_FULL[s])
             yield ("step",)
 
-        yield from issue_k(0)
-        for j in range(self.n):
-            if j + 1 < self.n:
-                yield from issue_k(j + 1)
+        def issue_v(j):
             s, n = j % self.vst, j // self.vst
             if n >= 1:
                 yield ("wait", self.PV_FREE[s], n - 1)
             self.PV_FULL[s].arrive(expect_tx=1)
             self.issue_tma("V", j, self.PV_FULL[s])
             yield ("step",)
+
+        lead = self.pkst - 1
+        for i in range(lead + self.n):
+            if self.kh and i >= lead:
+                yield from issue_v(i - lead)
+            if i < self.n:
+                yield from issue_k(i)
+            if not self.kh and i >= lead:
+                yield from issue_v(i - lead)
 
     def wait_free(self, bars, j):
         if j >= 2:
@@ -78,11 +84,11 @@ class Q4Sim(pm.Sim):
 
     def rotation(self):  # the keys' role
         for j in range(self.n):
-            yield ("wait", self.PK_FULL[j % 2], j // 2)
+            yield ("wait", self.PK_FULL[j % self.pkst], j // self.pkst)
             yield from self.wait_free(self.K_FREE, j)
             self.dequantise("K", j, self.kstage_users, "qk", self.kstage)
             yield ("step",)
-            self.PK_FREE[j % 2].arrive()
+            self.PK_FREE[j % self.pkst].arrive()
             self.K_READY[j % 2].arrive()
 
     def values(self):
