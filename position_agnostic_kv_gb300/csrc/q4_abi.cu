@@ -16,7 +16,8 @@ static int check_q4(const char* what, int B, int max_blocks, int Hq, int Hkv, in
   if (G > 8 && G % 8) return fail(LAZY_EINVAL, "%s: Hq/Hkv = %d: above 8 it must be a multiple of 8", what, G);
   if (G < 8 && (G & (G - 1))) return fail(LAZY_EINVAL, "%s: Hq/Hkv = %d must be a power of two below 8", what, G);
   if (num_pages > (1 << 24)) return fail(LAZY_ERANGE, "%s: num_pages above 2^24", what);
-  if (!(scale >= 0.f && scale <= 3.0e38f)) return fail(LAZY_EINVAL, "%s: scale must be positive (or 0 for the default)", what);
+  if (!(scale >= 0.f && scale <= 3.0e38f))
+    return fail(LAZY_EINVAL, "%s: scale must be positive (or 0 for the default)", what);
   if (!q4_factor(k_scale, kf) || !q4_factor(v_scale, vf))
     return fail(LAZY_EINVAL, "%s: k_scale and v_scale must be powers of two in [2^-32, 2^32] (or 0 for 1)", what);
   if (B == 0) return LAZY_OK;

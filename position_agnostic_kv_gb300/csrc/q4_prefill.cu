@@ -25,12 +25,13 @@
 // With one live Q tile S0 and S1 double-buffer its scores; in launches whose CTAs all have one (KH) the two
 // softmax warpgroups each take half of every tile's keys and merge in the epilogue.
 //
-// What bounds it: the softmax, one exponential and ~4 other instructions per score: 128 scores of a row
-// take ~2100 of a tile's ~3800 cycles, the products of both Q tiles 2048, and the two overlap in part (the
-// scores of one Q tile are computed while the other's are waited for).  The packed cache, 18 D / 16 bytes
-// per key and head, comes out of the L2.  8 x 64 queries of 64 heads (8 KV heads) over 10 300 keys: 157 us,
-// 1100 TFLOP/s; 32 x 32 queries of 32 heads of one KV head over 12 000 keys, ALiBi: 216 us, 935 TFLOP/s; 32
-// heads, 4 requests of 100 queries over 2000 keys: 37.5 us.
+// What bounds it: the softmax, one exponential and ~4 other instructions per score: 128 scores of a row take
+// ~2100 of a tile's ~3800 cycles, the products of both Q tiles 2048, and the two overlap in part (the scores
+// of one Q tile are computed while the other's are waited for).  KH waits for its keys' role.  The packed
+// cache, 18 D / 16 bytes per key and head, comes out of the L2.  8 x 64 queries of 64 heads (8 KV heads) over
+// 10 300 keys: 158 us, 1090 TFLOP/s; 32 x 32 queries of 32 heads of one KV head over 12 000 keys, ALiBi: 221
+// us, 911 TFLOP/s; 16 x 32 queries of 32 heads over 2000 keys (KH): 31 us, 540 TFLOP/s; 1600 tokens of one
+// document: 38 us.
 // Measured and left out: dequantisation of both operands by one warpgroup 232 us (first shape), scores in
 // halves of a tile with two buffers per Q tile 176 (second shape 200), values only in halves 171 (201), an
 // MMA thread per Q tile 229 (291).  Every wait is bounded.
@@ -52,9 +53,10 @@ constexpr int kThreads = 512;
 constexpr int kDeqWarp0 = 8, kProdWarp = 12, kMmaWarp = 13, kValWarp0 = 14;
 constexpr int kRegsLaunch = 128;
 // Registers per thread after the re-split: softmax, keys, and the warpgroup of producer, MMA and values; they
-// add up to the launch's.  (176, 72, 88) takes 163 us for the first shape above, (168, 72, 104) 160.
+// add up to the launch's.  (176, 72, 88) takes 163 us for the first shape above, (168, 72, 104) 160.  KH's
+// softmax holds half a row of scores; its keys' role has registers for two steps at once (below).
 template <bool KH> struct Regs {
-  static constexpr int softmax = 176, deq = 56, issue = 104;
+  static constexpr int softmax = KH ? 144 : 176, deq = KH ? 104 : 56, issue = KH ? 120 : 104;
   static_assert(2 * softmax + deq + issue == 4 * kRegsLaunch, "warpgroup register shares");
 };
 constexpr float kTau = 8.0f, kPOff = 7.0f;
@@ -312,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       const int first = KH ? qt : 0;
       if constexpr (kRotate) {
         const uint32_t m = uint32_t(max(m_row, 0));
-        const float* tab = a.pos.table != nullptr && m < uint32_t(a.pos.max_pos) ? a.pos.table + (size_t)m * rd : nullptr;
+        const bool in_table = a.pos.table != nullptr && m < uint32_t(a.pos.max_pos);
+        const float* tab = in_table ? a.pos.table + (size_t)m * rd : nullptr;
         auto csf = [&](int i, float (&sn)[4], float (&co)[4]) {  // frequencies i .. i + 3
           if (tab) {
 #pragma unroll
@@ -602,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           }
           // Two rows (r7, r7 + 8) a time, the next ones' words loaded ahead.  The loop stays rolled: five
           // roles run different code at once, and unrolled they miss the instruction cache (a third of
-          // all stalls).
+          // all stalls).  KH, which waits for its keys, takes two steps at once (31.3 us against 33.7 rolled
+          // and 31.9 with all four; 16 x 32 queries of 32 heads over 2000 keys).
           constexpr int NI = 8 / HG;
           const uint32_t wsrc = src + hg * (D / 2) + c * 4;
           const uint32_t ssrc = src + Q::KS + (D == 128 ? (hg * 4 + (c >> 2)) * 4 : (hg * 4 + (c >> 1)) * 2);
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           uint32_t nxt[6];
           load(0, nxt);
           // rows r7 + 8 lie 1024 bytes on, equally swizzled
-#pragma unroll 1
+#pragma unroll (KH ? 2 : 1)
           for (int i = 0; i < NI; ++i) {
             uint32_t cur[6];
 #pragma unroll
@@ -632,8 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
             const uint32_t a2 = (D == 128) ? a1 + uint32_t(L::BLK) : sK + swz(ps * kPage + hg + HG * i, c + 4);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t sc1 = __byte_perm(e4m3x2_to_h2(D == 128 && hh ? cur[4] >> 16 : cur[4] & 0xFFFFu), 0, hh ? sel_b : sel_a);
-              const uint32_t sc2 = __byte_perm(e4m3x2_to_h2(D == 128 && hh ? cur[5] >> 16 : cur[5] & 0xFFFFu), 0, hh ? sel_b : sel_a);
+              const uint32_t sel = hh ? sel_b : sel_a;
+              auto two = [&](uint32_t w) { return e4m3x2_to_h2(D == 128 && hh ? w >> 16 : w & 0xFFFFu); };
+              const uint32_t sc1 = __byte_perm(two(cur[4]), 0, sel), sc2 = __byte_perm(two(cur[5]), 0, sel);
               uint32_t x1[4], x2[4];
               e2m1x8_to_h2(cur[2 * hh], x1);
               e2m1x8_to_h2(cur[2 * hh + 1], x2);
@@ -660,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
             for (int w = 0; w < 4; ++w) x[w] = hmul2(x[w], sc);
           };
           auto put = [&](int t, int k, const uint32_t (&x)[4]) {
-            st_shared_v4(sK + uint32_t((k >> 3) * L::BLK) + swz(ps * kPage + t, k & 7), make_uint4(x[0], x[1], x[2], x[3]));
+            st_shared_v4(sK + uint32_t((k >> 3) * L::BLK) + swz(ps * kPage + t, k & 7),
+                         make_uint4(x[0], x[1], x[2], x[3]));
           };
           if (g_kind < 2 && pi.x != cur_delta) {
             cur_delta = pi.x;
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<KH>::issue));
     if (warp == kProdWarp) {
-      // ============================ block words and bulk copies: K0 K1 V0 K2 V1 ...
+      // ============================ block words and copies: K0 K1 V0 K2 V1 ... (KH: K0 K1 K2 V0 K3 V1 ...)
       const uint64_t* mrow = a.meta + (size_t)b * a.max_blocks;
       // ALiBi visits the tiles newest first: the first tile then fixes each row's running maximum
       auto tile_of = [&](int j) { return POS == kAlibi ? t0 + ntiles - 1 - j : t0 + j; };
@@ -799,7 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       if (elect_one()) {
         const uint64_t dQ = sdesc(sQ0, 16, 1024), dK = sdesc(sK0, 16, 1024), dV = sdesc(sV0, L::BLK, 1024);
-        auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };  // no carry: shared addresses end below 2^18
+        // no carry out of the address field: shared addresses end below 2^18
+        auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
         constexpr uint32_t IQK = idesc_mma(kM, kN, 0, 1);
         constexpr uint32_t IPV = idesc_mma(kM, D, 1, 1);
         bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
