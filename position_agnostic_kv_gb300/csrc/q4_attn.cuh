@@ -65,19 +65,6 @@ __device__ __forceinline__ int q4_exponent(float top) {
   return ex < -60 || ex > 128 ? 0 : min(ex, 126);
 }
 
-// mbar_wait that reads the clock at every 32nd poll only: a warp that waits for its copy leaves the issue
-// slots to the others.
-__device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity) {
-  if (mbar_test(bar, parity)) return true;
-  WaitClock clk;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_test(bar, parity)) return true;
-    if (clk.expired()) return false;
-  }
-}
-
 // Set a kernel's dynamic shared memory limit, once per device (`done`: one bit per device, per kernel).
 template <typename F>
 inline cudaError_t q4_smem_limit(F kern, int bytes, std::atomic<uint64_t>& done) {

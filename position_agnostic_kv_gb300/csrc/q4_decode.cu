@@ -22,11 +22,16 @@
 //  * P^T comes out of the S^T fragment by one 8x8 transpose per 8 keys.
 //
 // What bounds it: HBM and instruction issue together.  At the measured HBM rate an SM gets one page-head
-// (18 D bytes) per 99 cycles = 396 issue slots; a page costs about 250 warp instructions.
+// (18 D bytes) per 99 cycles = 396 issue slots; a page costs about 300 warp instructions (D = 128, 4 heads),
+// issued by 16 warps per SM at 0.6 per cycle and scheduler.  64 requests over 32 000 keys, 32 heads of 8 KV
+// heads: 434 us, 5440 GB/s, 80 % of the copy rate (the loads alone take 327 us); 16 requests over 2000 keys:
+// 21 us, most of it latency.  Measured and left out (first shape): 5 CTAs per SM at 96 registers 485 us
+// (spills), one page per step 474, three stages 469 (a CTA per SM less), one bulk copy per block 444 (84
+// cycles of issue each, lane by lane).
 //
 // Work: a CTA = (query row, KV head, head group, key split), 4 warps, each with its own run of pages
-// and a ring of stages of two page blocks, one bulk copy per block.  Block words are unpacked 32 at a time,
-// one per lane, which then issues its own copies.  The warps' partial (O, max, sum) are merged in shared
+// and a ring of stages of two page blocks, filled by its lanes' asynchronous 16-byte copies.  Block words are
+// unpacked 32 at a time, one per lane.  The warps' partial (O, max, sum) are merged in shared
 // memory; up to 8 splits form a thread-block cluster and are merged through distributed shared memory,
 // more of them (few long rows) through the workspace and a second kernel.
 #include <cfloat>
@@ -53,8 +58,8 @@ struct DecL {
   static constexpr int CS = QS + (H8 ? 8 : 4) * QROW * 4;      // float2 [warp][D/2]
   static constexpr int SC = CS + kWarps * (D / 2) * 8;         // float [8] score factor of each head
   static constexpr int SLOT = SC + 32;                         // int2 {Delta | rows << 24, first position} [warp][64]
-  static constexpr int BAR = SLOT + kWarps * 64 * 8;
-  static constexpr int SMEM = BAR + kWarps * kStages * 8;
+  static constexpr int SRC = SLOT + kWarps * 64 * 8;           // block addresses [warp][64] (0: nothing to read)
+  static constexpr int SMEM = SRC + kWarps * 64 * 8;
   // the stages are reused to merge: the warps' partials, then (clusters) this CTA's
   static constexpr int ML = kWarps * 8 * D * 4;
   static constexpr int CO = ML + kWarps * 8 * 8;
@@ -128,47 +133,53 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   float* scs = reinterpret_cast<float*>(smem + L::SC);
   float2* cs = reinterpret_cast<float2*>(smem + L::CS) + warp * (D / 2);
   int2* slots = reinterpret_cast<int2*>(smem + L::SLOT) + warp * 64;
-  const uint32_t bar0 = smem_u32(smem + L::BAR + warp * kStages * 8);
+  unsigned long long* srcs = reinterpret_cast<unsigned long long*>(smem + L::SRC) + warp * 64;
   const uint32_t stage0 = smem_u32(smem + warp * kStages * L::STAGE);
 
-  // Block words, 32 pages at a time, one per lane: the lane unpacks its word, publishes what the compute
-  // needs of it (slots: two batches) and later issues its page's copy.
+  // Block words, 32 pages at a time, one per lane: the lane unpacks its word and publishes its page's slot
+  // (what the compute needs of it) and address, in two batches.
   const uint64_t* mrow = a.meta + (size_t)row.b * a.max_blocks + wb;
   uint64_t mnxt = lane < n ? ldg_u64(mrow + lane) : 0;
-  int mbase = -32, my_rows = 0, my_loads = 0;
-  const uint8_t* my_src = nullptr;
+  int mbase = -32;
   auto next_batch = [&]() {
     const uint64_t w = mnxt;
     mbase += 32;
     mnxt = mbase + 32 + lane < n ? ldg_u64(mrow + mbase + 32 + lane) : 0;
-    my_rows = 0;
+    int rows = 0;
     if (mbase + lane < n) {
-      my_rows = q4_rows(w, m);
+      rows = q4_rows(w, m);
       if (word_page(w) >= uint32_t(a.num_pages)) {
         set_status(a.status, LAZY_STATUS_BAD_PAGE);
-        my_rows = 0;
+        rows = 0;
       }
     }
-    slots[(mbase + lane) & 63] =
-        make_int2(int(word_delta(w) | uint32_t(my_rows) << 24), int(word_delta(w) + kPage * word_pg(w)));
-    my_src = a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES;
-    my_loads = (my_rows > 0) + (__shfl_xor_sync(0xffffffffu, my_rows, 1) > 0);
-  };
-  if (lane == 0)
-    for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
-  fence_mbar_init();
-  __syncwarp();
-
-  auto issue = [&](int i) {  // stage i: pages 2i and 2i + 1
-    if (kPair * i >= mbase + 32) next_batch();
-    const int x = kPair * i - mbase;  // the lanes that hold them: x and x + 1
-    const uint32_t bar = bar0 + 8 * (i % kStages);
-    if (lane == x) mbar_arrive_expect_tx(bar, uint32_t(my_loads) * Q::BYTES);
+    const int x = (mbase + lane) & 63;
+    slots[x] = make_int2(int(word_delta(w) | uint32_t(rows) << 24), int(word_delta(w) + kPage * word_pg(w)));
+    srcs[x] = rows > 0 ? reinterpret_cast<unsigned long long>(a.cache + ((size_t)word_page(w) * a.Hkv + kvh) * Q::BYTES)
+                       : 0ull;
     __syncwarp();
-    if ((lane & ~1) == x && my_rows > 0)
-      bulk_g2s(stage0 + (i % kStages) * L::STAGE + (lane & 1) * Q::BYTES, my_src, Q::BYTES, bar);
   };
-  for (int i = 0; i < min(kStages, ns); ++i) issue(i);
+
+  auto issue = [&](int i) {  // stage i: pages 2i and 2i + 1; a group for every stage, empty ones past the end
+    if (i < ns) {
+      if (kPair * i >= mbase + 32) next_batch();
+      const ulonglong2 src = *reinterpret_cast<const ulonglong2*>(srcs + ((kPair * i) & 63));
+      const uint32_t dst = stage0 + uint32_t((i % kStages) * L::STAGE + lane * 16);
+#pragma unroll
+      for (int pp = 0; pp < kPair; ++pp) {
+        const unsigned long long x = pp ? src.y : src.x;
+        if (x == 0) continue;
+#pragma unroll
+        for (int c = 0; c < Q::BYTES; c += 512)
+          if (c + 512 <= Q::BYTES || lane * 16 < Q::BYTES - c)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + uint32_t(pp * Q::BYTES + c)),
+                         "l"(x + lane * 16 + c)
+                         : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < kStages; ++i) issue(i);
 
   // ---- queries: one warp per head, normalised by a power of two, in fp32
   for (int h = warp; h < (H8 ? 8 : 4); h += kWarps) {
@@ -290,12 +301,8 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
 
   for (int i = 0; i < ns; ++i) {
     const int st = i % kStages;
-    if (!mbar_wait_quiet(bar0 + 8 * st, uint32_t((i / kStages) & 1))) {
-      if (lane == 0) set_status(a.status, LAZY_STATUS_TIMEOUT);
-      for (int j = i + 1; j < min(ns, i + kStages); ++j)
-        mbar_wait_quiet(bar0 + 8 * (j % kStages), uint32_t((j / kStages) & 1));
-      break;
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
     const uint8_t* blk0 = smem + warp * kStages * L::STAGE + st * L::STAGE;
     const int4 w = *reinterpret_cast<const int4*>(slots + ((kPair * i) & 63));  // both pages' slots
     const int delta0 = w.x & 0xFFFFFF, delta1 = w.z & 0xFFFFFF, rows0 = w.x >> 24;
@@ -305,178 +312,179 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
     const bool split_pair = POS != kAlibi && rows0 > 0 && rows1 > 0 && delta0 != delta1;
 #pragma unroll 1
     for (int pass = 0; pass <= int(split_pair); ++pass) {
-    const int rows[kPair] = {split_pair && pass == 1 ? 0 : rows0, split_pair && pass == 0 ? 0 : rows1};
-    if constexpr (POS != kAlibi) {
-      const uint32_t delta = uint32_t(rows[0] > 0 ? delta0 : delta1);
-      if (delta != cur_delta && rows[0] + rows[1] > 0) {
-        cur_delta = delta;
-        rotate_q(delta);
+      const int rows[kPair] = {split_pair && pass == 1 ? 0 : rows0, split_pair && pass == 0 ? 0 : rows1};
+      if constexpr (POS != kAlibi) {
+        const uint32_t delta = uint32_t(rows[0] > 0 ? delta0 : delta1);
+        if (delta != cur_delta && rows[0] + rows[1] > 0) {
+          cur_delta = delta;
+          rotate_q(delta);
+        }
       }
-    }
-    // ---- S^T = K q^T
-    float acc[kPair][4];
-    uint32_t kw[kPair][2][NW_], ksc[kPair][2][NW_ / 2];
-#pragma unroll
-    for (int pp = 0; pp < kPair; ++pp) {
-      const uint8_t* blk = blk0 + pp * Q::BYTES;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[pp][e] = 0.f;
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(blk + lane * 16);
-        const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
-        kw[pp][0][0] = x.x; kw[pp][0][1] = x.y; kw[pp][0][2] = x.z; kw[pp][0][3] = x.w;
-        kw[pp][1][0] = y.x; kw[pp][1][1] = y.y; kw[pp][1][2] = y.z; kw[pp][1][3] = y.w;
-        const uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::KS + lane * 4);
-        const uint32_t sa = e4m3x2_to_h2(sw & 0xFFFFu), sb = e4m3x2_to_h2(sw >> 16);
-        ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
-        ksc[pp][0][1] = __byte_perm(sa, 0, 0x3232);
-        ksc[pp][1][0] = __byte_perm(sb, 0, 0x1010);
-        ksc[pp][1][1] = __byte_perm(sb, 0, 0x3232);
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(blk + lane * 8);
-        const uint2 y = *reinterpret_cast<const uint2*>(blk + 256 + lane * 8);
-        kw[pp][0][0] = x.x; kw[pp][0][1] = x.y;
-        kw[pp][1][0] = y.x; kw[pp][1][1] = y.y;
-        const uint32_t sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(blk + Q::KS + lane * 2));
-        ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
-        ksc[pp][1][0] = __byte_perm(sa, 0, 0x3232);
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < NW_; ++x)
+      // ---- S^T = K q^T
+      float acc[kPair][4];
+      uint32_t kw[kPair][2][NW_], ksc[kPair][2][NW_ / 2];
 #pragma unroll
       for (int pp = 0; pp < kPair; ++pp) {
-        uint32_t ra[4], rb[4];
-        e2m1x8_to_h2(kw[pp][0][x], ra);
-        e2m1x8_to_h2(kw[pp][1][x], rb);
+        const uint8_t* blk = blk0 + pp * Q::BYTES;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ra[e] = hmul2(ra[e], ksc[pp][0][x / 2]);
-          rb[e] = hmul2(rb[e], ksc[pp][1][x / 2]);
+        for (int e = 0; e < 4; ++e) acc[pp][e] = 0.f;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(blk + lane * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
+          kw[pp][0][0] = x.x; kw[pp][0][1] = x.y; kw[pp][0][2] = x.z; kw[pp][0][3] = x.w;
+          kw[pp][1][0] = y.x; kw[pp][1][1] = y.y; kw[pp][1][2] = y.z; kw[pp][1][3] = y.w;
+          const uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::KS + lane * 4);
+          const uint32_t sa = e4m3x2_to_h2(sw & 0xFFFFu), sb = e4m3x2_to_h2(sw >> 16);
+          ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
+          ksc[pp][0][1] = __byte_perm(sa, 0, 0x3232);
+          ksc[pp][1][0] = __byte_perm(sb, 0, 0x1010);
+          ksc[pp][1][1] = __byte_perm(sb, 0, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(blk + lane * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(blk + 256 + lane * 8);
+          kw[pp][0][0] = x.x; kw[pp][0][1] = x.y;
+          kw[pp][1][0] = y.x; kw[pp][1][1] = y.y;
+          const uint32_t sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(blk + Q::KS + lane * 2));
+          ksc[pp][0][0] = __byte_perm(sa, 0, 0x1010);
+          ksc[pp][1][0] = __byte_perm(sa, 0, 0x3232);
         }
+      }
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
-          if constexpr (H8)
-            mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0], qlo[2 * x + v][1]);
+      for (int x = 0; x < NW_; ++x)
+#pragma unroll
+        for (int pp = 0; pp < kPair; ++pp) {
+          uint32_t ra[4], rb[4];
+          e2m1x8_to_h2(kw[pp][0][x], ra);
+          e2m1x8_to_h2(kw[pp][1][x], rb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ra[e] = hmul2(ra[e], ksc[pp][0][x / 2]);
+            rb[e] = hmul2(rb[e], ksc[pp][1][x / 2]);
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qhi[2 * x + v][0], qhi[2 * x + v][1]);
+            if constexpr (H8)
+              mma16816(acc[pp], ra[2 * v], rb[2 * v], ra[2 * v + 1], rb[2 * v + 1], qlo[2 * x + v][0],
+                       qlo[2 * x + v][1]);
+          }
         }
-      }
-    // ---- scores: [set][row gr | gr + 8][column 2t | 2t + 1], still without the factor sc (ALiBi: logits)
-    float s[NS][4];
-    if constexpr (H8) {
+      // ---- scores: [set][row gr | gr + 8][column 2t | 2t + 1], still without the factor sc (ALiBi: logits)
+      float s[NS][4];
+      if constexpr (H8) {
 #pragma unroll
-      for (int pp = 0; pp < kPair; ++pp)
+        for (int pp = 0; pp < kPair; ++pp)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[pp][e] = acc[pp][e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)  // hi + lo: each lane gives away its part of the other page
-        s[0][e] = (mine1 ? acc[1][e] : acc[0][e]) + __shfl_xor_sync(0xffffffffu, mine1 ? acc[0][e] : acc[1][e], 2);
-    }
-    if constexpr (POS == kAlibi) {
-#pragma unroll
-      for (int x = 0; x < NS; ++x) {
-        const float dist = float(((H8 ? x == 1 : mine1) ? w.w : w.y) + gr - m);
-        s[x][0] = fmaf(s[x][0], sc0, sl0 * dist);
-        s[x][1] = fmaf(s[x][1], sc1, sl1 * dist);
-        s[x][2] = fmaf(s[x][2], sc0, sl0 * (dist + 8.f));
-        s[x][3] = fmaf(s[x][3], sc1, sl1 * (dist + 8.f));
-      }
-    }
-    if (min(rows[0], rows[1]) < kPage) {
-#pragma unroll
-      for (int x = 0; x < NS; ++x) {
-        const int rr = (H8 ? x == 1 : mine1) ? rows[1] : rows[0];
-        if (gr >= rr) s[x][0] = s[x][1] = -INFINITY;
-        if (gr + 8 >= rr) s[x][2] = s[x][3] = -INFINITY;
-      }
-    }
-    // ---- lazy running maximum of each column
-    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
-    if constexpr (H8) {
-      x0 = fmaxf(x0, fmaxf(s[NS - 1][0], s[NS - 1][2]));
-      x1 = fmaxf(x1, fmaxf(s[NS - 1][1], s[NS - 1][3]));
-    }
-    if constexpr (POS != kAlibi) {
-      x0 *= sc0;
-      x1 *= sc1;
-    }
-    if (__any_sync(0xffffffffu, first || x0 > m0 + kTau || x1 > m1 + kTau)) {
-      first = false;
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-      }
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float a0 = exp2f(m0 - n0), a1 = exp2f(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= a0;
-      l1 *= a1;
-#pragma unroll
-      for (int x = 0; x < NKS; ++x) {
-        o[x][0] *= a0;
-        o[x][1] *= a1;
-        o[x][2] *= a0;
-        o[x][3] *= a1;
-      }
-    }
-    const float f0 = kPOff - m0, f1 = kPOff - m1;
-    uint32_t pb[NS][2];  // P^T fragments: keys 0-7 and 8-15
-#pragma unroll
-    for (int x = 0; x < NS; ++x) {
-      const float k0 = POS == kAlibi ? 1.f : sc0, k1 = POS == kAlibi ? 1.f : sc1;
-      const float p0 = ex2_approx(fmaf(s[x][0], k0, f0)), p1 = ex2_approx(fmaf(s[x][1], k1, f1));
-      const float p2 = ex2_approx(fmaf(s[x][2], k0, f0)), p3 = ex2_approx(fmaf(s[x][3], k1, f1));
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      pb[x][0] = transpose8(pack_h2(p0, p1));
-      pb[x][1] = transpose8(pack_h2(p2, p3));
-    }
-#pragma unroll
-    for (int pp = 0; pp < kPair; ++pp) {
-      // columns of the other page take no part in this page's product
-      const bool use = H8 || (gr >= 4) == (pp == 1);
-      const uint32_t b0 = use ? pb[H8 ? pp : 0][0] : 0u, b1 = use ? pb[H8 ? pp : 0][1] : 0u;
-      // ---- O^T += V^T P^T
-      const uint8_t* blk = blk0 + pp * Q::BYTES;
-      const int vg = D == 128 ? lane : (gr >> 1) * 4 + t;
-      uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::VS + vg * 4);
-      if (rows[pp] < kPage) {  // rows without a key: scale 0, so that what they hold cannot matter
-        const int rr = rows[pp] - 2 * t;  // bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
-                              (rr > 9 ? 0xFF000000u : 0u);
-        sw &= keep;
-      }
-      const uint32_t vs0 = e4m3x2_to_h2(sw & 0xFFFFu), vs1 = e4m3x2_to_h2(sw >> 16);
-      uint32_t va[2][D / 64], vb[2][D / 64];  // [row half][word]: codes of the even and the odd row
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
-        const uint4 y = *reinterpret_cast<const uint4*>(blk + Q::VC + 512 + lane * 16);
-        va[0][0] = x.x; va[0][1] = x.y; vb[0][0] = x.z; vb[0][1] = x.w;
-        va[1][0] = y.x; va[1][1] = y.y; vb[1][0] = y.z; vb[1][1] = y.w;
+          for (int e = 0; e < 4; ++e) s[pp][e] = acc[pp][e];
       } else {
-        const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
-        va[0][0] = x.x; vb[0][0] = x.y; va[1][0] = x.z; vb[1][0] = x.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // hi + lo: each lane gives away its part of the other page
+          s[0][e] = (mine1 ? acc[1][e] : acc[0][e]) + __shfl_xor_sync(0xffffffffu, mine1 ? acc[0][e] : acc[1][e], 2);
+      }
+      if constexpr (POS == kAlibi) {
+#pragma unroll
+        for (int x = 0; x < NS; ++x) {
+          const float dist = float(((H8 ? x == 1 : mine1) ? w.w : w.y) + gr - m);
+          s[x][0] = fmaf(s[x][0], sc0, sl0 * dist);
+          s[x][1] = fmaf(s[x][1], sc1, sl1 * dist);
+          s[x][2] = fmaf(s[x][2], sc0, sl0 * (dist + 8.f));
+          s[x][3] = fmaf(s[x][3], sc1, sl1 * (dist + 8.f));
+        }
+      }
+      if (min(rows[0], rows[1]) < kPage) {
+#pragma unroll
+        for (int x = 0; x < NS; ++x) {
+          const int rr = (H8 ? x == 1 : mine1) ? rows[1] : rows[0];
+          if (gr >= rr) s[x][0] = s[x][1] = -INFINITY;
+          if (gr + 8 >= rr) s[x][2] = s[x][3] = -INFINITY;
+        }
+      }
+      // ---- lazy running maximum of each column
+      float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+      if constexpr (H8) {
+        x0 = fmaxf(x0, fmaxf(s[NS - 1][0], s[NS - 1][2]));
+        x1 = fmaxf(x1, fmaxf(s[NS - 1][1], s[NS - 1][3]));
+      }
+      if constexpr (POS != kAlibi) {
+        x0 *= sc0;
+        x1 *= sc1;
+      }
+      if (__any_sync(0xffffffffu, first || x0 > m0 + kTau || x1 > m1 + kTau)) {
+        first = false;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+        }
+        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+        const float a0 = exp2f(m0 - n0), a1 = exp2f(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int x = 0; x < NKS; ++x) {
+          o[x][0] *= a0;
+          o[x][1] *= a1;
+          o[x][2] *= a0;
+          o[x][3] *= a1;
+        }
+      }
+      const float f0 = kPOff - m0, f1 = kPOff - m1;
+      uint32_t pb[NS][2];  // P^T fragments: keys 0-7 and 8-15
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        const float k0 = POS == kAlibi ? 1.f : sc0, k1 = POS == kAlibi ? 1.f : sc1;
+        const float p0 = ex2_approx(fmaf(s[x][0], k0, f0)), p1 = ex2_approx(fmaf(s[x][1], k1, f1));
+        const float p2 = ex2_approx(fmaf(s[x][2], k0, f0)), p3 = ex2_approx(fmaf(s[x][3], k1, f1));
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        pb[x][0] = transpose8(pack_h2(p0, p1));
+        pb[x][1] = transpose8(pack_h2(p2, p3));
       }
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd dimensions of the word, both row halves
-        const uint32_t A0 = va[0][w], B0 = vb[0][w], A1 = va[1][w], B1 = vb[1][w];
-        // two rows' codes of one dimension side by side in a byte
-        e2m1x8_to_h2((A0 & 0x0F0F0F0Fu) | ((B0 << 4) & 0xF0F0F0F0u), e0);
-        e2m1x8_to_h2(((A0 >> 4) & 0x0F0F0F0Fu) | (B0 & 0xF0F0F0F0u), o0);
-        e2m1x8_to_h2((A1 & 0x0F0F0F0Fu) | ((B1 << 4) & 0xF0F0F0F0u), e1);
-        e2m1x8_to_h2(((A1 >> 4) & 0x0F0F0F0Fu) | (B1 & 0xF0F0F0F0u), o1);
+      for (int pp = 0; pp < kPair; ++pp) {
+        // columns of the other page take no part in this page's product
+        const bool use = H8 || (gr >= 4) == (pp == 1);
+        const uint32_t b0 = use ? pb[H8 ? pp : 0][0] : 0u, b1 = use ? pb[H8 ? pp : 0][1] : 0u;
+        // ---- O^T += V^T P^T
+        const uint8_t* blk = blk0 + pp * Q::BYTES;
+        const int vg = D == 128 ? lane : (gr >> 1) * 4 + t;
+        uint32_t sw = *reinterpret_cast<const uint32_t*>(blk + Q::VS + vg * 4);
+        if (rows[pp] < kPage) {  // rows without a key: scale 0, so that what they hold cannot matter
+          const int rr = rows[pp] - 2 * t;  // bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
+          const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
+                                (rr > 9 ? 0xFF000000u : 0u);
+          sw &= keep;
+        }
+        const uint32_t vs0 = e4m3x2_to_h2(sw & 0xFFFFu), vs1 = e4m3x2_to_h2(sw >> 16);
+        uint32_t va[2][D / 64], vb[2][D / 64];  // [row half][word]: codes of the even and the odd row
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(blk + Q::VC + 512 + lane * 16);
+          va[0][0] = x.x; va[0][1] = x.y; vb[0][0] = x.z; vb[0][1] = x.w;
+          va[1][0] = y.x; va[1][1] = y.y; vb[1][0] = y.z; vb[1][1] = y.w;
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(blk + Q::VC + lane * 16);
+          va[0][0] = x.x; vb[0][0] = x.y; va[1][0] = x.z; vb[1][0] = x.w;
+        }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          mma16816(o[4 * w + x], hmul2(e0[x], vs0), hmul2(o0[x], vs0), hmul2(e1[x], vs1), hmul2(o1[x], vs1), b0, b1);
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd dimensions of the word, both row halves
+          const uint32_t A0 = va[0][w], B0 = vb[0][w], A1 = va[1][w], B1 = vb[1][w];
+          // two rows' codes of one dimension side by side in a byte
+          e2m1x8_to_h2((A0 & 0x0F0F0F0Fu) | ((B0 << 4) & 0xF0F0F0F0u), e0);
+          e2m1x8_to_h2(((A0 >> 4) & 0x0F0F0F0Fu) | (B0 & 0xF0F0F0F0u), o0);
+          e2m1x8_to_h2((A1 & 0x0F0F0F0Fu) | ((B1 << 4) & 0xF0F0F0F0u), e1);
+          e2m1x8_to_h2(((A1 >> 4) & 0x0F0F0F0Fu) | (B1 & 0xF0F0F0F0u), o1);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mma16816(o[4 * w + x], hmul2(e0[x], vs0), hmul2(o0[x], vs0), hmul2(e1[x], vs1), hmul2(o1[x], vs1), b0, b1);
+        }
       }
-    }
     }
     __syncwarp();
-    if (i + kStages < ns) issue(i + kStages);
+    issue(i + kStages);
   }
   pdl_trigger();
 
@@ -633,7 +641,8 @@ int launch_q4(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
   LAZY_CUDA_TRY(q4_smem_limit(kern, DecL<D, H8>::SMEM, done));
   const int ngrp = a.Hq / a.Hkv / heads;
   if (a.S > 1 && a.S <= kMaxCluster)
-    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3(grid), dim3(kWarps * 32), DecL<D, H8>::SMEM, st, unsigned(a.S), a, heads, ngrp));
+    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3(grid), dim3(kWarps * 32), DecL<D, H8>::SMEM, st, unsigned(a.S), a,
+                                     heads, ngrp));
   else
     LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kWarps * 32), DecL<D, H8>::SMEM, st, a, heads, ngrp));
   return LAZY_OK;
