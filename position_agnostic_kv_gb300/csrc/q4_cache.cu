@@ -24,24 +24,31 @@ __device__ __forceinline__ uint32_t top8(const uint4& y) {
 // so a quotient that is not half way is at least 2^-8 away from it, and rounding it to 12 bits (ties away)
 // puts one that is exactly there.
 __device__ __forceinline__ uint32_t group_scale(uint32_t top, float inv6) {
-  const uint32_t a = __float_as_uint(__uint_as_float(top << 16) * inv6) + 0x800u & 0xFFFFF000u;
+  const uint32_t a = (__float_as_uint(__uint_as_float(top << 16) * inv6) + 0x800u) & 0xFFFFF000u;
   uint16_t s;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.0f), "f"(__uint_as_float(a)));
   return top >= 0x7F80u ? 0x7Fu : s & 0xFFu;
 }
 
 // Codes of 8 bf16 numbers (a word, low half of a byte = even dimension).  A quotient by the scale (times the
-// factor, a power of two) is a product with the approximate reciprocal, corrected once by its remainder, which
-// one fused multiply-add gives exactly: so a value half way between two codes stays half way, and others
-// stay on their side.  (Divisions cost ten instructions a value.)  Without a scale, or with a NaN one, every
-// code is 0.
+// factor, a power of two) is a product with the approximate reciprocal, corrected once by its remainder
+// (Markstein's correction), which one fused multiply-add gives exactly: so a value half way between two codes
+// stays half way, and others stay on their side.  (Divisions cost ten instructions a value.)  With a
+// factor below 2^-8 a quotient by the largest scale can exceed fp32: CUT cuts values at eight scales, more than
+// any code.  Without a scale, or with a NaN one, every code is 0.
+template <bool CUT>
 __device__ __forceinline__ uint32_t codes8(const uint4& y, uint32_t scale, float factor) {
   const float s = e4m3_to_f(scale) * factor;
   const bool some = s > 0.0f;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(some ? s : 1.0f));
   const float2 r2 = make_float2(r, r), ns2 = make_float2(-s, -s);
-  const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+  uint32_t w[4] = {y.x, y.y, y.z, y.w};
+  if (CUT && scale == 0x7Eu) {
+    const uint32_t lim = __float_as_uint(8.f * s) >> 16;  // a power of two times 3.5: exact in bf16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __vminu2(w[i] & 0x7FFF7FFFu, lim * 0x10001u) | (w[i] & 0x80008000u);
+  }
   float2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -50,8 +57,10 @@ __device__ __forceinline__ uint32_t codes8(const uint4& y, uint32_t scale, float
     q[i] = __ffma2_rn(__ffma2_rn(p, ns2, x), r2, p);
   }
   uint32_t c;
-  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(c)
       : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
   return some ? c : 0u;
@@ -137,12 +146,12 @@ __global__ void __launch_bounds__(256) kv_write_q4_any_kernel(const uint4* __res
     y[half] = make_uint4(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]), f2_to_bf2(x[4], x[5]), f2_to_bf2(x[6], x[7]));
   }
   const uint32_t ks = group_scale(max(top8(y[0]), top8(y[1])), 1.0f / (6.0f * kf));
-  *reinterpret_cast<uint2*>(blk + Q::k_code(r, q)) = make_uint2(codes8(y[0], ks, kf), codes8(y[1], ks, kf));
+  *reinterpret_cast<uint2*>(blk + Q::k_code(r, q)) = make_uint2(codes8<true>(y[0], ks, kf), codes8<true>(y[1], ks, kf));
   blk[Q::k_scale(r, q)] = uint8_t(ks);
   const uint4 a = vrow[2 * q], b = vrow[2 * q + 1];
   const uint32_t vs = group_scale(max(top8(a), top8(b)), 1.0f / (6.0f * vf));
-  *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 16 * q)) = codes8(a, vs, vf);
-  *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 16 * q + 8)) = codes8(b, vs, vf);
+  *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 16 * q)) = codes8<true>(a, vs, vf);
+  *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 16 * q + 8)) = codes8<true>(b, vs, vf);
   blk[Q::v_scale(r, q)] = uint8_t(vs);
 }
 
@@ -231,10 +240,10 @@ __global__ void __launch_bounds__(256, 4) kv_write_q4_kernel(const uint4* __rest
     if (!page || h >= Hkv) continue;
     uint8_t* blk = page + (size_t)h * Q::BYTES;
     const int qa = c >> 1, qb = qa + NC / 2;  // the groups
-    *reinterpret_cast<uint32_t*>(blk + Q::k_code(r, 0) + 4 * c) = codes8(a, sk & 0xFFu, kf);
-    *reinterpret_cast<uint32_t*>(blk + Q::k_code(r, 0) + 4 * (c + NC)) = codes8(b, sk >> 8, kf);
-    *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 8 * c)) = codes8(va, sv & 0xFFu, vf);
-    *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 8 * (c + NC))) = codes8(vb, sv >> 8, vf);
+    *reinterpret_cast<uint32_t*>(blk + Q::k_code(r, 0) + 4 * c) = codes8<HEADS == 1>(a, sk & 0xFFu, kf);
+    *reinterpret_cast<uint32_t*>(blk + Q::k_code(r, 0) + 4 * (c + NC)) = codes8<HEADS == 1>(b, sk >> 8, kf);
+    *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 8 * c)) = codes8<HEADS == 1>(va, sv & 0xFFu, vf);
+    *reinterpret_cast<uint32_t*>(blk + Q::v_code(r, 8 * (c + NC))) = codes8<HEADS == 1>(vb, sv >> 8, vf);
     blk[odd ? Q::v_scale(r, qa) : Q::k_scale(r, qa)] = uint8_t(mine);
     blk[odd ? Q::v_scale(r, qb) : Q::k_scale(r, qb)] = uint8_t(mine >> 8);
   }
@@ -269,7 +278,8 @@ __global__ void __launch_bounds__(256) kv_read_q4_kernel(const int32_t* __restri
   const int t = int(u % T), h0 = int(u / T) * HEADS;
   if (h0 >= Hkv) return;
   const int sl = slot[t], r = sl % kPage;
-  const uint8_t* blk = page_of(const_cast<uint8_t*>(cache), sl, num_pages, (size_t)Hkv * Q::BYTES, c == 0 && h0 == 0, status);
+  const uint8_t* blk = page_of(const_cast<uint8_t*>(cache), sl, num_pages, (size_t)Hkv * Q::BYTES, c == 0 && h0 == 0,
+                               status);
   if (!blk) return;
   blk += (size_t)h0 * Q::BYTES;
   uint32_t kc[HEADS], ks[HEADS], vc[HEADS], vs[HEADS];
@@ -332,8 +342,9 @@ extern "C" int lazy_kv_write_q4(const void* k, const void* v, const int32_t* slo
   // Four heads per thread share its cos/sin and overlap loads with arithmetic, once single heads would fill
   // the GPU (4 CTAs of 256 per SM) twice.  Measured, 32 000 tokens of 8 heads: 39 us with a table and 41 without,
   // against 46 and 67 with one head per thread; below 4096 tokens both take their launch's time.
+  // Only single heads cut values (codes8), which factors below 2^-8 need; four heads with it take 45 us.
   const long long rows = (long long)T * Hkv;
-  const bool many = rows * (D / 16) >= (long long)sm_count() * 2048;
+  const bool many = rows * (D / 16) >= (long long)sm_count() * 2048 && min(kf, vf) >= 0x1p-8f;
   const int threads = 256;
   const long long n = any ? rows * (D / 16) : (many ? (long long)T * ((Hkv + 3) / 4) : rows) * (D / 16);
   auto pick = [&](auto d) {

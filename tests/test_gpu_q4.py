@@ -164,6 +164,26 @@ def test_write_of_extreme_values(lk, D):
     _clean(lk)
 
 
+@pytest.mark.parametrize("factor", [2.0 ** -32, 1.0, 2.0 ** 32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_write_of_values_far_beyond_the_scales(lk, D, factor):
+    """Quotients by the largest scale that exceed fp32 saturate with their own sign."""
+    T = 5 if D == 64 else 40000  # enough for several heads per thread too
+    big = np.array([3e38, -3e38, 1e31, -1e31, 1e20, -1e20, 5e12, -5e12, 1.0, -1.0, 1e-7, -1e-7, 1e-38, -1e-38, 0, 7])
+    bits = f32_to_bf16_bits(np.resize(np.concatenate([big, big * 1e-6, big * 1e-30]), (T, 1, D)).astype(np.float32))
+    import torch
+    cache = torch.full(lk.q4_cache_shape(T // 16 + 1, 1, D), POISON, dtype=torch.uint8, device="cuda")
+    slots = np.arange(T) + 3
+    lk.kv_write_q4(_tensor(bits), _tensor(bits), _i32(slots), _i32(slots), cache, lk.pos_cfg_from("none", D), factor,
+                   factor)
+    ref = np.full(cache.shape, POISON, np.uint8)
+    val = lo.bf16_bits_to_f64(bits)
+    q4.store(ref, slots, val, val, factor, factor)
+    for g, r in zip(q4.load(cache.cpu().numpy(), D, factor, factor), q4.load(ref, D, factor, factor)):
+        np.testing.assert_array_equal(lo.bf16_bits_to_f64(g), lo.bf16_bits_to_f64(r))
+    _clean(lk)
+
+
 def test_write_and_read_skip_bad_slots(lk):
     import torch
     D, Hkv, pages = 128, 2, 3
