@@ -286,8 +286,8 @@ int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const int32_t* q_st
 #define LAZY_PHASE_PREFILL_Q4 3
 
 /*
- * lazy_workspace_size -- bytes of workspace the given call needs (0 if none).
- * rows = B for decode, total_q for prefill.  Uses the current device's SM count, so query it
+ * lazy_workspace_size -- bytes of workspace the given call needs (0 if none); phase is one of the
+ * LAZY_PHASE_* above.  rows = B for decode, total_q for prefill.  Uses the current device's SM count, so query it
  * with the device that will run the call current.
  */
 size_t lazy_workspace_size(int phase, int rows, int B, int max_blocks, int Hq, int Hkv, int D);
