@@ -28,6 +28,12 @@ static int check_q4(const char* what, int B, int max_blocks, int Hq, int Hkv, in
   return LAZY_OK;
 }
 
+// Scores are products of f16 operands times this factor and a row's power of two, which must not leave fp32.
+static int check_factor(const char* what, float scale_log2, float kf) {
+  if (scale_log2 * kf >= 0x1p-60f && scale_log2 * kf <= 0x1p60f) return LAZY_OK;
+  return fail(LAZY_EINVAL, "%s: scale times k_scale must lie in [2^-60, 2^60]", what);
+}
+
 static void fill_args(Q4Args& a, const void* q, const int32_t* q_start, const int32_t* doc_blocks,
                       const uint64_t* meta, int B, int max_blocks, const void* cache, int num_pages, int Hq, int Hkv,
                       float kf, float vf, void* out, float* lse) {
@@ -61,6 +67,7 @@ extern "C" int lazy_attn_decode_q4(const void* q, const int32_t* seq_len, const 
   if (rc) return rc;
   if (B > 0 && !seq_len) return fail(LAZY_EINVAL, "lazy_attn_decode_q4: seq_len is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
+  if (!rc) rc = check_factor("lazy_attn_decode_q4", a.pos.scale_log2, kf);
   if (rc) return rc;
   rc = check_device();
   if (rc || B == 0) return rc;
@@ -83,6 +90,7 @@ extern "C" int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const in
   if (rc) return rc;
   if (B > 0 && total_q > 0 && !cu_q) return fail(LAZY_EINVAL, "lazy_attn_prefill_q4: cu_q is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
+  if (!rc) rc = check_factor("lazy_attn_prefill_q4", a.pos.scale_log2, kf);
   if (rc) return rc;
   rc = check_device();
   if (rc || B <= 0 || total_q == 0) return rc;

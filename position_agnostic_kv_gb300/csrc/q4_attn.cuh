@@ -27,6 +27,12 @@ struct Q4Args {
   PosParams pos;
 };
 
+// Whether a query row belongs to a request (decode: every row does).  A batch padded to a fixed number of rows
+// has some behind the last sequence; their outputs stay as they were.
+__device__ __forceinline__ bool q4_in_request(const int32_t* cu_q, int B, int r) {
+  return cu_q == nullptr || (r >= cu_q[0] && r < cu_q[B]);
+}
+
 // Query row -> request b and absolute position m; number of blocks nb that m can see.
 struct Q4Row {
   int b, m, nb;

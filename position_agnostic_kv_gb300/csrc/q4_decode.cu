@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
   const int kvh = u % a.Hkv, r = u / a.Hkv;
   const int h0 = kvh * (a.Hq / a.Hkv) + grp * heads;
   pdl_wait();
+  if (!q4_in_request(a.cu_q, a.B, r)) return;  // the whole cluster: its CTAs share the row
   const Q4Row row = a.cu_q ? q4_row<true>(a, r) : q4_row<false>(a, r);
   const int m = row.m;
   int nb = row.nb;
@@ -571,12 +572,12 @@ constexpr int kMergeWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     q4_merge_kernel(const float* __restrict__ po, const float* __restrict__ pml, int S, long long n,
-                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, const int32_t* cu_q, int B, int Hq) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const long long rh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  if (rh >= n) return;
+  if (rh >= n || !q4_in_request(cu_q, B, int(rh / Hq))) return;
   const float2* ml = reinterpret_cast<const float2*>(pml) + rh * S;
   const float2 none = make_float2(-INFINITY, 0.f);
   const float2 x0 = lane < S ? ml[lane] : none, x1 = lane + 32 < S ? ml[lane + 32] : none;
@@ -689,7 +690,8 @@ cudaError_t q4_merge(const Q4Args& a, int D, cudaStream_t st) {
   const long long rh = (long long)a.rows * a.Hq;
   const dim3 grid(unsigned((rh + kMergeWarps - 1) / kMergeWarps)), block(kMergeWarps * 32);
   auto kern = D == 128 ? q4_merge_kernel<128> : q4_merge_kernel<64>;
-  return launch_pdl(kern, grid, block, 0, st, (const float*)a.part_o, (const float*)a.part_ml, a.S, rh, a.out, a.lse);
+  return launch_pdl(kern, grid, block, 0, st, (const float*)a.part_o, (const float*)a.part_ml, a.S, rh, a.out, a.lse,
+                    a.cu_q, a.B, a.Hq);
 }
 
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {

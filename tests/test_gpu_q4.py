@@ -518,6 +518,37 @@ def test_prefill_rows_beyond_the_last_request_stay(lk):
     assert (out[4:] == 5.0).all() and torch.isfinite(out[:4].float()).all()
 
 
+@pytest.mark.parametrize("blocks", [7, 4000])  # 4000: key splits merged through the workspace
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (32, 1), (24, 1), (48, 2)])
+def test_a_batch_padded_to_a_fixed_number_of_rows(lk, Hq, Hkv, blocks):
+    """Rows outside [cu_q[0], cu_q[B]) belong to no request: out and lse keep what they held.  The others
+    may be split over keys otherwise than without the padding: both results lie within 2^-8 |x| +
+    2^-10 max |v| of the exact one (_check_attention), so twice that apart."""
+    import torch
+    s = _one_request(lk, 128, Hq, Hkv)
+    meta = torch.zeros((1, blocks), dtype=torch.int64, device="cuda")
+    n = min(blocks, s["meta"].shape[1])
+    meta[:, :n] = s["meta"][:, :n]
+    q = _tensor(_bf(s["rng"], 40, Hq, 128))
+
+    def run(q, cu):
+        out, lse = torch.full_like(q, 5.0), torch.full((len(q), Hq), 5.0, device="cuda")
+        ws = _ws(lk, lk.PHASE_PREFILL_Q4, len(q), 1, blocks, Hq, Hkv, 128)
+        ws.fill_(0xFF)
+        lk.attn_prefill_q4(q, _i32(cu), _i32([60]), _i32([0]), meta, s["cache"], s["cfg"], out, 30, lse=lse, ws=ws)
+        _clean(lk)
+        return out, lse
+
+    out, lse = run(q, [3, 33])
+    want, wlse = run(q[3:33].contiguous(), [0, 30])
+    for x in (out, lse):
+        assert (x[:3] == 5.0).all() and (x[33:] == 5.0).all()
+    vmax = np.abs(lo.bf16_bits_to_f64(_load(s["cache"].cpu().numpy(), 128)[1])).max()
+    a, b = out[3:33].float(), want.float()
+    assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * vmax).all()
+    np.testing.assert_allclose(lse[3:33].cpu().numpy(), wlse.cpu().numpy(), rtol=1e-5, atol=1e-4)
+
+
 def test_offsets_beyond_32_bits(lk):
     """The request's pages lie past the first 4 GiB of the cache."""
     import torch

@@ -127,6 +127,8 @@ REFUSED = [
     (("decode", "prefill"), dict(scale=-0.1), -1, "scale must be positive"),
     (("decode", "prefill"), dict(scale=float("nan")), -1, "scale must be positive"),
     (("decode", "prefill"), dict(scale=float("inf")), -1, "scale must be positive"),
+    (("decode", "prefill"), dict(scale=1e-30, k_scale=2.0 ** -32), -1, "scale times k_scale"),
+    (("decode", "prefill"), dict(scale=1e30), -1, "scale times k_scale"),
     (("decode", "prefill"), dict(q=None), -1, "NULL pointer"),
     (("decode", "prefill"), dict(out=None), -1, "NULL pointer"),
     (("decode", "prefill"), dict(meta=None), -1, "NULL pointer"),
