@@ -274,13 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       // warpgroup half of the rows
       constexpr int CH = D / 8, RL = 32 / CH;  // chunks of a row, rows at a time
       constexpr int NR = KH ? 16 : 32;
-      const int lg = __ffs(G) - 1;  // G divides 128
+      const int recip = (65536 + G - 1) / G;  // row * recip >> 16 = row / G for rows and G up to 128
       const int tbase = tok0 + (KH ? 0 : qt * tpt), lim = min(tpt, Lq - tbase) * G;
       uint4 in[NR / RL];
 #pragma unroll
       for (int i = 0; i < NR / RL; ++i) {
         const int row = 32 * (warp & 3) + (KH ? 16 * qt : 0) + i * RL + lane / CH;
-        const size_t at = ((size_t)(q0 + tbase + (row >> lg)) * a.Hq + g * G + (row & (G - 1))) * D;
+        const int tok = row * recip >> 16;
+        const size_t at = ((size_t)(q0 + tbase + tok) * a.Hq + g * G + row - tok * G) * D;
         in[i] = row < lim ? *reinterpret_cast<const uint4*>(a.q + at + lane % CH * 8) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
@@ -1038,8 +1039,8 @@ int dispatch_q4_tc(int D, int kind, const Q4Args& a, int max_q, cudaStream_t st)
 
 }  // namespace
 
-// The tensor-core kernel holds whole tokens in 128-row tiles: head groups that divide 128.
-bool q4_use_tc(int Hq, int Hkv) { return 128 % (Hq / Hkv) == 0; }
+// The tensor-core kernel holds whole tokens in 128-row tiles, the rest of the rows empty.
+bool q4_use_tc(int Hq, int Hkv) { return Hq / Hkv <= tcq::kM; }
 
 // Decode of wide head groups runs on it too, the group's heads as the rows of one tile: the matrix
 // instructions of the decode kernel take 8 heads at a time and dequantise every page once for each 8

@@ -324,7 +324,7 @@ def _run(lk, w, reqs, n_steps, check, use_table=False, factors=(1.0, 1.0), sharp
 
 
 SHAPES = [(64, 4, 4), (64, 8, 2), (128, 8, 1), (128, 16, 2), (64, 16, 2), (128, 4, 2), (128, 24, 1), (64, 48, 2),
-          (128, 32, 1), (64, 16, 1), (128, 64, 1), (64, 128, 1)]
+          (128, 32, 1), (64, 16, 1), (128, 64, 1), (64, 128, 1), (128, 72, 1), (64, 120, 1), (128, 136, 1)]
 
 
 @pytest.mark.parametrize("D,Hq,Hkv", SHAPES)
@@ -358,7 +358,7 @@ def test_attention_workloads(lk, name, batch, reqs, steps):
 
 
 @pytest.mark.parametrize("Hq,Hkv,q_len", [(8, 2, [70, 33, 100, 1]), (8, 8, [300, 129, 1, 128]), (64, 8, [64, 16, 17, 40]),
-                                          (32, 1, [9, 4, 1, 5]), (24, 1, [20, 7, 32, 1]), (128, 1, [3, 2, 1, 5])])
+                                          (32, 1, [9, 4, 1, 5]), (24, 1, [20, 7, 32, 1]), (24, 1, [5, 4, 1, 3]), (128, 1, [3, 2, 1, 5])])
 @pytest.mark.parametrize("kind", ["rope", "alibi"])
 def test_prefill_query_lengths(lk, Hq, Hkv, q_len, kind):
     """Query segments longer and shorter than a tile of query rows, over no document at all too."""
@@ -519,7 +519,7 @@ def test_prefill_rows_beyond_the_last_request_stay(lk):
 
 
 @pytest.mark.parametrize("blocks", [7, 4000])  # 4000: key splits merged through the workspace
-@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (32, 1), (24, 1), (48, 2)])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (32, 1), (24, 1), (136, 1), (272, 2)])
 def test_a_batch_padded_to_a_fixed_number_of_rows(lk, Hq, Hkv, blocks):
     """Rows outside [cu_q[0], cu_q[B]) belong to no request: out and lse keep what they held.  The others
     may be split over keys otherwise than without the padding: both results lie within 2^-8 |x| +
