@@ -85,7 +85,6 @@ inline cudaError_t q4_smem_limit(F kern, int bytes, std::atomic<uint64_t>& done)
 }
 
 bool q4_use_tc(int Hq, int Hkv);
-bool q4_decode_on_tc(int Hq, int Hkv);
 int q4_tc_splits(int B, int Hkv, int max_blocks);
 cudaError_t q4_merge(const Q4Args& a, int D, cudaStream_t st);
 int run_q4_tc(Q4Args& a, int D, int max_q, cudaStream_t st);

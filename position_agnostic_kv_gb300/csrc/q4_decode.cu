@@ -618,21 +618,41 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 int q4_heads(int Hq, int Hkv) { return min(Hq / Hkv, 8); }
 
 // Key splits of a unit (query row, KV head, head group): 1, 2, 4, 8 (one cluster) or 16, 32, 64 (workspace).
-// The slowest SM carries k = ceil(units S / SMs) CTAs of ceil(blocks / S) pages and a fixed part worth about
-// 10 pages each; it needs about four CTAs to run at full rate.
-int q4_splits(int rows, int Hq, int Hkv, int max_blocks) {
-  const long long units = (long long)rows * (Hq / q4_heads(Hq, Hkv)), sms = sm_count();
-  int best = 1;
-  long long least = 0;
+// The slowest SM carries k = ceil(units S / SMs) CTAs of p = ceil(blocks / S) pages, at most C at a time.  In
+// units of the time that a page takes an SM at full rate (0.05 us; 0.07 us with 8 heads): k <= C CTAs take
+// (2 k + C) / 3 per page of one, and 25 each to start and end; each further one 40; a cluster 20 (of two
+// 40: they may land unevenly, 16 rows of ten documents took 21 us on one GPU and 25 on another), the merge through
+// the workspace 50.  Measured, us, S = 1, 2, 4, 8 (chosen: *): 16 rows of 8 KV heads, 4 heads each, 400 keys 9.5*
+// 11.0 12.0 12.0, 2000 keys 20.1 18.3 18.0* 25.3, 8000 keys 62 55 42* 49; 64 rows, 8000 keys 130 122* 131 157; 4
+// rows, 8000 keys 60 35 21 17*; 16 rows, 8 heads each, 400 keys 10.5* 14.1 21.7 21.6.
+struct Splits {
+  int S;
+  double cost;
+};
+Splits q4_splits(int rows, int Hq, int Hkv, int max_blocks) {
+  const int heads = q4_heads(Hq, Hkv), C = heads == 8 ? 3 : 4;
+  const long long units = (long long)rows * (Hq / heads), sms = sm_count();
+  Splits best = {1, 0.0};
   for (int S = 1; S <= 64 && S <= max(1, max_blocks / kWarps); S *= 2) {
-    const long long k = (units * S + sms - 1) / sms;
-    const long long cost = k * ((max_blocks + S - 1) / S + 10) * 4 / min(k, 4ll);
-    if (S == 1 || cost * 20 < least * 19) {  // a larger split has to gain 5 %
-      best = S;
-      least = cost;
-    }
+    const double k = double((units * S + sms - 1) / sms), p = (max_blocks + S - 1) / S, c = min(k, double(C));
+    const double cost = (k > C ? p * k : p * (2 * k + C) / 3) + 25 * c + 40 * (k - c) + (S == 2 ? 40 : S > 1 ? 20 : 0) +
+                        (S > kMaxCluster ? 50 : 0);
+    if (S == 1 || cost < 0.99 * best.cost) best = {S, cost};
   }
   return best;
+}
+
+// Decode of wide head groups may run on the tensor-core kernel instead, the group's heads as the rows of one
+// tile: the matrix instructions here take 8 heads at a time and dequantise every page once for each 8.  In the
+// units above (8 heads) a CTA there takes 45 to start and end, 14 per tile of 128 keys, 35 more for the merge
+// of key splits.  Measured, 64 rows of 16 heads of one KV head: 400 keys 10.5 us here, 12.0 there; 1600 keys 18
+// and 16; 32 rows of 32 heads, 12 000 keys 74 and 32; one row of 16 heads, 1600 keys 8.9 and 11.9.
+bool q4_decode_on_tc(int rows, int Hq, int Hkv, int max_blocks) {
+  if (Hq / Hkv < 16 || !q4_use_tc(Hq, Hkv)) return false;
+  const int S = q4_tc_splits(rows, Hkv, max_blocks), tiles = (max_blocks + 7) / 8;
+  const long long waves = ((long long)rows * Hkv * S + sm_count() - 1) / sm_count();
+  const double cost = double(waves) * (45 + 14 * ((tiles + S - 1) / S)) + (S > 1 ? 35 : 0);
+  return cost < q4_splits(rows, Hq, Hkv, max_blocks).cost;
 }
 
 template <int D, bool H8, int POS>
@@ -660,9 +680,9 @@ int launch_q4_pos(const Q4Args& a, int heads, unsigned grid, cudaStream_t st) {
 
 // Key splits whose partials go through the workspace (1: none do).
 static int ws_splits(int rows, int Hq, int Hkv, int max_blocks, bool rows_mode) {
-  if (!rows_mode && q4_decode_on_tc(Hq, Hkv)) return q4_tc_splits(rows, Hkv, max_blocks);
+  if (!rows_mode && q4_decode_on_tc(rows, Hq, Hkv, max_blocks)) return q4_tc_splits(rows, Hkv, max_blocks);
   if (rows_mode && q4_use_tc(Hq, Hkv)) return 1;
-  const int S = q4_splits(rows, Hq, Hkv, max_blocks);
+  const int S = q4_splits(rows, Hq, Hkv, max_blocks).S;
   return S <= kMaxCluster ? 1 : S;
 }
 
@@ -697,7 +717,7 @@ cudaError_t q4_merge(const Q4Args& a, int D, cudaStream_t st) {
 int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cudaStream_t st) {
   if ((long long)a.rows * a.Hq > 0x7FFFFFFFll)
     return fail(LAZY_ERANGE, "too many query rows (%d rows, %d heads)", a.rows, a.Hq);
-  if (!rows_mode && q4_decode_on_tc(a.Hq, a.Hkv)) {
+  if (!rows_mode && q4_decode_on_tc(a.rows, a.Hq, a.Hkv, a.max_blocks)) {
     a.S = q4_tc_splits(a.rows, a.Hkv, a.max_blocks);
     int rc = take_ws(a, D, rows_mode, ws, ws_bytes);
     if (rc == LAZY_OK) rc = run_q4_tc(a, D, 1, st);
@@ -705,7 +725,7 @@ int run_q4_rows(Q4Args& a, int D, bool rows_mode, void* ws, size_t ws_bytes, cud
     return rc;
   }
   const int heads = q4_heads(a.Hq, a.Hkv);
-  a.S = q4_splits(a.rows, a.Hq, a.Hkv, a.max_blocks);
+  a.S = q4_splits(a.rows, a.Hq, a.Hkv, a.max_blocks).S;
   int rc = take_ws(a, D, rows_mode, ws, ws_bytes);
   if (rc) return rc;
   const long long ctas = (long long)a.rows * (a.Hq / heads) * a.S;

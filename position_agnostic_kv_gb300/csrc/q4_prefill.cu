@@ -1042,12 +1042,7 @@ int dispatch_q4_tc(int D, int kind, const Q4Args& a, int max_q, cudaStream_t st)
 // The tensor-core kernel holds whole tokens in 128-row tiles, the rest of the rows empty.
 bool q4_use_tc(int Hq, int Hkv) { return Hq / Hkv <= tcq::kM; }
 
-// Decode of wide head groups runs on it too, the group's heads as the rows of one tile: the matrix
-// instructions of the decode kernel take 8 heads at a time and dequantise every page once for each 8
-// (32 heads over 32 x 12 000 keys: 52 us against 74).
-bool q4_decode_on_tc(int Hq, int Hkv) { return Hq / Hkv >= 16 && q4_use_tc(Hq, Hkv); }
-
-// Key splits of such a decode: one wave of CTAs, at least two tiles of 128 keys each.
+// Key splits of a decode on it: one wave of CTAs, at least two tiles of 128 keys each.
 int q4_tc_splits(int B, int Hkv, int max_blocks) {
   const int tiles = (max_blocks + tcq::kPagesPerTile - 1) / tcq::kPagesPerTile;
   const long long units = (long long)B * Hkv;
