@@ -82,7 +82,8 @@ __device__ __forceinline__ uint8_t* page_of(uint8_t* cache, int sl, int num_page
   return cache + (size_t)(sl / kPage) * page_bytes;
 }
 
-// Partial or interleaved rotations: one thread per (token, head, group), which reads its partners' inputs too.
+// Partial or interleaved rotations, or a cos/sin table off a 16-byte boundary: one thread per (token, head,
+// group), which reads its partners' inputs too.
 template <int D>
 __global__ void __launch_bounds__(256) kv_write_q4_any_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                                                               const int32_t* __restrict__ slot,
@@ -338,7 +339,9 @@ extern "C" int lazy_kv_write_q4(const void* k, const void* v, const int32_t* slo
   if (rotate && T > 0 && !local_pos) return fail(LAZY_EINVAL, "lazy_kv_write_q4: local_pos is NULL");
   rc = check_device();
   if (rc || T == 0) return rc;
-  const bool any = rotate && (pos.rotary_dim != D || pos.interleaved);
+  // the full rotation's kernel reads the caller's cos/sin table 16 bytes at a time, the other one by floats (the
+  // same arithmetic): a table that starts off a 16-byte boundary, inside a larger buffer, goes there
+  const bool any = rotate && (pos.rotary_dim != D || pos.interleaved || !aligned16(pos.table));
   // Four heads per thread share its cos/sin and overlap loads with arithmetic, once single heads would fill
   // the GPU (4 CTAs of 256 per SM) twice.  Measured, 32 000 tokens of 8 heads: 39 us with a table and 41 without,
   // against 46 and 67 with one head per thread; below 4096 tokens both take their launch's time.
