@@ -266,7 +266,8 @@ int lazy_kv_read_q4(const int32_t* slot, int T, int Hkv, int D, const void* kv_c
  * lazy_attn_decode_q4 / lazy_attn_prefill_q4 -- lazy_attn_decode / lazy_attn_prefill over a
  * 4-bit cache.  Workspace: lazy_workspace_size with LAZY_PHASE_DECODE_Q4 / LAZY_PHASE_PREFILL_Q4.
  * A row without a visible key gets out = 0 and lse = -inf; rows of q outside [cu_q[0], cu_q[B])
- * (a batch padded to a fixed size) keep what out and lse held.  A negative or non-finite scale is
+ * (a batch padded to a fixed size) keep what out and lse held.  max_q may be any upper bound of the
+ * requests' query rows.  A negative or non-finite scale is
  * refused, and one whose product with k_scale (0: the default 1/sqrt(D); with YaRN's factor and
  * log2 e) lies outside [2^-60, 2^60].
  */

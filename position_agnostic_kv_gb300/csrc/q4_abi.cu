@@ -97,6 +97,7 @@ extern "C" int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const in
   fill_args(a, q, q_start, doc_blocks, meta, B, max_blocks, kv_cache, num_pages, Hq, Hkv, kf, vf, out, lse);
   a.cu_q = cu_q;
   a.rows = total_q;
+  if (max_q > total_q) max_q = total_q;  // any upper bound will do; no request has more rows than there are
   if (q4_use_tc(Hq, Hkv)) return max_q > 0 ? run_q4_tc(a, D, max_q, static_cast<cudaStream_t>(stream)) : LAZY_OK;
   return run_q4_rows(a, D, true, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }

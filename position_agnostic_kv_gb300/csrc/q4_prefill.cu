@@ -1016,11 +1016,11 @@ int launch_q4_tc(const Q4Args& a, int max_q, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   LAZY_CUDA_TRY(q4_smem_limit(kern, L::SMEM, done));
   const int rows_tok = tcq::kQT * (tcq::kM / (a.Hq / a.Hkv));
-  const int nmp = (max_q + rows_tok - 1) / rows_tok;
+  const long long nmp = ((long long)max_q + rows_tok - 1) / rows_tok;
   const long long pairs = (long long)a.B * a.Hkv;
-  const long long ctas = pairs * nmp * a.S;
-  if (ctas > 0x7FFFFFFFll) return fail(LAZY_ERANGE, "too many query rows (B=%d, max_q=%d)", a.B, max_q);
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(unsigned(ctas)), dim3(tcq::kThreads), L::SMEM, st, a, nmp,
+  if (pairs > 0x7FFFFFFFll || nmp * a.S > 0x7FFFFFFFll / pairs)
+    return fail(LAZY_ERANGE, "too many query rows (B=%d, max_q=%d)", a.B, max_q);
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(unsigned(pairs * nmp * a.S)), dim3(tcq::kThreads), L::SMEM, st, a, int(nmp),
                            int(pairs < sm_count())));
   return LAZY_OK;
 }

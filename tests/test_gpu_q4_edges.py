@@ -1,13 +1,15 @@
 """GPU tests of calls on the 4-bit cache that lie at the edge of what its interface allows.
 
-Where two calls compute the same numbers (a table at another address) their results are
-compared bit for bit.
+Where two calls compute the same numbers (a table at another address, a looser bound on the query
+lengths) their results are compared bit for bit.
 """
 import numpy as np
 import pytest
 
+from oracle import lazy_oracle as lo
+from tests import q4_reference as q4
 from tests.gpu_common import lib
-from tests.test_gpu_q4 import POISON, _bf, _clean, _i32, _tensor
+from tests.test_gpu_q4 import POISON, _bf, _clean, _dev, _i32, _tensor, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +43,38 @@ def test_a_table_may_start_at_any_float(lk, D, Hkv, T, offset):
         caches.append(c)
     _clean(lk)
     assert torch.equal(*caches)
+
+
+# ------------------------------------------------------------------ bounds on the query lengths
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (32, 1), (136, 1)])
+@pytest.mark.parametrize("q_len", [[5, 0, 3], [70, 9, 1]])
+def test_max_q_may_be_any_upper_bound(lk, Hq, Hkv, q_len):
+    """A looser bound than the longest question, up to the largest int, changes nothing."""
+    import torch
+    D, B = 128, len(q_len)
+    rng = np.random.default_rng([Hq, q_len[0]])
+    T, n = max(q_len), -(-max(q_len) // 16)
+    cache = torch.full(lk.q4_cache_shape(n, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+    cfg, t = lk.pos_cfg_from("rope", D), np.arange(T)
+    lk.kv_write_q4(_tensor(_bf(rng, T, Hkv, D)), _tensor(_bf(rng, T, Hkv, D)), _i32(t), _i32(t), cache, cfg)
+    _, meta, _, _, _ = lk.build_doc_meta([0, 0], [], [], [0], [], [T], [0, n], t[:n], n)
+    meta, cu = _dev(meta.view(np.int64)).repeat(B, 1), np.r_[0, np.cumsum(q_len)]
+    q = _tensor(_bf(rng, cu[-1], Hq, D))
+    ws = _ws(lk, lk.PHASE_PREFILL_Q4, len(q), B, n, Hq, Hkv, D)
+    outs = []
+    for max_q in (max(q_len), max(q_len) + 1, len(q) + 1000, 2 ** 31 - 1):
+        out, lse = torch.full_like(q, np.nan), torch.full((len(q), Hq), np.nan, device="cuda")
+        lk.attn_prefill_q4(q, _i32(cu), _i32([0] * B), _i32([0] * B), meta, cache, cfg, out, max_q, lse=lse, ws=ws)
+        _clean(lk)
+        assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+        outs.append((out, lse))
+    # the bound decides which warps share a row's keys: the same operands and scores, the weights rounded (2^-11)
+    # against other maxima and summed in another order.  Both results lie within 2^-8 |x| + 2^-10 max |v| of the
+    # exact one for those scores, so twice that apart.
+    vmax = np.nanmax(np.abs(lo.bf16_bits_to_f64(q4.load(cache.cpu().numpy(), D)[1])))
+    for out, lse in outs[1:]:
+        a, b = out.float(), outs[0][0].float()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * vmax).all()
+        np.testing.assert_allclose(lse.cpu().numpy(), outs[0][1].cpu().numpy(), rtol=1e-5, atol=1e-4)
+    for out, lse in outs[3:]:
+        assert torch.equal(out, outs[2][0]) and torch.equal(lse, outs[2][1])
