@@ -237,9 +237,11 @@ int lazy_attn_prefill(const void* q, const int32_t* cu_q, const int32_t* q_start
  *   V code   9 D + (r / 8) A + (d / (D/8) 4 + (r % 8) / 2) 16 + (r % 2) D/16 + (d % (D/8)) / 2,
  *            A = 512 for D = 128 and 8 for D = 64 (low half of the byte: even d)
  *   V scale  17 D + (d / 16) 16 + ((r % 8) / 2) 4 + (r / 8) 2 + r % 2
- * Rows that hold no visible key may hold anything.  Slots, block words, query and workspace
- * conventions are those of the bf16 entry points above; so are the head shapes they accept, the
- * status bits and the return codes.  Arguments are checked before the device is.
+ * Rows that hold no visible key may hold anything; a NaN makes NaN only of the query rows that see
+ * it (in a key: all of their outputs for its KV head, in a value: those of its group).  Slots, block
+ * words, query and workspace conventions are those of the bf16 entry points above; so are the head
+ * shapes they accept, the status bits and the return codes.  Arguments are checked before the
+ * device is.
  * ------------------------------------------------------------------------------------------ */
 
 /*

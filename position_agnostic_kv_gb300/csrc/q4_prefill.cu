@@ -16,7 +16,10 @@
 //              8 frequencies (two runs of 8 dimensions) of 8 rows of a page; the packed pages lie 9 D + pad
 //              bytes apart, so that its word loads meet no bank conflicts.
 //   warps 14-15 values: the same, exact in f16; even and odd groups store their rows in opposite order,
-//              against bank conflicts.
+//              against bank conflicts.  A weight of 0 does not hide a NaN from a product, so NaN scales become 0
+//              before the conversion (while it waits for its stage), and the first position of one in each 16
+//              columns is noted: at the end the rows at or behind it, which are those that see it, become
+//              NaN there.
 //   warp 12    producer: block words four tiles at a time, asynchronous 16-byte copies into a ring of packed
 //              keys (2 stages, KH 4) and one of packed values (1, KH 2).
 //   warp 13    TMEM owner and MMA issuer: QK0(j) QK1(j) | PV0(j) QK0(j+1) PV1(j) QK1(j+1) | ...
@@ -36,6 +39,7 @@
 // halves of a tile with two buffers per Q tile 176 (second shape 200), values only in halves 171 (201), an
 // MMA thread per Q tile 229 (291).  Every wait is bounded.
 #include <cfloat>
+#include <climits>
 
 #include "q4_attn.cuh"
 #include "tcgen05.cuh"
@@ -100,7 +104,9 @@ struct Layout {
   static constexpr int TURNS_OFF = FLAG_OFF + kSlots * 8;
   static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  // int [D / 16] first key with a NaN in 16 columns, [1] in any; [4] {first query row and head, tokens, m_min}
+  static constexpr int NANPOS_OFF = MISC_OFF + 16;
+  static constexpr int SMEM = NANPOS_OFF + (D / 16 + 5) * 4 + 1024;
 };
 static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
 
@@ -127,6 +133,9 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   uint16_t v;
@@ -221,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
 
+  volatile int* nanpos = reinterpret_cast<volatile int*>(sm + L::NANPOS_OFF);
+
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPK; ++s) {
       mbar_init(BAR(B_PK_FULL + s), 33);
@@ -241,6 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
     mbar_init(BAR(B_PV_DONE), 1);
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (threadIdx.x >= 32 && threadIdx.x <= 32 + D / 16) nanpos[threadIdx.x - 32] = INT_MAX;
+  if (threadIdx.x == 64) {
+    nanpos[D / 16 + 1] = q0 + tok0;
+    nanpos[D / 16 + 2] = g * G;
+    nanpos[D / 16 + 3] = ntok;
+    nanpos[D / 16 + 4] = m_min;
   }
   if constexpr (kRotate)
     for (int i = threadIdx.x; i < D / 2; i += blockDim.x) turns[i] = a.pos.turns[i];
@@ -913,22 +931,41 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
       for (int j = 0; j < ntiles; ++j) {
         const int s = j & 1, slot = j % kSlots;
         if (ok) ok = wait_bar(BAR(B_PV_FULL + j % kPV), uint32_t((j / kPV) & 1), abort_flag, a.status);
+        const uint32_t src = PVS(j) + uint32_t(ps * L::PVS);
+        const uint32_t csrc = src + (l >> 2) * 64 + t * 16, ssrc = src + 8 * D + (D == 128 ? l >> 2 : 0) * 16 + t * 4;
+        // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
+        const int rr = (ok ? pinfo[slot * kPagesPerTile + ps].y : 0) - 2 * t;
+        const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
+                              (rr > 9 ? 0xFF000000u : 0u);  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
+        if (a.seq_len == nullptr) {  // a decode's one row sees every key that is kept
+          constexpr uint32_t step = D == 128 ? 32 : 16;  // between this thread's scale words
+          auto nan_bits = [](uint32_t sw) { return ((sw & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };  // 0x7F, 0xFF
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) any |= nan_bits(ld_shared_u32(ssrc + k * step) & keep);
+          if (__any_sync(0xffffffffu, any != 0)) {
+            const int page0 = pstart[slot * kPagesPerTile + ps];
+            int* first = const_cast<int*>(nanpos);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t sw = ld_shared_u32(ssrc + k * step), bits = nan_bits(sw & keep);
+              if (bits == 0) continue;
+              const int byte = (__ffs(int(bits)) - 1) >> 3, p = page0 + 2 * t + (byte & 1) + (byte >> 1) * 8;
+              atomicMin(first + (D == 128 ? (l >> 2) + 2 * k : k), p);
+              atomicMin(first + D / 16, p);
+              st_shared_u32(ssrc + k * step, sw & ~((bits >> 7) * 0xFFu));  // D = 64: the same by both lanes
+            }
+          }
+        }
         if (ok && j >= 2) ok = wait_bar(BAR(B_V_FREE + s), uint32_t(((j >> 1) - 1) & 1), abort_flag, a.status);
         if (ok) {
-          // rows without a key (and page slots without a page) become zeros: their scales are replaced by 0
-          const int rows = pinfo[slot * kPagesPerTile + ps].y;
-          const uint32_t src = PVS(j) + uint32_t(ps * L::PVS);
           const uint32_t sV = sV0 + uint32_t(s * L::TILE);
-          const int rr = rows - 2 * t;  // scale bytes: rows 2t, 2t + 1, 2t + 8, 2t + 9
-          const uint32_t keep = (rr > 0 ? 0xFFu : 0u) | (rr > 1 ? 0xFF00u : 0u) | (rr > 8 ? 0xFF0000u : 0u) |
-                                (rr > 9 ? 0xFF000000u : 0u);
           auto put = [&](int row, int cb, int ch, uint32_t codes, uint32_t scale) {
             uint32_t x[4];
             e2m1x8_to_h2(codes, x);
             st_shared_v4(sV + uint32_t(cb * L::BLK) + swz(ps * kPage + row, ch),
                          make_uint4(hmul2(x[0], scale), hmul2(x[1], scale), hmul2(x[2], scale), hmul2(x[3], scale)));
           };
-          const uint32_t csrc = src + (l >> 2) * 64 + t * 16, ssrc = src + 8 * D + (D == 128 ? l >> 2 : 0) * 16 + t * 4;
           if constexpr (D == 128) {
             // groups q = l / 4 + 2 k; odd ones store their odd row first: no two lanes share a bank
             const int odd = l >> 2;
@@ -992,6 +1029,22 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  // NaN over the columns where a row sees one (the row's sizes come out of shared memory: kept in registers they
+  // would be spilled by every role)
+  if (warp < 8 && nanpos[D / 16] != INT_MAX) {
+    const int G = a.Hq / a.Hkv, r0 = nanpos[D / 16 + 1], h0 = nanpos[D / 16 + 2], m0 = nanpos[D / 16 + 4];
+    const int n = nanpos[D / 16 + 3] * G * D;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int c = i % D, t = i / D / G, h = i / D % G;
+      if (m0 + t < nanpos[c / 16]) continue;
+      const size_t rh = (size_t)(r0 + t) * a.Hq + h0 + h;
+      if (a.S > 1)
+        a.part_o[(rh * a.S + int(blockIdx.x) % a.S) * D + c] = NAN;
+      else
+        a.out[rh * D + c] = __float2bfloat16_rn(NAN);
+    }
   }
 }
 

@@ -1,7 +1,7 @@
 """GPU tests of calls on the 4-bit cache that lie at the edge of what its interface allows.
 
 Where two calls compute the same numbers (a table at another address, a looser bound on the query
-lengths) their results are compared bit for bit.
+lengths, values that a row does not see) their results are compared bit for bit.
 """
 import numpy as np
 import pytest
@@ -10,6 +10,7 @@ from oracle import lazy_oracle as lo
 from tests import q4_reference as q4
 from tests.gpu_common import lib
 from tests.test_gpu_q4 import POISON, _bf, _clean, _dev, _i32, _tensor, _ws
+from workloads import alibi_slopes_input
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,110 @@ def test_max_q_may_be_any_upper_bound(lk, Hq, Hkv, q_len):
         np.testing.assert_allclose(lse.cpu().numpy(), outs[0][1].cpu().numpy(), rtol=1e-5, atol=1e-4)
     for out, lse in outs[3:]:
         assert torch.equal(out, outs[2][0]) and torch.equal(lse, outs[2][1])
+
+
+# ------------------------------------------------------------------ NaN in values that some rows do not see
+@pytest.mark.parametrize("D,Hq,Hkv,L", [(128, 8, 2, 150), (64, 8, 2, 150), (128, 8, 2, 30), (64, 8, 8, 300), (128, 32, 1, 9),
+                                        (64, 16, 1, 8), (128, 24, 1, 40), (128, 136, 1, 20)])
+@pytest.mark.parametrize("kind", ["rope", "interleaved", "alibi"])
+def test_a_nan_value_reaches_only_the_rows_that_see_it(lk, D, Hq, Hkv, L, kind):
+    """Values with an infinity or a NaN at the document's end, inside the query segment and at its last token.
+    A row's outputs are NaN in exactly the groups of 16 dimensions (and KV heads) where it sees one, even where
+    the key's weight is 0 in f16; all else keeps its bits.  Prefill, then the decode of the same rows with few
+    blocks and with many (key splits)."""
+    import torch
+    rng = np.random.default_rng([D, Hq, L])
+    P, T = 41, 41 + L
+    nd, nq = -(-P // 16), -(-L // 16)
+    ids = rng.permutation(nd + nq + 2)[:nd + nq]
+    t = np.arange(T)
+    own = np.where(t < P, t, t - P)
+    slot = np.where(t < P, ids[own // 16 % nd], ids[(nd + own // 16) % (nd + nq)]) * 16 + own % 16
+    extra = dict(interleaved=True) if kind == "interleaved" else {}
+    if kind == "alibi":
+        extra = dict(alibi_slopes=_dev(np.asarray(alibi_slopes_input(Hq), np.float32)))
+    cfg = lk.pos_cfg_from("alibi" if kind == "alibi" else "rope", D, rotary_dim=D, **extra)
+    q, k, v = _tensor(_bf(rng, L, Hq, D)), _tensor(_bf(rng, T, Hkv, D)), _tensor(_bf(rng, T, Hkv, D))
+    bad = [(P - 1, 0, D // 16 - 1, np.nan), (P + L // 3, 0, 1, -np.inf), (P + L // 3 + 2, Hkv - 1, 1, np.nan),
+           (P + L // 2, Hkv - 1, 2, np.inf), (T - 1, 0, 0, np.nan)]  # position, KV head, group, value
+    _, meta, _, q_start, doc_blocks = lk.build_doc_meta([0, 1], [0], [P], [0, nd], ids[:nd], [L], [0, nq], ids[nd:],
+                                                       nd + nq)
+    assert q_start[0] == P and doc_blocks[0] == nd
+    caches = []
+    for spoil in (False, True):
+        x = v.clone()
+        if spoil:
+            for p, h, g, val in bad:
+                x[p, h, 16 * g + p % 16] = val
+        c = torch.full(lk.q4_cache_shape(nd + nq + 2, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+        lk.kv_write_q4(k, x, _i32(slot), _i32(own), c, cfg)
+        caches.append(c)
+    m = P + np.arange(L)
+    want = np.zeros((L, Hq, D // 16), bool)
+    for p, h, g, _ in bad:
+        want[m >= p, h * (Hq // Hkv):(h + 1) * (Hq // Hkv), g] = True
+    want = torch.from_numpy(want).cuda().repeat_interleave(16, 2)
+    assert want.any() and not want.all()
+
+    def check(what, outs):
+        (a, la), (b, lb) = outs
+        assert torch.isfinite(a.float()).all(), what
+        assert torch.equal(torch.isnan(b), want), f"{what}: NaN in {int(torch.isnan(b).sum())}, not {int(want.sum())}"
+        assert torch.equal(a[~want], b[~want]) and torch.equal(la, lb), what
+
+    def both(call):
+        res = []
+        for c in caches:
+            out, lse = torch.full_like(q, 7.0), torch.full((L, Hq), np.nan, device="cuda")
+            call(c, out, lse)
+            _clean(lk)
+            res.append((out, lse))
+        return res
+
+    md = _dev(meta.view(np.int64))
+    ws = _ws(lk, lk.PHASE_PREFILL_Q4, L, 1, nd + nq, Hq, Hkv, D)
+    check("prefill", both(lambda c, out, lse: lk.attn_prefill_q4(
+        q, _i32([0, L]), _i32([P]), _i32([nd]), md, c, cfg, out, L, lse=lse, ws=ws)))
+    for blocks in (nd + nq, 3000):
+        wide = torch.zeros((L, blocks), dtype=torch.int64, device="cuda")
+        wide[:, :nd + nq] = md
+        wd = _ws(lk, lk.PHASE_DECODE_Q4, L, L, blocks, Hq, Hkv, D)
+        check(f"decode, {blocks} blocks", both(lambda c, out, lse: lk.attn_decode_q4(
+            q, _i32(m + 1), _i32([P] * L), _i32([nd] * L), wide, c, cfg, out, lse=lse, ws=wd)))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,L", [(128, 8, 2, 150), (64, 8, 8, 300), (128, 8, 2, 30), (64, 16, 1, 8), (128, 136, 1, 20)])
+@pytest.mark.parametrize("kind", ["rope", "none"])
+def test_a_nan_key_reaches_only_the_rows_that_see_it(lk, D, Hq, Hkv, L, kind):
+    """A key with a NaN inside the query segment: its KV head's outputs and lse are NaN in the rows that see
+    it, and keep their bits in the others."""
+    import torch
+    rng = np.random.default_rng([D, Hq, L])
+    blocks, t, bad = -(-L // 16), np.arange(L), L // 2
+    cfg = lk.pos_cfg_from(kind, D)
+    q, k, v = _tensor(_bf(rng, L, Hq, D)), _tensor(_bf(rng, L, Hkv, D)), _tensor(_bf(rng, L, Hkv, D))
+    _, meta, _, _, _ = lk.build_doc_meta([0, 0], [], [], [0], [], [L], [0, blocks], t[:blocks], blocks)
+    md = _dev(meta.view(np.int64))
+    res = []
+    for spoil in (False, True):
+        x = k.clone()
+        if spoil:
+            x[bad, Hkv - 1, 5] = np.nan
+        c = torch.full(lk.q4_cache_shape(blocks, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+        lk.kv_write_q4(x, v, _i32(t), _i32(t), c, cfg)
+        for call in ("prefill", "decode"):
+            out, lse = torch.full_like(q, 7.0), torch.full((L, Hq), 7.0, device="cuda")
+            if call == "prefill":
+                lk.attn_prefill_q4(q, _i32([0, L]), _i32([0]), _i32([0]), md, c, cfg, out, L, lse=lse,
+                                   ws=_ws(lk, lk.PHASE_PREFILL_Q4, L, 1, blocks, Hq, Hkv, D))
+            else:
+                lk.attn_decode_q4(q, _i32(t + 1), _i32([0] * L), _i32([0] * L), md.repeat(L, 1), c, cfg, out, lse=lse,
+                                  ws=_ws(lk, lk.PHASE_DECODE_Q4, L, L, blocks, Hq, Hkv, D))
+            _clean(lk)
+            res.append((out, lse))
+    want = torch.zeros((L, Hq), dtype=torch.bool, device="cuda")
+    want[bad:, (Hkv - 1) * (Hq // Hkv):] = True
+    for (a, la), (b, lb) in zip(res[:2], res[2:]):
+        assert torch.isfinite(a.float()).all() and torch.isfinite(la).all()
+        assert torch.equal(torch.isnan(b), want[..., None].expand_as(b)) and torch.equal(torch.isnan(lb), want)
+        assert torch.equal(a[~want], b[~want]) and torch.equal(la[~want], lb[~want])
