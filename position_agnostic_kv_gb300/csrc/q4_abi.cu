@@ -48,6 +48,7 @@ static void fill_args(Q4Args& a, const void* q, const int32_t* q_start, const in
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.qk_log2 = a.pos.scale_log2 * kf;
+  a.lowest_ex = q4_lowest_exponent(a.qk_log2);
   a.v_factor = vf;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;

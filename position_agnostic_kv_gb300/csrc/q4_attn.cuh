@@ -1,7 +1,9 @@
 // Arguments of the attention kernels over the 4-bit cache.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "q4.cuh"
 
@@ -17,6 +19,7 @@ struct Q4Args {
   const uint8_t* cache;       // [num_pages][Hkv][18 D]
   int num_pages, B, max_blocks, Hq, Hkv, rows;
   float qk_log2;              // softmax scale * log2(e) * k factor: scores in base-2 units
+  int lowest_ex;              // q4_lowest_exponent(qk_log2)
   float v_factor;
   __nv_bfloat16* out;
   float* lse;
@@ -64,12 +67,14 @@ __device__ __forceinline__ int q4_rows(uint64_t w, int m) {
 }
 
 // Exponent ex of the power of two that normalises a query row whose largest magnitude is `top`: the row
-// times 2^-ex lies in [-1, 1] (rows below 2^-60 keep ex = 0: their scores vanish; infinities and NaN too, and
-// pass through).
-__device__ __forceinline__ int q4_exponent(float top) {
+// times 2^-ex lies in [-1, 1].  Rows below 2^lowest keep ex = 0 and become zeros (infinities and NaN too, and
+// pass through): a sum of D products with keys below 2^12 times the score factor is then below 2^-100.
+__device__ __forceinline__ int q4_exponent(float top, int lowest) {
   const int ex = int(__float_as_uint(top) >> 23) - 126;
-  return ex < -60 || ex > 128 ? 0 : min(ex, 126);
+  return ex < lowest || ex > 128 ? 0 : min(ex, 126);
 }
+// The lowest exponent that leaves 2^-ex, and the score factor times 2^ex, normal numbers.
+inline int q4_lowest_exponent(float qk_log2) { return std::max(-126, -120 - std::ilogb(qk_log2)); }
 
 // Set a kernel's dynamic shared memory limit, once per device (`done`: one bit per device, per kernel).
 template <typename F>

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, H8 ? 3 : 4) q4_decode_kernel(cons
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const int ex = q4_exponent(top);
+    const int ex = q4_exponent(top, a.lowest_ex);
     const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {

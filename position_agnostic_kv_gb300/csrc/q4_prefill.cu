@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
         for (int e = 0; e < 4; ++e) top = max(top, max(xs[e] & 0x7FFFu, (xs[e] >> 16) & 0x7FFFu));
       }
       if (KH) named_sync(1, 2 * kM);  // both have read every row: it may be rotated in place
-      const int ex = q4_exponent(__uint_as_float(top << 16));
+      const int ex = q4_exponent(__uint_as_float(top << 16), a.lowest_ex);
       rf = a.qk_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
       const float sc = __uint_as_float(uint32_t(127 - ex) << 23);
       auto pack = [&](const float (&y)[8]) {

@@ -1,7 +1,8 @@
 """GPU tests of calls on the 4-bit cache that lie at the edge of what its interface allows.
 
 Where two calls compute the same numbers (a table at another address, a looser bound on the query
-lengths, values that a row does not see) their results are compared bit for bit.
+lengths, values that a row does not see, operands scaled by powers of two) their results are
+compared bit for bit.
 """
 import numpy as np
 import pytest
@@ -186,3 +187,73 @@ def test_a_nan_key_reaches_only_the_rows_that_see_it(lk, D, Hq, Hkv, L, kind):
         assert torch.isfinite(a.float()).all() and torch.isfinite(la).all()
         assert torch.equal(torch.isnan(b), want[..., None].expand_as(b)) and torch.equal(torch.isnan(lb), want)
         assert torch.equal(a[~want], b[~want]) and torch.equal(la[~want], lb[~want])
+
+
+# ------------------------------------------------------------------ small queries under a large scale
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 16, 2), (64, 32, 1), (128, 136, 1)])
+@pytest.mark.parametrize("shift", [40, 55, 62, 70])
+def test_small_queries_under_a_large_scale(lk, D, Hq, Hkv, shift):
+    """Queries times 2^-shift and the scale times 2^shift: every product is the same number, so are the
+    results' bits.  (The scale stays below 2^60, the queries above bf16's smallest normal number.)"""
+    import torch
+    rng = np.random.default_rng([D, Hq, shift])
+    T, blocks, cfg = 200, 13, lk.pos_cfg_from("rope", D)
+    t = np.arange(T)
+    cache = torch.full(lk.q4_cache_shape(blocks, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+    k = (_tensor(_bf(rng, T, Hkv, D)).float() * 256).to(torch.bfloat16)
+    lk.kv_write_q4(k, _tensor(_bf(rng, T, Hkv, D)), _i32(t), _i32(t), cache, cfg)
+    _, meta, _, _, _ = lk.build_doc_meta([0, 0], [], [], [0], [], [T], [0, blocks], t[:blocks], blocks)
+    md = _dev(meta.view(np.int64))
+    q = _tensor(_bf(rng, T, Hq, D))
+    res = []
+    for s in (0, shift):
+        x = (q.float() * 2.0 ** -s).to(torch.bfloat16)
+        scale = 2.0 ** (s - 11)
+        out, lse = torch.empty_like(q), torch.empty((T, Hq), device="cuda")
+        lk.attn_prefill_q4(x, _i32([0, T]), _i32([0]), _i32([0]), md, cache, cfg, out, T, lse=lse, scale=scale,
+                           ws=_ws(lk, lk.PHASE_PREFILL_Q4, T, 1, blocks, Hq, Hkv, D))
+        res.append([out, lse])
+        for n, wide in ((6, md), (6, torch.cat([md, torch.zeros((1, 3000), dtype=torch.int64, device="cuda")], 1))):
+            out, lse = torch.empty_like(q[:n]), torch.empty((n, Hq), device="cuda")
+            lk.attn_decode_q4(x[-n:], _i32(t[-n:] + 1), _i32([0] * n), _i32([0] * n), wide.repeat(n, 1), cache, cfg, out,
+                              lse=lse, scale=scale,
+                              ws=_ws(lk, lk.PHASE_DECODE_Q4, n, n, wide.shape[1], Hq, Hkv, D))
+            res[-1] += [out, lse]
+    _clean(lk)
+    assert (res[0][1] - torch.log(_dev(t + 1.0))[:, None]).abs().max() > 0.3  # the logits do not vanish
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 2), (32, 1)])
+@pytest.mark.parametrize("scale", [2.0 ** -59, 2.0 ** -11, 2.0 ** 59])
+def test_queries_next_to_zero(lk, Hq, Hkv, scale):
+    """Rows of zeros, of subnormal numbers and of bf16's smallest normal ones: the logits vanish under every
+    scale that is accepted, so each visible key weighs the same.  2^-8 for the output's rounding and 2^-10
+    of the mean magnitude for the weights'."""
+    import torch
+    D, T, blocks, cfg = 128, 100, 7, lk.pos_cfg_from("rope", 128)
+    rng = np.random.default_rng(Hq)
+    t = np.arange(T)
+    cache = torch.full(lk.q4_cache_shape(blocks, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+    lk.kv_write_q4(_tensor(_bf(rng, T, Hkv, D)), _tensor(_bf(rng, T, Hkv, D)), _i32(t), _i32(t), cache, cfg)
+    vv = lo.bf16_bits_to_f64(q4.load(cache.cpu().numpy(), D)[1]).transpose(0, 2, 1, 3).reshape(-1, Hkv, D)[:T]
+    want = np.cumsum(vv, 0) / (t + 1.0)[:, None, None]
+    mag = np.cumsum(np.abs(vv), 0) / (t + 1.0)[:, None, None]
+    _, meta, _, _, _ = lk.build_doc_meta([0, 0], [], [], [0], [], [T], [0, blocks], t[:blocks], blocks)
+    md = _dev(meta.view(np.int64))
+    for top in (0.0, 2.0 ** -130, 2.0 ** -126):
+        x = (_tensor(_bf(rng, T, Hq, D)).sign().double() * top).to(torch.bfloat16)
+        assert float(x.abs().max()) == top
+        out, lse = torch.empty_like(x), torch.empty((T, Hq), device="cuda")
+        lk.attn_prefill_q4(x, _i32([0, T]), _i32([0]), _i32([0]), md, cache, cfg, out, T, lse=lse, scale=scale,
+                           ws=_ws(lk, lk.PHASE_PREFILL_Q4, T, 1, blocks, Hq, Hkv, D))
+        one, lone = torch.empty_like(x[-1:]), torch.empty((1, Hq), device="cuda")
+        lk.attn_decode_q4(x[-1:], _i32([T]), _i32([0]), _i32([0]), md, cache, cfg, one, lse=lone, scale=scale,
+                          ws=_ws(lk, lk.PHASE_DECODE_Q4, 1, 1, blocks, Hq, Hkv, D))
+        _clean(lk)
+        for got, l, rows in ((out, lse, slice(None)), (one, lone, slice(T - 1, T))):
+            w, a = (np.repeat(z[rows], Hq // Hkv, 1) for z in (want, mag))
+            err = np.abs(got.float().cpu().numpy() - w)
+            assert (err <= 2.0 ** -8 * np.abs(w) + 2.0 ** -10 * a + 1e-30).all()
+            np.testing.assert_allclose(l.cpu().numpy(), np.log(t[rows] + 1.0)[:, None].repeat(Hq, 1), atol=1e-5)
