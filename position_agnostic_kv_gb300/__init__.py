@@ -292,9 +292,9 @@ _torch = None  # torch and what the 4-bit calls look up of it, bound by the firs
 def _bind_torch():
     global _torch, _BF16, _I32, _I64, _F32, _U8, _raw_stream, _device_index
     import torch
-    _torch = torch
     _BF16, _I32, _I64, _F32, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8
     _raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _torch = torch  # last: another thread that sees it set uses the others
 
 
 def _q4_refuse(what, tensors):
