@@ -2,7 +2,8 @@
 
 Where two calls compute the same numbers (a table at another address, a looser bound on the query
 lengths, values that a row does not see, operands scaled by powers of two) their results are
-compared bit for bit.
+compared bit for bit; bytes of the cache are compared with the numpy restatement of the format
+(tests/q4_reference.py).
 """
 import numpy as np
 import pytest
@@ -10,7 +11,7 @@ import pytest
 from oracle import lazy_oracle as lo
 from tests import q4_reference as q4
 from tests.gpu_common import lib
-from tests.test_gpu_q4 import POISON, _bf, _clean, _dev, _i32, _tensor, _ws
+from tests.test_gpu_q4 import POISON, _bf, _bits, _clean, _dev, _i32, _tensor, _ws
 from workloads import alibi_slopes_input
 
 pytestmark = pytest.mark.gpu
@@ -257,3 +258,76 @@ def test_queries_next_to_zero(lk, Hq, Hkv, scale):
             err = np.abs(got.float().cpu().numpy() - w)
             assert (err <= 2.0 ** -8 * np.abs(w) + 2.0 ** -10 * a + 1e-30).all()
             np.testing.assert_allclose(l.cpu().numpy(), np.log(t[rows] + 1.0)[:, None].repeat(Hq, 1), atol=1e-5)
+
+
+# ------------------------------------------------------------------ calls large enough for several heads per thread
+def _store_all(cache, slots, k, v):
+    """q4_reference.store for many tokens at once."""
+    D = k.shape[-1]
+    kc, ks, vc, vs = q4.offsets(D)
+    p, r, h = (slots // 16)[:, None, None], slots % 16, np.arange(k.shape[1])[None, :, None]
+    for x, co, so in ((k, kc, ks), (v, vc, vs)):
+        code, scale = q4.quantise(x)
+        cache[p, h, co[r][:, None, 0::2]] = code[..., 0::2] | (code[..., 1::2] << 4)
+        cache[p, h, so[r][:, None, ::16]] = scale
+
+
+def _tokens(Hkv, D, per_sm, dims):
+    """Tokens that give each SM `per_sm` threads of `dims` dimensions and a head, and a few more."""
+    import torch
+    n = torch.cuda.get_device_properties(0).multi_processor_count * per_sm
+    return -(-n // (Hkv * (D // dims))) + 13
+
+
+@pytest.mark.parametrize("D,Hkv", [(128, 8), (128, 3), (64, 5), (64, 8), (128, 1), (64, 2)])
+@pytest.mark.parametrize("rotate", [True, False])
+def test_write_of_many_tokens_is_bit_exact(lk, D, Hkv, rotate):
+    """Four heads per thread from 2048 threads per SM on, head counts that are no multiple of four, and
+    some bad slots among them."""
+    import torch
+    T, n = _tokens(Hkv, D, 2048, 16), 1500
+    rng = np.random.default_rng([D, Hkv, rotate])
+    pages = T // 16 + 3
+    slots, lp = rng.permutation(16 * pages)[:T], rng.integers(0, n, T)
+    k, v = _bf(rng, T, Hkv, D), _bf(rng, T, Hkv, D)
+    kf = lo.bf16_bits_to_f64(k)
+    cfg = lk.pos_cfg_from("none", D)
+    if rotate:
+        table = torch.empty((n, D), dtype=torch.float32, device="cuda")
+        lk.build_rope_table(lk.pos_cfg_from("rope", D), n, table)
+        cfg = lk.pos_cfg_from("rope", D, cos_sin=table)
+        kf = q4.rotate_f32(kf, lp, table.cpu().numpy(), False)
+    bad = rng.choice(T, 9, replace=False)
+    given = slots.copy()
+    given[bad] = rng.choice([-1, 16 * pages, 2 ** 31 - 1], 9)
+    cache = torch.full(lk.q4_cache_shape(pages, Hkv, D), POISON, dtype=torch.uint8, device="cuda")
+    lk.kv_write_q4(_tensor(k), _tensor(v), _i32(given), _i32(lp), cache, cfg)
+    assert lk.device_status() == 2  # LAZY_STATUS_BAD_SLOT
+    ref = np.full(cache.shape, POISON, np.uint8)
+    ok = np.setdiff1d(np.arange(T), bad)
+    _store_all(ref, slots[ok], kf[ok], lo.bf16_bits_to_f64(v[ok]))
+    np.testing.assert_array_equal(cache.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("D,Hkv", [(128, 8), (128, 3), (64, 5), (64, 8), (128, 1)])
+def test_read_of_many_tokens_is_exact(lk, D, Hkv):
+    """Two heads per thread from 4096 threads per SM on, odd head counts, some bad slots (rows that stay)."""
+    import torch
+    T = _tokens(Hkv, D, 4096, 8)
+    rng = np.random.default_rng([D, Hkv])
+    pages = 300
+    raw = rng.integers(0, 256, (pages, Hkv, 18 * D), dtype=np.uint8)
+    for a, b in ((8 * D, 9 * D), (17 * D, 18 * D)):
+        raw[..., a:b] = np.minimum(raw[..., a:b] & 0x7F, 0x7E)  # no NaN
+    slots = rng.integers(0, 16 * pages, T)
+    bad = rng.choice(T, 9, replace=False)
+    given = slots.copy()
+    given[bad] = rng.choice([-1, 16 * pages, 2 ** 31 - 1], 9)
+    ko = torch.full((T, Hkv, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    vo = ko.clone()
+    lk.kv_read_q4(_i32(given), _dev(raw), ko, vo, k_scale=0.25, v_scale=2.0)
+    assert lk.device_status() == 2  # LAZY_STATUS_BAD_SLOT
+    for got, want in zip((ko, vo), q4.load(raw, D, 0.25, 2.0)):
+        w = lo.bf16_bits_to_f64(want)[slots // 16, :, slots % 16]
+        w[bad] = 7.0
+        np.testing.assert_array_equal(lo.bf16_bits_to_f64(_bits(got)), w)
