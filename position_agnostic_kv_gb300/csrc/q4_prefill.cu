@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_prefill_kernel(const Q4Args a,
           uint32_t any = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) any |= nan_bits(ld_shared_u32(ssrc + k * step) & keep);
-          if (__any_sync(0xffffffffu, any != 0)) {
+          if (any) {
             const int page0 = pstart[slot * kPagesPerTile + ps];
             int* first = const_cast<int*>(nanpos);
 #pragma unroll 1
