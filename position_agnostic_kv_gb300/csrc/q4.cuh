@@ -41,14 +41,7 @@ struct Q4 {
   }
 };
 
-// Two e2m1 codes of a byte (low half first) as two f16; exact.
-__device__ __forceinline__ uint32_t e2m1x2_to_h2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}\n" : "=r"(r) : "r"(byte));
-  return r;
-}
-
-// The eight codes of a word as four f16 pairs.
+// The eight e2m1 codes of a word (low half of a byte first) as four f16 pairs; exact.
 __device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t (&r)[4]) {
   asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
       " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
