@@ -75,4 +75,10 @@ inline bool q4_factor(float f, float* out) {
   return true;
 }
 
+// The kernels compare positions with max_pos as unsigned numbers: a negative one would cover every position.
+inline int q4_check_table(const char* what, const PosParams& pos) {
+  if (pos.max_pos >= 0) return LAZY_OK;
+  return fail(LAZY_EINVAL, "%s: max_pos (%d) must not be negative", what, pos.max_pos);
+}
+
 }  // namespace lazykv

@@ -68,6 +68,7 @@ extern "C" int lazy_attn_decode_q4(const void* q, const int32_t* seq_len, const 
   if (rc) return rc;
   if (B > 0 && !seq_len) return fail(LAZY_EINVAL, "lazy_attn_decode_q4: seq_len is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
+  if (!rc) rc = q4_check_table("lazy_attn_decode_q4", a.pos);
   if (!rc) rc = check_factor("lazy_attn_decode_q4", a.pos.scale_log2, kf);
   if (rc) return rc;
   rc = check_device();
@@ -91,6 +92,7 @@ extern "C" int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const in
   if (rc) return rc;
   if (B > 0 && total_q > 0 && !cu_q) return fail(LAZY_EINVAL, "lazy_attn_prefill_q4: cu_q is NULL");
   rc = prepare_pos(cfg, Hq, D, scale, &a.pos);
+  if (!rc) rc = q4_check_table("lazy_attn_prefill_q4", a.pos);
   if (!rc) rc = check_factor("lazy_attn_prefill_q4", a.pos.scale_log2, kf);
   if (rc) return rc;
   rc = check_device();

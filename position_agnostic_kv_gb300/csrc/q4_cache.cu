@@ -334,6 +334,7 @@ extern "C" int lazy_kv_write_q4(const void* k, const void* v, const int32_t* slo
   if (rc) return rc;
   PosParams pos;
   rc = prepare_pos(cfg, 1, D, 0.f, &pos);
+  if (!rc) rc = q4_check_table("lazy_kv_write_q4", pos);
   if (rc) return rc;
   const bool rotate = pos.kind == kRope || pos.kind == kYarn;
   if (rotate && T > 0 && !local_pos) return fail(LAZY_EINVAL, "lazy_kv_write_q4: local_pos is NULL");

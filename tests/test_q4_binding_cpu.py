@@ -1,7 +1,9 @@
-"""CPU tests of the 4-bit calls' Python binding."""
+"""CPU tests of the 4-bit calls: the Python binding, and refusals of positional tables."""
 import sys
 
 import pytest
+
+from tests.test_q4_cpu import _Args
 
 
 @pytest.fixture(scope="module")
@@ -35,3 +37,18 @@ def test_first_calls_of_two_threads(lk, monkeypatch):
     assert lk._torch is not None and all(hasattr(lk, n) for n in names)
     lk._bind_torch()
     assert lk._torch is torch
+
+
+@pytest.mark.parametrize("what", ["write", "decode", "prefill"])
+def test_a_table_of_a_negative_number_of_rows_is_refused(lk, what):
+    a = _Args(lk)
+    a.cfg.cos_sin, a.cfg.max_pos = a.p, -1
+    assert a.call(what) == -1
+    assert "max_pos" in lk.lib.lazy_last_error().decode()
+    a.cfg.max_pos = 0  # no rows: angles on the fly
+    a.call(what, D=96)
+    assert "head_dim" in lk.lib.lazy_last_error().decode()
+    a.cfg.cos_sin, a.cfg.max_pos = None, -1  # without a table it says nothing
+    import torch
+    if not torch.cuda.is_available():
+        assert a.call(what) in (-3, -4)
