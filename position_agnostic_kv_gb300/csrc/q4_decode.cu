@@ -5,13 +5,14 @@
 //   S^T [16 keys x 8] = K [16 x D] (R_{m - Delta} q)^T,   O^T [D x 8] += V^T [D x 16] P^T [16 x 8]
 // with an online softmax in base 2 between them.  Both products run on 16x8x16 f16 matrix
 // instructions whose 16-row operand (K rows, V columns) is dequantised into registers: a tile of a
-// decode step has 8 rows of queries, so the 128-row tcgen05 tiles would be nearly empty, and their
+// decode step has up to 8 rows of queries here, so the 128-row tcgen05 tiles would be nearly empty, and their
 // operands would cross shared memory once more (2 x 2 bytes per value against 0.56 loaded).
 //  * The cache block is laid out in fragment order (q4.cuh), so a page is four 16-byte shared loads
 //    per lane plus two scale words, all without bank conflicts.
 //  * A code times its e4m3 scale is exact in f16.  q is normalised per head by a power of two and
-//    split in two f16 (hi + lo), so the scores carry fp32 accuracy.  Groups of at most 4 heads put hi
-//    in columns 0-3 and lo in columns 4-7 of one instruction; groups of 8 use two instructions.
+//    split in two f16 (hi + lo), 22 bits of the row's largest value; without a cos/sin table the angles'
+//    sine and cosine are good to about 2^-20 (turn_sincos_fast).  Groups of at most 4 heads put hi in columns 0-3
+//    and lo in columns 4-7 of one instruction; groups of 8 use two instructions.
 //  * With at most 4 heads the two pages of a step share one softmax: the hi and lo parts are added so that
 //    lanes t < 2 hold the even page's scores and lanes t >= 2 the odd page's, and the columns 0-3 and 4-7 of
 //    O^T accumulate even and odd pages (P's other columns are zeroed), merged in the epilogue.
@@ -646,7 +647,7 @@ Splits q4_splits(int rows, int Hq, int Hkv, int max_blocks) {
 // tile: the matrix instructions here take 8 heads at a time and dequantise every page once for each 8.  In the
 // units above (8 heads) a CTA there takes 45 to start and end, 14 per tile of 128 keys, 35 more for the merge
 // of key splits.  Measured, 64 rows of 16 heads of one KV head: 400 keys 10.5 us here, 12.0 there; 1600 keys 18
-// and 16; 32 rows of 32 heads, 12 000 keys 74 and 32; one row of 16 heads, 1600 keys 8.9 and 11.9.
+// and 16; 32 rows of 32 heads, 12 000 keys 74 and 34; one row of 16 heads, 1600 keys 8.9 and 11.9.
 bool q4_decode_on_tc(int rows, int Hq, int Hkv, int max_blocks) {
   if (Hq / Hkv < 16 || !q4_use_tc(Hq, Hkv)) return false;
   const int S = q4_tc_splits(rows, Hkv, max_blocks), tiles = (max_blocks + 7) / 8;

@@ -32,12 +32,13 @@
 // ~2100 of a tile's ~3800 cycles, the products of both Q tiles 2048, and the two overlap in part (the scores
 // of one Q tile are computed while the other's are waited for).  KH waits for its keys' role.  The packed
 // cache, 18 D / 16 bytes per key and head, comes out of the L2.  8 x 64 queries of 64 heads (8 KV heads) over
-// 10 300 keys: 158 us, 1090 TFLOP/s; 32 x 32 queries of 32 heads of one KV head over 12 000 keys, ALiBi: 221
-// us, 911 TFLOP/s; 16 x 32 queries of 32 heads over 2000 keys (KH): 31 us, 540 TFLOP/s; 1600 tokens of one
+// 10 300 keys: 159 us, 1083 TFLOP/s; 32 x 32 queries of 32 heads of one KV head over 12 000 keys, ALiBi: 223
+// us, 903 TFLOP/s; 16 x 32 queries of 32 heads over 2000 keys (KH): 32 us, 528 TFLOP/s; 1600 tokens of one
 // document: 38 us.
 // Measured and left out: dequantisation of both operands by one warpgroup 232 us (first shape), scores in
 // halves of a tile with two buffers per Q tile 176 (second shape 200), values only in halves 171 (201), an
-// MMA thread per Q tile 229 (291).  Every wait is bounded.
+// MMA thread per Q tile 229 (291).  Replacing NaN scales during the conversion (a minimum per pair) 161 (220)
+// and 33.5 against 34.0 for the decode of wide head groups.  Every wait is bounded.
 #include <cfloat>
 #include <climits>
 
