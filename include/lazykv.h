@@ -285,14 +285,108 @@ int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const int32_t* q_st
                          const lazy_pos_cfg* cfg, void* out, float* lse, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Batches that share documents, and eviction inside a context (bf16 caches).  Slots, block words,
+ * query and workspace conventions are those of the entry points above; so are the status bits and the
+ * return codes.  Arguments are checked before the device is.  cfg->cos_sin is not read: angles come from
+ * exact turn counts.  A negative or non-finite scale is refused, and one that (0: the default 1/sqrt(D),
+ * with YaRN's factor; times log2 e) lies outside [2^-60, 2^60].  Hq / Hkv may be any whole number.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * lazy_attn_decode_shared -- lazy_attn_decode for a batch in which groups of requests list the same first
+ * documents: their common keys are read once per group instead of once per request.
+ *   group_off      (device) int32 [n_groups + 1], not decreasing: requests group_off[g] ..
+ *                  group_off[g+1]-1 form group g; requests outside every group are decoded alone
+ *   shared_blocks  (device) int32 [n_groups]: the first shared_blocks[g] words of the group's lists are the
+ *                  same; document blocks only (at most the doc_blocks of each of its requests).  They are
+ *                  read from the list of the group's first request.
+ *   max_group      upper bound (host) of the groups' sizes
+ *   max_shared     upper bound (host) of shared_blocks; a larger group or value is cut to it (with
+ *                  LAZY_STATUS_BAD_ROW), and what is cut off is decoded alone: the results are the same
+ *   ws             lazy_decode_shared_workspace_size bytes, 256-byte aligned
+ * q, seq_len, q_start, doc_blocks, meta, out and lse as in lazy_attn_decode.  seq_len[b] <= 0 marks an idle
+ * request (a batch padded to a fixed size); it and one without a visible key get out = 0 and lse = -inf.
+ * Common keys are rotated and taken in f16 (as in lazy_attn_prefill: magnitudes above 65504 overflow).
+ */
+int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, const int32_t* q_start,
+                            const int32_t* doc_blocks, const uint64_t* meta, const int32_t* group_off,
+                            const int32_t* shared_blocks, int n_groups, int max_group, int max_shared, int B,
+                            int max_blocks, const void* k_cache, const void* v_cache, int num_pages, int Hq,
+                            int Hkv, int D, float scale, const lazy_pos_cfg* cfg, void* out, float* lse,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of a lazy_attn_decode_shared call with these sizes (query it with the device that
+ * will run the call current). */
+size_t lazy_decode_shared_workspace_size(int B, int n_groups, int max_group, int max_shared, int max_blocks,
+                                         int Hq, int Hkv, int D);
+
+/*
+ * lazy_attn_key_weights -- the attention weight that every cached key receives:
+ *   weights[b][16 j + t] (+)= sum over query rows i and heads h of exp(scale q_ih . R k - lse_ih)
+ * for the key in row t of the request's j-th block, over the rows that see it.
+ *   q        (device) bf16 [total_q][Hq][D] raw queries; rows cu_q[b] .. cu_q[b+1] are the last tokens of
+ *            request b, the last of them at position seq_len[b] - 1 (a decode step: cu_q[b] = b; a prefill:
+ *            its own cu_q, and seq_len from lazy_build_doc_meta)
+ *   lse      (device) float [total_q][Hq], from the attention call over the same list
+ *   max_q    upper bound (host) of the rows of a request
+ *   window   > 0: only the last `window` rows of each request count; 0: all of them
+ *   accumulate  0: weights is written, 0 where no key lies; 1: added to
+ *   weights  (device) float [B][16 max_blocks]
+ *   ws       lazy_workspace_size(LAZY_PHASE_KEY_WEIGHTS, ...) bytes, 256-byte aligned
+ * A row with lse = -inf (nothing visible) counts nothing.  Sums are in fp32, in a fixed order: two calls
+ * give the same bits.
+ */
+int lazy_attn_key_weights(const void* q, const float* lse, const int32_t* cu_q, const int32_t* seq_len,
+                          const int32_t* q_start, const int32_t* doc_blocks, const uint64_t* meta, int B,
+                          int max_blocks, int total_q, int max_q, int window, const void* k_cache,
+                          int num_pages, int Hq, int Hkv, int D, float scale, const lazy_pos_cfg* cfg,
+                          int accumulate, float* weights, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lazy_evict_plan -- which document keys of each request stay, and where they go.  A stored key carries its
+ * rotation by its position in the document and attention adds the document's, so a key may move to any row
+ * of a page with the same Delta: keys that stay are packed document by document into new pages, in order,
+ * and keep their positions.  (With ALiBi the position is the row's: refused.)
+ *   weights    (device) float [B][16 max_blocks], as lazy_attn_key_weights leaves them
+ *   keep       (device) int32 [B]: document keys to keep; < 0 leaves the request's list as it is (nothing to
+ *              move).  The first `first` and the last `recent` document keys go before all others, then the
+ *              largest weights (NaN last); among equals the one that is earlier in the list.
+ *   dst_pages  (device) int32 [B][max_dst]: pages for the kept keys, none of them in a list of this call.  A
+ *              document with n kept keys takes ceil(n / 16) of them; keep / 16 + its number of documents
+ *              always suffice.  Where they do not, or a page lies outside [0, num_pages), the status gets
+ *              LAZY_STATUS_BAD_PAGE and the block's word is left without keys.
+ *   new_meta   (device, written) uint64 [B][max_blocks]: the new list, kept keys first, then the query
+ *              segment's blocks (all words from doc_blocks[b] on); the rest 0
+ *   new_doc_blocks  (device, written) int32 [B];  seq_len and q_start stay valid
+ *   src_slot, dst_slot  (device, written) int32 [B][16 max_dst]: rows to move (lazy_kv_move), -1 where none
+ *   new_weights  (device, written) float [B][16 max_blocks]: the weights in the new list's order
+ * A document is a run of blocks with one Delta.  meta and weights are only read.
+ */
+int lazy_evict_plan(const float* weights, const uint64_t* meta, const int32_t* doc_blocks,
+                    const int32_t* keep, int first, int recent, const int32_t* dst_pages, int max_dst, int B,
+                    int max_blocks, int num_pages, const lazy_pos_cfg* cfg, uint64_t* new_meta,
+                    int32_t* new_doc_blocks, int32_t* src_slot, int32_t* dst_slot, float* new_weights,
+                    void* stream);
+
+/*
+ * lazy_kv_move -- copy T rows of the caches: keys and values of slot src_slot[i] to dst_slot[i], every head,
+ * bit for bit (eviction, or a private copy of a page that several requests share).  Entries with a
+ * negative source or destination are skipped; one outside the caches sets LAZY_STATUS_BAD_SLOT and is
+ * skipped.  Destinations must be distinct, and none may be a source of the same call.
+ */
+int lazy_kv_move(const int32_t* src_slot, const int32_t* dst_slot, int T, int Hkv, int D, void* k_cache,
+                 void* v_cache, int num_pages, void* stream);
+
 #define LAZY_PHASE_DECODE 0
 #define LAZY_PHASE_PREFILL 1
 #define LAZY_PHASE_DECODE_Q4 2
 #define LAZY_PHASE_PREFILL_Q4 3
+#define LAZY_PHASE_KEY_WEIGHTS 4
 
 /*
  * lazy_workspace_size -- bytes of workspace the given call needs (0 if none); phase is one of the
- * LAZY_PHASE_* above.  rows = B for decode, total_q for prefill.  Uses the current device's SM count, so query it
+ * LAZY_PHASE_* above.  rows = B for decode, total_q for prefill and key weights.  Uses the current device's SM count, so query it
  * with the device that will run the call current.
  */
 size_t lazy_workspace_size(int phase, int rows, int B, int max_blocks, int Hq, int Hkv, int D);

@@ -8,7 +8,9 @@ this package raises.
 
 Functions mirror the C entry points: ``build_doc_meta`` (host), ``build_rope_table``,
 ``kv_write``, ``attn_decode``, ``attn_prefill``, ``workspace_size``, ``device_status``; over a
-4-bit cache ``kv_write_q4``, ``kv_read_q4``, ``attn_decode_q4``, ``attn_prefill_q4``.
+4-bit cache ``kv_write_q4``, ``kv_read_q4``, ``attn_decode_q4``, ``attn_prefill_q4``; for batches that
+share documents ``attn_decode_shared``; for eviction inside a context ``attn_key_weights``,
+``evict_plan``, ``kv_move``.
 """
 from __future__ import annotations
 
@@ -21,17 +23,19 @@ __all__ = ["LIB_PATH", "lib", "PosCfg", "LazyError", "DocCache", "POS_ROPE", "PO
            "POS_NONE", "PHASE_DECODE", "PHASE_PREFILL", "EXPORTED_SYMBOLS", "build_doc_meta",
            "build_rope_table", "kv_write", "attn_decode", "attn_decode_noalloc", "attn_prefill", "workspace_size",
            "device_status", "pos_cfg_from", "PHASE_DECODE_Q4", "PHASE_PREFILL_Q4", "q4_cache_shape", "kv_write_q4",
-           "kv_read_q4", "attn_decode_q4", "attn_prefill_q4"]
+           "kv_read_q4", "attn_decode_q4", "attn_prefill_q4", "PHASE_KEY_WEIGHTS", "attn_decode_shared",
+           "decode_shared_workspace_size", "attn_key_weights", "evict_plan", "kv_move"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblazykv.so")
 POS_ROPE, POS_YARN, POS_ALIBI, POS_NONE = 0, 1, 2, 3
-PHASE_DECODE, PHASE_PREFILL, PHASE_DECODE_Q4, PHASE_PREFILL_Q4 = 0, 1, 2, 3
+PHASE_DECODE, PHASE_PREFILL, PHASE_DECODE_Q4, PHASE_PREFILL_Q4, PHASE_KEY_WEIGHTS = 0, 1, 2, 3, 4
 EXPORTED_SYMBOLS = ("lazy_build_doc_meta", "lazy_build_rope_table", "lazy_kv_write",
                     "lazy_attn_decode", "lazy_attn_decode_noalloc", "lazy_attn_prefill", "lazy_workspace_size",
                     "lazy_device_status", "lazy_last_error", "lazy_version", "lazy_doc_cache_create",
                     "lazy_doc_cache_destroy", "lazy_doc_cache_lookup", "lazy_doc_cache_acquire",
                     "lazy_doc_cache_release", "lazy_doc_cache_stats", "lazy_kv_write_q4", "lazy_kv_read_q4",
-                    "lazy_attn_decode_q4", "lazy_attn_prefill_q4")
+                    "lazy_attn_decode_q4", "lazy_attn_prefill_q4", "lazy_attn_decode_shared",
+                    "lazy_decode_shared_workspace_size", "lazy_attn_key_weights", "lazy_evict_plan", "lazy_kv_move")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -73,6 +77,13 @@ _sig = {
                             ctypes.c_float, ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
     "lazy_attn_prefill_q4": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float,
                              ctypes.c_float, ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
+    "lazy_attn_decode_shared": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _I, _I,
+                                ctypes.c_float, ctypes.POINTER(PosCfg), _P, _P, _P, _SZ, _P],
+    "lazy_decode_shared_workspace_size": [_I, _I, _I, _I, _I, _I, _I, _I],
+    "lazy_attn_key_weights": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I,
+                              ctypes.c_float, ctypes.POINTER(PosCfg), _I, _P, _P, _SZ, _P],
+    "lazy_evict_plan": [_P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, ctypes.POINTER(PosCfg), _P, _P, _P, _P, _P, _P],
+    "lazy_kv_move": [_P, _P, _I, _I, _I, _P, _P, _I, _P],
     "lazy_workspace_size": [_I, _I, _I, _I, _I, _I, _I],
     "lazy_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],
     "lazy_last_error": [],
@@ -83,6 +94,7 @@ for _name, _args in _sig.items():
     _f.argtypes = _args
     _f.restype = _I
 lib.lazy_workspace_size.restype = _SZ
+lib.lazy_decode_shared_workspace_size.restype = _SZ
 lib.lazy_last_error.restype = ctypes.c_char_p
 _LL = ctypes.POINTER(ctypes.c_longlong)
 _IP = ctypes.POINTER(ctypes.c_int)
@@ -434,6 +446,151 @@ def attn_prefill_q4(q, cu_q, q_start, doc_blocks, meta, kv_cache, cfg: PosCfg, o
         _bind_torch()
     _q4_attn("attn_prefill_q4", lib.lazy_attn_prefill_q4, q, cu_q, meta.shape[0] + 1, q_start, doc_blocks, meta,
              kv_cache, cfg, out, lse, ws, (q.shape[0], max_q), scale, k_scale, v_scale, stream)
+
+
+# ------------------------------------------------------------------ shared lists and eviction
+def _ws_arg(what, ws, like):
+    if ws is None:
+        return None, 0
+    if ws.dtype is not _U8 or ws.get_device() != like.get_device() or not ws.is_contiguous():
+        _q4_refuse(what, (("q", like, like.dtype, like.shape), ("ws", ws, _U8, ws.shape)))
+    return ws.data_ptr(), ws.numel()
+
+
+def decode_shared_workspace_size(B: int, n_groups: int, max_group: int, max_shared: int, max_blocks: int, Hq: int,
+                                 Hkv: int, D: int) -> int:
+    """Bytes of workspace of an ``attn_decode_shared`` call with these sizes."""
+    return int(lib.lazy_decode_shared_workspace_size(B, n_groups, max_group, max_shared, max_blocks, Hq, Hkv, D))
+
+
+def attn_decode_shared(q, seq_len, q_start, doc_blocks, meta, group_off, shared_blocks, max_group: int,
+                       max_shared: int, k_cache, v_cache, cfg: PosCfg, out, lse=None, ws=None, scale: float = 0.0,
+                       stream=None):
+    """``attn_decode`` for a batch in which requests group_off[g] .. group_off[g+1]-1 list the same first
+    shared_blocks[g] document blocks: their keys are read once per group.  ``max_group`` and ``max_shared``
+    are upper bounds of the groups' sizes and of shared_blocks; ``ws`` (uint8) holds at least
+    ``decode_shared_workspace_size(...)`` bytes."""
+    if _torch is None:
+        _bind_torch()
+    what = "attn_decode_shared"
+    shape, words, cache = q.shape, meta.shape, k_cache.shape
+    B, Hq, D = shape
+    dev, n = q.get_device(), shared_blocks.shape[0] if shared_blocks.dim() == 1 else -1
+    if not (dev >= 0 and q.dtype is _BF16 and out.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+            and seq_len.dtype is _I32 and q_start.dtype is _I32 and doc_blocks.dtype is _I32 and meta.dtype is _I64
+            and group_off.dtype is _I32 and shared_blocks.dtype is _I32 and out.shape == shape
+            and seq_len.shape == (B,) and q_start.shape == (B,) and doc_blocks.shape == (B,) and len(words) == 2
+            and words[0] == B and group_off.shape == (n + 1,) and len(cache) == 4 and cache[2:] == (16, D)
+            and v_cache.shape == cache and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and seq_len.is_contiguous() and q_start.is_contiguous()
+            and doc_blocks.is_contiguous() and meta.is_contiguous() and group_off.is_contiguous()
+            and shared_blocks.is_contiguous() and dev == out.get_device() == k_cache.get_device()
+            == v_cache.get_device() == seq_len.get_device() == q_start.get_device() == doc_blocks.get_device()
+            == meta.get_device() == group_off.get_device() == shared_blocks.get_device()
+            and (lse is None or (lse.dtype is _F32 and lse.shape == (B, Hq) and lse.is_contiguous()
+                                 and lse.get_device() == dev))):
+        pages = (cache[0], cache[1], 16, D)
+        _q4_refuse(what, (("q", q, _BF16, shape), ("seq_len", seq_len, _I32, (B,)), ("q_start", q_start, _I32, (B,)),
+                          ("doc_blocks", doc_blocks, _I32, (B,)), ("meta", meta, _I64, (B, words[-1])),
+                          ("shared_blocks", shared_blocks, _I32, (max(n, 0),)),
+                          ("group_off", group_off, _I32, (max(n, 0) + 1,)), ("k_cache", k_cache, _BF16, pages),
+                          ("v_cache", v_cache, _BF16, pages), ("out", out, _BF16, shape), ("lse", lse, _F32, shape[:2])))
+    wsp, wsb = _ws_arg(what, ws, q)
+    _q4_run(lib.lazy_attn_decode_shared, what, dev, stream, q.data_ptr(), seq_len.data_ptr(), q_start.data_ptr(),
+            doc_blocks.data_ptr(), meta.data_ptr(), group_off.data_ptr(), shared_blocks.data_ptr(), n, max_group,
+            max_shared, B, words[1], k_cache.data_ptr(), v_cache.data_ptr(), cache[0], Hq, cache[1], D, scale,
+            ctypes.byref(cfg), out.data_ptr(), None if lse is None else lse.data_ptr(), wsp, wsb)
+
+
+def attn_key_weights(q, lse, cu_q, seq_len, q_start, doc_blocks, meta, k_cache, cfg: PosCfg, weights, max_q: int,
+                     window: int = 0, accumulate: bool = False, ws=None, scale: float = 0.0, stream=None):
+    """The attention weight that every key of the lists receives, in ``weights`` [B, 16 max_blocks] (fp32),
+    written or (``accumulate``) added to.  ``q`` [rows, Hq, D] raw queries with the attention call's ``lse``
+    [rows, Hq]; rows cu_q[b] .. cu_q[b+1] are request b's last tokens, of which the last ``window`` count (0:
+    all).  ``ws`` (uint8) holds at least ``workspace_size(PHASE_KEY_WEIGHTS, ...)`` bytes."""
+    if _torch is None:
+        _bind_torch()
+    what = "attn_key_weights"
+    shape, words, cache = q.shape, meta.shape, k_cache.shape
+    rows, Hq, D = shape
+    B, dev = words[0], q.get_device()
+    if not (dev >= 0 and q.dtype is _BF16 and lse.dtype is _F32 and weights.dtype is _F32 and k_cache.dtype is _BF16
+            and cu_q.dtype is _I32 and seq_len.dtype is _I32 and q_start.dtype is _I32 and doc_blocks.dtype is _I32
+            and meta.dtype is _I64 and lse.shape == (rows, Hq) and cu_q.shape == (B + 1,) and seq_len.shape == (B,)
+            and q_start.shape == (B,) and doc_blocks.shape == (B,) and len(words) == 2
+            and weights.shape == (B, 16 * words[1]) and len(cache) == 4 and cache[2:] == (16, D) and q.is_contiguous()
+            and lse.is_contiguous() and weights.is_contiguous() and k_cache.is_contiguous() and cu_q.is_contiguous()
+            and seq_len.is_contiguous() and q_start.is_contiguous() and doc_blocks.is_contiguous()
+            and meta.is_contiguous() and dev == lse.get_device() == weights.get_device() == k_cache.get_device()
+            == cu_q.get_device() == seq_len.get_device() == q_start.get_device() == doc_blocks.get_device()
+            == meta.get_device()):
+        _q4_refuse(what, (("q", q, _BF16, shape), ("lse", lse, _F32, (rows, Hq)), ("cu_q", cu_q, _I32, (B + 1,)),
+                          ("seq_len", seq_len, _I32, (B,)), ("q_start", q_start, _I32, (B,)),
+                          ("doc_blocks", doc_blocks, _I32, (B,)), ("meta", meta, _I64, (B, words[-1])),
+                          ("k_cache", k_cache, _BF16, (cache[0], cache[1], 16, D)),
+                          ("weights", weights, _F32, (B, 16 * words[-1]))))
+    wsp, wsb = _ws_arg(what, ws, q)
+    _q4_run(lib.lazy_attn_key_weights, what, dev, stream, q.data_ptr(), lse.data_ptr(), cu_q.data_ptr(),
+            seq_len.data_ptr(), q_start.data_ptr(), doc_blocks.data_ptr(), meta.data_ptr(), B, words[1], rows, max_q,
+            window, k_cache.data_ptr(), cache[0], Hq, cache[1], D, scale, ctypes.byref(cfg), int(bool(accumulate)),
+            weights.data_ptr(), wsp, wsb)
+
+
+def evict_plan(weights, meta, doc_blocks, keep, dst_pages, num_pages: int, cfg: PosCfg, new_meta, new_doc_blocks,
+               src_slot, dst_slot, new_weights, first: int = 0, recent: int = 0, stream=None):
+    """Which document keys of each request stay (the ``first`` and ``recent`` ones, then the largest
+    ``weights``, ``keep`` [B] in all) and where they go: ``new_meta``, ``new_doc_blocks`` and ``new_weights``
+    describe the new list, ``src_slot`` / ``dst_slot`` [B, 16 max_dst] the rows for ``kv_move`` (-1: none).
+    ``dst_pages`` [B, max_dst] names free pages; keep / 16 + the number of documents suffice."""
+    if _torch is None:
+        _bind_torch()
+    what = "evict_plan"
+    words, dst = meta.shape, dst_pages.shape
+    B, dev = words[0], meta.get_device()
+    if len(words) != 2 or len(dst) != 2:
+        raise ValueError(f"{what}: meta must be [B, max_blocks] and dst_pages [B, max_dst], got {tuple(words)}, {tuple(dst)}")
+    keys, slots = (B, 16 * words[1]), (B, 16 * dst[1])
+    if not (dev >= 0 and weights.dtype is _F32 and new_weights.dtype is _F32 and meta.dtype is _I64
+            and new_meta.dtype is _I64 and doc_blocks.dtype is _I32 and keep.dtype is _I32 and dst_pages.dtype is _I32
+            and new_doc_blocks.dtype is _I32 and src_slot.dtype is _I32 and dst_slot.dtype is _I32
+            and weights.shape == keys and new_weights.shape == keys and new_meta.shape == words
+            and doc_blocks.shape == (B,) and keep.shape == (B,) and dst[0] == B and new_doc_blocks.shape == (B,)
+            and src_slot.shape == slots and dst_slot.shape == slots and weights.is_contiguous()
+            and new_weights.is_contiguous() and meta.is_contiguous() and new_meta.is_contiguous()
+            and doc_blocks.is_contiguous() and keep.is_contiguous() and dst_pages.is_contiguous()
+            and new_doc_blocks.is_contiguous() and src_slot.is_contiguous() and dst_slot.is_contiguous()
+            and dev == weights.get_device() == new_weights.get_device() == new_meta.get_device()
+            == doc_blocks.get_device() == keep.get_device() == dst_pages.get_device() == new_doc_blocks.get_device()
+            == src_slot.get_device() == dst_slot.get_device()):
+        _q4_refuse(what, (("meta", meta, _I64, words), ("weights", weights, _F32, keys),
+                          ("doc_blocks", doc_blocks, _I32, (B,)), ("keep", keep, _I32, (B,)),
+                          ("dst_pages", dst_pages, _I32, (B, dst[1])), ("new_meta", new_meta, _I64, words),
+                          ("new_doc_blocks", new_doc_blocks, _I32, (B,)), ("src_slot", src_slot, _I32, slots),
+                          ("dst_slot", dst_slot, _I32, slots), ("new_weights", new_weights, _F32, keys)))
+    _q4_run(lib.lazy_evict_plan, what, dev, stream, weights.data_ptr(), meta.data_ptr(), doc_blocks.data_ptr(),
+            keep.data_ptr(), first, recent, dst_pages.data_ptr(), dst[1], B, words[1], num_pages, ctypes.byref(cfg),
+            new_meta.data_ptr(), new_doc_blocks.data_ptr(), src_slot.data_ptr(), dst_slot.data_ptr(),
+            new_weights.data_ptr())
+
+
+def kv_move(src_slot, dst_slot, k_cache, v_cache, stream=None):
+    """Copy rows of the caches: keys and values of every head from src_slot[i] to dst_slot[i] (int32, any one
+    shape; entries with a negative slot are skipped).  Destinations are distinct and none is a source."""
+    if _torch is None:
+        _bind_torch()
+    cache, slots = k_cache.shape, src_slot.shape
+    dev = k_cache.get_device()
+    if not (dev >= 0 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and src_slot.dtype is _I32
+            and dst_slot.dtype is _I32 and len(cache) == 4 and cache[2] == 16 and v_cache.shape == cache
+            and dst_slot.shape == slots and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and src_slot.is_contiguous() and dst_slot.is_contiguous() and dev == v_cache.get_device()
+            == src_slot.get_device() == dst_slot.get_device()):
+        if len(cache) != 4 or cache[2] != 16:
+            raise ValueError(f"kv_move: k_cache must be [num_pages, Hkv, 16, D], got {tuple(cache)}")
+        _q4_refuse("kv_move", (("k_cache", k_cache, _BF16, cache), ("v_cache", v_cache, _BF16, cache),
+                               ("src_slot", src_slot, _I32, slots), ("dst_slot", dst_slot, _I32, slots)))
+    _q4_run(lib.lazy_kv_move, "kv_move", dev, stream, src_slot.data_ptr(), dst_slot.data_ptr(), src_slot.numel(),
+            cache[1], cache[3], k_cache.data_ptr(), v_cache.data_ptr(), cache[0])
 
 
 def device_status(stream=None) -> int:

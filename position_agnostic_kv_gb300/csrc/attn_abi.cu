@@ -2,6 +2,10 @@
 #include "decode.cuh"
 #include "q4_attn.cuh"
 
+namespace lazykv {
+size_t key_weights_ws_bytes(int B, int Hkv, int max_blocks);
+}
+
 using namespace lazykv;
 
 static int check_common(int B, int max_blocks, int Hq, int Hkv, int D, int num_pages, const void* kc,
@@ -96,7 +100,7 @@ extern "C" int lazy_attn_prefill(const void* q, const int32_t* cu_q, const int32
 }
 
 extern "C" size_t lazy_workspace_size(int phase, int rows, int B, int max_blocks, int Hq, int Hkv, int D) {
-  (void)B;
+  if (phase == LAZY_PHASE_KEY_WEIGHTS) return B > 0 && max_blocks > 0 && Hkv > 0 ? key_weights_ws_bytes(B, Hkv, max_blocks) : 0;
   if (rows <= 0 || max_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return 0;
   if (phase == LAZY_PHASE_DECODE) return decode_ws_bytes(rows, Hq, Hkv, D, max_blocks);
   if (phase == LAZY_PHASE_DECODE_Q4) return q4_ws_bytes(rows, Hq, Hkv, D, max_blocks, false);

@@ -1,0 +1,359 @@
+// Eviction inside a context: the plan (which keys stay, where they go) and the rows' copies.
+//
+// A stored key is R_j k with j its position in the document, and attention applies R_Delta per page: the row
+// a key lies in does not enter.  So keys of one document may move between pages with its Delta as plain row
+// copies, and what attention computes over the keys that stay does not change.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace lazykv {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kWarps = kPlanThreads / 32;
+constexpr uint32_t kProtected = 0xFFFFFFFFu;
+
+// Whole numbers in the order of the weights: NaN lowest (0), then -inf ... +inf (0xFF800000); -0 equals 0.
+__device__ __forceinline__ uint32_t order_of(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct PlanArgs {
+  const float* weights;
+  const uint64_t* meta;
+  const int32_t* doc_blocks;
+  const int32_t* keep;
+  const int32_t* dst_pages;
+  uint64_t* new_meta;
+  int32_t* new_doc_blocks;
+  int32_t* src_slot;
+  int32_t* dst_slot;
+  float* new_weights;
+  uint32_t* status;
+  int first, recent, max_dst, max_blocks, num_pages;
+};
+
+// Where a stretch of blocks leaves the packing: whether a document starts in it, the kept keys before its
+// first start, the new blocks of the documents that begin and end in it, and the kept keys since its last start.
+struct Packed {
+  int starts, head, blocks, tail;
+};
+__device__ __forceinline__ int pages_of(int keys) { return (keys + kPage - 1) / kPage; }
+__device__ __forceinline__ Packed join(Packed a, Packed b) {
+  Packed r;
+  r.starts = a.starts | b.starts;
+  r.head = a.starts ? a.head : a.head + b.head;
+  r.blocks = a.blocks + b.blocks + (a.starts && b.starts ? pages_of(a.tail + b.head) : 0);
+  r.tail = b.starts ? b.tail : a.tail + (a.starts ? b.head : 0);
+  return r;
+}
+__device__ __forceinline__ Packed shfl_up(Packed p, int n) {
+  Packed r;
+  r.starts = __shfl_up_sync(0xffffffffu, p.starts, n);
+  r.head = __shfl_up_sync(0xffffffffu, p.head, n);
+  r.blocks = __shfl_up_sync(0xffffffffu, p.blocks, n);
+  r.tail = __shfl_up_sync(0xffffffffu, p.tail, n);
+  return r;
+}
+
+// Sum over the threads before this one; `total` gets the block's.
+__device__ __forceinline__ int scan_before(int x, int* buf, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) buf[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int w = buf[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    buf[lane] = w;
+  }
+  __syncthreads();
+  total = buf[kWarps - 1];
+  const int r = v - x + (warp ? buf[warp - 1] : 0);
+  __syncthreads();
+  return r;
+}
+
+// One block of threads per request.  Thread t owns a run of consecutive list blocks, so that prefix sums over
+// the threads are prefix sums over the list.  The keep-th largest weight is found digit by digit (8 bits of
+// the ordered value at a time, counts in shared memory); keys above it stay, and as many of its equals as are
+// needed, in list order.
+__global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const PlanArgs a) {
+  __shared__ int hist[256];
+  __shared__ int buf[kWarps];
+  __shared__ Packed pbuf[kWarps];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_left;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const size_t MB = a.max_blocks;
+  const uint64_t* meta = a.meta + b * MB;
+  const float* w = a.weights + b * MB * kPage;
+  uint64_t* new_meta = a.new_meta + b * MB;
+  float* new_w = a.new_weights + b * MB * kPage;
+  const int32_t* pages = a.dst_pages + (size_t)b * a.max_dst;
+  int32_t* src = a.src_slot + (size_t)b * a.max_dst * kPage;
+  int32_t* dst = a.dst_slot + (size_t)b * a.max_dst * kPage;
+  const int nd = min(max(a.doc_blocks[b], 0), a.max_blocks);
+  const int want = a.keep[b];
+  for (int i = tid; i < a.max_dst * kPage; i += kPlanThreads) src[i] = dst[i] = -1;
+  if (want < 0) {
+    for (int i = tid; i < a.max_blocks; i += kPlanThreads) new_meta[i] = meta[i];
+    for (int i = tid; i < a.max_blocks * kPage; i += kPlanThreads) new_w[i] = w[i];
+    if (tid == 0) a.new_doc_blocks[b] = nd;
+    return;
+  }
+
+  const int per = (nd + kPlanThreads - 1) / kPlanThreads;
+  const int beg = min(nd, tid * per), end = min(nd, beg + per);
+  int mine = 0, total;
+  for (int j = beg; j < end; ++j) mine += min(int(word_nvalid(meta[j])), kPage);
+  const int before = scan_before(mine, buf, total);
+  const int keep = min(want, total);
+  auto value = [&](int j, int t, int rank) -> uint32_t {
+    return rank < a.first || rank >= total - a.recent ? kProtected : order_of(w[(size_t)j * kPage + t]);
+  };
+
+  // ---- the keep-th largest value: s_prefix, of which s_left equals stay
+  if (tid == 0) {
+    s_prefix = 0;
+    s_left = keep;
+  }
+  if (keep > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      int rank = before;
+      for (int j = beg; j < end; ++j) {
+        const int nv = min(int(word_nvalid(meta[j])), kPage);
+        for (int t = 0; t < nv; ++t, ++rank) {
+          const uint32_t v = value(j, t, rank);
+          if ((v & mask) == prefix) atomicAdd(&hist[(v >> shift) & 255], 1);
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane l holds digits 255 - 8 l downwards
+        int c[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+        int up = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += y;
+        }
+        int left = s_left - (up - sum);
+        __syncwarp();
+        if (left > 0 && left <= sum) {
+          int i = 0;
+          while (left > c[i]) left -= c[i++];
+          s_prefix = prefix | uint32_t(255 - 8 * lane - i) << shift;
+          s_left = left;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  const uint32_t limit = s_prefix;
+  const int ties = keep > 0 ? s_left : 0;
+
+  // ---- how many equals come before this thread's blocks
+  int same = 0, all_same;
+  {
+    int rank = before;
+    for (int j = beg; j < end; ++j) {
+      const int nv = min(int(word_nvalid(meta[j])), kPage);
+      for (int t = 0; t < nv; ++t, ++rank) same += value(j, t, rank) == limit;
+    }
+  }
+  const int same_before = scan_before(same, buf, all_same);
+
+  // ---- packing: kept keys per document
+  auto walk = [&](auto&& on_start, auto&& on_key, auto&& on_end) {
+    int rank = before, tie = same_before;
+    for (int j = beg; j < end; ++j) {
+      const uint64_t word = meta[j];
+      if (j == 0 || word_delta(meta[j - 1]) != word_delta(word)) on_start();
+      const int nv = min(int(word_nvalid(word)), kPage);
+      for (int t = 0; t < nv; ++t, ++rank) {
+        const uint32_t v = value(j, t, rank);
+        const bool stays = keep > 0 && (v > limit || (v == limit && tie++ < ties));
+        if (stays) on_key(j, t, word);
+      }
+      if (j + 1 == nd || word_delta(meta[j + 1]) != word_delta(word)) on_end(word);
+    }
+  };
+  Packed me = {0, 0, 0, 0};
+  walk([&] {
+    me = join(me, Packed{1, 0, 0, 0});
+  }, [&](int, int, uint64_t) {
+    if (me.starts) ++me.tail; else ++me.head;
+  }, [](uint64_t) {});
+  Packed inc = me;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Packed y = shfl_up(inc, o);
+    if (lane >= o) inc = join(y, inc);
+  }
+  if (lane == 31) pbuf[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    Packed x = pbuf[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Packed y = shfl_up(x, o);
+      if (lane >= o) x = join(y, x);
+    }
+    pbuf[lane] = x;
+  }
+  __syncthreads();
+  Packed pre = shfl_up(inc, 1);
+  if (lane == 0) pre = Packed{0, 0, 0, 0};
+  if (warp > 0) pre = join(pbuf[warp - 1], pre);
+  const Packed whole = pbuf[kWarps - 1];
+  const int nn = whole.blocks + (whole.starts ? pages_of(whole.tail) : 0);  // document blocks of the new list
+
+  // ---- the rest of the new list: the query segment's blocks and weights, and zeros
+  for (int i = tid; i < nn * kPage; i += kPlanThreads) new_w[i] = 0.f;
+  for (int i = tid + nn; i < a.max_blocks; i += kPlanThreads) new_meta[i] = i - nn + nd < a.max_blocks ? meta[i - nn + nd] : 0;
+  for (int i = tid + nn * kPage; i < a.max_blocks * kPage; i += kPlanThreads)
+    new_w[i] = i + (nd - nn) * kPage < a.max_blocks * kPage ? w[i + (nd - nn) * kPage] : 0.f;
+  if (tid == 0) {
+    a.new_doc_blocks[b] = nn;
+    if (a.doc_blocks[b] > a.max_blocks) set_status(a.status, LAZY_STATUS_BAD_ROW);
+  }
+  __syncthreads();
+
+  // ---- kept keys: slots, weights, words
+  int base = pre.blocks, run = pre.tail;  // new blocks before the document, kept keys of it so far
+  if (!pre.starts) base = run = 0;
+  auto put_word = [&](int rows, uint64_t word) {  // of the page that holds the document's kept key `run - 1`
+    const int blk = base + (run - 1) / kPage;
+    const int page = blk < a.max_dst ? pages[blk] : -1;
+    const bool bad = page < 0 || page >= a.num_pages;
+    if (bad) set_status(a.status, LAZY_STATUS_BAD_PAGE);
+    new_meta[blk] = uint64_t(bad ? 0 : rows) | uint64_t((run - 1) / kPage) << 5 | uint64_t(word_delta(word)) << 16 |
+                    uint64_t(bad ? 0 : page) << 40;
+  };
+  walk([&] {
+    base += pages_of(run);
+    run = 0;
+  }, [&](int j, int t, uint64_t word) {
+    const int blk = base + run / kPage, row = run % kPage;
+    ++run;
+    const int page = blk < a.max_dst ? pages[blk] : -1;
+    if (page >= 0 && page < a.num_pages) {
+      src[blk * kPage + row] = int(word_page(word)) * kPage + t;
+      dst[blk * kPage + row] = page * kPage + row;
+      new_w[(size_t)blk * kPage + row] = w[(size_t)j * kPage + t];
+    }
+    if (row == kPage - 1) put_word(kPage, word);
+  }, [&](uint64_t word) {
+    if (run % kPage) put_word(run % kPage, word);
+  });
+}
+
+// A warp copies one row of every head, keys and values: D / 8 lanes to a row, 16 bytes a lane.
+template <int D>
+__global__ void __launch_bounds__(256) kv_move_kernel(const int32_t* __restrict__ src_slot,
+                                                      const int32_t* __restrict__ dst_slot, int T, int Hkv,
+                                                      uint4* k_cache, uint4* v_cache, int num_pages, uint32_t* status) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int LPR = D / 8, HPS = 32 / LPR;  // lanes per row, heads per step
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= T) return;
+  const int from = src_slot[i], to = dst_slot[i];
+  if (from < 0 || to < 0) return;
+  if (from >= num_pages * kPage || to >= num_pages * kPage) {
+    if (lane == 0) set_status(status, LAZY_STATUS_BAD_SLOT);
+    return;
+  }
+  const int h0 = lane / LPR, c = lane % LPR;
+  const size_t at = (size_t)(from / kPage) * Hkv * kPage * LPR + (from % kPage) * LPR + c;
+  const size_t go = (size_t)(to / kPage) * Hkv * kPage * LPR + (to % kPage) * LPR + c;
+  for (int h = h0; h < Hkv; h += HPS) {
+    const uint4 k = k_cache[at + (size_t)h * kPage * LPR], v = v_cache[at + (size_t)h * kPage * LPR];
+    k_cache[go + (size_t)h * kPage * LPR] = k;
+    v_cache[go + (size_t)h * kPage * LPR] = v;
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace lazykv
+
+using namespace lazykv;
+
+extern "C" int lazy_evict_plan(const float* weights, const uint64_t* meta, const int32_t* doc_blocks,
+                               const int32_t* keep, int first, int recent, const int32_t* dst_pages, int max_dst,
+                               int B, int max_blocks, int num_pages, const lazy_pos_cfg* cfg, uint64_t* new_meta,
+                               int32_t* new_doc_blocks, int32_t* src_slot, int32_t* dst_slot, float* new_weights,
+                               void* stream) {
+  const char* what = "lazy_evict_plan";
+  if (B < 0 || max_blocks <= 0 || max_dst <= 0 || num_pages <= 0)
+    return fail(LAZY_EINVAL, "%s: bad sizes (B=%d max_blocks=%d max_dst=%d num_pages=%d)", what, B, max_blocks, max_dst,
+                num_pages);
+  if (first < 0 || recent < 0) return fail(LAZY_EINVAL, "%s: first and recent must not be negative", what);
+  if (num_pages > (1 << 24)) return fail(LAZY_ERANGE, "%s: num_pages above 2^24", what);
+  if (max_blocks > (1 << 26) || max_dst > (1 << 26)) return fail(LAZY_ERANGE, "%s: lists above 2^26 blocks", what);
+  if (!cfg) return fail(LAZY_EINVAL, "%s: pos cfg is NULL", what);
+  if (cfg->kind < LAZY_POS_ROPE || cfg->kind > LAZY_POS_NONE)
+    return fail(LAZY_EINVAL, "%s: unknown positional kind %d", what, cfg->kind);
+  if (cfg->kind == LAZY_POS_ALIBI)
+    return fail(LAZY_EINVAL, "%s: with ALiBi a key's position is its row's, so keys cannot be packed", what);
+  if (B > 0) {
+    if (!weights || !meta || !doc_blocks || !keep || !dst_pages || !new_meta || !new_doc_blocks || !src_slot || !dst_slot ||
+        !new_weights)
+      return fail(LAZY_EINVAL, "%s: NULL pointer", what);
+    if (!aligned(meta, 8) || !aligned(new_meta, 8)) return fail(LAZY_EINVAL, "%s: meta must be 8-byte aligned", what);
+    if (meta == new_meta || weights == new_weights)
+      return fail(LAZY_EINVAL, "%s: the new list and weights cannot take the place of the old", what);
+  }
+  int rc = check_device();
+  if (rc || B == 0) return rc;
+  const PlanArgs a = {weights,  meta,     doc_blocks,  keep,          dst_pages, new_meta, new_doc_blocks, src_slot,
+                      dst_slot, new_weights, status_word(), first,    recent,    max_dst,  max_blocks,     num_pages};
+  LAZY_CUDA_TRY(launch_pdl(evict_plan_kernel, dim3(B), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), a));
+  return LAZY_OK;
+}
+
+extern "C" int lazy_kv_move(const int32_t* src_slot, const int32_t* dst_slot, int T, int Hkv, int D, void* k_cache,
+                            void* v_cache, int num_pages, void* stream) {
+  const char* what = "lazy_kv_move";
+  if (T < 0 || Hkv <= 0 || num_pages <= 0)
+    return fail(LAZY_EINVAL, "%s: bad sizes (T=%d Hkv=%d num_pages=%d)", what, T, Hkv, num_pages);
+  if (D != 64 && D != 128) return fail(LAZY_EINVAL, "%s: head_dim must be 64 or 128, got %d", what, D);
+  if (num_pages > (1 << 24)) return fail(LAZY_ERANGE, "%s: num_pages above 2^24", what);
+  if (T > 0) {
+    if (!src_slot || !dst_slot || !k_cache || !v_cache) return fail(LAZY_EINVAL, "%s: NULL pointer", what);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(LAZY_EINVAL, "%s: caches must be 16-byte aligned", what);
+  }
+  int rc = check_device();
+  if (rc || T == 0) return rc;
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, dim3((T + 7) / 8), dim3(256), 0, static_cast<cudaStream_t>(stream), src_slot, dst_slot, T,
+                      Hkv, static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache), num_pages, status_word());
+  };
+  LAZY_CUDA_TRY(D == 128 ? go(kv_move_kernel<128>) : go(kv_move_kernel<64>));
+  return LAZY_OK;
+}
