@@ -3,7 +3,7 @@
 #include "q4_attn.cuh"
 
 namespace lazykv {
-size_t key_weights_ws_bytes(int B, int Hkv, int max_blocks);
+size_t key_weights_ws_bytes(int rows, int B, int max_blocks, int Hq, int Hkv);
 }
 
 using namespace lazykv;
@@ -100,8 +100,9 @@ extern "C" int lazy_attn_prefill(const void* q, const int32_t* cu_q, const int32
 }
 
 extern "C" size_t lazy_workspace_size(int phase, int rows, int B, int max_blocks, int Hq, int Hkv, int D) {
-  if (phase == LAZY_PHASE_KEY_WEIGHTS) return B > 0 && max_blocks > 0 && Hkv > 0 ? key_weights_ws_bytes(B, Hkv, max_blocks) : 0;
+  if (phase == LAZY_PHASE_KEY_WEIGHTS && rows == 0) rows = 1;
   if (rows <= 0 || max_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return 0;
+  if (phase == LAZY_PHASE_KEY_WEIGHTS) return B > 0 ? key_weights_ws_bytes(rows, B, max_blocks, Hq, Hkv) : 0;
   if (phase == LAZY_PHASE_DECODE) return decode_ws_bytes(rows, Hq, Hkv, D, max_blocks);
   if (phase == LAZY_PHASE_DECODE_Q4) return q4_ws_bytes(rows, Hq, Hkv, D, max_blocks, false);
   if (phase == LAZY_PHASE_PREFILL_Q4) return q4_ws_bytes(rows, Hq, Hkv, D, max_blocks, true);

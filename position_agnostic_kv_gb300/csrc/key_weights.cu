@@ -1,10 +1,23 @@
 // The attention weight that every cached key receives: w_k = sum over query rows i and heads h of
 // 2^(s_ihk - lse_ih), s in base 2.
-#include "share.cuh"
+#include <algorithm>
+#include <climits>
+
+#include "shared_decode.cuh"
+#include "tcgen05.cuh"
 
 namespace lazykv {
 
 namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128, kPagesPerTile = kTile / kPage;  // keys per tile: the rows of a product
+constexpr int kRows = 128;                                  // most query rows per block: its columns
+constexpr int kRowsAlibi = 64;                              // (ALiBi keeps two more numbers per row)
+constexpr int kGroups = 8;                                  // most partial sums of a key and KV head
+constexpr int kThreads = 512, kPrepWarp0 = 8, kProdWarp = 12, kMmaWarp = 13;
+constexpr int kMaxStages = 6, kMaxSlots = kMaxStages + 3, kLse = 4;
 
 struct Args {
   const __nv_bfloat16* q;
@@ -14,75 +27,594 @@ struct Args {
   const int32_t* q_start;
   const int32_t* doc_blocks;
   const uint64_t* meta;
-  const __nv_bfloat16* k_cache;
-  float* part;  // [Hkv][B][16 max_blocks]
+  float* part;  // [groups][Hkv][B][16 max_blocks]
   float* weights;
   uint32_t* status;
-  int B, max_blocks, Hq, Hkv, num_pages, window, accumulate;
+  int B, max_blocks, Hq, Hkv, num_pages, window, accumulate, groups;
+  int rows;             // columns of the Q buffers: query rows per block at most, a multiple of 16
+  int stages;           // K tiles in flight
   PosParams pos;
 };
 
-// One block of 128 threads per (list block, KV head, request): 8 threads to a key.
+// What a request's weights take: its window's rows, the row blocks and their groups, its list.
+struct Request {
+  int nb, docs, n, first, m0;  // visible blocks, document blocks; rows per head, the first of them, its position
+  int R, nrb, size, rgc; // rows per KV head, blocks of `size` rows, groups of row blocks
+};
+__device__ __forceinline__ Request request_of(const Args& a, int b) {
+  Request r;
+  const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
+  r.n = max(0, hi - lo);
+  if (a.window > 0) r.n = min(r.n, a.window);
+  r.nb = visible_blocks(len, a.q_start[b], a.doc_blocks[b], a.max_blocks);
+  r.docs = a.doc_blocks[b];
+  r.first = hi - r.n;
+  r.m0 = len - r.n;
+  r.R = r.nb > 0 ? r.n * (a.Hq / a.Hkv) : 0;
+  r.nrb = (r.R + a.rows - 1) / a.rows;
+  r.size = r.nrb ? ((r.R + r.nrb - 1) / r.nrb + 15) / 16 * 16 : 16;
+  r.nrb = (r.R + r.size - 1) / r.size;
+  r.rgc = min(r.nrb, a.groups);
+  return r;
+}
+// group g covers row blocks [group_start(g), group_start(g + 1))
+__device__ __forceinline__ int group_start(const Request& r, int g) { return int((long long)g * r.nrb / r.rgc); }
+
+enum : int { F_END = 1, F_NEWQ = 2, F_ADD = 4, F_MASK = 8, F_NOP = 16 };
+struct Item {  // one tile of keys against one block of query rows
+  int flags, b, j0, np;            // list blocks j0 .. j0 + np - 1, of one Delta
+  int rows, r0, delta, kvh;        // query rows (of the request's) r0 .. r0 + rows - 1
+  int rg, m0, qn, first;           // group, position of row 0's token, number of the Q operand, its query row
+  int2 page[kPagesPerTile];        // position of the page's first key, keys (0: none)
+};
+
+enum : int {
+  B_META = 0,                      // [slots] item published (1)
+  B_QOK = B_META + kMaxSlots,      // [slots] its Q operand is ready (4: a lane per warp)
+  B_KFULL = B_QOK + kMaxSlots,     // [stages] K landed
+  B_KFREE = B_KFULL + kMaxStages,  // [stages] products with the stage done (commit)
+  B_SFULL = B_KFREE + kMaxStages,  // [2] scores written (commit)
+  B_SFREE = B_SFULL + 2,           // [2] scores read (4)
+  B_QFREE = B_SFREE + 2,           // [2] products with the Q buffer done (commit)
+  B_FINAL = B_QFREE + 2,
+  NBAR
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) weights_kernel(const Args a) {
-  __shared__ float qs[D], qr[D];
-  pdl_wait();
-  pdl_trigger();
-  const int j = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int G = a.Hq / a.Hkv, key = tid / 8, c0 = tid % 8 * (D / 8);
-  const int nb = visible_blocks(a.seq_len[b], a.q_start[b], a.doc_blocks[b], a.max_blocks);
-  float sum = 0.f;
-  if (j < nb) {
-    const uint64_t w = a.meta[(size_t)b * a.max_blocks + j];
-    const int delta = int(word_delta(w)), p = delta + kPage * int(word_pg(w)) + key;
-    const uint32_t page = word_page(w);
-    if (page < uint32_t(a.num_pages)) {
-      const __nv_bfloat16* k = a.k_cache + (((size_t)page * a.Hkv + kvh) * kPage + key) * D + c0;
-      const int hi = a.cu_q[b + 1], n = a.window > 0 ? min(a.window, hi - a.cu_q[b]) : hi - a.cu_q[b];
-      const bool rotary = a.pos.kind == kRope || a.pos.kind == kYarn;
-      const int hr = a.pos.rotary_dim / 2;
-      for (int i = 0; i < n * G; ++i) {
-        const int row = hi - n + i / G, h = kvh * G + i % G, m = a.seq_len[b] - (hi - row);
-        __syncthreads();
-        for (int d = tid; d < D; d += 128) qs[d] = __bfloat162float(a.q[((size_t)row * a.Hq + h) * D + d]);
-        __syncthreads();
-        for (int d = tid; d < D; d += 128) {
-          float y = qs[d];
-          if (rotary && d < 2 * hr) {
-            const int f = a.pos.interleaved ? d / 2 : d % hr, other = a.pos.interleaved ? d ^ 1 : (d < hr ? d + hr : d - hr);
-            float sn, cs;
-            turn_sincos_signed(m - delta, a.pos.turns[f], sn, cs);
-            y = y * cs + (other > d ? -qs[other] : qs[other]) * sn;
-          }
-          qr[d] = y * a.pos.scale_log2;
-        }
-        __syncthreads();
-        float s = 0.f;
-        if (key < int(word_nvalid(w)) && p <= m)
-          for (int e = 0; e < D / 8; ++e) s += __bfloat162float(k[e]) * qr[c0 + e];
-        for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (a.pos.kind == kAlibi) s += a.pos.slopes[h] * 1.4426950408889634f * float(p - m);
-        const float lse = a.lse[(size_t)row * a.Hq + h];
-        if (key < int(word_nvalid(w)) && p <= m && lse != -INFINITY) sum += exp2f(s - lse * 1.4426950408889634f);
-      }
-    } else if (tid == 0) {
-      set_status(a.status, LAZY_STATUS_BAD_PAGE);
-    }
+struct WLayout {
+  static constexpr int TILE = kTile * D * 2, KBLK = kTile * 128;
+  static constexpr int LIMIT = 227 * 1024;
+  __host__ __device__ static constexpr int qbuf(int rows) { return 2 * rows * D * 2; }  // high and low parts
+  __host__ __device__ static constexpr int ring(int rows, bool alibi) { return kLse * rows * 4 * (alibi ? 3 : 1); }
+  __host__ static int smem(int rows, int st, bool alibi) {
+    return st * TILE + 2 * qbuf(rows) + ring(rows, alibi) + (st + 3) * int(sizeof(Item)) + NBAR * 8 + 16;
   }
-  if (tid % 8 == 0) a.part[(((size_t)kvh * a.B + b) * a.max_blocks + j) * kPage + key] = sum;
+  __host__ static int stages(int rows, bool alibi) {  // at least 3 (D 128, 128 rows: 3)
+    int n = kMaxStages;
+    while (smem(rows, n, alibi) > LIMIT) --n;
+    return n;
+  }
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
 }
 
-// Adds the KV heads' parts in order.
-__global__ void __launch_bounds__(256) weights_sum_kernel(const float* __restrict__ part, int Hkv, size_t n,
-                                                          int accumulate, float* __restrict__ weights) {
+__device__ __forceinline__ void split8(const float (&y)[8], uint4& hi, uint4& lo) {
+  uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
+  uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = f2_to_bf2(y[2 * i], y[2 * i + 1]);
+    l[i] = f2_to_bf2(y[2 * i] - bf_lo(h[i]), y[2 * i + 1] - bf_hi(h[i]));
+  }
+}
+__device__ __forceinline__ void unpack8(uint4 u, float (&y)[8]) {
+  y[0] = bf_lo(u.x); y[1] = bf_hi(u.x); y[2] = bf_lo(u.y); y[3] = bf_hi(u.y);
+  y[4] = bf_lo(u.z); y[5] = bf_hi(u.z); y[6] = bf_lo(u.w); y[7] = bf_hi(u.w);
+}
+
+// Where a block's share of the work begins or ends: total work is cut into equal parts in the order request,
+// KV head, group of row blocks, list block; a list block costs one unit per row block.
+struct Place {
+  int b, kvh, rg, page;
+};
+
+template <int D, int POS>
+__global__ void __launch_bounds__(kThreads, 1)
+weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
+  using L = WLayout<D>;
+  constexpr bool kAl = POS == kAlibi;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NS = a.stages, slots = NS + 3, rows = a.rows;
+  const uint32_t QBUF = uint32_t(L::qbuf(rows)), QBLK = uint32_t(rows) * 128, QLO = QBUF / 2;
+  const uint32_t sK = sb, sQ = sb + NS * L::TILE;
+  float* ring = reinterpret_cast<float*>(sm + NS * L::TILE + 2 * QBUF);  // [kLse][rows] lse (ALiBi: and slope, position)
+  Item* items = reinterpret_cast<Item*>(sm + NS * L::TILE + 2 * QBUF + L::ring(rows, kAl));
+  const uint32_t bar0 = smem_u32(items + slots);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(items + slots) + NBAR * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBAR; ++i)
+      mbar_init(BAR(i), (i >= B_QOK && i < B_KFULL) || (i >= B_SFREE && i < B_QFREE) ? 4 : 1);
+    *abort_flag = (sb & 1023u) ? 1 : 0;  // the operands' swizzle goes by addresses
+    if (sb & 1023u) set_status(a.status, LAZY_STATUS_TIMEOUT);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int G = a.Hq / a.Hkv;
+  bool ok = *abort_flag == 0;
+
+  if (warp < 8) {
+    // ============================ weights of every second item: a thread owns a key
+    const int wg = warp >> 2, row = threadIdx.x & 127;  // TMEM lane = key of the tile
+    const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(wg * kRows);
+    for (int i = wg; ok; i += 2) {
+      const bool got = wait_bar(BAR(B_SFULL + wg), uint32_t((i >> 1) & 1), abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, got)) break;
+      const Item& it = items[i % slots];
+      const int flags = it.flags;
+      if (flags & F_END) break;
+      if (!(flags & F_NOP)) {
+        tc_fence_after();
+        const int2 pg = it.page[row / kPage];
+        const int p = pg.x + row % kPage, n16 = (it.rows + 15) / 16;
+        // rows from n0 on see the key
+        const long long see = (long long)(p - it.m0) * G - it.r0;
+        const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
+        const float* lse = ring + (it.qn % kLse) * rows * (kAl ? 3 : 1);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add16 = [&](const uint32_t* s, int c0) {
+          if constexpr (kAl) {
+            const float *sl = lse + rows, *mm = sl + rows;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = fmaf(sl[c0 + e], float(p) - mm[c0 + e], __uint_as_float(s[e])) - lse[c0 + e];
+              acc[e & 3] += c0 + e >= n0 ? ex2(x) : 0.f;
+            }
+          } else if (flags & F_MASK) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = ex2(__uint_as_float(s[e]) - lse[c0 + e]);
+              acc[e & 3] += c0 + e >= n0 ? x : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(lse + c0 + e);
+              acc[0] += ex2(__uint_as_float(s[e]) - l4.x);
+              acc[1] += ex2(__uint_as_float(s[e + 1]) - l4.y);
+              acc[2] += ex2(__uint_as_float(s[e + 2]) - l4.z);
+              acc[3] += ex2(__uint_as_float(s[e + 3]) - l4.w);
+            }
+          }
+        };
+        int c = 0;
+        for (; c + 2 <= n16; c += 2) {
+          uint32_t s[32];
+          tmem_ld32(tS + uint32_t(16 * c), s);
+          tmem_wait_ld();
+          add16(s, 16 * c);
+          add16(s + 16, 16 * c + 16);
+        }
+        if (c < n16) {
+          uint32_t s[16];
+          tmem_ld16(tS + uint32_t(16 * c), s);
+          tmem_wait_ld();
+          add16(s, 16 * c);
+        }
+        if (row < it.np * kPage) {
+          float w = row % kPage < pg.y ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
+          float* to = a.part + ((((size_t)it.rg * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks + it.j0) * kPage + row;
+          if (flags & F_ADD) w += *to;  // this thread's own, of the row block before
+          *to = w;
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_SFREE + wg));
+    }
+  } else if (warp < kProdWarp) {
+    // ============================ Q operands: rows turned by m - Delta, scaled, split into two bf16 numbers
+    const int t = threadIdx.x - kPrepWarp0 * 32;
+    for (int i = 0; ok; ++i) {
+      const int sl = i % slots;
+      bool got = wait_bar(BAR(B_META + sl), uint32_t((i / slots) & 1), abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, got)) break;
+      const Item& it = items[sl];
+      const int flags = it.flags;
+      if (flags & F_NEWQ) {
+        const int qn = it.qn, buf = qn & 1;
+        if (qn >= 2) {
+          got = wait_bar(BAR(B_QFREE + buf), uint32_t(((qn >> 1) - 1) & 1), abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, got)) break;
+        }
+        const int n16 = (it.rows + 15) / 16 * 16, r0 = it.r0, delta = it.delta;
+        float* lse = ring + (qn % kLse) * rows * (kAl ? 3 : 1);
+        for (int n = t; n < n16; n += 128) {
+          const int r = r0 + n, h = it.kvh * G + r % G;
+          float l = INFINITY;  // an empty column weighs nothing
+          if (n < it.rows) {
+            l = a.lse[(size_t)(it.first + r / G) * a.Hq + h] * 1.4426950408889634f;
+            if (l == -INFINITY) l = INFINITY;  // nor does a row that saw nothing
+          }
+          lse[n] = l;
+          if constexpr (kAl) {
+            lse[rows + n] = n < it.rows ? a.pos.slopes[h] * 1.4426950408889634f : 0.f;
+            lse[2 * rows + n] = float(it.m0 + r / G);
+          }
+        }
+        const uint32_t q0 = sQ + uint32_t(buf) * QBUF;
+        auto put = [&](int n, int k, const float (&y)[8]) {  // chunk k (8 dimensions) of column n
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = y[e] * a.pos.scale_log2;
+          uint4 hi, lo;
+          split8(z, hi, lo);
+          const uint32_t at = q0 + uint32_t(k >> 3) * QBLK + swz(n, k & 7);
+          st_shared_v4(at, hi);
+          st_shared_v4(at + QLO, lo);
+        };
+        auto src = [&](int n) {  // query row of column n; null behind the last
+          const int r = r0 + n;
+          return n < it.rows ? reinterpret_cast<const uint4*>(
+                                   a.q + ((size_t)(it.first + r / G) * a.Hq + it.kvh * G + r % G) * D)
+                             : nullptr;
+        };
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (POS == kRope) {  // half-split pairs over the whole head: a thread owns a chunk and its partner
+          constexpr int NC = D / 16, NG = 128 / NC;
+          const int c = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
+          float co[8], sn[8];
+          int token = -1;
+          for (int n = n0; n < min(n0 + per, n16); ++n) {
+            const uint4* s = src(n);
+            float x1[8], x2[8], y1[8], y2[8];
+            unpack8(s ? s[c] : zero, x1);
+            unpack8(s ? s[c + NC] : zero, x2);
+            if ((r0 + n) / G != token) {
+              token = (r0 + n) / G;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) turn_sincos_signed(it.m0 + token - delta, a.pos.turns[8 * c + e], sn[e], co[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y1[e] = x1[e] * co[e] - x2[e] * sn[e];
+              y2[e] = x1[e] * sn[e] + x2[e] * co[e];
+            }
+            put(n, c, y1);
+            put(n, c + NC, y2);
+          }
+        } else {
+          constexpr int NC = D / 8, NG = 128 / NC;
+          const int k = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
+          const int rd = POS == kRopeX ? a.pos.rotary_dim : 0, hr = rd / 2;
+          const bool inter = a.pos.interleaved != 0;
+          for (int n = n0; n < min(n0 + per, n16); ++n) {
+            const uint4* s = src(n);
+            float x[8], y[8];
+            unpack8(s ? s[k] : zero, x);
+            if (8 * k >= rd) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = x[e];
+            } else if (inter) {
+              const int dp = it.m0 + (r0 + n) / G - delta;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float s1, c1;
+                turn_sincos_signed(dp, a.pos.turns[4 * k + e], s1, c1);
+                y[2 * e] = x[2 * e] * c1 - x[2 * e + 1] * s1;
+                y[2 * e + 1] = x[2 * e] * s1 + x[2 * e + 1] * c1;
+              }
+            } else {
+              const int dp = it.m0 + (r0 + n) / G - delta;
+              const bool low = 8 * k < hr;
+              float z[8];
+              unpack8(s ? s[low ? k + hr / 8 : k - hr / 8] : zero, z);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float s1, c1;
+                turn_sincos_signed(dp, a.pos.turns[8 * k + e - (low ? 0 : hr)], s1, c1);
+                y[e] = x[e] * c1 + (low ? -z[e] : z[e]) * s1;
+              }
+            }
+            put(n, k, y);
+          }
+        }
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_QOK + sl));
+      if (flags & F_END) {  // a second one ends the other warpgroup
+        got = wait_bar(BAR(B_META + (i + 1) % slots), uint32_t(((i + 1) / slots) & 1), abort_flag, a.status);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_QOK + (i + 1) % slots));
+        break;
+      }
+    }
+  } else if (warp == kProdWarp) {
+    // ============================ the block's share of the work, item by item: words, TMA
+    long long total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      long long c = 0;
+      if (b0 + lane < a.B) {
+        const Request r = request_of(a, b0 + lane);
+        c = (long long)r.nb * r.nrb * a.Hkv;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      total += c;
+    }
+    auto locate = [&](long long x) -> Place {  // x < total
+      long long base = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        long long c = 0;
+        if (b0 + lane < a.B) {
+          const Request r = request_of(a, b0 + lane);
+          c = (long long)r.nb * r.nrb * a.Hkv;
+        }
+        long long up = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += y;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, x < base + up);
+        if (in) {
+          const int l = __ffs(in) - 1, b = b0 + l;
+          const Request r = request_of(a, b);
+          const long long y = x - base - __shfl_sync(0xffffffffu, up - c, l), one = (long long)r.nb * r.nrb;
+          const long long z = y % one;
+          const int kvh = int(y / one), rb = int(z / r.nb);
+          int g = int((long long)rb * r.rgc / r.nrb);
+          while (group_start(r, g + 1) <= rb) ++g;
+          const int first = group_start(r, g);
+          return {b, kvh, g, int((z - (long long)first * r.nb) / (group_start(r, g + 1) - first))};
+        }
+        base += __shfl_sync(0xffffffffu, up, 31);
+      }
+      return {a.B, 0, 0, 0};
+    };
+    const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+    Place at = {a.B, 0, 0, 0}, end = at;
+    if (x0 < x1) {
+      at = locate(x0);
+      if (x1 < total) end = locate(x1);
+    }
+    int i = 0, qn = -1, last_real = -1;
+    auto slot_free = [&](int j) -> bool {  // item j's stage and slot
+      if (j < NS) return true;
+      const bool got = wait_bar(BAR(B_KFREE + j % NS), uint32_t((j / NS - 1) & 1), abort_flag, a.status);
+      return __all_sync(0xffffffffu, got);
+    };
+    auto bare = [&](int flags) -> bool {  // an item without a product
+      if (!slot_free(i)) return false;
+      if (lane == 0) {
+        items[i % slots].flags = flags;
+        mbar_arrive(BAR(B_META + i % slots));
+      }
+      __syncwarp();
+      ++i;
+      return true;
+    };
+    auto before = [](const Place& p, const Place& e) {
+      return p.b != e.b ? p.b < e.b : p.kvh != e.kvh ? p.kvh < e.kvh : p.rg != e.rg ? p.rg < e.rg : p.page < e.page;
+    };
+    while (ok && before(at, end)) {
+      const Request r = request_of(a, at.b);
+      if (r.R == 0) {
+        at = {at.b + 1, 0, 0, 0};
+        continue;
+      }
+      const bool same = at.b == end.b && at.kvh == end.kvh && at.rg == end.rg;
+      const int p1 = same ? end.page : r.nb, rb0 = group_start(r, at.rg), rb1 = group_start(r, at.rg + 1);
+      const uint64_t* words = a.meta + (size_t)at.b * a.max_blocks;
+      for (int rb = rb0; rb < rb1 && ok; ++rb) {
+        const int r0 = rb * r.size, nr = min(r.size, r.R - r0);
+        const int m_lo = r.m0 + r0 / G, m_hi = r.m0 + (r0 + nr - 1) / G;
+        const int m_before = rb > rb0 ? r.m0 + (r0 - 1) / G : INT_MIN;
+        int wbase = INT_MIN / 2, delta = -1, count = 0;
+        bool fresh = true;
+        uint64_t win = 0;
+        for (int p = at.page; p < p1 && ok;) {
+          if (p + kPagesPerTile > wbase + 32) {
+            wbase = p;
+            win = p + lane < p1 ? ldg_u64(words + p + lane) : 0;
+          }
+          const uint64_t w = __shfl_sync(0xffffffffu, win, (p - wbase + lane) & 31);
+          const int d = int(word_delta(w)), d0 = __shfl_sync(0xffffffffu, d, 0);
+          const uint32_t alike = __ballot_sync(0xffffffffu, lane < kPagesPerTile && p + lane < p1 && d == d0);
+          const int np = __ffs(~alike) - 1;
+          const int start = d + kPage * int(word_pg(w));
+          int nv = min(int(word_nvalid(w)), kPage);
+          const uint32_t seen = __ballot_sync(0xffffffffu, lane < np && start <= m_hi);
+          if (!seen) {  // behind every row of this block; in the query segment, so is the rest
+            if (p >= r.docs) break;
+            ok = bare(F_NOP);
+            ++count;
+            p += np;
+            continue;
+          }
+          if (lane < np && word_page(w) >= uint32_t(a.num_pages)) {
+            if (rb == rb0) set_status(a.status, LAZY_STATUS_BAD_PAGE);
+            nv = 0;
+          }
+          ok = slot_free(i);
+          if (!ok) break;
+          const bool newq = fresh || (d0 != delta && (POS == kRope || POS == kRopeX));
+          delta = d0;
+          fresh = false;
+          if (newq) ++qn;
+          // the thread that stored this tile's sums for the row block before adds to them
+          const uint32_t stored = __ballot_sync(0xffffffffu, lane < np && start <= m_before);
+          const uint32_t mask = __ballot_sync(0xffffffffu, lane < np && start + kPage - 1 > m_lo);
+          Item& it = items[i % slots];
+          const int s = i % NS;
+          const uint32_t load = __ballot_sync(0xffffffffu, lane < np && nv > 0);
+          if (lane < kPagesPerTile) it.page[lane] = make_int2(start, lane < np ? nv : 0);
+          if (lane == 0) {
+            it.flags = (newq ? F_NEWQ : 0) | (stored ? F_ADD : 0) | (mask ? F_MASK : 0);
+            it.b = at.b;
+            it.j0 = p;
+            it.np = np;
+            it.rows = nr;
+            it.r0 = r0;
+            it.delta = d0;
+            it.kvh = at.kvh;
+            it.rg = at.rg;
+            it.m0 = r.m0;
+            it.qn = qn;
+            it.first = r.first;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(B_META + i % slots));
+            mbar_arrive_expect_tx(BAR(B_KFULL + s), uint32_t(__popc(load)) * kPage * D * 2);
+          }
+          __syncwarp();
+          if ((load >> lane) & 1u)
+#pragma unroll
+            for (int cb = 0; cb < D / 64; ++cb)
+              tma_load_page(sK + uint32_t(s * L::TILE + cb * L::KBLK + lane * kPage * 128), &tmk, cb * 64, 0,
+                            int(word_page(w)) * a.Hkv + at.kvh, BAR(B_KFULL + s));
+          __syncwarp();
+          last_real = i;
+          ++i;
+          ++count;
+          p += np;
+        }
+        // a tile's sums stay with one warpgroup through the row blocks
+        if (ok && (count & 1) && rb + 1 < rb1) ok = bare(F_NOP);
+      }
+      at = {at.b, at.kvh, at.rg + 1, 0};
+      if (at.rg == r.rgc) at = {at.b, at.kvh + 1, 0, 0};
+      if (at.kvh == a.Hkv) at = {at.b + 1, 0, 0, 0};
+    }
+    if (ok) ok = bare(F_END) && bare(F_END);
+    if (lane == 0)  // never leave copies in flight: the last items' stages
+      for (int j = max(0, last_real - NS + 1); j <= last_real; ++j) {
+        // a stage whose phase has passed answers at once; items without a copy leave their stage's phase alone
+        WaitClock clk;
+        while (*abort_flag && !mbar_test(BAR(B_KFULL + j % NS), uint32_t((j / NS) & 1)) && !clk.expired()) {
+        }
+      }
+  } else if (warp == kMmaWarp) {
+    // ============================ products (one thread): S = K (Qhi + Qlo)^T, keys x query rows
+    if (lane == 0) {
+      int newest = -1;
+      for (int i = 0; ok; ++i) {
+        const int sl = i % slots, s = i % NS, buf = i & 1;
+        if (!(ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / slots) & 1), abort_flag, a.status))) break;
+        const Item& it = items[sl];
+        const int flags = it.flags;
+        if ((flags & F_NEWQ) && newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
+        if (i >= 2 && !(ok = wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status))) break;
+        if (!(flags & (F_END | F_NOP))) {
+          newest = it.qn;
+          if (!(ok = wait_bar(BAR(B_KFULL + s), uint32_t((i / NS) & 1), abort_flag, a.status))) break;
+          tc_fence_after();
+          const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t((it.rows + 15) / 16 * 2 - 2) << 17);
+          const uint32_t q0 = sQ + uint32_t(newest & 1) * QBUF, k0 = sK + uint32_t(s * L::TILE);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16(tmem + uint32_t(buf * kRows), sdesc(k0 + uint32_t((kk >> 2) * L::KBLK + (kk & 3) * 32), 16, 1024),
+                       sdesc(q0 + uint32_t(part) * QLO + uint32_t(kk >> 2) * QBLK + uint32_t((kk & 3) * 32), 16, 1024), idesc,
+                       part || kk ? 1u : 0u);
+        } else {
+          // the stage stays unused this time: its phase is closed without a copy
+          mbar_arrive(BAR(B_KFULL + s));
+        }
+        mma_commit(BAR(B_SFULL + buf));
+        mma_commit(BAR(B_KFREE + s));
+        if (flags & F_END) {
+          ok = wait_bar(BAR(B_QOK + (i + 1) % slots), uint32_t(((i + 1) / slots) & 1), abort_flag, a.status) &&
+               (i < 1 || wait_bar(BAR(B_SFREE + (buf ^ 1)), uint32_t((((i + 1) >> 1) - 1) & 1), abort_flag, a.status));
+          if (ok) mma_commit(BAR(B_SFULL + (buf ^ 1)));
+          break;
+        }
+      }
+      mma_commit(BAR(B_FINAL));  // every product is done before TMEM goes
+      WaitClock clk;
+      while (!mbar_test(BAR(B_FINAL), 0) && !clk.expired()) {
+      }
+    }
+    __syncwarp();
+  }
+
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Adds the parts of a key: groups of row blocks, KV heads, in order.  Only what was computed is read.
+__global__ void __launch_bounds__(256) weights_sum_kernel(const Args a) {
   pdl_wait();
   pdl_trigger();
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = accumulate ? weights[i] : 0.f;
-  float t = 0.f;
-  for (int h = 0; h < Hkv; ++h) t += part[h * n + i];
-  weights[i] = s + t;
+  const int b = blockIdx.y, N = a.max_blocks * kPage;
+  const size_t n = (size_t)a.B * N;
+  const Request r = request_of(a, b);
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < N; i += gridDim.x * 256) {
+    const int j = i / kPage;
+    const size_t at = (size_t)b * N + i;
+    float t = 0.f;
+    if (r.R > 0 && j < r.nb) {
+      const uint64_t w = a.meta[(size_t)b * a.max_blocks + j];
+      const int p = int(word_delta(w)) + kPage * int(word_pg(w)) + i % kPage;
+      if (i % kPage < int(word_nvalid(w)))
+        for (int g = 0; g < r.rgc; ++g) {
+          const int last = min(r.R, group_start(r, g + 1) * r.size) - 1;
+          if (p <= r.m0 + last / (a.Hq / a.Hkv))
+            for (int h = 0; h < a.Hkv; ++h) t += a.part[((size_t)g * a.Hkv + h) * n + at];
+        }
+    }
+    a.weights[at] = a.accumulate ? a.weights[at] + t : t;
+  }
+}
+
+int most_rows(bool alibi, long long R) {
+  const long long m = alibi ? kRowsAlibi : kRows, x = (R + 15) / 16 * 16;
+  return int(x < 16 ? 16 : (x < m ? x : m));
+}
+int groups_of(bool alibi, long long R) {
+  const long long n = (R + most_rows(alibi, R) - 1) / most_rows(alibi, R);
+  return int(n < 1 ? 1 : (n < kGroups ? n : kGroups));
+}
+
+template <int D, int POS>
+int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
+  using L = WLayout<D>;
+  static std::atomic<uint64_t> done{0};
+  auto kern = weights_kernel<D, POS>;
+  LAZY_CUDA_TRY(smem_limit(kern, L::LIMIT, done));
+  a.stages = L::stages(a.rows, POS == kAlibi);
+  // A block's share is at least about a tile.
+  const long long most = (long long)a.B * a.Hkv * ((a.max_blocks + kPagesPerTile - 1) / kPagesPerTile) * a.groups;
+  const int grid = int(std::min<long long>(most, sm_count()));
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.stages, POS == kAlibi), st, mk, a));
+  return LAZY_OK;
 }
 
 }  // namespace
@@ -123,7 +655,10 @@ int check_workspace(const char* what, const void* ws, size_t got, size_t need) {
   return LAZY_OK;
 }
 
-size_t key_weights_ws_bytes(int B, int Hkv, int max_blocks) { return (size_t)Hkv * B * max_blocks * kPage * 4; }
+size_t key_weights_ws_bytes(int rows, int B, int max_blocks, int Hq, int Hkv) {
+  // ALiBi's smaller row blocks make no fewer groups, so they give the bound
+  return (size_t)groups_of(true, (long long)rows * (Hq / Hkv)) * Hkv * B * max_blocks * kPage * 4;
+}
 
 }  // namespace lazykv
 
@@ -142,9 +677,13 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   if (rc) return rc;
   if (B > 0 && total_q > 0 && (!q || !lse)) return fail(LAZY_EINVAL, "%s: NULL pointer", what);
   if (reinterpret_cast<uintptr_t>(q) & 15u) return fail(LAZY_EINVAL, "%s: tensors must be 16-byte aligned", what);
-  rc = check_workspace(what, ws, ws_bytes, key_weights_ws_bytes(B, Hkv, max_blocks));
+  if ((uint64_t)num_pages * Hkv > 0x7fffffffull) return fail(LAZY_ERANGE, "%s: num_pages * Hkv above 2^31", what);
+  rc = check_workspace(what, ws, ws_bytes, B > 0 ? key_weights_ws_bytes(total_q, B, max_blocks, Hq, Hkv) : 0);
   if (!rc) rc = check_device();
   if (rc || B == 0) return rc;
+  CUtensorMap mk;
+  rc = cache_tensor_map(&mk, k_cache, num_pages, Hkv, D);
+  if (rc) return rc;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.lse = lse;
   a.cu_q = cu_q;
@@ -152,7 +691,6 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   a.q_start = q_start;
   a.doc_blocks = doc_blocks;
   a.meta = meta;
-  a.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
   a.part = static_cast<float*>(ws);
   a.weights = weights;
   a.status = status_word();
@@ -163,13 +701,28 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   a.num_pages = num_pages;
   a.window = window;
   a.accumulate = accumulate;
+  long long n = std::min(max_q, total_q);
+  if (window > 0) n = std::min<long long>(n, window);
+  const bool alibi = a.pos.kind == kAlibi;
+  a.rows = most_rows(alibi, n * (Hq / Hkv));
+  a.groups = groups_of(alibi, n * (Hq / Hkv));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(max_blocks, Hkv, B);
-  LAZY_CUDA_TRY(D == 128 ? launch_pdl(weights_kernel<128>, grid, dim3(128), 0, st, a)
-                         : launch_pdl(weights_kernel<64>, grid, dim3(128), 0, st, a));
-  const size_t n = (size_t)B * max_blocks * kPage;
-  if ((n + 255) / 256 > 0x7fffffffu) return fail(LAZY_ERANGE, "%s: more than 2^39 weights", what);
-  LAZY_CUDA_TRY(launch_pdl(weights_sum_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st,
-                           (const float*)a.part, Hkv, n, accumulate, weights));
+  int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
+  if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
+  if (total_q > 0) {
+    if (D == 128)
+      rc = kind == kRope    ? launch_weights<128, kRope>(a, mk, st)
+           : kind == kRopeX ? launch_weights<128, kRopeX>(a, mk, st)
+           : kind == kAlibi ? launch_weights<128, kAlibi>(a, mk, st)
+                            : launch_weights<128, kNone>(a, mk, st);
+    else
+      rc = kind == kRope    ? launch_weights<64, kRope>(a, mk, st)
+           : kind == kRopeX ? launch_weights<64, kRopeX>(a, mk, st)
+           : kind == kAlibi ? launch_weights<64, kAlibi>(a, mk, st)
+                            : launch_weights<64, kNone>(a, mk, st);
+    if (rc) return rc;
+  }
+  const int blocks = int(std::min<long long>(((long long)max_blocks * kPage + 255) / 256, 65535));
+  LAZY_CUDA_TRY(launch_pdl(weights_sum_kernel, dim3(blocks, B), dim3(256), 0, st, a));
   return LAZY_OK;
 }
