@@ -16,8 +16,11 @@ constexpr int kTile = 128, kPagesPerTile = kTile / kPage;  // keys per tile: the
 constexpr int kRows = 128;                                  // most query rows per block: its columns
 constexpr int kRowsAlibi = 64;                              // (ALiBi keeps two more numbers per row)
 constexpr int kGroups = 8;                                  // most partial sums of a key and KV head
-constexpr int kThreads = 512, kPrepWarp0 = 8, kProdWarp = 12, kMmaWarp = 13;
-constexpr int kMaxStages = 6, kMaxSlots = kMaxStages + 3, kLse = 4;
+constexpr int kPrepWarps = 8, kPrep = 32 * kPrepWarps;
+constexpr int kCopyWarps = 2;
+constexpr int kPrepWarp0 = 8, kPlanWarp = kPrepWarp0 + kPrepWarps, kCopyWarp0 = kPlanWarp + 1,
+              kMmaWarp = kCopyWarp0 + kCopyWarps, kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMaxStages = 6, kSlots = 8, kLse = 4;
 
 struct Args {
   const __nv_bfloat16* q;
@@ -32,6 +35,7 @@ struct Args {
   uint32_t* status;
   int B, max_blocks, Hq, Hkv, num_pages, window, accumulate, groups;
   int rows;             // columns of the Q buffers: query rows per block at most, a multiple of 16
+  int parts;            // bf16 numbers that hold a query value: 3 (24 bits) in blocks of few rows, else 2 (16)
   int stages;           // K tiles in flight
   PosParams pos;
 };
@@ -62,36 +66,38 @@ __device__ __forceinline__ int group_start(const Request& r, int g) { return int
 
 enum : int { F_END = 1, F_NEWQ = 2, F_ADD = 4, F_MASK = 8, F_NOP = 16 };
 struct Item {  // one tile of keys against one block of query rows
-  int flags, b, j0, np;            // list blocks j0 .. j0 + np - 1, of one Delta
-  int rows, r0, delta, kvh;        // query rows (of the request's) r0 .. r0 + rows - 1
-  int rg, m0, qn, first;           // group, position of row 0's token, number of the Q operand, its query row
-  int2 page[kPagesPerTile];        // position of the page's first key, keys (0: none)
+  uint8_t flags, np, rg, rows;     // np list blocks, of one Delta; group; query rows (of the request's) from r0 on
+  int b, j0, kvh;                  // first list block
+  int r0, delta, m0, first, qn;    // position of row 0's token, its query row; number of the Q operand
+  uint16_t pg[kPagesPerTile];      // page index in the document
+  uint32_t page[kPagesPerTile];    // physical page << 8 | keys (0: none)
 };
+static_assert(sizeof(Item) == 84, "the layout below counts on it");
 
 enum : int {
-  B_META = 0,                      // [slots] item published (1)
-  B_QOK = B_META + kMaxSlots,      // [slots] its Q operand is ready (4: a lane per warp)
-  B_KFULL = B_QOK + kMaxSlots,     // [stages] K landed
-  B_KFREE = B_KFULL + kMaxStages,  // [stages] products with the stage done (commit)
-  B_SFULL = B_KFREE + kMaxStages,  // [2] scores written (commit)
+  B_META = 0,                      // [kSlots] item published (1)
+  B_QOK = B_META + kSlots,         // [kSlots] its Q operand is ready (a lane per warp)
+  B_DONE = B_QOK + kSlots,         // [kSlots] item finished (4: a lane per warp)
+  B_SFULL = B_DONE + kSlots,       // [2] scores written (commit)
   B_SFREE = B_SFULL + 2,           // [2] scores read (4)
   B_QFREE = B_SFREE + 2,           // [2] products with the Q buffer done (commit)
   B_FINAL = B_QFREE + 2,
-  NBAR
+  B_KFULL = B_FINAL + 1,           // [stages] K landed (a lane per copying warp)
+  NBAR_FIXED = B_KFULL             // then [stages] products with the stage done (commit)
 };
 
 template <int D>
 struct WLayout {
   static constexpr int TILE = kTile * D * 2, KBLK = kTile * 128;
   static constexpr int LIMIT = 227 * 1024;
-  __host__ __device__ static constexpr int qbuf(int rows) { return 2 * rows * D * 2; }  // high and low parts
+  __host__ __device__ static constexpr int qbuf(int rows, int parts) { return parts * rows * D * 2; }
   __host__ __device__ static constexpr int ring(int rows, bool alibi) { return kLse * rows * 4 * (alibi ? 3 : 1); }
-  __host__ static int smem(int rows, int st, bool alibi) {
-    return st * TILE + 2 * qbuf(rows) + ring(rows, alibi) + (st + 3) * int(sizeof(Item)) + NBAR * 8 + 16;
+  __host__ static int smem(int rows, int parts, int st, bool alibi) {
+    return st * TILE + 2 * qbuf(rows, parts) + ring(rows, alibi) + kSlots * int(sizeof(Item)) + (NBAR_FIXED + 2 * st) * 8 + 8;
   }
-  __host__ static int stages(int rows, bool alibi) {  // at least 3 (D 128, 128 rows: 3)
+  __host__ static int stages(int rows, int parts, bool alibi) {  // at least 3 (D 128, 128 rows: 3)
     int n = kMaxStages;
-    while (smem(rows, n, alibi) > LIMIT) --n;
+    while (smem(rows, parts, n, alibi) > LIMIT) --n;
     return n;
   }
 };
@@ -104,14 +110,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void split8(const float (&y)[8], uint4& hi, uint4& lo) {
-  uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
-  uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+// The next bf16 part of eight values, which it is taken from.
+__device__ __forceinline__ uint4 take8(float (&y)[8]) {
+  uint4 part;
+  uint32_t* h = reinterpret_cast<uint32_t*>(&part);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[i] = f2_to_bf2(y[2 * i], y[2 * i + 1]);
-    l[i] = f2_to_bf2(y[2 * i] - bf_lo(h[i]), y[2 * i + 1] - bf_hi(h[i]));
+    y[2 * i] -= bf_lo(h[i]);
+    y[2 * i + 1] -= bf_hi(h[i]);
   }
+  return part;
 }
 __device__ __forceinline__ void unpack8(uint4 u, float (&y)[8]) {
   y[0] = bf_lo(u.x); y[1] = bf_hi(u.x); y[2] = bf_lo(u.y); y[3] = bf_hi(u.y);
@@ -132,19 +141,24 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int NS = a.stages, slots = NS + 3, rows = a.rows;
-  const uint32_t QBUF = uint32_t(L::qbuf(rows)), QBLK = uint32_t(rows) * 128, QLO = QBUF / 2;
+  const int NS = a.stages, rows = a.rows, G = a.Hq / a.Hkv;
+  const uint32_t QBUF = uint32_t(L::qbuf(rows, a.parts)), QBLK = uint32_t(rows) * 128, QPART = uint32_t(rows) * D * 2;
   const uint32_t sK = sb, sQ = sb + NS * L::TILE;
-  float* ring = reinterpret_cast<float*>(sm + NS * L::TILE + 2 * QBUF);  // [kLse][rows] lse (ALiBi: and slope, position)
-  Item* items = reinterpret_cast<Item*>(sm + NS * L::TILE + 2 * QBUF + L::ring(rows, kAl));
-  const uint32_t bar0 = smem_u32(items + slots);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(items + slots) + NBAR * 8);
+  uint8_t* const tail = sm + NS * L::TILE + 2 * QBUF;
+  float* ring = reinterpret_cast<float*>(tail);  // [kLse][rows] lse (ALiBi: and slope, position)
+  const uint32_t bar0 = smem_u32(tail + L::ring(rows, kAl));
+  const int B_KFREE = B_KFULL + NS;
+  Item* items = reinterpret_cast<Item*>(tail + L::ring(rows, kAl) + (NBAR_FIXED + 2 * NS) * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + kSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NBAR; ++i)
-      mbar_init(BAR(i), (i >= B_QOK && i < B_KFULL) || (i >= B_SFREE && i < B_QFREE) ? 4 : 1);
+    for (int i = 0; i < NBAR_FIXED + 2 * NS; ++i)
+      mbar_init(BAR(i), i >= B_QOK && i < B_DONE                                            ? kPrepWarps
+                        : (i >= B_DONE && i < B_SFULL) || (i >= B_SFREE && i < B_QFREE)      ? 4
+                        : i >= B_KFULL && i < B_KFREE                                        ? kCopyWarps
+                                                                                             : 1);
     *abort_flag = (sb & 1023u) ? 1 : 0;  // the operands' swizzle goes by addresses
     if (sb & 1023u) set_status(a.status, LAZY_STATUS_TIMEOUT);
     fence_mbar_init();
@@ -159,7 +173,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int G = a.Hq / a.Hkv;
   bool ok = *abort_flag == 0;
 
   if (warp < 8) {
@@ -169,13 +182,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
     for (int i = wg; ok; i += 2) {
       const bool got = wait_bar(BAR(B_SFULL + wg), uint32_t((i >> 1) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
-      const Item& it = items[i % slots];
+      const Item& it = items[i % kSlots];
       const int flags = it.flags;
       if (flags & F_END) break;
       if (!(flags & F_NOP)) {
         tc_fence_after();
-        const int2 pg = it.page[row / kPage];
-        const int p = pg.x + row % kPage, n16 = (it.rows + 15) / 16;
+        const int keys = int(it.page[row / kPage] & 0xFFu);
+        const int p = it.delta + kPage * int(it.pg[row / kPage]) + row % kPage, n16 = (it.rows + 15) / 16;
         // rows from n0 on see the key
         const long long see = (long long)(p - it.m0) * G - it.r0;
         const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
@@ -221,7 +234,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           add16(s, 16 * c);
         }
         if (row < it.np * kPage) {
-          float w = row % kPage < pg.y ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
+          float w = row % kPage < keys ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
           float* to = a.part + ((((size_t)it.rg * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks + it.j0) * kPage + row;
           if (flags & F_ADD) w += *to;  // this thread's own, of the row block before
           *to = w;
@@ -229,68 +242,90 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(B_SFREE + wg));
+      if (lane == 0) {
+        mbar_arrive(BAR(B_SFREE + wg));
+        mbar_arrive(BAR(B_DONE + i % kSlots));
+      }
     }
-  } else if (warp < kProdWarp) {
+  } else if (warp < kPlanWarp) {
     // ============================ Q operands: rows turned by m - Delta, scaled, split into two bf16 numbers
     const int t = threadIdx.x - kPrepWarp0 * 32;
-    for (int i = 0; ok; ++i) {
-      const int sl = i % slots;
-      bool got = wait_bar(BAR(B_META + sl), uint32_t((i / slots) & 1), abort_flag, a.status);
+    for (int i = 0, ends = 0; ok && ends < 2; ++i) {
+      const int sl = i % kSlots;
+      bool got = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
       const Item& it = items[sl];
       const int flags = it.flags;
+      ends += flags & F_END;
       if (flags & F_NEWQ) {
-        const int qn = it.qn, buf = qn & 1;
-        if (qn >= 2) {
-          got = wait_bar(BAR(B_QFREE + buf), uint32_t(((qn >> 1) - 1) & 1), abort_flag, a.status);
-          if (!__all_sync(0xffffffffu, got)) break;
-        }
-        const int n16 = (it.rows + 15) / 16 * 16, r0 = it.r0, delta = it.delta;
+        const int qn = it.qn, buf = qn & 1, nr = it.rows;
+        const int n16 = (nr + 15) / 16 * 16, r0 = it.r0, delta = it.delta, kvh = it.kvh;
         float* lse = ring + (qn % kLse) * rows * (kAl ? 3 : 1);
-        for (int n = t; n < n16; n += 128) {
-          const int r = r0 + n, h = it.kvh * G + r % G;
-          float l = INFINITY;  // an empty column weighs nothing
-          if (n < it.rows) {
-            l = a.lse[(size_t)(it.first + r / G) * a.Hq + h] * 1.4426950408889634f;
-            if (l == -INFINITY) l = INFINITY;  // nor does a row that saw nothing
-          }
-          lse[n] = l;
-          if constexpr (kAl) {
-            lse[rows + n] = n < it.rows ? a.pos.slopes[h] * 1.4426950408889634f : 0.f;
-            lse[2 * rows + n] = float(it.m0 + r / G);
-          }
+        float l = INFINITY, sl2 = 0.f;  // an empty column weighs nothing
+        if (t < nr) {
+          const int r = r0 + t, h = kvh * G + r % G;
+          l = a.lse[(size_t)(it.first + r / G) * a.Hq + h] * 1.4426950408889634f;
+          if (l == -INFINITY) l = INFINITY;  // nor does a row that saw nothing
+          if constexpr (kAl) sl2 = a.pos.slopes[h] * 1.4426950408889634f;
         }
+        // the buffer's last products are done
+        auto buffer_free = [&]() -> bool {
+          const bool g = qn < 2 || wait_bar(BAR(B_QFREE + buf), uint32_t(((qn >> 1) - 1) & 1), abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, g)) return false;
+          if (t < n16) {
+            lse[t] = l;
+            if constexpr (kAl) {
+              lse[rows + t] = sl2;
+              lse[2 * rows + t] = float(it.m0 + (r0 + t) / G);
+            }
+          }
+          return true;
+        };
         const uint32_t q0 = sQ + uint32_t(buf) * QBUF;
         auto put = [&](int n, int k, const float (&y)[8]) {  // chunk k (8 dimensions) of column n
           float z[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] = y[e] * a.pos.scale_log2;
-          uint4 hi, lo;
-          split8(z, hi, lo);
           const uint32_t at = q0 + uint32_t(k >> 3) * QBLK + swz(n, k & 7);
-          st_shared_v4(at, hi);
-          st_shared_v4(at + QLO, lo);
+          st_shared_v4(at, take8(z));
+          st_shared_v4(at + QPART, take8(z));
+          if (a.parts == 3) st_shared_v4(at + 2 * QPART, take8(z));
         };
-        auto src = [&](int n) {  // query row of column n; null behind the last
-          const int r = r0 + n;
-          return n < it.rows ? reinterpret_cast<const uint4*>(
-                                   a.q + ((size_t)(it.first + r / G) * a.Hq + it.kvh * G + r % G) * D)
-                             : nullptr;
+        // query row of column n, head `h` of the token's `token`; null behind the last
+        auto src = [&](int n, int token, int h) {
+          return n < nr ? reinterpret_cast<const uint4*>(a.q + ((size_t)(it.first + token) * a.Hq + kvh * G + h) * D)
+                        : nullptr;
         };
         const uint4 zero = make_uint4(0, 0, 0, 0);
         if constexpr (POS == kRope) {  // half-split pairs over the whole head: a thread owns a chunk and its partner
-          constexpr int NC = D / 16, NG = 128 / NC;
+          constexpr int NC = D / 16, NG = kPrep / NC, PER = (kRows + NG - 1) / NG;
           const int c = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
           float co[8], sn[8];
-          int token = -1;
-          for (int n = n0; n < min(n0 + per, n16); ++n) {
-            const uint4* s = src(n);
+          int token = (r0 + n0) / G, h = (r0 + n0) % G;
+          uint4 raw[PER][2];  // its rows, all loads in flight at once
+          {
+            int tk = token, hh = h;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              const uint4* s = e < per ? src(n0 + e, tk, hh) : nullptr;
+              raw[e][0] = s ? s[c] : zero;
+              raw[e][1] = s ? s[c + NC] : zero;
+              if (++hh == G) {
+                hh = 0;
+                ++tk;
+              }
+            }
+          }
+          bool turn = true;  // the token has changed
+          ok = buffer_free();
+#pragma unroll
+          for (int e0 = 0; e0 < PER; ++e0) {
+            const int n = n0 + e0;
+            if (!ok || e0 >= per || n >= n16) break;
             float x1[8], x2[8], y1[8], y2[8];
-            unpack8(s ? s[c] : zero, x1);
-            unpack8(s ? s[c + NC] : zero, x2);
-            if ((r0 + n) / G != token) {
-              token = (r0 + n) / G;
+            unpack8(raw[e0][0], x1);
+            unpack8(raw[e0][1], x2);
+            if (turn) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) turn_sincos_signed(it.m0 + token - delta, a.pos.turns[8 * c + e], sn[e], co[e]);
             }
@@ -301,21 +336,32 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             }
             put(n, c, y1);
             put(n, c + NC, y2);
+            turn = ++h == G;
+            if (turn) {
+              h = 0;
+              ++token;
+            }
           }
         } else {
-          constexpr int NC = D / 8, NG = 128 / NC;
+          constexpr int NC = D / 8, NG = kPrep / NC;
           const int k = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
           const int rd = POS == kRopeX ? a.pos.rotary_dim : 0, hr = rd / 2;
           const bool inter = a.pos.interleaved != 0;
-          for (int n = n0; n < min(n0 + per, n16); ++n) {
-            const uint4* s = src(n);
+          int token = (r0 + n0) / G, h = (r0 + n0) % G;
+          ok = buffer_free();
+          for (int n = n0; ok && n < min(n0 + per, n16); ++n) {
+            const uint4* s = src(n, token, h);
+            const int dp = it.m0 + token - delta;
+            if (++h == G) {
+              h = 0;
+              ++token;
+            }
             float x[8], y[8];
             unpack8(s ? s[k] : zero, x);
             if (8 * k >= rd) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = x[e];
             } else if (inter) {
-              const int dp = it.m0 + (r0 + n) / G - delta;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float s1, c1;
@@ -324,7 +370,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
                 y[2 * e + 1] = x[2 * e] * s1 + x[2 * e + 1] * c1;
               }
             } else {
-              const int dp = it.m0 + (r0 + n) / G - delta;
               const bool low = 8 * k < hr;
               float z[8];
               unpack8(s ? s[low ? k + hr / 8 : k - hr / 8] : zero, z);
@@ -340,17 +385,12 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         }
         fence_async_smem();
       }
+      if (!__all_sync(0xffffffffu, ok)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_QOK + sl));
-      if (flags & F_END) {  // a second one ends the other warpgroup
-        got = wait_bar(BAR(B_META + (i + 1) % slots), uint32_t(((i + 1) / slots) & 1), abort_flag, a.status);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_QOK + (i + 1) % slots));
-        break;
-      }
     }
-  } else if (warp == kProdWarp) {
-    // ============================ the block's share of the work, item by item: words, TMA
+  } else if (warp == kPlanWarp) {
+    // ============================ the block's share of the work, item by item
     long long total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       long long c = 0;
@@ -398,17 +438,16 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       at = locate(x0);
       if (x1 < total) end = locate(x1);
     }
-    int i = 0, qn = -1, last_real = -1;
-    auto slot_free = [&](int j) -> bool {  // item j's stage and slot
-      if (j < NS) return true;
-      const bool got = wait_bar(BAR(B_KFREE + j % NS), uint32_t((j / NS - 1) & 1), abort_flag, a.status);
+    int i = 0, qn = -1;
+    auto slot_free = [&](int j) -> bool {
+      const bool got = j < kSlots || wait_bar(BAR(B_DONE + j % kSlots), uint32_t((j / kSlots - 1) & 1), abort_flag, a.status);
       return __all_sync(0xffffffffu, got);
     };
     auto bare = [&](int flags) -> bool {  // an item without a product
       if (!slot_free(i)) return false;
       if (lane == 0) {
-        items[i % slots].flags = flags;
-        mbar_arrive(BAR(B_META + i % slots));
+        items[i % kSlots].flags = uint8_t(flags);
+        mbar_arrive(BAR(B_META + i % kSlots));
       }
       __syncwarp();
       ++i;
@@ -430,15 +469,19 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         const int r0 = rb * r.size, nr = min(r.size, r.R - r0);
         const int m_lo = r.m0 + r0 / G, m_hi = r.m0 + (r0 + nr - 1) / G;
         const int m_before = rb > rb0 ? r.m0 + (r0 - 1) / G : INT_MIN;
-        int wbase = INT_MIN / 2, delta = -1, count = 0;
+        int wbase = at.page, delta = -1, count = 0;
         bool fresh = true;
-        uint64_t win = 0;
+        auto fetch = [&](int p) -> uint64_t { return p + lane < p1 ? ldg_u64(words + p + lane) : 0; };
+        uint64_t win = fetch(wbase), next = fetch(wbase + 32);  // 64 words from wbase on
         for (int p = at.page; p < p1 && ok;) {
-          if (p + kPagesPerTile > wbase + 32) {
-            wbase = p;
-            win = p + lane < p1 ? ldg_u64(words + p + lane) : 0;
+          if (p >= wbase + 32) {
+            wbase += 32;
+            win = next;
+            next = fetch(wbase + 32);
           }
-          const uint64_t w = __shfl_sync(0xffffffffu, win, (p - wbase + lane) & 31);
+          const int wi = p - wbase + lane;
+          const uint64_t w_here = __shfl_sync(0xffffffffu, win, wi & 31), w_next = __shfl_sync(0xffffffffu, next, wi & 31);
+          const uint64_t w = wi < 32 ? w_here : w_next;
           const int d = int(word_delta(w)), d0 = __shfl_sync(0xffffffffu, d, 0);
           const uint32_t alike = __ballot_sync(0xffffffffu, lane < kPagesPerTile && p + lane < p1 && d == d0);
           const int np = __ffs(~alike) - 1;
@@ -465,37 +508,27 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           // the thread that stored this tile's sums for the row block before adds to them
           const uint32_t stored = __ballot_sync(0xffffffffu, lane < np && start <= m_before);
           const uint32_t mask = __ballot_sync(0xffffffffu, lane < np && start + kPage - 1 > m_lo);
-          Item& it = items[i % slots];
-          const int s = i % NS;
-          const uint32_t load = __ballot_sync(0xffffffffu, lane < np && nv > 0);
-          if (lane < kPagesPerTile) it.page[lane] = make_int2(start, lane < np ? nv : 0);
+          Item& it = items[i % kSlots];
+          if (lane < kPagesPerTile) {
+            it.pg[lane] = uint16_t(word_pg(w));
+            it.page[lane] = lane < np && nv > 0 ? word_page(w) << 8 | uint32_t(nv) : 0u;
+          }
           if (lane == 0) {
-            it.flags = (newq ? F_NEWQ : 0) | (stored ? F_ADD : 0) | (mask ? F_MASK : 0);
+            it.flags = uint8_t((newq ? F_NEWQ : 0) | (stored ? F_ADD : 0) | (mask ? F_MASK : 0));
+            it.np = uint8_t(np);
+            it.rg = uint8_t(at.rg);
+            it.rows = uint8_t(nr);
             it.b = at.b;
             it.j0 = p;
-            it.np = np;
-            it.rows = nr;
+            it.kvh = at.kvh;
             it.r0 = r0;
             it.delta = d0;
-            it.kvh = at.kvh;
-            it.rg = at.rg;
             it.m0 = r.m0;
-            it.qn = qn;
             it.first = r.first;
+            it.qn = qn;
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(BAR(B_META + i % slots));
-            mbar_arrive_expect_tx(BAR(B_KFULL + s), uint32_t(__popc(load)) * kPage * D * 2);
-          }
-          __syncwarp();
-          if ((load >> lane) & 1u)
-#pragma unroll
-            for (int cb = 0; cb < D / 64; ++cb)
-              tma_load_page(sK + uint32_t(s * L::TILE + cb * L::KBLK + lane * kPage * 128), &tmk, cb * 64, 0,
-                            int(word_page(w)) * a.Hkv + at.kvh, BAR(B_KFULL + s));
-          __syncwarp();
-          last_real = i;
+          if (lane == 0) mbar_arrive(BAR(B_META + i % kSlots));
           ++i;
           ++count;
           p += np;
@@ -508,49 +541,77 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       if (at.kvh == a.Hkv) at = {at.b + 1, 0, 0, 0};
     }
     if (ok) ok = bare(F_END) && bare(F_END);
-    if (lane == 0)  // never leave copies in flight: the last items' stages
-      for (int j = max(0, last_real - NS + 1); j <= last_real; ++j) {
-        // a stage whose phase has passed answers at once; items without a copy leave their stage's phase alone
+  } else if (warp < kMmaWarp) {
+    // ============================ copies: each warp takes every second page of a tile (a copy costs its issuer ~75 cycles)
+    const int part = warp - kCopyWarp0;
+    int i = 0, ends = 0;
+    for (; ok && ends < 2; ++i) {
+      const int sl = i % kSlots, st = i % NS;
+      const bool got = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status) &&
+                       (i < NS || wait_bar(BAR(B_KFREE + st), uint32_t((i / NS - 1) & 1), abort_flag, a.status));
+      if (!__all_sync(0xffffffffu, got)) break;
+      const Item& it = items[sl];
+      const int flags = it.flags;
+      ends += flags & F_END;
+      uint32_t pg = 0;
+      if (!(flags & (F_END | F_NOP)) && lane < kPagesPerTile && lane % kCopyWarps == part) pg = it.page[lane];
+      const uint32_t load = __ballot_sync(0xffffffffu, pg != 0);
+      if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + st), uint32_t(__popc(load)) * kPage * D * 2);
+      __syncwarp();
+      if (pg)
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+          tma_load_page(sK + uint32_t(st * L::TILE + cb * L::KBLK + lane * kPage * 128), &tmk, cb * 64, 0,
+                        int(pg >> 8) * a.Hkv + it.kvh, BAR(B_KFULL + st));
+      __syncwarp();
+    }
+    if (lane == 0)  // never leave copies in flight
+      for (int j = max(0, i - NS); j < i; ++j) {
         WaitClock clk;
         while (*abort_flag && !mbar_test(BAR(B_KFULL + j % NS), uint32_t((j / NS) & 1)) && !clk.expired()) {
         }
       }
   } else if (warp == kMmaWarp) {
     // ============================ products (one thread): S = K (Qhi + Qlo)^T, keys x query rows
-    if (lane == 0) {
-      int newest = -1;
-      for (int i = 0; ok; ++i) {
-        const int sl = i % slots, s = i % NS, buf = i & 1;
-        if (!(ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / slots) & 1), abort_flag, a.status))) break;
-        const Item& it = items[sl];
-        const int flags = it.flags;
-        if ((flags & F_NEWQ) && newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
-        if (i >= 2 && !(ok = wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status))) break;
+    if (elect_one()) {
+      // Descriptors are built from launch constants and counters alone, and a branch chooses the Q buffer, so that
+      // they stay in uniform registers.
+      const uint64_t kd = sdesc(sK, 16, 1024), qd0 = sdesc(sQ, 16, 1024), qd1 = sdesc(sQ + QBUF, 16, 1024);
+      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(rows / 16 * 2 - 2) << 17);
+      const uint64_t qblk = QBLK >> 4, qpart = QPART >> 4;
+      const int parts = a.parts;
+      auto products = [&](uint32_t d, uint64_t k0, uint64_t q0) {
+        for (int part = 0; part < parts; ++part, q0 += qpart)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16(d, k0 + uint64_t(((kk >> 2) * L::KBLK + (kk & 3) * 32) >> 4), q0 + (kk >> 2) * qblk + (kk & 3) * 2, idesc,
+                     part || kk ? 1u : 0u);
+      };
+      int st = 0, newest = -1;
+      for (int i = 0, ends = 0; ok && ends < 2; ++i) {
+        const int sl = i % kSlots, buf = i & 1;
+        ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
+        if (!ok) break;
+        const int flags = items[sl].flags;
+        ends += flags & F_END;
+        if (flags & F_NEWQ) {
+          if (newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
+          ++newest;
+        }
+        ok = (i < 2 || wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status)) &&
+             wait_bar(BAR(B_KFULL + st), uint32_t((i / NS) & 1), abort_flag, a.status);
+        if (!ok) break;
         if (!(flags & (F_END | F_NOP))) {
-          newest = it.qn;
-          if (!(ok = wait_bar(BAR(B_KFULL + s), uint32_t((i / NS) & 1), abort_flag, a.status))) break;
           tc_fence_after();
-          const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t((it.rows + 15) / 16 * 2 - 2) << 17);
-          const uint32_t q0 = sQ + uint32_t(newest & 1) * QBUF, k0 = sK + uint32_t(s * L::TILE);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16(tmem + uint32_t(buf * kRows), sdesc(k0 + uint32_t((kk >> 2) * L::KBLK + (kk & 3) * 32), 16, 1024),
-                       sdesc(q0 + uint32_t(part) * QLO + uint32_t(kk >> 2) * QBLK + uint32_t((kk & 3) * 32), 16, 1024), idesc,
-                       part || kk ? 1u : 0u);
-        } else {
-          // the stage stays unused this time: its phase is closed without a copy
-          mbar_arrive(BAR(B_KFULL + s));
+          const uint64_t k0 = kd + uint64_t(st * (L::TILE >> 4));
+          if (newest & 1)
+            products(tmem + uint32_t(buf * kRows), k0, qd1);
+          else
+            products(tmem + uint32_t(buf * kRows), k0, qd0);
         }
         mma_commit(BAR(B_SFULL + buf));
-        mma_commit(BAR(B_KFREE + s));
-        if (flags & F_END) {
-          ok = wait_bar(BAR(B_QOK + (i + 1) % slots), uint32_t(((i + 1) / slots) & 1), abort_flag, a.status) &&
-               (i < 1 || wait_bar(BAR(B_SFREE + (buf ^ 1)), uint32_t((((i + 1) >> 1) - 1) & 1), abort_flag, a.status));
-          if (ok) mma_commit(BAR(B_SFULL + (buf ^ 1)));
-          break;
-        }
+        mma_commit(BAR(B_KFREE + st));
+        if (++st == NS) st = 0;
       }
       mma_commit(BAR(B_FINAL));  // every product is done before TMEM goes
       WaitClock clk;
@@ -609,11 +670,12 @@ int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = weights_kernel<D, POS>;
   LAZY_CUDA_TRY(smem_limit(kern, L::LIMIT, done));
-  a.stages = L::stages(a.rows, POS == kAlibi);
+  a.stages = L::stages(a.rows, a.parts, POS == kAlibi);
   // A block's share is at least about a tile.
   const long long most = (long long)a.B * a.Hkv * ((a.max_blocks + kPagesPerTile - 1) / kPagesPerTile) * a.groups;
   const int grid = int(std::min<long long>(most, sm_count()));
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.stages, POS == kAlibi), st, mk, a));
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.parts, a.stages, POS == kAlibi), st, mk,
+                           a));
   return LAZY_OK;
 }
 
@@ -705,6 +767,7 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   if (window > 0) n = std::min<long long>(n, window);
   const bool alibi = a.pos.kind == kAlibi;
   a.rows = most_rows(alibi, n * (Hq / Hkv));
+  a.parts = a.rows <= 64 ? 3 : 2;
   a.groups = groups_of(alibi, n * (Hq / Hkv));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
