@@ -21,6 +21,8 @@ constexpr int kCopyWarps = 2;
 constexpr int kPrepWarp0 = 8, kPlanWarp = kPrepWarp0 + kPrepWarps, kCopyWarp0 = kPlanWarp + 1,
               kMmaWarp = kCopyWarp0 + kCopyWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxStages = 6, kSlots = 8, kLse = 4;
+constexpr int kFew = 64;  // up to so many rows a query value is three bf16 numbers (24 bits), else two (16)
+constexpr int kScore = 256;  // columns of a score buffer
 
 struct Args {
   const __nv_bfloat16* q;
@@ -35,7 +37,8 @@ struct Args {
   uint32_t* status;
   int B, max_blocks, Hq, Hkv, num_pages, window, accumulate, groups;
   int rows;             // columns of the Q buffers: query rows per block at most, a multiple of 16
-  int parts;            // bf16 numbers that hold a query value: 3 (24 bits) in blocks of few rows, else 2 (16)
+  int halves;           // sums per group: 2 in blocks of many rows
+  int parts;            // bf16 numbers that hold a query value
   int stages;           // K tiles in flight
   PosParams pos;
 };
@@ -77,9 +80,9 @@ static_assert(sizeof(Item) == 84, "the layout below counts on it");
 enum : int {
   B_META = 0,                      // [kSlots] item published (1)
   B_QOK = B_META + kSlots,         // [kSlots] its Q operand is ready (a lane per warp)
-  B_DONE = B_QOK + kSlots,         // [kSlots] item finished (4: a lane per warp)
+  B_DONE = B_QOK + kSlots,         // [kSlots] item finished (the same)
   B_SFULL = B_DONE + kSlots,       // [2] scores written (commit)
-  B_SFREE = B_SFULL + 2,           // [2] scores read (4)
+  B_SFREE = B_SFULL + 2,           // [2] scores read (a lane per reading warp)
   B_QFREE = B_SFREE + 2,           // [2] products with the Q buffer done (commit)
   B_FINAL = B_QFREE + 2,
   B_KFULL = B_FINAL + 1,           // [stages] K landed (a lane per copying warp)
@@ -111,20 +114,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 }
 
 // The next bf16 part of eight values, which it is taken from.
-__device__ __forceinline__ uint4 take8(float (&y)[8]) {
+__device__ __forceinline__ uint4 take8(float2 (&y)[4]) {
   uint4 part;
   uint32_t* h = reinterpret_cast<uint32_t*>(&part);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    h[i] = f2_to_bf2(y[2 * i], y[2 * i + 1]);
-    y[2 * i] -= bf_lo(h[i]);
-    y[2 * i + 1] -= bf_hi(h[i]);
+    h[i] = f2_to_bf2(y[i].x, y[i].y);
+    y[i].x -= bf_lo(h[i]);
+    y[i].y -= bf_hi(h[i]);
   }
   return part;
 }
-__device__ __forceinline__ void unpack8(uint4 u, float (&y)[8]) {
-  y[0] = bf_lo(u.x); y[1] = bf_hi(u.x); y[2] = bf_lo(u.y); y[3] = bf_hi(u.y);
-  y[4] = bf_lo(u.z); y[5] = bf_hi(u.z); y[6] = bf_lo(u.w); y[7] = bf_hi(u.w);
+__device__ __forceinline__ void unpack8(uint4 u, float2 (&y)[4]) {
+  y[0] = bf2_to_f2(u.x);
+  y[1] = bf2_to_f2(u.y);
+  y[2] = bf2_to_f2(u.z);
+  y[3] = bf2_to_f2(u.w);
+}
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {  // asks, and never waits
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
 }
 
 // Where a block's share of the work begins or ends: total work is cut into equal parts in the order request,
@@ -142,7 +154,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   const uint32_t sb = smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NS = a.stages, rows = a.rows, G = a.Hq / a.Hkv;
-  const uint32_t QBUF = uint32_t(L::qbuf(rows, a.parts)), QBLK = uint32_t(rows) * 128, QPART = uint32_t(rows) * D * 2;
+  // Blocks of many rows: both warpgroups read each item's scores, half of the columns each (their sums stay
+  // apart); of few rows: every second item each.
+  const bool split = rows > kFew;
+  const uint32_t QBUF = uint32_t(L::qbuf(rows, a.parts)), QPART = uint32_t(rows) * 128, QBLK = QPART * a.parts;
   const uint32_t sK = sb, sQ = sb + NS * L::TILE;
   uint8_t* const tail = sm + NS * L::TILE + 2 * QBUF;
   float* ring = reinterpret_cast<float*>(tail);  // [kLse][rows] lse (ALiBi: and slope, position)
@@ -156,7 +171,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR_FIXED + 2 * NS; ++i)
       mbar_init(BAR(i), i >= B_QOK && i < B_DONE                                            ? kPrepWarps
-                        : (i >= B_DONE && i < B_SFULL) || (i >= B_SFREE && i < B_QFREE)      ? 4
+                        : (i >= B_DONE && i < B_SFULL) || (i >= B_SFREE && i < B_QFREE)      ? (split ? 8 : 4)
                         : i >= B_KFULL && i < B_KFREE                                        ? kCopyWarps
                                                                                              : 1);
     *abort_flag = (sb & 1023u) ? 1 : 0;  // the operands' swizzle goes by addresses
@@ -164,7 +179,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(tmem_slot))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -178,64 +193,71 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   if (warp < 8) {
     // ============================ weights of every second item: a thread owns a key
     const int wg = warp >> 2, row = threadIdx.x & 127;  // TMEM lane = key of the tile
-    const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(wg * kRows);
-    for (int i = wg; ok; i += 2) {
-      const bool got = wait_bar(BAR(B_SFULL + wg), uint32_t((i >> 1) & 1), abort_flag, a.status);
-      if (!__all_sync(0xffffffffu, got)) break;
+    for (int i = split ? 0 : wg; ok; i += split ? 1 : 2) {
       const Item& it = items[i % kSlots];
+      const int buf = i & 1;
+      const bool got = wait_bar(BAR(B_SFULL + buf), uint32_t((i >> 1) & 1), abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, got)) break;
       const int flags = it.flags;
       if (flags & F_END) break;
       if (!(flags & F_NOP)) {
         tc_fence_after();
-        const int keys = int(it.page[row / kPage] & 0xFFu);
-        const int p = it.delta + kPage * int(it.pg[row / kPage]) + row % kPage, n16 = (it.rows + 15) / 16;
+        const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(buf * kScore);
+        const int p = it.delta + kPage * int(it.pg[row / kPage]) + row % kPage;
         // rows from n0 on see the key
         const long long see = (long long)(p - it.m0) * G - it.r0;
         const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
         const float* lse = ring + (it.qn % kLse) * rows * (kAl ? 3 : 1);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add16 = [&](const uint32_t* s, int c0) {
+        const int n16 = (it.rows + 15) / 16, cut = (n16 + 1) / 2;
+        const int c1 = split && wg == 0 ? cut : n16;
+        for (int c = split && wg == 1 ? cut : 0; c < c1; ++c) {
+          const int c0 = 16 * c;
+          uint32_t u[16], u1[16];
+          float s[16];
+          tmem_ld16(tS + uint32_t(c0), u);  // a score is the sum of its parts' columns
+          tmem_ld16(tS + uint32_t(rows + c0), u1);
+          if (split) {
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(u[e]) + __uint_as_float(u1[e]);
+          } else {
+            uint32_t u2[16];
+            tmem_ld16(tS + uint32_t(2 * rows + c0), u2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[e] = __uint_as_float(u[e]) + (__uint_as_float(u1[e]) + __uint_as_float(u2[e]));
+          }
           if constexpr (kAl) {
             const float *sl = lse + rows, *mm = sl + rows;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float x = fmaf(sl[c0 + e], float(p) - mm[c0 + e], __uint_as_float(s[e])) - lse[c0 + e];
+              const float x = fmaf(sl[c0 + e], float(p) - mm[c0 + e], s[e]) - lse[c0 + e];
               acc[e & 3] += c0 + e >= n0 ? ex2(x) : 0.f;
             }
           } else if (flags & F_MASK) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float x = ex2(__uint_as_float(s[e]) - lse[c0 + e]);
+              const float x = ex2(s[e] - lse[c0 + e]);
               acc[e & 3] += c0 + e >= n0 ? x : 0.f;
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               const float4 l4 = *reinterpret_cast<const float4*>(lse + c0 + e);
-              acc[0] += ex2(__uint_as_float(s[e]) - l4.x);
-              acc[1] += ex2(__uint_as_float(s[e + 1]) - l4.y);
-              acc[2] += ex2(__uint_as_float(s[e + 2]) - l4.z);
-              acc[3] += ex2(__uint_as_float(s[e + 3]) - l4.w);
+              acc[0] += ex2(s[e] - l4.x);
+              acc[1] += ex2(s[e + 1] - l4.y);
+              acc[2] += ex2(s[e + 2] - l4.z);
+              acc[3] += ex2(s[e + 3] - l4.w);
             }
           }
-        };
-        int c = 0;
-        for (; c + 2 <= n16; c += 2) {
-          uint32_t s[32];
-          tmem_ld32(tS + uint32_t(16 * c), s);
-          tmem_wait_ld();
-          add16(s, 16 * c);
-          add16(s + 16, 16 * c + 16);
-        }
-        if (c < n16) {
-          uint32_t s[16];
-          tmem_ld16(tS + uint32_t(16 * c), s);
-          tmem_wait_ld();
-          add16(s, 16 * c);
         }
         if (row < it.np * kPage) {
+          const int keys = int(it.page[row / kPage] & 0xFFu);
           float w = row % kPage < keys ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
-          float* to = a.part + ((((size_t)it.rg * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks + it.j0) * kPage + row;
+          const int part = split ? 2 * it.rg + wg : it.rg;
+          float* to = a.part + ((((size_t)part * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks + it.j0) * kPage + row;
           if (flags & F_ADD) w += *to;  // this thread's own, of the row block before
           *to = w;
         }
@@ -243,7 +265,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(BAR(B_SFREE + wg));
+        mbar_arrive(BAR(B_SFREE + buf));
         mbar_arrive(BAR(B_DONE + i % kSlots));
       }
     }
@@ -282,15 +304,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           return true;
         };
         const uint32_t q0 = sQ + uint32_t(buf) * QBUF;
-        auto put = [&](int n, int k, const float (&y)[8]) {  // chunk k (8 dimensions) of column n
-          float z[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = y[e] * a.pos.scale_log2;
+        auto put = [&](int n, int k, float2 (&y)[4]) {  // chunk k (8 dimensions) of column n
           const uint32_t at = q0 + uint32_t(k >> 3) * QBLK + swz(n, k & 7);
-          st_shared_v4(at, take8(z));
-          st_shared_v4(at + QPART, take8(z));
-          if (a.parts == 3) st_shared_v4(at + 2 * QPART, take8(z));
+          st_shared_v4(at, take8(y));
+          st_shared_v4(at + QPART, take8(y));
+          if (a.parts == 3) st_shared_v4(at + 2 * QPART, take8(y));
         };
+        const float sc = a.pos.scale_log2;
         // query row of column n, head `h` of the token's `token`; null behind the last
         auto src = [&](int n, int token, int h) {
           return n < nr ? reinterpret_cast<const uint4*>(a.q + ((size_t)(it.first + token) * a.Hq + kvh * G + h) * D)
@@ -300,7 +320,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         if constexpr (POS == kRope) {  // half-split pairs over the whole head: a thread owns a chunk and its partner
           constexpr int NC = D / 16, NG = kPrep / NC, PER = (kRows + NG - 1) / NG;
           const int c = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
-          float co[8], sn[8];
+          float2 co[4], sn[4], ns[4];  // times the scale
           int token = (r0 + n0) / G, h = (r0 + n0) % G;
           uint4 raw[PER][2];  // its rows, all loads in flight at once
           {
@@ -322,17 +342,23 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           for (int e0 = 0; e0 < PER; ++e0) {
             const int n = n0 + e0;
             if (!ok || e0 >= per || n >= n16) break;
-            float x1[8], x2[8], y1[8], y2[8];
+            float2 x1[4], x2[4], y1[4], y2[4];
             unpack8(raw[e0][0], x1);
             unpack8(raw[e0][1], x2);
             if (turn) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) turn_sincos_signed(it.m0 + token - delta, a.pos.turns[8 * c + e], sn[e], co[e]);
+              for (int e = 0; e < 4; ++e) {
+                turn_sincos_signed(it.m0 + token - delta, a.pos.turns[8 * c + 2 * e], sn[e].x, co[e].x);
+                turn_sincos_signed(it.m0 + token - delta, a.pos.turns[8 * c + 2 * e + 1], sn[e].y, co[e].y);
+                co[e] = make_float2(co[e].x * sc, co[e].y * sc);
+                sn[e] = make_float2(sn[e].x * sc, sn[e].y * sc);
+                ns[e] = make_float2(-sn[e].x, -sn[e].y);
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              y1[e] = x1[e] * co[e] - x2[e] * sn[e];
-              y2[e] = x1[e] * sn[e] + x2[e] * co[e];
+            for (int e = 0; e < 4; ++e) {
+              y1[e] = __ffma2_rn(x1[e], co[e], __fmul2_rn(x2[e], ns[e]));
+              y2[e] = __ffma2_rn(x1[e], sn[e], __fmul2_rn(x2[e], co[e]));
             }
             put(n, c, y1);
             put(n, c + NC, y2);
@@ -356,28 +382,30 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
               h = 0;
               ++token;
             }
-            float x[8], y[8];
+            float2 x[4], y[4];
             unpack8(s ? s[k] : zero, x);
             if (8 * k >= rd) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = x[e];
+              for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].x * sc, x[e].y * sc);
             } else if (inter) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float s1, c1;
                 turn_sincos_signed(dp, a.pos.turns[4 * k + e], s1, c1);
-                y[2 * e] = x[2 * e] * c1 - x[2 * e + 1] * s1;
-                y[2 * e + 1] = x[2 * e] * s1 + x[2 * e + 1] * c1;
+                y[e] = make_float2((x[e].x * c1 - x[e].y * s1) * sc, (x[e].x * s1 + x[e].y * c1) * sc);
               }
             } else {
               const bool low = 8 * k < hr;
-              float z[8];
+              const int f0 = 8 * k - (low ? 0 : hr);
+              float2 z[4];
               unpack8(s ? s[low ? k + hr / 8 : k - hr / 8] : zero, z);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float s1, c1;
-                turn_sincos_signed(dp, a.pos.turns[8 * k + e - (low ? 0 : hr)], s1, c1);
-                y[e] = x[e] * c1 + (low ? -z[e] : z[e]) * s1;
+              for (int e = 0; e < 4; ++e) {
+                float s1, c1, s2, c2;
+                turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e], s1, c1);
+                turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e + 1], s2, c2);
+                y[e] = make_float2((x[e].x * c1 + (low ? -z[e].x : z[e].x) * s1) * sc,
+                                   (x[e].y * c2 + (low ? -z[e].y : z[e].y) * s2) * sc);
               }
             }
             put(n, k, y);
@@ -490,7 +518,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           const uint32_t seen = __ballot_sync(0xffffffffu, lane < np && start <= m_hi);
           if (!seen) {  // behind every row of this block; in the query segment, so is the rest
             if (p >= r.docs) break;
-            ok = bare(F_NOP);
+            if (!split) ok = bare(F_NOP);
             ++count;
             p += np;
             continue;
@@ -534,7 +562,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           p += np;
         }
         // a tile's sums stay with one warpgroup through the row blocks
-        if (ok && (count & 1) && rb + 1 < rb1) ok = bare(F_NOP);
+        if (ok && !split && (count & 1) && rb + 1 < rb1) ok = bare(F_NOP);
       }
       at = {at.b, at.kvh, at.rg + 1, 0};
       if (at.rg == r.rgc) at = {at.b, at.kvh + 1, 0, 0};
@@ -577,20 +605,22 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       // Descriptors are built from launch constants and counters alone, and a branch chooses the Q buffer, so that
       // they stay in uniform registers.
       const uint64_t kd = sdesc(sK, 16, 1024), qd0 = sdesc(sQ, 16, 1024), qd1 = sdesc(sQ + QBUF, 16, 1024);
-      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(rows / 16 * 2 - 2) << 17);
-      const uint64_t qblk = QBLK >> 4, qpart = QPART >> 4;
-      const int parts = a.parts;
+      // One product for all parts of a query, side by side: it reads the keys once (a product of 16 columns costs
+      // what one of 64 does, the keys' 4 KB from shared memory).
+      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(a.parts * rows / 16 * 2 - 2) << 17);
+      const uint64_t qblk = QBLK >> 4;
       auto products = [&](uint32_t d, uint64_t k0, uint64_t q0) {
-        for (int part = 0; part < parts; ++part, q0 += qpart)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16(d, k0 + uint64_t(((kk >> 2) * L::KBLK + (kk & 3) * 32) >> 4), q0 + (kk >> 2) * qblk + (kk & 3) * 2, idesc,
-                     part || kk ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16(d, k0 + uint64_t(((kk >> 2) * L::KBLK + (kk & 3) * 32) >> 4), q0 + (kk >> 2) * qblk + (kk & 3) * 2, idesc,
+                   kk ? 1u : 0u);
       };
       int st = 0, newest = -1;
+      bool seen_q = false, seen_k = false;  // the next item's barriers, asked for while this one's products queue
       for (int i = 0, ends = 0; ok && ends < 2; ++i) {
-        const int sl = i % kSlots, buf = i & 1;
-        ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
+        const int sl = i % kSlots, buf = i & 1, next = st + 1 == NS ? 0 : st + 1;
+        ok = (seen_q || wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status)) &&
+             (seen_k || wait_bar(BAR(B_KFULL + st), uint32_t((i / NS) & 1), abort_flag, a.status));
         if (!ok) break;
         const int flags = items[sl].flags;
         ends += flags & F_END;
@@ -598,20 +628,21 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           if (newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
           ++newest;
         }
-        ok = (i < 2 || wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status)) &&
-             wait_bar(BAR(B_KFULL + st), uint32_t((i / NS) & 1), abort_flag, a.status);
+        ok = i < 2 || wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status);
         if (!ok) break;
         if (!(flags & (F_END | F_NOP))) {
           tc_fence_after();
           const uint64_t k0 = kd + uint64_t(st * (L::TILE >> 4));
           if (newest & 1)
-            products(tmem + uint32_t(buf * kRows), k0, qd1);
+            products(tmem + uint32_t(buf * kScore), k0, qd1);
           else
-            products(tmem + uint32_t(buf * kRows), k0, qd0);
+            products(tmem + uint32_t(buf * kScore), k0, qd0);
         }
         mma_commit(BAR(B_SFULL + buf));
         mma_commit(BAR(B_KFREE + st));
-        if (++st == NS) st = 0;
+        seen_q = mbar_peek(BAR(B_QOK + (i + 1) % kSlots), uint32_t(((i + 1) / kSlots) & 1));
+        seen_k = mbar_peek(BAR(B_KFULL + next), uint32_t(((i + 1) / NS) & 1));
+        st = next;
       }
       mma_commit(BAR(B_FINAL));  // every product is done before TMEM goes
       WaitClock clk;
@@ -626,7 +657,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -648,7 +679,7 @@ __global__ void __launch_bounds__(256) weights_sum_kernel(const Args a) {
         for (int g = 0; g < r.rgc; ++g) {
           const int last = min(r.R, group_start(r, g + 1) * r.size) - 1;
           if (p <= r.m0 + last / (a.Hq / a.Hkv))
-            for (int h = 0; h < a.Hkv; ++h) t += a.part[((size_t)g * a.Hkv + h) * n + at];
+            for (int h = 0; h < a.halves * a.Hkv; ++h) t += a.part[((size_t)g * a.halves * a.Hkv + h) * n + at];
         }
     }
     a.weights[at] = a.accumulate ? a.weights[at] + t : t;
@@ -718,8 +749,9 @@ int check_workspace(const char* what, const void* ws, size_t got, size_t need) {
 }
 
 size_t key_weights_ws_bytes(int rows, int B, int max_blocks, int Hq, int Hkv) {
-  // ALiBi's smaller row blocks make no fewer groups, so they give the bound
-  return (size_t)groups_of(true, (long long)rows * (Hq / Hkv)) * Hkv * B * max_blocks * kPage * 4;
+  // sums of a key and KV head, at most: groups of row blocks of 64 (ALiBi) or twice those of 128
+  const long long R = (long long)rows * (Hq / Hkv), sums = R <= kFew ? 1 : std::min<long long>(2 * kGroups, R / 64 + 2);
+  return (size_t)sums * Hkv * B * max_blocks * kPage * 4;
 }
 
 }  // namespace lazykv
@@ -767,7 +799,8 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   if (window > 0) n = std::min<long long>(n, window);
   const bool alibi = a.pos.kind == kAlibi;
   a.rows = most_rows(alibi, n * (Hq / Hkv));
-  a.parts = a.rows <= 64 ? 3 : 2;
+  a.parts = a.rows <= kFew ? 3 : 2;
+  a.halves = a.rows <= kFew ? 1 : 2;
   a.groups = groups_of(alibi, n * (Hq / Hkv));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
