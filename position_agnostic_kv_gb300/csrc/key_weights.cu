@@ -20,8 +20,9 @@ constexpr int kPrepWarps = 8, kPrep = 32 * kPrepWarps;
 constexpr int kCopyWarps = 2;
 constexpr int kPrepWarp0 = 8, kPlanWarp = kPrepWarp0 + kPrepWarps, kCopyWarp0 = kPlanWarp + 1,
               kMmaWarp = kCopyWarp0 + kCopyWarps, kThreads = 32 * (kMmaWarp + 1);
-constexpr int kMaxStages = 6, kSlots = 8, kLse = 4;
-constexpr int kFew = 64;  // up to so many rows a query value is three bf16 numbers (24 bits), else two (16)
+constexpr int kMaxStages = 6, kSlots = 4, kLse = 4;
+constexpr int kRun = 32;     // pages per item
+constexpr int kFew = 32;     // up to so many rows a query value is three bf16 numbers (24 bits), else two (16)
 constexpr int kScore = 256;  // columns of a score buffer
 
 struct Args {
@@ -37,8 +38,8 @@ struct Args {
   uint32_t* status;
   int B, max_blocks, Hq, Hkv, num_pages, window, accumulate, groups;
   int rows;             // columns of the Q buffers: query rows per block at most, a multiple of 16
+  int most;             // rows per head of a request at most (the call's bound)
   int halves;           // sums per group: 2 in blocks of many rows
-  int parts;            // bf16 numbers that hold a query value
   int stages;           // K tiles in flight
   PosParams pos;
 };
@@ -53,6 +54,7 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
   r.n = max(0, hi - lo);
   if (a.window > 0) r.n = min(r.n, a.window);
+  r.n = min(r.n, a.most);
   r.nb = visible_blocks(len, a.q_start[b], a.doc_blocks[b], a.max_blocks);
   r.docs = a.doc_blocks[b];
   r.first = hi - r.n;
@@ -67,25 +69,25 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
 // group g covers row blocks [group_start(g), group_start(g + 1))
 __device__ __forceinline__ int group_start(const Request& r, int g) { return int((long long)g * r.nrb / r.rgc); }
 
-enum : int { F_END = 1, F_NEWQ = 2, F_ADD = 4, F_MASK = 8, F_NOP = 16 };
-struct Item {  // one tile of keys against one block of query rows
-  uint8_t flags, np, rg, rows;     // np list blocks, of one Delta; group; query rows (of the request's) from r0 on
-  int b, j0, kvh;                  // first list block
-  int r0, delta, m0, first, qn;    // position of row 0's token, its query row; number of the Q operand
-  uint16_t pg[kPagesPerTile];      // page index in the document
-  uint32_t page[kPagesPerTile];    // physical page << 8 | keys (0: none)
+enum : int { F_END = 1, F_NEWQ = 2, F_MASK = 4 };
+struct Item {  // a run of pages of one document against one block of query rows: tiles of 8 pages
+  uint8_t flags, np, rg, rows;  // np list blocks; group; query rows (of the request's) from r0 on
+  int b, j0, kvh;               // first list block
+  int r0, delta, m0, first;     // position of row 0's token, its query row
+  int qn, pg0, stored;          // number of the Q operand; first page's index; pages up to this position have a sum
+  uint32_t page[kRun];          // physical page << 8 | keys (0: none)
 };
-static_assert(sizeof(Item) == 84, "the layout below counts on it");
+static_assert(sizeof(Item) == 172, "the layout below counts on it");
 
 enum : int {
   B_META = 0,                      // [kSlots] item published (1)
   B_QOK = B_META + kSlots,         // [kSlots] its Q operand is ready (a lane per warp)
-  B_DONE = B_QOK + kSlots,         // [kSlots] item finished (the same)
-  B_SFULL = B_DONE + kSlots,       // [2] scores written (commit)
+  B_DONE = B_QOK + kSlots,         // [kSlots] item finished (a lane per reading warp)
+  B_SFULL = B_DONE + kSlots,       // [2] a tile's scores written (commit)
   B_SFREE = B_SFULL + 2,           // [2] scores read (a lane per reading warp)
   B_QFREE = B_SFREE + 2,           // [2] products with the Q buffer done (commit)
   B_FINAL = B_QFREE + 2,
-  B_KFULL = B_FINAL + 1,           // [stages] K landed (a lane per copying warp)
+  B_KFULL = B_FINAL + 1,           // [stages] K tile landed (a lane per copying warp)
   NBAR_FIXED = B_KFULL             // then [stages] products with the stage done (commit)
 };
 
@@ -93,14 +95,15 @@ template <int D>
 struct WLayout {
   static constexpr int TILE = kTile * D * 2, KBLK = kTile * 128;
   static constexpr int LIMIT = 227 * 1024;
-  __host__ __device__ static constexpr int qbuf(int rows, int parts) { return parts * rows * D * 2; }
+  __host__ __device__ static constexpr int parts(int rows) { return rows <= kFew ? 3 : 2; }
+  __host__ __device__ static constexpr int qbuf(int rows) { return parts(rows) * rows * D * 2; }
   __host__ __device__ static constexpr int ring(int rows, bool alibi) { return kLse * rows * 4 * (alibi ? 3 : 1); }
-  __host__ static int smem(int rows, int parts, int st, bool alibi) {
-    return st * TILE + 2 * qbuf(rows, parts) + ring(rows, alibi) + kSlots * int(sizeof(Item)) + (NBAR_FIXED + 2 * st) * 8 + 8;
+  __host__ static int smem(int rows, int st, bool alibi) {
+    return st * TILE + 2 * qbuf(rows) + ring(rows, alibi) + kSlots * int(sizeof(Item)) + (NBAR_FIXED + 2 * st) * 8 + 8;
   }
-  __host__ static int stages(int rows, int parts, bool alibi) {  // at least 3 (D 128, 128 rows: 3)
+  __host__ static int stages(int rows, bool alibi) {  // at least 3 (D 128, 128 rows: 3)
     int n = kMaxStages;
-    while (smem(rows, parts, n, alibi) > LIMIT) --n;
+    while (smem(rows, n, alibi) > LIMIT) --n;
     return n;
   }
 };
@@ -154,13 +157,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   const uint32_t sb = smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NS = a.stages, rows = a.rows, G = a.Hq / a.Hkv;
-  // Blocks of many rows: both warpgroups read each item's scores, half of the columns each (their sums stay
-  // apart); of few rows: every second item each.
+  // Blocks of many rows: both warpgroups read each tile's scores, half of the columns each (their sums stay
+  // apart); of few rows: every second tile each.
   const bool split = rows > kFew;
-  const uint32_t QBUF = uint32_t(L::qbuf(rows, a.parts)), QPART = uint32_t(rows) * 128, QBLK = QPART * a.parts;
+  const uint32_t QBUF = uint32_t(L::qbuf(rows)), QPART = uint32_t(rows) * 128, QBLK = QPART * L::parts(rows);
   const uint32_t sK = sb, sQ = sb + NS * L::TILE;
   uint8_t* const tail = sm + NS * L::TILE + 2 * QBUF;
-  float* ring = reinterpret_cast<float*>(tail);  // [kLse][rows] lse (ALiBi: and slope, position)
+  float* ring = reinterpret_cast<float*>(tail);  // [kLse][rows] -lse (ALiBi: and slope, position)
   const uint32_t bar0 = smem_u32(tail + L::ring(rows, kAl));
   const int B_KFREE = B_KFULL + NS;
   Item* items = reinterpret_cast<Item*>(tail + L::ring(rows, kAl) + (NBAR_FIXED + 2 * NS) * 8);
@@ -171,7 +174,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR_FIXED + 2 * NS; ++i)
       mbar_init(BAR(i), i >= B_QOK && i < B_DONE                                            ? kPrepWarps
-                        : (i >= B_DONE && i < B_SFULL) || (i >= B_SFREE && i < B_QFREE)      ? (split ? 8 : 4)
+                        : i >= B_DONE && i < B_SFULL                                          ? 8
+                        : i >= B_SFREE && i < B_QFREE                                        ? (split ? 8 : 4)
                         : i >= B_KFULL && i < B_KFREE                                        ? kCopyWarps
                                                                                              : 1);
     *abort_flag = (sb & 1023u) ? 1 : 0;  // the operands' swizzle goes by addresses
@@ -193,101 +197,118 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   if (warp < 8) {
     // ============================ weights of every second item: a thread owns a key
     const int wg = warp >> 2, row = threadIdx.x & 127;  // TMEM lane = key of the tile
-    for (int i = split ? 0 : wg; ok; i += split ? 1 : 2) {
+    uint32_t tile = 0;  // of this block's tiles
+    for (int i = 0; ok; ++i) {
       const Item& it = items[i % kSlots];
-      const int buf = i & 1;
-      const bool got = wait_bar(BAR(B_SFULL + buf), uint32_t((i >> 1) & 1), abort_flag, a.status);
+      // the first tile's scores say that the item is there; a warpgroup without a tile in it asks for the item itself
+      bool got = wait_bar(BAR(B_META + i % kSlots), uint32_t((i / kSlots) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
-      const int flags = it.flags;
+      const int flags = it.flags, np = it.np;
       if (flags & F_END) break;
-      if (!(flags & F_NOP)) {
+      const int n16 = (it.rows + 15) / 16, stored = it.stored, delta = it.delta, pg0 = it.pg0, m0 = it.m0, r0 = it.r0;
+      const float* lse = ring + (it.qn % kLse) * rows * (kAl ? 3 : 1);
+      float* to = a.part + ((((size_t)(split ? 2 * it.rg + wg : it.rg) * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks +
+                            it.j0) * kPage + row;
+      for (int j = 0; j < np; j += kPagesPerTile, ++tile) {
+        const int buf = int(tile & 1u);
+        if (!split && buf != wg) continue;
+        got = wait_bar(BAR(B_SFULL + buf), (tile >> 1) & 1u, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(buf * kScore);
-        const int p = it.delta + kPage * int(it.pg[row / kPage]) + row % kPage;
+        const int mine = j + row / kPage, start = delta + kPage * (pg0 + mine), p = start + row % kPage;
         // rows from n0 on see the key
-        const long long see = (long long)(p - it.m0) * G - it.r0;
+        const long long see = (long long)(p - m0) * G - r0;
         const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
-        const float* lse = ring + (it.qn % kLse) * rows * (kAl ? 3 : 1);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const int n16 = (it.rows + 15) / 16, cut = (n16 + 1) / 2;
-        const int c1 = split && wg == 0 ? cut : n16;
-        for (int c = split && wg == 1 ? cut : 0; c < c1; ++c) {
-          const int c0 = 16 * c;
-          uint32_t u[16], u1[16];
-          float s[16];
-          tmem_ld16(tS + uint32_t(c0), u);  // a score is the sum of its parts' columns
-          tmem_ld16(tS + uint32_t(rows + c0), u1);
-          if (split) {
-            tmem_wait_ld();
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const bool masked = flags & F_MASK;
+        // 16 scores, each the sum of its parts' columns: acc += 2^(s - lse)
+        auto weigh = [&](float2 (&x)[8], int c0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(u[e]) + __uint_as_float(u1[e]);
-          } else {
-            uint32_t u2[16];
-            tmem_ld16(tS + uint32_t(2 * rows + c0), u2);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              s[e] = __uint_as_float(u[e]) + (__uint_as_float(u1[e]) + __uint_as_float(u2[e]));
+          for (int e = 0; e < 8; e += 2) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse + c0 + 2 * e);  // negative log-sum-exps
+            if constexpr (kAl) {
+              const float *sl = lse + rows + c0 + 2 * e, *mm = sl + rows;
+              x[e].x = fmaf(sl[0], float(p) - mm[0], x[e].x);
+              x[e].y = fmaf(sl[1], float(p) - mm[1], x[e].y);
+              x[e + 1].x = fmaf(sl[2], float(p) - mm[2], x[e + 1].x);
+              x[e + 1].y = fmaf(sl[3], float(p) - mm[3], x[e + 1].y);
+            }
+            x[e] = __fadd2_rn(x[e], make_float2(l4.x, l4.y));
+            x[e + 1] = __fadd2_rn(x[e + 1], make_float2(l4.z, l4.w));
           }
-          if constexpr (kAl) {
-            const float *sl = lse + rows, *mm = sl + rows;
+          if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = fmaf(sl[c0 + e], float(p) - mm[c0 + e], s[e]) - lse[c0 + e];
-              acc[e & 3] += c0 + e >= n0 ? ex2(x) : 0.f;
-            }
-          } else if (flags & F_MASK) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = ex2(s[e] - lse[c0 + e]);
-              acc[e & 3] += c0 + e >= n0 ? x : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(lse + c0 + e);
-              acc[0] += ex2(s[e] - l4.x);
-              acc[1] += ex2(s[e + 1] - l4.y);
-              acc[2] += ex2(s[e + 2] - l4.z);
-              acc[3] += ex2(s[e + 3] - l4.w);
+            for (int e = 0; e < 8; ++e) {
+              if (c0 + 2 * e < n0) x[e].x = -INFINITY;
+              if (c0 + 2 * e + 1 < n0) x[e].y = -INFINITY;
             }
           }
-        }
-        if (row < it.np * kPage) {
-          const int keys = int(it.page[row / kPage] & 0xFFu);
-          float w = row % kPage < keys ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : 0.f;
-          const int part = split ? 2 * it.rg + wg : it.rg;
-          float* to = a.part + ((((size_t)part * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks + it.j0) * kPage + row;
-          if (flags & F_ADD) w += *to;  // this thread's own, of the row block before
-          *to = w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x[e].x), ex2(x[e].y)));
+        };
+        auto pair = [](const uint32_t* u, int e) {
+          return make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+        };
+        if (split) {  // two parts
+          const int cut = (n16 + 1) / 2, c1 = wg == 0 ? cut : n16;
+          int c = wg == 0 ? 0 : cut;
+          for (; c < c1; ++c) {
+            uint32_t u[2][16];
+            tmem_ld16(tS + uint32_t(16 * c), u[0]);
+            tmem_ld16(tS + uint32_t(rows + 16 * c), u[1]);
+            tmem_wait_ld();
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fadd2_rn(pair(u[0], e), pair(u[1], e));
+            weigh(x, 16 * c);
+          }
+        } else {  // three parts
+          for (int c = 0; c < n16; ++c) {
+            uint32_t u[3][16];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) tmem_ld16(tS + uint32_t(e * rows + 16 * c), u[e]);
+            tmem_wait_ld();
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fadd2_rn(pair(u[0], e), __fadd2_rn(pair(u[1], e), pair(u[2], e)));
+            weigh(x, 16 * c);
+          }
         }
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_SFREE + buf));
+        if (mine < np) {
+          const int keys = int(it.page[mine] & 0xFFu);
+          float w = row % kPage < keys ? ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) : 0.f;
+          if (start <= stored) w += to[j * kPage];  // this thread's own, of the row block before
+          to[j * kPage] = w;
+        }
       }
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(BAR(B_SFREE + buf));
-        mbar_arrive(BAR(B_DONE + i % kSlots));
-      }
+      if (lane == 0) mbar_arrive(BAR(B_DONE + i % kSlots));
     }
   } else if (warp < kPlanWarp) {
     // ============================ Q operands: rows turned by m - Delta, scaled, split into two bf16 numbers
     const int t = threadIdx.x - kPrepWarp0 * 32;
-    for (int i = 0, ends = 0; ok && ends < 2; ++i) {
+    for (int i = 0; ok; ++i) {
       const int sl = i % kSlots;
       bool got = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
       const Item& it = items[sl];
       const int flags = it.flags;
-      ends += flags & F_END;
+      if (flags & F_END) break;
       if (flags & F_NEWQ) {
         const int qn = it.qn, buf = qn & 1, nr = it.rows;
         const int n16 = (nr + 15) / 16 * 16, r0 = it.r0, delta = it.delta, kvh = it.kvh;
         float* lse = ring + (qn % kLse) * rows * (kAl ? 3 : 1);
-        float l = INFINITY, sl2 = 0.f;  // an empty column weighs nothing
+        float l = -INFINITY, sl2 = 0.f;  // an empty column weighs nothing
         if (t < nr) {
           const int r = r0 + t, h = kvh * G + r % G;
-          l = a.lse[(size_t)(it.first + r / G) * a.Hq + h] * 1.4426950408889634f;
-          if (l == -INFINITY) l = INFINITY;  // nor does a row that saw nothing
+          l = a.lse[(size_t)(it.first + r / G) * a.Hq + h] * -1.4426950408889634f;
+          if (l == INFINITY) l = -INFINITY;  // nor does a row that saw nothing
           if constexpr (kAl) sl2 = a.pos.slopes[h] * 1.4426950408889634f;
         }
         // the buffer's last products are done
@@ -308,7 +329,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           const uint32_t at = q0 + uint32_t(k >> 3) * QBLK + swz(n, k & 7);
           st_shared_v4(at, take8(y));
           st_shared_v4(at + QPART, take8(y));
-          if (a.parts == 3) st_shared_v4(at + 2 * QPART, take8(y));
+          if (!split) st_shared_v4(at + 2 * QPART, take8(y));
         };
         const float sc = a.pos.scale_log2;
         // query row of column n, head `h` of the token's `token`; null behind the last
@@ -471,21 +492,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       const bool got = j < kSlots || wait_bar(BAR(B_DONE + j % kSlots), uint32_t((j / kSlots - 1) & 1), abort_flag, a.status);
       return __all_sync(0xffffffffu, got);
     };
-    auto bare = [&](int flags) -> bool {  // an item without a product
-      if (!slot_free(i)) return false;
-      if (lane == 0) {
-        items[i % kSlots].flags = uint8_t(flags);
-        mbar_arrive(BAR(B_META + i % kSlots));
-      }
-      __syncwarp();
-      ++i;
-      return true;
-    };
     auto before = [](const Place& p, const Place& e) {
       return p.b != e.b ? p.b < e.b : p.kvh != e.kvh ? p.kvh < e.kvh : p.rg != e.rg ? p.rg < e.rg : p.page < e.page;
     };
+    Request r = {};
+    int known = -1;
     while (ok && before(at, end)) {
-      const Request r = request_of(a, at.b);
+      if (at.b != known) r = request_of(a, known = at.b);
       if (r.R == 0) {
         at = {at.b + 1, 0, 0, 0};
         continue;
@@ -497,7 +510,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         const int r0 = rb * r.size, nr = min(r.size, r.R - r0);
         const int m_lo = r.m0 + r0 / G, m_hi = r.m0 + (r0 + nr - 1) / G;
         const int m_before = rb > rb0 ? r.m0 + (r0 - 1) / G : INT_MIN;
-        int wbase = at.page, delta = -1, count = 0;
+        int wbase = at.page, delta = -1;
         bool fresh = true;
         auto fetch = [&](int p) -> uint64_t { return p + lane < p1 ? ldg_u64(words + p + lane) : 0; };
         uint64_t win = fetch(wbase), next = fetch(wbase + 32);  // 64 words from wbase on
@@ -511,38 +524,32 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           const uint64_t w_here = __shfl_sync(0xffffffffu, win, wi & 31), w_next = __shfl_sync(0xffffffffu, next, wi & 31);
           const uint64_t w = wi < 32 ? w_here : w_next;
           const int d = int(word_delta(w)), d0 = __shfl_sync(0xffffffffu, d, 0);
-          const uint32_t alike = __ballot_sync(0xffffffffu, lane < kPagesPerTile && p + lane < p1 && d == d0);
-          const int np = __ffs(~alike) - 1;
-          const int start = d + kPage * int(word_pg(w));
-          int nv = min(int(word_nvalid(w)), kPage);
-          const uint32_t seen = __ballot_sync(0xffffffffu, lane < np && start <= m_hi);
-          if (!seen) {  // behind every row of this block; in the query segment, so is the rest
+          const int pg0 = __shfl_sync(0xffffffffu, int(word_pg(w)), 0), start = d + kPage * int(word_pg(w));
+          // a run: consecutive pages of one document; of them, those that some row of the block sees
+          const uint32_t run = __ballot_sync(0xffffffffu, p + lane < p1 && d == d0 && int(word_pg(w)) == pg0 + lane);
+          const uint32_t seen = __ballot_sync(0xffffffffu, start <= m_hi) & run;
+          const int len = ~run ? __ffs(~run) - 1 : 32, np = ~seen ? __ffs(~seen) - 1 : 32;
+          if (np == 0) {  // behind every row; in the query segment, so is the rest
             if (p >= r.docs) break;
-            if (!split) ok = bare(F_NOP);
-            ++count;
-            p += np;
+            p += len;
             continue;
           }
+          int nv = min(int(word_nvalid(w)), kPage);
           if (lane < np && word_page(w) >= uint32_t(a.num_pages)) {
             if (rb == rb0) set_status(a.status, LAZY_STATUS_BAD_PAGE);
             nv = 0;
           }
-          ok = slot_free(i);
-          if (!ok) break;
           const bool newq = fresh || (d0 != delta && (POS == kRope || POS == kRopeX));
           delta = d0;
           fresh = false;
           if (newq) ++qn;
-          // the thread that stored this tile's sums for the row block before adds to them
-          const uint32_t stored = __ballot_sync(0xffffffffu, lane < np && start <= m_before);
-          const uint32_t mask = __ballot_sync(0xffffffffu, lane < np && start + kPage - 1 > m_lo);
+          const bool mask = d0 + kPage * (pg0 + np) - 1 > m_lo;
+          ok = slot_free(i);
+          if (!ok) break;
           Item& it = items[i % kSlots];
-          if (lane < kPagesPerTile) {
-            it.pg[lane] = uint16_t(word_pg(w));
-            it.page[lane] = lane < np && nv > 0 ? word_page(w) << 8 | uint32_t(nv) : 0u;
-          }
+          it.page[lane] = lane < np && nv > 0 ? word_page(w) << 8 | uint32_t(nv) : 0u;
           if (lane == 0) {
-            it.flags = uint8_t((newq ? F_NEWQ : 0) | (stored ? F_ADD : 0) | (mask ? F_MASK : 0));
+            it.flags = uint8_t((newq ? F_NEWQ : 0) | (mask ? F_MASK : 0));
             it.np = uint8_t(np);
             it.rg = uint8_t(at.rg);
             it.rows = uint8_t(nr);
@@ -554,47 +561,58 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             it.m0 = r.m0;
             it.first = r.first;
             it.qn = qn;
+            it.pg0 = pg0;
+            it.stored = m_before;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(B_META + i % kSlots));
           ++i;
-          ++count;
           p += np;
         }
-        // a tile's sums stay with one warpgroup through the row blocks
-        if (ok && !split && (count & 1) && rb + 1 < rb1) ok = bare(F_NOP);
       }
       at = {at.b, at.kvh, at.rg + 1, 0};
       if (at.rg == r.rgc) at = {at.b, at.kvh + 1, 0, 0};
       if (at.kvh == a.Hkv) at = {at.b + 1, 0, 0, 0};
     }
-    if (ok) ok = bare(F_END) && bare(F_END);
+    if (ok && slot_free(i) && lane == 0) {
+      items[i % kSlots].flags = F_END;
+      mbar_arrive(BAR(B_META + i % kSlots));
+    }
   } else if (warp < kMmaWarp) {
     // ============================ copies: each warp takes every second page of a tile (a copy costs its issuer ~75 cycles)
     const int part = warp - kCopyWarp0;
-    int i = 0, ends = 0;
-    for (; ok && ends < 2; ++i) {
-      const int sl = i % kSlots, st = i % NS;
-      const bool got = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status) &&
-                       (i < NS || wait_bar(BAR(B_KFREE + st), uint32_t((i / NS - 1) & 1), abort_flag, a.status));
+    int tiles = 0, st = 0;
+    uint32_t phase = 1;  // parity of the stage's last use (none: passes at once)
+    for (int i = 0; ok; ++i) {
+      const int sl = i % kSlots;
+      bool got = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
       const Item& it = items[sl];
-      const int flags = it.flags;
-      ends += flags & F_END;
-      uint32_t pg = 0;
-      if (!(flags & (F_END | F_NOP)) && lane < kPagesPerTile && lane % kCopyWarps == part) pg = it.page[lane];
-      const uint32_t load = __ballot_sync(0xffffffffu, pg != 0);
-      if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + st), uint32_t(__popc(load)) * kPage * D * 2);
-      __syncwarp();
-      if (pg)
+      if (it.flags & F_END) break;
+      const int np = it.np, kvh = it.kvh;
+      for (int j = 0; j < np; j += kPagesPerTile) {
+        const uint32_t pg = lane < kPagesPerTile && lane % kCopyWarps == part && j + lane < np ? it.page[j + lane] : 0u;
+        const uint32_t load = __ballot_sync(0xffffffffu, pg != 0);
+        got = wait_bar(BAR(B_KFREE + st), phase, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_KFULL + st), uint32_t(__popc(load)) * kPage * D * 2);
+        __syncwarp();
+        if (pg)
 #pragma unroll
-        for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_page(sK + uint32_t(st * L::TILE + cb * L::KBLK + lane * kPage * 128), &tmk, cb * 64, 0,
-                        int(pg >> 8) * a.Hkv + it.kvh, BAR(B_KFULL + st));
-      __syncwarp();
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_page(sK + uint32_t(st * L::TILE + cb * L::KBLK + lane * kPage * 128), &tmk, cb * 64, 0,
+                          int(pg >> 8) * a.Hkv + kvh, BAR(B_KFULL + st));
+        __syncwarp();
+        ++tiles;
+        if (++st == NS) {
+          st = 0;
+          phase ^= 1u;
+        }
+      }
     }
     if (lane == 0)  // never leave copies in flight
-      for (int j = max(0, i - NS); j < i; ++j) {
+      for (int j = max(0, tiles - NS); j < tiles; ++j) {
         WaitClock clk;
         while (*abort_flag && !mbar_test(BAR(B_KFULL + j % NS), uint32_t((j / NS) & 1)) && !clk.expired()) {
         }
@@ -607,7 +625,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       const uint64_t kd = sdesc(sK, 16, 1024), qd0 = sdesc(sQ, 16, 1024), qd1 = sdesc(sQ + QBUF, 16, 1024);
       // One product for all parts of a query, side by side: it reads the keys once (a product of 16 columns costs
       // what one of 64 does, the keys' 4 KB from shared memory).
-      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(a.parts * rows / 16 * 2 - 2) << 17);
+      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(L::parts(rows) * rows / 16 * 2 - 2) << 17);
       const uint64_t qblk = QBLK >> 4;
       auto products = [&](uint32_t d, uint64_t k0, uint64_t q0) {
 #pragma unroll
@@ -616,33 +634,39 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
                    kk ? 1u : 0u);
       };
       int st = 0, newest = -1;
-      bool seen_q = false, seen_k = false;  // the next item's barriers, asked for while this one's products queue
-      for (int i = 0, ends = 0; ok && ends < 2; ++i) {
-        const int sl = i % kSlots, buf = i & 1, next = st + 1 == NS ? 0 : st + 1;
-        ok = (seen_q || wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status)) &&
-             (seen_k || wait_bar(BAR(B_KFULL + st), uint32_t((i / NS) & 1), abort_flag, a.status));
+      uint32_t tile = 0, kpar = 0;
+      bool seen_k = false, seen_s = true;  // the next tile's barriers, asked for while this one's products queue
+      for (int i = 0; ok; ++i) {
+        const int sl = i % kSlots;
+        ok = wait_bar(BAR(B_META + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
         if (!ok) break;
-        const int flags = items[sl].flags;
-        ends += flags & F_END;
+        const int flags = items[sl].flags, np = items[sl].np;
+        if (flags & F_END) break;
         if (flags & F_NEWQ) {
           if (newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
           ++newest;
         }
-        ok = i < 2 || wait_bar(BAR(B_SFREE + buf), uint32_t(((i >> 1) - 1) & 1), abort_flag, a.status);
-        if (!ok) break;
-        if (!(flags & (F_END | F_NOP))) {
+        ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
+        for (int j = 0; j < np && ok; j += kPagesPerTile, ++tile) {
+          const int buf = int(tile & 1u);
+          ok = (seen_k || wait_bar(BAR(B_KFULL + st), kpar, abort_flag, a.status)) &&
+               (seen_s || wait_bar(BAR(B_SFREE + buf), (tile >> 1) & 1u ^ 1u, abort_flag, a.status));
+          if (!ok) break;
           tc_fence_after();
           const uint64_t k0 = kd + uint64_t(st * (L::TILE >> 4));
           if (newest & 1)
             products(tmem + uint32_t(buf * kScore), k0, qd1);
           else
             products(tmem + uint32_t(buf * kScore), k0, qd0);
+          mma_commit(BAR(B_SFULL + buf));
+          mma_commit(BAR(B_KFREE + st));
+          if (++st == NS) {
+            st = 0;
+            kpar ^= 1u;
+          }
+          seen_k = mbar_peek(BAR(B_KFULL + st), kpar);
+          seen_s = mbar_peek(BAR(B_SFREE + (buf ^ 1)), ((tile + 1) >> 1) & 1u ^ 1u);
         }
-        mma_commit(BAR(B_SFULL + buf));
-        mma_commit(BAR(B_KFREE + st));
-        seen_q = mbar_peek(BAR(B_QOK + (i + 1) % kSlots), uint32_t(((i + 1) / kSlots) & 1));
-        seen_k = mbar_peek(BAR(B_KFULL + next), uint32_t(((i + 1) / NS) & 1));
-        st = next;
       }
       mma_commit(BAR(B_FINAL));  // every product is done before TMEM goes
       WaitClock clk;
@@ -668,6 +692,10 @@ __global__ void __launch_bounds__(256) weights_sum_kernel(const Args a) {
   const int b = blockIdx.y, N = a.max_blocks * kPage;
   const size_t n = (size_t)a.B * N;
   const Request r = request_of(a, b);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const int n = a.cu_q[b + 1] - a.cu_q[b];
+    if ((a.window > 0 ? min(n, a.window) : n) > a.most) set_status(a.status, LAZY_STATUS_BAD_ROW);
+  }
   for (int i = blockIdx.x * 256 + threadIdx.x; i < N; i += gridDim.x * 256) {
     const int j = i / kPage;
     const size_t at = (size_t)b * N + i;
@@ -701,11 +729,11 @@ int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = weights_kernel<D, POS>;
   LAZY_CUDA_TRY(smem_limit(kern, L::LIMIT, done));
-  a.stages = L::stages(a.rows, a.parts, POS == kAlibi);
+  a.stages = L::stages(a.rows, POS == kAlibi);
   // A block's share is at least about a tile.
   const long long most = (long long)a.B * a.Hkv * ((a.max_blocks + kPagesPerTile - 1) / kPagesPerTile) * a.groups;
   const int grid = int(std::min<long long>(most, sm_count()));
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.parts, a.stages, POS == kAlibi), st, mk,
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.stages, POS == kAlibi), st, mk,
                            a));
   return LAZY_OK;
 }
@@ -799,7 +827,7 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   if (window > 0) n = std::min<long long>(n, window);
   const bool alibi = a.pos.kind == kAlibi;
   a.rows = most_rows(alibi, n * (Hq / Hkv));
-  a.parts = a.rows <= kFew ? 3 : 2;
+  a.most = int(n);
   a.halves = a.rows <= kFew ? 1 : 2;
   a.groups = groups_of(alibi, n * (Hq / Hkv));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
