@@ -116,17 +116,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr));
 }
 
-// The next bf16 part of eight values, which it is taken from.
-__device__ __forceinline__ uint4 take8(float2 (&y)[4]) {
-  uint4 part;
-  uint32_t* h = reinterpret_cast<uint32_t*>(&part);
+// Eight values in bf16, and what that leaves of them.
+__device__ __forceinline__ uint4 round8(const float2 (&y)[4]) {
+  return make_uint4(f2_to_bf2(y[0].x, y[0].y), f2_to_bf2(y[1].x, y[1].y), f2_to_bf2(y[2].x, y[2].y),
+                    f2_to_bf2(y[3].x, y[3].y));
+}
+__device__ __forceinline__ void less8(float2 (&y)[4], uint4 part) {
+  const uint32_t h[4] = {part.x, part.y, part.z, part.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = f2_to_bf2(y[i].x, y[i].y);
-    y[i].x -= bf_lo(h[i]);
-    y[i].y -= bf_hi(h[i]);
-  }
-  return part;
+  for (int i = 0; i < 4; ++i) y[i] = __ffma2_rn(bf2_to_f2(h[i]), make_float2(-1.f, -1.f), y[i]);
 }
 __device__ __forceinline__ void unpack8(uint4 u, float2 (&y)[4]) {
   y[0] = bf2_to_f2(u.x);
@@ -212,12 +210,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       for (int j = 0; j < np; j += kPagesPerTile, ++tile) {
         const int buf = int(tile & 1u);
         if (!split && buf != wg) continue;
+        const int mine = j + row / kPage, start = delta + kPage * (pg0 + mine), p = start + row % kPage;
+        const float old = mine < np && start <= stored ? to[j * kPage] : 0.f;  // this thread's own, of the row block before
         got = wait_bar(BAR(B_SFULL + buf), (tile >> 1) & 1u, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(buf * kScore);
-        const int mine = j + row / kPage, start = delta + kPage * (pg0 + mine), p = start + row % kPage;
         // rows from n0 on see the key
         const long long see = (long long)(p - m0) * G - r0;
         const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
@@ -254,6 +253,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         if (split) {  // two parts
           const int cut = (n16 + 1) / 2, c1 = wg == 0 ? cut : n16;
           int c = wg == 0 ? 0 : cut;
+#pragma unroll 1
           for (; c < c1; ++c) {
             uint32_t u[2][16];
             tmem_ld16(tS + uint32_t(16 * c), u[0]);
@@ -281,9 +281,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         if (lane == 0) mbar_arrive(BAR(B_SFREE + buf));
         if (mine < np) {
           const int keys = int(it.page[mine] & 0xFFu);
-          float w = row % kPage < keys ? ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) : 0.f;
-          if (start <= stored) w += to[j * kPage];  // this thread's own, of the row block before
-          to[j * kPage] = w;
+          const float w = row % kPage < keys ? ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) : 0.f;
+          to[j * kPage] = old + w;
         }
       }
       if (!ok) break;
@@ -327,9 +326,15 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         const uint32_t q0 = sQ + uint32_t(buf) * QBUF;
         auto put = [&](int n, int k, float2 (&y)[4]) {  // chunk k (8 dimensions) of column n
           const uint32_t at = q0 + uint32_t(k >> 3) * QBLK + swz(n, k & 7);
-          st_shared_v4(at, take8(y));
-          st_shared_v4(at + QPART, take8(y));
-          if (!split) st_shared_v4(at + 2 * QPART, take8(y));
+          uint4 u = round8(y);
+          st_shared_v4(at, u);
+          less8(y, u);
+          u = round8(y);
+          st_shared_v4(at + QPART, u);
+          if (!split) {
+            less8(y, u);
+            st_shared_v4(at + 2 * QPART, round8(y));
+          }
         };
         const float sc = a.pos.scale_log2;
         // query row of column n, head `h` of the token's `token`; null behind the last
@@ -339,33 +344,31 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         };
         const uint4 zero = make_uint4(0, 0, 0, 0);
         if constexpr (POS == kRope) {  // half-split pairs over the whole head: a thread owns a chunk and its partner
-          constexpr int NC = D / 16, NG = kPrep / NC, PER = (kRows + NG - 1) / NG;
+          constexpr int NC = D / 16, NG = kPrep / NC;
           const int c = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
           float2 co[4], sn[4], ns[4];  // times the scale
           int token = (r0 + n0) / G, h = (r0 + n0) % G;
-          uint4 raw[PER][2];  // its rows, all loads in flight at once
-          {
-            int tk = token, hh = h;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-              const uint4* s = e < per ? src(n0 + e, tk, hh) : nullptr;
-              raw[e][0] = s ? s[c] : zero;
-              raw[e][1] = s ? s[c + NC] : zero;
-              if (++hh == G) {
-                hh = 0;
-                ++tk;
-              }
+          int tk = token, hh = h;  // of the row that is loaded next, one ahead of the one in use
+          uint4 raw[2];
+          auto load = [&](int e) {
+            const uint4* s = e < per ? src(n0 + e, tk, hh) : nullptr;
+            raw[0] = s ? s[c] : zero;
+            raw[1] = s ? s[c + NC] : zero;
+            if (++hh == G) {
+              hh = 0;
+              ++tk;
             }
-          }
+          };
+          load(0);
           bool turn = true;  // the token has changed
           ok = buffer_free();
-#pragma unroll
-          for (int e0 = 0; e0 < PER; ++e0) {
-            const int n = n0 + e0;
-            if (!ok || e0 >= per || n >= n16) break;
+          const int n1 = ok ? min(n0 + per, n16) : n0;
+#pragma unroll 1
+          for (int n = n0; n < n1; ++n) {
             float2 x1[4], x2[4], y1[4], y2[4];
-            unpack8(raw[e0][0], x1);
-            unpack8(raw[e0][1], x2);
+            unpack8(raw[0], x1);
+            unpack8(raw[1], x2);
+            load(n + 1 - n0);
             if (turn) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -506,50 +509,47 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       const bool same = at.b == end.b && at.kvh == end.kvh && at.rg == end.rg;
       const int p1 = same ? end.page : r.nb, rb0 = group_start(r, at.rg), rb1 = group_start(r, at.rg + 1);
       const uint64_t* words = a.meta + (size_t)at.b * a.max_blocks;
-      for (int rb = rb0; rb < rb1 && ok; ++rb) {
-        const int r0 = rb * r.size, nr = min(r.size, r.R - r0);
-        const int m_lo = r.m0 + r0 / G, m_hi = r.m0 + (r0 + nr - 1) / G;
-        const int m_before = rb > rb0 ? r.m0 + (r0 - 1) / G : INT_MIN;
-        int wbase = at.page, delta = -1;
-        bool fresh = true;
-        auto fetch = [&](int p) -> uint64_t { return p + lane < p1 ? ldg_u64(words + p + lane) : 0; };
-        uint64_t win = fetch(wbase), next = fetch(wbase + 32);  // 64 words from wbase on
-        for (int p = at.page; p < p1 && ok;) {
-          if (p >= wbase + 32) {
-            wbase += 32;
-            win = next;
-            next = fetch(wbase + 32);
-          }
-          const int wi = p - wbase + lane;
-          const uint64_t w_here = __shfl_sync(0xffffffffu, win, wi & 31), w_next = __shfl_sync(0xffffffffu, next, wi & 31);
-          const uint64_t w = wi < 32 ? w_here : w_next;
-          const int d = int(word_delta(w)), d0 = __shfl_sync(0xffffffffu, d, 0);
-          const int pg0 = __shfl_sync(0xffffffffu, int(word_pg(w)), 0), start = d + kPage * int(word_pg(w));
-          // a run: consecutive pages of one document; of them, those that some row of the block sees
-          const uint32_t run = __ballot_sync(0xffffffffu, p + lane < p1 && d == d0 && int(word_pg(w)) == pg0 + lane);
-          const uint32_t seen = __ballot_sync(0xffffffffu, start <= m_hi) & run;
-          const int len = ~run ? __ffs(~run) - 1 : 32, np = ~seen ? __ffs(~seen) - 1 : 32;
-          if (np == 0) {  // behind every row; in the query segment, so is the rest
-            if (p >= r.docs) break;
-            p += len;
-            continue;
-          }
-          int nv = min(int(word_nvalid(w)), kPage);
-          if (lane < np && word_page(w) >= uint32_t(a.num_pages)) {
-            if (rb == rb0) set_status(a.status, LAZY_STATUS_BAD_PAGE);
-            nv = 0;
-          }
-          const bool newq = fresh || (d0 != delta && (POS == kRope || POS == kRopeX));
+      int wbase = at.page;
+      auto fetch = [&](int p) -> uint64_t { return p + lane < p1 ? ldg_u64(words + p + lane) : 0; };
+      uint64_t win = fetch(wbase), next = fetch(wbase + 32);  // 64 words from wbase on
+      int delta = -1, last_rb = -1;  // of the Q operand
+      for (int p = at.page; p < p1 && ok;) {
+        if (p >= wbase + 32) {
+          wbase += 32;
+          win = next;
+          next = fetch(wbase + 32);
+        }
+        const int wi = p - wbase + lane;
+        const uint64_t w_here = __shfl_sync(0xffffffffu, win, wi & 31), w_next = __shfl_sync(0xffffffffu, next, wi & 31);
+        const uint64_t w = wi < 32 ? w_here : w_next;
+        const int d = int(word_delta(w)), d0 = __shfl_sync(0xffffffffu, d, 0);
+        const int pg0 = __shfl_sync(0xffffffffu, int(word_pg(w)), 0), start = d + kPage * int(word_pg(w));
+        // a run: consecutive pages of one document
+        const uint32_t run = __ballot_sync(0xffffffffu, p + lane < p1 && d == d0 && int(word_pg(w)) == pg0 + lane);
+        const int len = ~run ? __ffs(~run) - 1 : 32;
+        int nv = min(int(word_nvalid(w)), kPage);
+        if (lane < len && word_page(w) >= uint32_t(a.num_pages)) {
+          set_status(a.status, LAZY_STATUS_BAD_PAGE);
+          nv = 0;
+        }
+        const uint32_t page = nv > 0 ? word_page(w) << 8 | uint32_t(nv) : 0u;
+        // every row block of the group over the run, while its pages are in the L2
+        for (int rb = rb0; rb < rb1 && ok; ++rb) {
+          const int r0 = rb * r.size, nr = min(r.size, r.R - r0);
+          const int m_lo = r.m0 + r0 / G, m_hi = r.m0 + (r0 + nr - 1) / G;
+          const uint32_t seen = __ballot_sync(0xffffffffu, lane < len && start <= m_hi);
+          const int np = ~seen ? __ffs(~seen) - 1 : 32;  // pages that some row of the block sees
+          if (np == 0) continue;
+          const bool newq = rb != last_rb || (d0 != delta && (POS == kRope || POS == kRopeX));
           delta = d0;
-          fresh = false;
+          last_rb = rb;
           if (newq) ++qn;
-          const bool mask = d0 + kPage * (pg0 + np) - 1 > m_lo;
           ok = slot_free(i);
           if (!ok) break;
           Item& it = items[i % kSlots];
-          it.page[lane] = lane < np && nv > 0 ? word_page(w) << 8 | uint32_t(nv) : 0u;
+          it.page[lane] = lane < np ? page : 0u;
           if (lane == 0) {
-            it.flags = uint8_t((newq ? F_NEWQ : 0) | (mask ? F_MASK : 0));
+            it.flags = uint8_t((newq ? F_NEWQ : 0) | (d0 + kPage * (pg0 + np) - 1 > m_lo ? F_MASK : 0));
             it.np = uint8_t(np);
             it.rg = uint8_t(at.rg);
             it.rows = uint8_t(nr);
@@ -562,13 +562,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             it.first = r.first;
             it.qn = qn;
             it.pg0 = pg0;
-            it.stored = m_before;
+            it.stored = rb > rb0 ? r.m0 + (r0 - 1) / G : INT_MIN;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(B_META + i % kSlots));
           ++i;
-          p += np;
         }
+        p += len;
       }
       at = {at.b, at.kvh, at.rg + 1, 0};
       if (at.rg == r.rgc) at = {at.b, at.kvh + 1, 0, 0};
@@ -718,11 +718,6 @@ int most_rows(bool alibi, long long R) {
   const long long m = alibi ? kRowsAlibi : kRows, x = (R + 15) / 16 * 16;
   return int(x < 16 ? 16 : (x < m ? x : m));
 }
-int groups_of(bool alibi, long long R) {
-  const long long n = (R + most_rows(alibi, R) - 1) / most_rows(alibi, R);
-  return int(n < 1 ? 1 : (n < kGroups ? n : kGroups));
-}
-
 template <int D, int POS>
 int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   using L = WLayout<D>;
@@ -731,8 +726,8 @@ int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   LAZY_CUDA_TRY(smem_limit(kern, L::LIMIT, done));
   a.stages = L::stages(a.rows, POS == kAlibi);
   // A block's share is at least about a tile.
-  const long long most = (long long)a.B * a.Hkv * ((a.max_blocks + kPagesPerTile - 1) / kPagesPerTile) * a.groups;
-  const int grid = int(std::min<long long>(most, sm_count()));
+  const long long shares = (long long)a.B * a.Hkv * ((a.max_blocks + kPagesPerTile - 1) / kPagesPerTile) * a.groups;
+  const int grid = int(std::min<long long>(shares, sm_count()));
   LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.stages, POS == kAlibi), st, mk,
                            a));
   return LAZY_OK;
@@ -829,7 +824,11 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   a.rows = most_rows(alibi, n * (Hq / Hkv));
   a.most = int(n);
   a.halves = a.rows <= kFew ? 1 : 2;
-  a.groups = groups_of(alibi, n * (Hq / Hkv));
+  // Row blocks in one block's share, so that it still has runs of 32 pages: a Q operand then serves four tiles, and a
+  // run's pages are read from memory once for all of them.  The more groups, the more parts to add.
+  const long long nrb = (n * (Hq / Hkv) + a.rows - 1) / a.rows;
+  const long long per = std::max(1ll, nrb * max_blocks * B * Hkv / (32ll * sm_count()));
+  a.groups = int(std::min<long long>(kGroups, std::max(1ll, (nrb + per - 1) / per)));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
   if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
