@@ -49,9 +49,7 @@ Sizes sizes_of(int B, int n_groups, int max_group, int max_shared, int max_block
   Sizes s;
   max_shared = std::min(max_shared, max_blocks);
   max_group = std::min(max_group, B);
-  s.SA = 0;
-  (void)n_groups;
-  (void)max_group;
+  s.SA = shared_prefix_splits(n_groups, max_group, max_shared, Hq, Hkv);
   // Own blocks: enough warps for about four waves, runs of at least 32 blocks a split.
   const int own = max_blocks - (s.SA ? max_shared : 0);
   const long long units = (long long)B * Hkv * ((Hq / Hkv + 7) / 8), slots = 3ll * sm_count();
@@ -153,7 +151,8 @@ extern "C" int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, co
   a.SB = z.SB;
   a.status = status_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = run_shared_own(a, D, mk, mv, false, st);
+  if (a.SA > 0) rc = run_shared_prefix(a, D, mk, mv, st);
+  if (!rc) rc = run_shared_own(a, D, mk, mv, a.SA > 0, st);
   if (rc) return rc;
   const dim3 grid(Hq, B);
   LAZY_CUDA_TRY(D == 128 ? launch_pdl(join_kernel<128>, grid, dim3(128), 0, st, a)

@@ -1,0 +1,695 @@
+// Decode of the keys that a group of requests shares, read once for all of its rows, on the 5th-generation tensor
+// cores.
+//
+// Mathematics: the rows of a group and KV head are its (request, head) pairs; per 128-key tile S = Q K^T with
+// Q = R_m q (each row turned by its own position m) and K = R_Delta k (each page by its document's offset), an online
+// softmax in base 2, O += P V.  The result is partial: unnormalised O, maximum and sum per key split, joined with the
+// requests' own keys afterwards.
+//
+// One block per (key split, KV head, 256 rows of a group), 512 threads, one block per SM:
+//   warps 0-3 / 4-7  softmax (thread = TMEM lane = row).  With more than 128 rows each warpgroup has a Q tile of its
+//              own and sees every key tile; with up to 128 both have the same rows, one the even key tiles and one
+//              the odd, and join their results at the end.  Either way step s of the block is key tile s/2 or s
+//              against score buffer s % 2, and the products of one buffer run under the other's softmax.
+//              Rows are normalised by a power of two each, so that f16 holds any query.
+//   warps 8-11 the keys' rotation in place (f16; without rotation only the conversion); a thread owns 8 frequencies of
+//              a page's rows and keeps their cosines while Delta stays.
+//   warp 12 / 14  block words and TMA copies (64 columns x 16 rows of a page) of keys (3 stages) and of values (2).
+//              A page with r < 16 keys is loaded from row r - 16: zeros, then its keys in the last rows.
+//   warp 13    TMEM owner and MMA issuer: QK(0) QK(1) | PV(0) QK(2) | PV(1) QK(3) | ...
+// TMEM: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P_i in the first half of S_i, as bf16.
+// Every wait is bounded.
+#include <cfloat>
+#include <climits>
+
+#include "q4_attn.cuh"
+#include "shared_decode.cuh"
+#include "tcgen05.cuh"
+
+namespace lazykv {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128, kN = 128;
+constexpr int kPagesPerTile = kN / kPage;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kSlots = 6;  // per-tile metadata: published up to 4 tiles ahead of the softmax's last use
+constexpr int kThreads = 512;
+constexpr int kRotWarp0 = 8, kKWarp = 12, kMmaWarp = 13, kVWarp = 14;
+// Registers per thread: at launch, and after the split (softmax, rotation, the four single warps), which adds up to it.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsRot = 56, kRegsIssue = 88;
+static_assert(2 * kRegsSoftmax + kRegsRot + kRegsIssue == 4 * kRegsLaunch, "warpgroup register shares");
+constexpr float kTau = 8.0f;
+
+enum : int {
+  B_K_FULL = 0,    // [3] K tile landed
+  B_K_READY = 3,   // [3] K tile rotated (128 arrivals)
+  B_K_FREE = 6,    // [3] every QK^T with the stage done (commit)
+  B_V_FULL = 9,    // [2] V tile landed
+  B_V_FREE = 11,   // [2] every PV with the stage done (commit)
+  B_S_FULL = 13,   // [2] scores written (commit; covers the buffer's PV before)
+  B_P_FULL = 15,   // [2] P in TMEM, O rescaled (128)
+  B_Q_READY = 17,  // Q tiles prepared (256)
+  B_FINAL = 18,    // all products done (commit)
+  NBAR = 19
+};
+
+template <int D>
+struct Layout {
+  static constexpr int BLK = kM * 128;
+  static constexpr int TILE = kN * D * 2, QTILE = kM * D * 2;
+  static constexpr int K_OFF = 2 * QTILE;
+  static constexpr int V_OFF = K_OFF + kKStages * TILE;
+  static constexpr int PSTART_OFF = V_OFF + kVStages * TILE;                // int [slot][8] position of stage row 0
+  static constexpr int PINFO_OFF = PSTART_OFF + kSlots * kPagesPerTile * 4;  // int2 [slot][8] {Delta, first row with a key}
+  static constexpr int FLAG_OFF = PINFO_OFF + kSlots * kPagesPerTile * 8;    // int [slot] every key visible to every row
+  static constexpr int TURNS_OFF = FLAG_OFF + kSlots * 8;
+  static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+};
+static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
+
+template <int D, int POS>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const SharedArgs a,
+              const int lowest_ex) {
+  using L = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (sb - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = int(blockIdx.x) % a.SA, pair = int(blockIdx.x) / a.SA, kvh = blockIdx.y, grp = blockIdx.z;
+  const int G = a.Hq / a.Hkv;
+  pdl_wait();
+  pdl_trigger();  // what comes behind and does not wait itself (own_kernel) touches other results
+  const int b0 = max(0, a.group_off[grp]);
+  const int nreq = min(min(a.group_off[grp + 1], a.B) - b0, a.max_group);
+  const int row0 = pair * 2 * kM, rows = min(2 * kM, nreq * G - row0);
+  const int nb = shared_blocks_of(a, grp);
+  const int ntiles_all = (nb + kPagesPerTile - 1) / kPagesPerTile, chunk = split_tiles(ntiles_all, a.SA);
+  const int t0 = split * chunk, ntiles = min(ntiles_all, t0 + chunk) - t0;
+  if (rows <= 0 || ntiles <= 0) return;  // uniform for the block
+  const bool two = rows > kM;
+  const int nsteps = two ? 2 * ntiles : ntiles;
+
+  const uint32_t sQ0 = sb, sK0 = sb + L::K_OFF, sV0 = sb + L::V_OFF;
+  int* pstart = reinterpret_cast<int*>(sm + L::PSTART_OFF);
+  int2* pinfo = reinterpret_cast<int2*>(sm + L::PINFO_OFF);
+  int* flags = reinterpret_cast<int*>(sm + L::FLAG_OFF);
+  unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + L::TURNS_OFF);
+  const uint32_t bar0 = sb + L::BAR_OFF;
+  auto BAR = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBAR; ++i)
+      mbar_init(BAR(i), (i >= B_K_READY && i < B_K_FREE) || (i >= B_P_FULL && i < B_Q_READY) ? 128
+                        : i == B_Q_READY                                                     ? 256
+                                                                                             : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < D / 2; i += kThreads) turns[i] = a.pos.turns[i];
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    // ============================ Q preparation, softmax, epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int sl = warp >> 2, r = threadIdx.x & (kM - 1);  // score buffer; row of the tile = TMEM lane
+    const int row = row0 + (two ? sl * kM : 0) + r;
+    const int b = b0 + row / G, h = kvh * G + row % G;
+    const bool valid = row < row0 + rows;
+    const int m_row = valid ? a.seq_len[b] - 1 : -1;
+    float f = 0.f;  // scores are the products times this
+    {
+      const uint32_t sQ = sQ0 + uint32_t(two ? sl * L::QTILE : 0);
+      auto qaddr = [&](int k) { return sQ + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)b * a.Hq + h) * D);
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint4 u = valid ? src[k] : make_uint4(0, 0, 0, 0);
+        if (two || sl == 0) st_shared_v4(qaddr(k), u);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max3f(top, fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i])));
+      }
+      // A power of two per row takes it into [-1, 1], where f16 keeps 11 bits of what matters.
+      const int ex = q4_exponent(top, lowest_ex);
+      const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
+      f = a.pos.scale_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
+      if (two || sl == 0) {
+        auto pack = [&](const float (&y)[8]) {
+          return make_uint4(f2_to_h2(y[0], y[1]), f2_to_h2(y[2], y[3]), f2_to_h2(y[4], y[5]), f2_to_h2(y[6], y[7]));
+        };
+        auto unpack = [&](uint4 u, float (&y)[8]) {
+          y[0] = bf_lo(u.x) * inv; y[1] = bf_hi(u.x) * inv; y[2] = bf_lo(u.y) * inv; y[3] = bf_hi(u.y) * inv;
+          y[4] = bf_lo(u.z) * inv; y[5] = bf_hi(u.z) * inv; y[6] = bf_lo(u.w) * inv; y[7] = bf_hi(u.w) * inv;
+        };
+        int done = 0;  // chunks [0, done) are in their final form
+        if constexpr (POS == kRope || POS == kRopeX) {
+          const uint32_t m = uint32_t(max(m_row, 0));
+          const int rd = POS == kRope ? D : a.pos.rotary_dim, hr = rd / 2;
+          if (POS == kRope || !a.pos.interleaved) {
+#pragma unroll 1
+            for (int c = 0; c < hr / 8; ++c) {  // chunk c against its partner
+              float x1[8], x2[8], y1[8], y2[8];
+              unpack(ld_shared_v4(qaddr(c)), x1);
+              unpack(ld_shared_v4(qaddr(c + hr / 8)), x2);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float sn, co;
+                turn_sincos_fast(m, turns[c * 8 + e], sn, co);
+                y1[e] = x1[e] * co - x2[e] * sn;
+                y2[e] = x1[e] * sn + x2[e] * co;
+              }
+              st_shared_v4(qaddr(c), pack(y1));
+              st_shared_v4(qaddr(c + hr / 8), pack(y2));
+            }
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < rd / 8; ++k) {  // adjacent pairs
+              float x[8], y[8];
+              unpack(ld_shared_v4(qaddr(k)), x);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                float sn, co;
+                turn_sincos_fast(m, turns[k * 4 + w], sn, co);
+                y[2 * w] = x[2 * w] * co - x[2 * w + 1] * sn;
+                y[2 * w + 1] = x[2 * w] * sn + x[2 * w + 1] * co;
+              }
+              st_shared_v4(qaddr(k), pack(y));
+            }
+          }
+          done = rd / 8;
+        }
+#pragma unroll 1
+        for (int k = done; k < D / 8; ++k) {
+          float x[8];
+          unpack(ld_shared_v4(qaddr(k)), x);
+          st_shared_v4(qaddr(k), pack(x));
+        }
+        fence_async_smem();
+      }
+      mbar_arrive(BAR(B_Q_READY));
+    }
+    float slope = 0.f;
+    if constexpr (POS == kAlibi) slope = valid ? a.pos.slopes[h] * 1.4426950408889634f : 0.f;
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t tS = tl + uint32_t(sl * kN), tO = tl + uint32_t(2 * kN + sl * 128);
+    const float2 ff = make_float2(f, f);
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int k = 0; ok && 2 * k + sl < nsteps; ++k) {
+      const int j = two ? k : 2 * k + sl, slot = j % kSlots;
+      const bool got = wait_bar(BAR(B_S_FULL + sl), uint32_t(k & 1), abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      const bool fast = flags[slot] != 0;
+      uint32_t v[kN];
+#pragma unroll
+      for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + uint32_t(32 * c), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+      tmem_wait_ld();
+      // ALiBi's bias -slope (m - p), p = pstart + t: slope t on each score, slope (pstart - m) on the page's maximum and
+      // on its exponents' offset
+      float bpg[kPagesPerTile];
+      if constexpr (POS == kAlibi) {
+#pragma unroll
+        for (int pp = 0; pp < kPagesPerTile; ++pp) {
+          bpg[pp] = slope * float(pstart[slot * kPagesPerTile + pp] - m_row);
+#pragma unroll
+          for (int t = 0; t < kPage; t += 2) {
+            float2 x = make_float2(__uint_as_float(v[pp * kPage + t]), __uint_as_float(v[pp * kPage + t + 1]));
+            x = __ffma2_rn(x, ff, make_float2(slope * float(t), slope * float(t + 1)));
+            v[pp * kPage + t] = __float_as_uint(x.x);
+            v[pp * kPage + t + 1] = __float_as_uint(x.y);
+          }
+        }
+      }
+      if (!fast) {  // stage row t of a page holds key pstart + t, from row `lo` on
+#pragma unroll
+        for (int pp = 0; pp < kPagesPerTile; ++pp) {
+          const int lo = pinfo[slot * kPagesPerTile + pp].y, hi = m_row - pstart[slot * kPagesPerTile + pp] + 1;
+#pragma unroll
+          for (int t = 0; t < kPage; ++t)
+            if (!(t >= lo && t < hi)) v[pp * kPage + t] = __float_as_uint(-INFINITY);
+        }
+      }
+      float mq[kPagesPerTile];
+#pragma unroll
+      for (int q = 0; q < kPagesPerTile; ++q) {
+        const float* x = reinterpret_cast<const float*>(v + 16 * q);
+        float m = max3f(x[0], x[1], x[2]);
+#pragma unroll
+        for (int e = 3; e < 15; e += 2) m = max3f(m, x[e], x[e + 1]);
+        mq[q] = fmaxf(m, x[15]);
+        if constexpr (POS == kAlibi) mq[q] += bpg[q];
+      }
+      float mx = max3f(max3f(mq[0], mq[1], mq[2]), max3f(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
+      if constexpr (POS != kAlibi) mx *= f;
+      const bool need = mx > m_run + kTau;
+      const float m_new = need ? mx : m_run;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int e = 0; e < kN / 2; ++e) {
+        float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        if constexpr (POS == kAlibi) {
+          const float o = bpg[e / (kPage / 2)] - m_use;
+          x = __fadd2_rn(x, make_float2(o, o));
+        } else {
+          x = __ffma2_rn(x, ff, make_float2(-m_use, -m_use));
+        }
+        const float2 ev = make_float2(ex2(x.x), ex2(x.y));
+        sum4[e & 3] = __fadd2_rn(sum4[e & 3], ev);
+        v[e] = f2_to_bf2(ev.x, ev.y);
+      }
+      const float2 s03 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
+      const float alpha = (need && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
+      l_run = l_run * alpha + (s03.x + s03.y);
+      if (__any_sync(0xffffffffu, k > 0 && alpha != 1.f)) {  // O holds the products of the steps before
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + uint32_t(c * 32), o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(tO + uint32_t(c * 32), o);
+        }
+      }
+      m_run = m_new;
+#pragma unroll
+      for (int c = 0; c < kN / 64; ++c) tmem_st32(tS + uint32_t(32 * c), *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(BAR(B_P_FULL + sl));
+    }
+    ok = ok && wait_bar(BAR(B_FINAL), 0, abort_flag, a.status);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      // what a row's result is relative to; -inf where it has seen no key (a NaN stays)
+      float M = l_run == 0.f ? -INFINITY : (m_run == -INFINITY ? 0.f : m_run), Lt = l_run;
+      const size_t pi = ((size_t)b * a.Hq + h) * (a.SA + a.SB) + split;
+      float4* dst = reinterpret_cast<float4*>(a.part_o + pi * D);
+      if (two) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + uint32_t(c * 32), o);
+          tmem_wait_ld();
+          if (valid)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[c * 8 + q] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
+                                           __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
+        }
+      } else {
+        // Even and odd tiles joined; each warpgroup writes half of the columns.  (The exchange is in the second Q tile.)
+        float2* xml = reinterpret_cast<float2*>(sm + L::QTILE);
+        xml[sl * kM + r] = make_float2(M, Lt);
+        named_sync(1, 2 * kM);
+        const float2 hA = xml[r], hB = xml[kM + r];
+        M = fmaxf(hA.x, hB.x);
+        const float wA = hA.x == -INFINITY ? 0.f : ex2(hA.x - M), wB = hB.x == -INFINITY ? 0.f : ex2(hB.x - M);
+        Lt = (wA != 0.f ? wA * hA.y : 0.f) + (wB != 0.f ? wB * hB.y : 0.f);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          const int col = sl * (D / 2) + c * 32;
+          uint32_t oa[32], ob[32];
+          tmem_ld32(tl + uint32_t(2 * kN + col), oa);
+          tmem_ld32(tl + uint32_t(3 * kN + col), ob);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = (wA != 0.f ? wA * __uint_as_float(oa[e]) : 0.f) + (wB != 0.f ? wB * __uint_as_float(ob[e]) : 0.f);
+          if (valid)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[col / 4 + q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+      if (valid && (two || sl == 0)) {
+        a.part_ml[pi * 2] = M;
+        a.part_ml[pi * 2 + 1] = Lt;
+      }
+    }
+  } else if (warp < kKWarp) {
+    // ============================ keys: rotation by the page's Delta, f16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRot));
+    const int rt = threadIdx.x - kRotWarp0 * 32;
+    const int ps = rt / kPage, l = rt % kPage;  // page slot of the tile, and this thread's part of it
+    constexpr int NCP = D / 16;
+    bool ok = true;  // once a wait gives up, the thread skips the work but keeps arriving
+    float co[8], sn[8];
+    int cur = -1;
+    // other than half-split rotation of the whole head: one chunk task for all 16 rows of the page (0: rotated chunk
+    // pair, 1: chunk of adjacent pairs, 2: a chunk that is only converted, 3: none)
+    int kind = 3, chunk8 = 0, part = 0, f0 = 0;
+    if constexpr (POS != kRope) {
+      const int rd = POS == kRopeX ? a.pos.rotary_dim : 0;
+      const int nrot = a.pos.interleaved ? rd / 8 : rd / 16, ntail = (D - rd) / 8;
+      if (l < nrot) {
+        kind = a.pos.interleaved ? 1 : 0;
+        chunk8 = l;
+        part = l + rd / 16;
+        f0 = a.pos.interleaved ? 4 * l : 8 * l;
+      } else if (l < nrot + ntail) {
+        kind = 2;
+        chunk8 = rd / 8 + (l - nrot);
+      }
+    }
+    for (int j = 0; j < ntiles; ++j) {
+      const int s = j % kKStages, slot = j % kSlots;
+      if (ok) ok = wait_bar(BAR(B_K_FULL + s), uint32_t((j / kKStages) & 1), abort_flag, a.status);
+      const int2 pi = ok ? pinfo[slot * kPagesPerTile + ps] : make_int2(0, kPage);
+      const uint32_t sK = sK0 + uint32_t(s * L::TILE);
+      if (pi.y < kPage) {
+        if constexpr (POS == kRope) {
+          const int c = l % NCP, g = l / NCP;
+          if (pi.x != cur) {
+            cur = pi.x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn_sincos_fast(uint32_t(pi.x), turns[8 * c + e], sn[e], co[e]);
+          }
+#pragma unroll
+          for (int i = 0; i < NCP; ++i) {
+            const int t = g * NCP + i;
+            if (t < pi.y) continue;
+            const int r = ps * kPage + t;
+            const uint32_t a1 = sK + swz(r, c);
+            const uint32_t a2 = D == 128 ? sK + uint32_t(L::BLK) + swz(r, c) : sK + swz(r, c + 4);
+            uint4 u1 = ld_shared_v4(a1), u2 = ld_shared_v4(a2);
+            uint32_t* p1 = reinterpret_cast<uint32_t*>(&u1);
+            uint32_t* p2 = reinterpret_cast<uint32_t*>(&u2);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 cv = make_float2(co[2 * w], co[2 * w + 1]), sv = make_float2(sn[2 * w], sn[2 * w + 1]);
+              const float2 x1 = bf2_to_f2(p1[w]), x2 = bf2_to_f2(p2[w]);
+              const float2 t1 = __fmul2_rn(x2, sv), t2 = __fmul2_rn(x2, cv);
+              const float2 y1 = __ffma2_rn(x1, cv, make_float2(-t1.x, -t1.y)), y2 = __ffma2_rn(x1, sv, t2);
+              p1[w] = f2_to_h2(y1.x, y1.y);
+              p2[w] = f2_to_h2(y2.x, y2.y);
+            }
+            st_shared_v4(a1, u1);
+            st_shared_v4(a2, u2);
+          }
+        } else {
+          auto kaddr = [&](int r, int k) { return sK + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
+          if (POS == kRopeX && kind < 2 && pi.x != cur) {
+            cur = pi.x;
+            const int nf = kind == 0 ? 8 : 4;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < nf) turn_sincos_fast(uint32_t(pi.x), turns[f0 + e], sn[e], co[e]);
+          }
+#pragma unroll 1
+          for (int t = pi.y; t < kPage && kind < 3; ++t) {
+            const int r = ps * kPage + t;
+            const uint32_t a1 = kaddr(r, chunk8);
+            uint4 u1 = ld_shared_v4(a1);
+            uint32_t* p1 = reinterpret_cast<uint32_t*>(&u1);
+            if (POS == kRopeX && kind == 0) {
+              const uint32_t a2 = kaddr(r, part);
+              uint4 u2 = ld_shared_v4(a2);
+              uint32_t* p2 = reinterpret_cast<uint32_t*>(&u2);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float2 x1 = bf2_to_f2(p1[w]), x2 = bf2_to_f2(p2[w]);
+                p1[w] = f2_to_h2(x1.x * co[2 * w] - x2.x * sn[2 * w], x1.y * co[2 * w + 1] - x2.y * sn[2 * w + 1]);
+                p2[w] = f2_to_h2(x1.x * sn[2 * w] + x2.x * co[2 * w], x1.y * sn[2 * w + 1] + x2.y * co[2 * w + 1]);
+              }
+              st_shared_v4(a2, u2);
+            } else if (POS == kRopeX && kind == 1) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float x0 = bf_lo(p1[w]), x1 = bf_hi(p1[w]);
+                p1[w] = f2_to_h2(x0 * co[w] - x1 * sn[w], x0 * sn[w] + x1 * co[w]);
+              }
+            } else {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) p1[w] = f2_to_h2(bf_lo(p1[w]), bf_hi(p1[w]));
+            }
+            st_shared_v4(a1, u1);
+          }
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(BAR(B_K_READY + s));
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    const uint64_t* words = a.meta + (size_t)b0 * a.max_blocks;
+    // With ALiBi the newest tiles come first: they hold the rows' maxima, so O is hardly ever rescaled.
+    auto tile_of = [&](int j) { return POS == kAlibi ? t0 + ntiles - 1 - j : t0 + j; };
+    auto fetch = [&](int j) -> uint64_t {  // lane < 8: the block word of its page slot
+      const int jb = tile_of(j) * kPagesPerTile + lane;
+      return lane < kPagesPerTile && j < ntiles && jb < nb ? ldg_u64(words + jb) : 0ull;
+    };
+    auto keys_of = [&](uint64_t w) {  // 0 behind the list and outside the cache
+      return word_page(w) < uint32_t(a.num_pages) ? min(int(word_nvalid(w)), kPage) : 0;
+    };
+    if (warp == kKWarp) {
+      // ============================ block words, K copies
+      int m_min = INT_MAX;  // of the block's rows
+      for (int i = row0 / G + lane; i <= (row0 + rows - 1) / G; i += 32) m_min = min(m_min, a.seq_len[b0 + i] - 1);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m_min = min(m_min, __shfl_xor_sync(0xffffffffu, m_min, o));
+      uint64_t w_next = fetch(0);
+      int issued = 0;
+      bool ok = true;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int s = j % kKStages, slot = j % kSlots;
+        const uint64_t w = w_next;
+        w_next = fetch(j + 1);
+        const int rows_k = keys_of(w), lo = kPage - rows_k, delta = int(word_delta(w));
+        const int start = delta + kPage * int(word_pg(w));
+        if (word_page(w) >= uint32_t(a.num_pages)) set_status(a.status, LAZY_STATUS_BAD_PAGE);
+        if (j >= kKStages) {
+          const bool freed = wait_bar(BAR(B_K_FREE + s), uint32_t((j / kKStages - 1) & 1), abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, freed);
+          if (!ok) break;
+        }
+        if (lane < kPagesPerTile) {
+          pinfo[slot * kPagesPerTile + lane] = make_int2(delta, lo);
+          pstart[slot * kPagesPerTile + lane] = start - lo;
+        }
+        const bool all = __all_sync(0xffffffffu, lane >= kPagesPerTile || (rows_k == kPage && start + kPage - 1 <= m_min));
+        const uint32_t load = __ballot_sync(0xffffffffu, lane < kPagesPerTile && rows_k > 0);
+        if (lane == 0) {
+          flags[slot] = all;
+          mbar_arrive_expect_tx(BAR(B_K_FULL + s), uint32_t(__popc(load)) * kPage * D * 2);
+        }
+        __syncwarp();
+        if ((load >> lane) & 1u)
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_page(sK0 + uint32_t(s * L::TILE + cb * L::BLK + lane * kPage * 128), &tmk, cb * 64, -lo,
+                          int(word_page(w)) * a.Hkv + kvh, BAR(B_K_FULL + s));
+        __syncwarp();
+        issued = j + 1;
+      }
+      if (lane == 0)  // never leave copies in flight
+        for (int j = max(0, issued - kKStages); j < issued; ++j) {
+          WaitClock clk;
+          while (!mbar_test(BAR(B_K_FULL + j % kKStages), uint32_t((j / kKStages) & 1)) && !clk.expired()) {
+          }
+        }
+    } else if (warp == kVWarp) {
+      // ============================ V copies
+      uint64_t w_next = fetch(0);
+      int issued = 0;
+      bool ok = true;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int s = j % kVStages;
+        const uint64_t w = w_next;
+        w_next = fetch(j + 1);
+        const int rows_v = keys_of(w), lo = kPage - rows_v;
+        if (j >= kVStages) {
+          const bool freed = wait_bar(BAR(B_V_FREE + s), uint32_t((j / kVStages - 1) & 1), abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, freed);
+          if (!ok) break;
+        }
+        const uint32_t sV = sV0 + uint32_t(s * L::TILE);
+        const uint32_t load = __ballot_sync(0xffffffffu, lane < kPagesPerTile && rows_v > 0);
+        const uint32_t empty = ~load & ((1u << kPagesPerTile) - 1u);
+        if (empty) {  // page slots without keys meet PV with zero weights, and must not hold a NaN
+          for (int pp = 0; pp < kPagesPerTile; ++pp) {
+            if (!((empty >> pp) & 1u)) continue;
+#pragma unroll
+            for (int cb = 0; cb < D / 64; ++cb)
+#pragma unroll
+              for (int i = 0; i < kPage * 8 / 32; ++i)
+                st_shared_v4(sV + uint32_t(cb * L::BLK) + swz(pp * kPage + (i * 32 + lane) / 8, (i * 32 + lane) % 8),
+                             make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(BAR(B_V_FULL + s), uint32_t(__popc(load)) * kPage * D * 2);
+        __syncwarp();
+        if ((load >> lane) & 1u)
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_page(sV + uint32_t(cb * L::BLK + lane * kPage * 128), &tmv, cb * 64, -lo,
+                          int(word_page(w)) * a.Hkv + kvh, BAR(B_V_FULL + s));
+        __syncwarp();
+        issued = j + 1;
+      }
+      if (lane == 0)
+        for (int j = max(0, issued - kVStages); j < issued; ++j) {
+          WaitClock clk;
+          while (!mbar_test(BAR(B_V_FULL + j % kVStages), uint32_t((j / kVStages) & 1)) && !clk.expired()) {
+          }
+        }
+    } else if (warp == kMmaWarp) {
+      // ============================ products (one thread)
+      if (elect_one()) {
+        constexpr uint32_t IQK = idesc_mma(kM, kN, 0, 1), IPV = idesc_mma(kM, D, 1, 0);
+        const uint64_t qd = sdesc(sQ0, 16, 1024), kd = sdesc(sK0, 16, 1024), vd = sdesc(sV0, L::BLK, 1024);
+        bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
+        int ks = 0, vs = 0;            // stages of the next QK^T's and PV's tiles
+        uint32_t kpar = 0, vpar = 0;
+        auto qk = [&](int s) -> bool {  // step s: scores into buffer s % 2
+          const bool first = !two || !(s & 1), last = !two || (s & 1);
+          if (first && !wait_bar(BAR(B_K_READY + ks), kpar, abort_flag, a.status)) return false;
+          tc_fence_after();
+          const uint64_t k0 = kd + uint64_t(ks * (L::TILE >> 4));
+          auto go = [&](uint32_t d, uint64_t q0) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              constexpr uint64_t blk = L::BLK >> 4;
+              mma_bf16(d, q0 + (kk >> 2) * blk + (kk & 3) * 2, k0 + (kk >> 2) * blk + (kk & 3) * 2, IQK, kk > 0 ? 1u : 0u);
+            }
+          };
+          if (s & 1)
+            go(tmem + kN, two ? qd + (L::QTILE >> 4) : qd);
+          else
+            go(tmem, qd);
+          mma_commit(BAR(B_S_FULL + (s & 1)));
+          if (last) {
+            mma_commit(BAR(B_K_FREE + ks));
+            if (++ks == kKStages) {
+              ks = 0;
+              kpar ^= 1u;
+            }
+          }
+          return true;
+        };
+        if (ok) ok = qk(0);
+        if (ok && nsteps > 1) ok = qk(1);
+        for (int s = 0; s < nsteps && ok; ++s) {
+          const bool first = !two || !(s & 1), last = !two || (s & 1);
+          ok = wait_bar(BAR(B_P_FULL + (s & 1)), uint32_t((s >> 1) & 1), abort_flag, a.status) &&
+               (!first || wait_bar(BAR(B_V_FULL + vs), vpar, abort_flag, a.status));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v0 = vd + uint64_t(vs * (L::TILE >> 4));
+          auto go = [&](uint32_t o, uint32_t p) {
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+              mma_ts(o, p + uint32_t(kk * 8), v0 + uint64_t(kk * (16 * 128 >> 4)), IPV, (s > 1 || kk > 0) ? 1u : 0u);
+          };
+          if (s & 1)
+            go(tmem + 3 * kN, tmem + kN);
+          else
+            go(tmem + 2 * kN, tmem);
+          if (last) {
+            mma_commit(BAR(B_V_FREE + vs));
+            if (++vs == kVStages) {
+              vs = 0;
+              vpar ^= 1u;
+            }
+          }
+          if (s + 2 < nsteps) ok = qk(s + 2);
+        }
+        mma_commit(BAR(B_FINAL));  // every product is done before O is read, and before TMEM goes
+        WaitClock clk;
+        while (!mbar_test(BAR(B_FINAL), 0) && !clk.expired()) {
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int D, int POS>
+int launch_prefix(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  using L = Layout<D>;
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> regs{0};
+  auto kern = prefix_kernel<D, POS>;
+  LAZY_CUDA_TRY(smem_limit(kern, L::SMEM, done));
+  if (!regs.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa;
+    LAZY_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  // the split of registers is only valid for the number that it was made for
+  if (regs.load(std::memory_order_relaxed) != kRegsLaunch)
+    return fail(LAZY_ECUDA, "shared decode kernel built with %d registers per thread, expected %d",
+                regs.load(std::memory_order_relaxed), kRegsLaunch);
+  const long long rows = (long long)a.max_group * (a.Hq / a.Hkv);
+  const unsigned pairs = unsigned((rows + 2 * kM - 1) / (2 * kM));
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(unsigned(a.SA) * pairs, a.Hkv, a.n_groups), dim3(kThreads), L::SMEM, st, mk, mv, a,
+                           q4_lowest_exponent(a.pos.scale_log2)));
+  return LAZY_OK;
+}
+
+}  // namespace
+
+// Key splits of the common keys (0: too little to share, every request is decoded alone).
+int shared_prefix_splits(int n_groups, int max_group, int max_shared, int Hq, int Hkv) {
+  if (n_groups <= 0 || max_group <= 0 || max_shared <= 0) return 0;
+  const int sms = sm_count(), tiles = (max_shared + kPagesPerTile - 1) / kPagesPerTile;
+  const long long rows = (long long)max_group * (Hq / Hkv), pairs = (rows + 2 * kM - 1) / (2 * kM);
+  const long long units = (long long)n_groups * Hkv * pairs;
+  // Time of a launch in tiles: waves of blocks, each its tiles and about 4 for its start and its results.
+  long long best = 0;
+  int S = 1;
+  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+    const long long t = ((units * s + sms - 1) / sms) * ((tiles + s - 1) / s + 4);
+    if (s == 1 || t < best) {
+      best = t;
+      S = s;
+    }
+  }
+  return S;
+}
+
+int run_shared_prefix(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
+  if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
+  if (D == 128) {
+    if (kind == kRope) return launch_prefix<128, kRope>(a, mk, mv, st);
+    if (kind == kRopeX) return launch_prefix<128, kRopeX>(a, mk, mv, st);
+    if (kind == kAlibi) return launch_prefix<128, kAlibi>(a, mk, mv, st);
+    return launch_prefix<128, kNone>(a, mk, mv, st);
+  }
+  if (kind == kRope) return launch_prefix<64, kRope>(a, mk, mv, st);
+  if (kind == kRopeX) return launch_prefix<64, kRopeX>(a, mk, mv, st);
+  if (kind == kAlibi) return launch_prefix<64, kAlibi>(a, mk, mv, st);
+  return launch_prefix<64, kNone>(a, mk, mv, st);
+}
+
+}  // namespace lazykv
