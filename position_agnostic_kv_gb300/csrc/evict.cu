@@ -87,7 +87,239 @@ __device__ __forceinline__ int scan_before(int x, int* buf, int& total) {
   return r;
 }
 
-// One block of threads per request.  Thread t owns a run of consecutive list blocks, so that prefix sums over
+// The scan of `me` over the threads: what lies before this thread, and the whole.
+__device__ __forceinline__ Packed scan_packed(Packed me, Packed* pbuf, Packed& whole) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Packed inc = me;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Packed y = shfl_up(inc, o);
+    if (lane >= o) inc = join(y, inc);
+  }
+  if (lane == 31) pbuf[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    Packed x = pbuf[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Packed y = shfl_up(x, o);
+      if (lane >= o) x = join(y, x);
+    }
+    pbuf[lane] = x;
+  }
+  __syncthreads();
+  Packed pre = shfl_up(inc, 1);
+  if (lane == 0) pre = Packed{0, 0, 0, 0};
+  if (warp > 0) pre = join(pbuf[warp - 1], pre);
+  whole = pbuf[kWarps - 1];
+  return pre;
+}
+
+// The new word of list block `blk` with its document's kept keys [16 pg, 16 pg + rows).
+__device__ __forceinline__ void put_word(const PlanArgs& a, uint64_t* new_meta, const int32_t* pages, int blk, int pg,
+                                         int rows, uint32_t delta) {
+  const int page = blk < a.max_dst ? pages[blk] : -1;
+  const bool bad = page < 0 || page >= a.num_pages;
+  if (bad) set_status(a.status, LAZY_STATUS_BAD_PAGE);
+  new_meta[blk] = uint64_t(bad ? 0 : rows) | uint64_t(pg) << 5 | uint64_t(delta) << 16 | uint64_t(bad ? 0 : page) << 40;
+}
+
+// Lists of up to 64 IT document blocks: one block of threads per request, the ordered weights in registers (key
+// 1024 i + t of the list is thread t's i-th).  The keep-th largest is found in digits of 11, 11 and 10 bits (the first
+// takes sign, exponent and two bits of fraction, which spreads weights over enough counters).  Kept keys are 16 bits
+// per list block; a scan over the blocks then gives each block the place of its first kept key in the new list.
+template <int IT>
+__global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const PlanArgs a) {
+  constexpr int kBlocks = 64 * IT, kPer = (kBlocks + kPlanThreads - 1) / kPlanThreads;
+  constexpr int kBins = 2048;
+  __shared__ int hist[kBins];
+  __shared__ int buf[kWarps];
+  __shared__ Packed pbuf[kWarps];
+  __shared__ int place[kBlocks];       // keys before the block; then the new place of its first kept key
+  __shared__ int base[kBlocks];        // first new block of its document
+  __shared__ uint16_t stays[kBlocks];  // kept keys
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_left, s_same;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const size_t MB = a.max_blocks;
+  const uint64_t* meta = a.meta + b * MB;
+  const float* w = a.weights + b * MB * kPage;
+  uint64_t* new_meta = a.new_meta + b * MB;
+  float* new_w = a.new_weights + b * MB * kPage;
+  const int32_t* pages = a.dst_pages + (size_t)b * a.max_dst;
+  int32_t* src = a.src_slot + (size_t)b * a.max_dst * kPage;
+  int32_t* dst = a.dst_slot + (size_t)b * a.max_dst * kPage;
+  const int nd = min(max(a.doc_blocks[b], 0), a.max_blocks);
+  const int want = a.keep[b];
+  uint32_t v[IT];  // the weights, all loads in flight at once; then their ordered values, 0 where no key lies, NaN 1
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = i * kPlanThreads + tid;
+    v[i] = k < nd * kPage ? __float_as_uint(w[k]) : 0u;
+  }
+  // this thread's list blocks: kPer consecutive ones, so that scans over the threads are scans over the list
+  uint64_t word[kPer + 2];  // and a neighbour on either side
+#pragma unroll
+  for (int e = 0; e < kPer + 2; ++e) {
+    const int j = tid * kPer + e - 1;
+    word[e] = j >= 0 && j < nd ? meta[j] : 0;
+  }
+  for (int i = tid; i < a.max_dst * kPage; i += kPlanThreads) src[i] = dst[i] = -1;
+  if (want < 0) {
+    for (int i = tid; i < a.max_blocks; i += kPlanThreads) new_meta[i] = meta[i];
+    for (int i = tid; i < a.max_blocks * kPage; i += kPlanThreads) new_w[i] = w[i];
+    if (tid == 0) a.new_doc_blocks[b] = nd;
+    return;
+  }
+  if (tid == 0) {
+    s_prefix = 0;
+    if (a.doc_blocks[b] > a.max_blocks) set_status(a.status, LAZY_STATUS_BAD_ROW);
+  }
+
+  int nv[kPer], mine = 0, total;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) mine += nv[e] = min(int(word_nvalid(word[e + 1])), kPage);
+  int before = scan_before(mine, buf, total);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int j = tid * kPer + e;
+    if (j < kBlocks) {
+      place[j] = before;
+      stays[j] = uint16_t(nv[e]);
+    }
+    before += nv[e];
+  }
+  const int keep = min(want, total);
+  __syncthreads();
+
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = (i * kPlanThreads + tid) / kPage, t = tid % kPage, rank = place[j] + t;
+    const uint32_t x = rank < a.first || rank >= total - a.recent ? kProtected : max(order_of(__uint_as_float(v[i])), 1u);
+    v[i] = j < nd && t < stays[j] ? x : 0u;
+  }
+
+  // ---- the keep-th largest value, `limit`, of which `ties` equals stay
+  int ties = keep;
+  uint32_t limit = 0;
+  if (keep > 0) {
+#pragma unroll
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bins = round == 2 ? 1024 : kBins;
+      const uint32_t mask = round == 0 ? 0u : 0xFFFFFFFFu << (round == 1 ? 21 : 10);
+      hist[tid] = hist[tid + 1024] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+        if (v[i] != 0 && (v[i] & mask) == limit) atomicAdd(&hist[(v[i] >> shift) & (bins - 1)], 1);
+      __syncthreads();
+      // thread t holds the digits bins - 1 - 2 t and the one below
+      const int d = kBins - 1 - 2 * tid;
+      const int c0 = d < bins ? hist[d] : 0, c1 = d < bins ? hist[d - 1] : 0;
+      int all;
+      const int above = scan_before(c0 + c1, buf, all);
+      if (above < ties && ties <= above + c0 + c1) {
+        const bool second = ties > above + c0;
+        s_prefix = limit | uint32_t(second ? d - 1 : d) << shift;
+        s_left = ties - above - (second ? c0 : 0);
+        s_same = second ? c1 : c0;
+      }
+      __syncthreads();
+      limit = s_prefix;
+      ties = s_left;
+    }
+  }
+
+  // ---- who stays, 16 bits per list block; among equals the earlier in the list
+  if (keep > 0 && s_same != ties) {  // (uniform) not all of them: count the equals before each warp's keys
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, v[i] == limit);
+      if (lane == 0) hist[i * kWarps + warp] = __popc(eq);
+    }
+    __syncthreads();
+    int sum;
+    const int c = tid < IT * kWarps ? hist[tid] : 0, c_before = scan_before(c, buf, sum);
+    if (tid < IT * kWarps) hist[tid] = c_before;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    bool stay = keep > 0 && v[i] >= limit && v[i] != 0;
+    if (keep > 0 && s_same != ties) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, v[i] == limit);
+      if (v[i] == limit) stay = hist[i * kWarps + warp] + __popc(eq & ((1u << lane) - 1u)) < ties;
+    }
+    const uint32_t bits = __ballot_sync(0xffffffffu, stay);
+    const int j = (i * kPlanThreads + tid) / kPage;
+    if (lane % kPage == 0) stays[j] = uint16_t(bits >> lane);
+  }
+  __syncthreads();
+
+  // ---- packing, document by document
+  uint32_t kept[kPer];
+  bool starts[kPer], ends[kPer];
+  Packed me = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int j = tid * kPer + e;
+    const uint32_t delta = word_delta(word[e + 1]);
+    kept[e] = j < nd ? __popc(uint32_t(stays[j])) : 0;
+    starts[e] = j < nd && (j == 0 || word_delta(word[e]) != delta);
+    ends[e] = j < nd && (j + 1 == nd || word_delta(word[e + 2]) != delta);
+    if (starts[e]) me = join(me, Packed{1, 0, 0, 0});
+    if (me.starts) me.tail += kept[e]; else me.head += kept[e];
+  }
+  Packed whole;
+  const Packed pre = scan_packed(me, pbuf, whole);
+  const int nn = whole.blocks + (whole.starts ? pages_of(whole.tail) : 0);  // document blocks of the new list
+  int first_block = pre.starts ? pre.blocks : 0, run = pre.starts ? pre.tail : 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int j = tid * kPer + e;
+    if (starts[e]) {
+      first_block += pages_of(run);
+      run = 0;
+    }
+    if (j < kBlocks) {
+      place[j] = first_block * kPage + run;
+      base[j] = first_block;
+    }
+    run += kept[e];
+    if (ends[e] && run % kPage)
+      put_word(a, new_meta, pages, first_block + run / kPage, run / kPage, run % kPage, word_delta(word[e + 1]));
+  }
+
+  // ---- the rest of the new list: the query segment's blocks and weights, and zeros
+  for (int i = tid; i < nn * kPage; i += kPlanThreads) new_w[i] = 0.f;
+  for (int i = tid + nn; i < a.max_blocks; i += kPlanThreads) new_meta[i] = i - nn + nd < a.max_blocks ? meta[i - nn + nd] : 0;
+  for (int i = tid + nn * kPage; i < a.max_blocks * kPage; i += kPlanThreads)
+    new_w[i] = i + (nd - nn) * kPage < a.max_blocks * kPage ? w[i + (nd - nn) * kPage] : 0.f;
+  if (tid == 0) a.new_doc_blocks[b] = nn;
+  __syncthreads();
+
+  // ---- kept keys: slots, weights, and the words of full pages
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = (i * kPlanThreads + tid) / kPage, t = tid % kPage;
+    if (j >= nd) break;
+    const uint32_t bits = stays[j];
+    if (!((bits >> t) & 1u)) continue;
+    const int at = place[j] + __popc(bits & ((1u << t) - 1u)), blk = at / kPage, row = at % kPage;
+    const uint64_t here = meta[j];
+    const int page = blk < a.max_dst ? pages[blk] : -1;
+    if (page >= 0 && page < a.num_pages) {
+      src[at] = int(word_page(here)) * kPage + t;
+      dst[at] = page * kPage + row;
+      new_w[at] = w[i * kPlanThreads + tid];
+    }
+    if (row == kPage - 1) put_word(a, new_meta, pages, blk, blk - base[j], kPage, word_delta(here));
+  }
+}
+
+// Longer lists.  One block of threads per request.  Thread t owns a run of consecutive list blocks, so that prefix sums over
 // the threads are prefix sums over the list.  The keep-th largest weight is found digit by digit (8 bits of
 // the ordered value at a time, counts in shared memory); keys above it stay, and as many of its equals as are
 // needed, in list order.
@@ -205,28 +437,8 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const PlanArgs
   }, [&](int, int, uint64_t) {
     if (me.starts) ++me.tail; else ++me.head;
   }, [](uint64_t) {});
-  Packed inc = me;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Packed y = shfl_up(inc, o);
-    if (lane >= o) inc = join(y, inc);
-  }
-  if (lane == 31) pbuf[warp] = inc;
-  __syncthreads();
-  if (warp == 0) {
-    Packed x = pbuf[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Packed y = shfl_up(x, o);
-      if (lane >= o) x = join(y, x);
-    }
-    pbuf[lane] = x;
-  }
-  __syncthreads();
-  Packed pre = shfl_up(inc, 1);
-  if (lane == 0) pre = Packed{0, 0, 0, 0};
-  if (warp > 0) pre = join(pbuf[warp - 1], pre);
-  const Packed whole = pbuf[kWarps - 1];
+  Packed whole;
+  const Packed pre = scan_packed(me, pbuf, whole);
   const int nn = whole.blocks + (whole.starts ? pages_of(whole.tail) : 0);  // document blocks of the new list
 
   // ---- the rest of the new list: the query segment's blocks and weights, and zeros
@@ -243,13 +455,8 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const PlanArgs
   // ---- kept keys: slots, weights, words
   int base = pre.blocks, run = pre.tail;  // new blocks before the document, kept keys of it so far
   if (!pre.starts) base = run = 0;
-  auto put_word = [&](int rows, uint64_t word) {  // of the page that holds the document's kept key `run - 1`
-    const int blk = base + (run - 1) / kPage;
-    const int page = blk < a.max_dst ? pages[blk] : -1;
-    const bool bad = page < 0 || page >= a.num_pages;
-    if (bad) set_status(a.status, LAZY_STATUS_BAD_PAGE);
-    new_meta[blk] = uint64_t(bad ? 0 : rows) | uint64_t((run - 1) / kPage) << 5 | uint64_t(word_delta(word)) << 16 |
-                    uint64_t(bad ? 0 : page) << 40;
+  auto put = [&](int rows, uint64_t word) {  // of the page that holds the document's kept key `run - 1`
+    put_word(a, new_meta, pages, base + (run - 1) / kPage, (run - 1) / kPage, rows, word_delta(word));
   };
   walk([&] {
     base += pages_of(run);
@@ -263,9 +470,9 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const PlanArgs
       dst[blk * kPage + row] = page * kPage + row;
       new_w[(size_t)blk * kPage + row] = w[(size_t)j * kPage + t];
     }
-    if (row == kPage - 1) put_word(kPage, word);
+    if (row == kPage - 1) put(kPage, word);
   }, [&](uint64_t word) {
-    if (run % kPage) put_word(run % kPage, word);
+    if (run % kPage) put(run % kPage, word);
   });
 }
 
@@ -333,7 +540,8 @@ extern "C" int lazy_evict_plan(const float* weights, const uint64_t* meta, const
   if (rc || B == 0) return rc;
   const PlanArgs a = {weights,  meta,     doc_blocks,  keep,          dst_pages, new_meta, new_doc_blocks, src_slot,
                       dst_slot, new_weights, status_word(), first,    recent,    max_dst,  max_blocks,     num_pages};
-  LAZY_CUDA_TRY(launch_pdl(evict_plan_kernel, dim3(B), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), a));
+  auto kern = max_blocks <= 256 ? evict_plan_short_kernel<4> : max_blocks <= 2048 ? evict_plan_short_kernel<32> : evict_plan_kernel;
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(B), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), a));
   return LAZY_OK;
 }
 

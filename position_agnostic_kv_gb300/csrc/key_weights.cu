@@ -707,6 +707,7 @@ __global__ void __launch_bounds__(256) weights_sum_kernel(const Args a) {
         for (int g = 0; g < r.rgc; ++g) {
           const int last = min(r.R, group_start(r, g + 1) * r.size) - 1;
           if (p <= r.m0 + last / (a.Hq / a.Hkv))
+#pragma unroll 8
             for (int h = 0; h < a.halves * a.Hkv; ++h) t += a.part[((size_t)g * a.halves * a.Hkv + h) * n + at];
         }
     }

@@ -8,32 +8,73 @@ namespace lazykv {
 
 namespace {
 
-// A row's partial results joined by their maxima: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// A row's partial results joined by their maxima: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  One warp per
+// row: its lanes take the maxima and sums of up to 4 partial results each, then the columns.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const SharedArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SharedArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x, b = blockIdx.y, col = threadIdx.x;
+  constexpr int V = D / 32;  // columns per lane
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= (long long)a.B * a.Hq) return;
+  const int b = int(row / a.Hq);
   const Share sh = share_of(a, b);
-  const int tiles = (sh.blocks + 7) / 8;
-  const int na = tiles ? (tiles + split_tiles(tiles, a.SA) - 1) / split_tiles(tiles, a.SA) : 0;
+  const int tiles = (sh.blocks + 7) / 8, chunk = tiles ? split_tiles(tiles, a.SA) : 1, na = (tiles + chunk - 1) / chunk;
   const int nb = visible_blocks(a.seq_len[b], a.q_start[b], a.doc_blocks[b], a.max_blocks);
-  const int no = own_splits(max(0, nb - sh.blocks), a.SB);
-  const size_t row = (size_t)b * a.Hq + h, at = row * (a.SA + a.SB);
-  float M = -INFINITY;
-  for (int i = 0; i < na + no; ++i) M = fmaxf(M, a.part_ml[2 * (at + (i < na ? i : a.SA + i - na))]);
-  float O = 0.f, L = 0.f;
-  if (M != -INFINITY)
-    for (int i = 0; i < na + no; ++i) {
-      const size_t s = at + (i < na ? i : a.SA + i - na);
-      const float ms = a.part_ml[2 * s];
-      if (ms == -INFINITY) continue;
-      const float f = exp2f(ms - M);
-      O += f * a.part_o[s * D + col];
-      L += f * a.part_ml[2 * s + 1];
+  const int n = na + own_splits(max(0, nb - sh.blocks), a.SB);
+  const size_t at = (size_t)row * (a.SA + a.SB);
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
+  auto index = [&](int s) { return s < na ? s : a.SA + s - na; };
+  float2 mine[4];
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int s = 32 * e + lane;
+    mine[e] = s < n ? ml[index(s)] : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, mine[e].x);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e] = mine[e].x == -INFINITY ? 0.f : exp2f(mine[e].x - M);
+    if (f[e] != 0.f) L += f[e] * mine[e].y;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float O[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) O[c] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll 4
+    for (int s = 32 * e; s < min(n, 32 * e + 32); ++s) {
+      const float g = __shfl_sync(0xffffffffu, f[e], s & 31);
+      const float* o = a.part_o + (at + index(s)) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(o);
+        if (g != 0.f) {  // a split that saw no key has written nothing
+          O[0] += g * x.x;
+          O[1] += g * x.y;
+          O[2] += g * x.z;
+          O[3] += g * x.w;
+        }
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(o);
+        if (g != 0.f) {
+          O[0] += g * x.x;
+          O[1] += g * x.y;
+        }
+      }
     }
-  a.out[row * D + col] = __float2bfloat16_rn(L > 0.f ? O / L : (L == 0.f ? 0.f : O + L));
-  if (a.lse && col == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (size_t)row * D + lane * V);
+#pragma unroll
+  for (int c = 0; c < V / 2; ++c) out[c] = f2_to_bf2(O[2 * c] * inv, O[2 * c + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -154,8 +195,8 @@ extern "C" int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, co
   if (a.SA > 0) rc = run_shared_prefix(a, D, mk, mv, st);
   if (!rc) rc = run_shared_own(a, D, mk, mv, a.SA > 0, st);
   if (rc) return rc;
-  const dim3 grid(Hq, B);
-  LAZY_CUDA_TRY(D == 128 ? launch_pdl(join_kernel<128>, grid, dim3(128), 0, st, a)
-                         : launch_pdl(join_kernel<64>, grid, dim3(64), 0, st, a));
+  const dim3 grid(unsigned(((long long)B * Hq + kJoinWarps - 1) / kJoinWarps));
+  LAZY_CUDA_TRY(D == 128 ? launch_pdl(join_kernel<128>, grid, dim3(32 * kJoinWarps), 0, st, a)
+                         : launch_pdl(join_kernel<64>, grid, dim3(32 * kJoinWarps), 0, st, a));
   return LAZY_OK;
 }

@@ -36,19 +36,28 @@ __device__ __forceinline__ int shared_blocks_of(const SharedArgs& a, int g) {
 }
 __device__ __forceinline__ Share share_of(const SharedArgs& a, int b) {
   if (a.SA == 0 || b < a.group_off[0] || b >= a.group_off[a.n_groups]) return {-1, 0};
-  int lo = 0, hi = a.n_groups;  // last group with group_off[g] <= b
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.group_off[mid] <= b) lo = mid; else hi = mid;
+  int lo = 0;  // last group with group_off[g] <= b; up to 31 by one load of the warp (every lane has the same b)
+  if (a.n_groups <= 31) {
+    const int lane = threadIdx.x & 31;
+    const bool at = lane < a.n_groups && a.group_off[lane] <= b;
+    lo = 31 - __clz(int(__ballot_sync(0xffffffffu, at)));
+  } else {
+    int hi = a.n_groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.group_off[mid] <= b) lo = mid; else hi = mid;
+    }
   }
   if (b - a.group_off[lo] >= a.max_group) return {-1, 0};
   return {lo, shared_blocks_of(a, lo)};
 }
 
-// Reports a list that is longer than max_blocks, and a group or its common blocks above the call's bounds.
+// Reports a list that is longer than max_blocks, and a group or its common blocks above the call's bounds (a block of
+// threads per request).
 __device__ __forceinline__ void check_request(const SharedArgs& a, int b, int m) {
-  bool bad = m >= a.q_start[b] && (long long)a.doc_blocks[b] + (m - a.q_start[b]) / kPage + 1 > a.max_blocks;
-  for (int g = 0; b == 0 && g < a.n_groups; ++g)
+  bool bad = threadIdx.x == 0 && m >= a.q_start[b] &&
+             (long long)a.doc_blocks[b] + (m - a.q_start[b]) / kPage + 1 > a.max_blocks;
+  for (int g = threadIdx.x; b == 0 && g < a.n_groups; g += blockDim.x)
     bad |= a.group_off[g + 1] - a.group_off[g] > a.max_group || a.shared_blocks[g] > a.max_shared;
   if (bad) set_status(a.status, LAZY_STATUS_BAD_ROW);
 }

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kNW * 32) own_kernel(const __grid_constant__ C
   const Share sh = share_of(a, b);
   const int m = a.seq_len[b] - 1;
   const int nb = visible_blocks(m + 1, a.q_start[b], a.doc_blocks[b], a.max_blocks);
-  if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) check_request(a, b, m);
+  if (split == 0 && blockIdx.y == 0) check_request(a, b, m);
   const int blocks = max(0, nb - sh.blocks), S = own_splits(blocks, a.SB);
   if (split >= S) {  // uniform for the block
     pdl_trigger();
