@@ -132,14 +132,6 @@ __device__ __forceinline__ void unpack8(uint4 u, float2 (&y)[4]) {
   y[2] = bf2_to_f2(u.z);
   y[3] = bf2_to_f2(u.w);
 }
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {  // asks, and never waits
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-
 // Where a block's share of the work begins or ends: total work is cut into equal parts in the order request,
 // KV head, group of row blocks, list block; a list block costs one unit per row block.
 struct Place {

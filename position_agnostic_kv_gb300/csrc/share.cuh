@@ -28,6 +28,14 @@ int check_shared_call(const char* what, int B, int max_blocks, int Hq, int Hkv, 
                       std::initializer_list<const void*> ints);
 int check_workspace(const char* what, const void* ws, size_t got, size_t need);
 
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {  // asks, and never waits
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // sin and cos of p * theta for a signed position difference p.
 __device__ __forceinline__ void turn_sincos_signed(int p, unsigned long long turns, float& s, float& c) {
   const unsigned long long frac = (unsigned long long)(long long)p * turns;

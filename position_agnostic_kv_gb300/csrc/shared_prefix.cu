@@ -45,13 +45,13 @@ constexpr float kTau = 8.0f;
 
 enum : int {
   B_K_FULL = 0,    // [3] K tile landed
-  B_K_READY = 3,   // [3] K tile rotated (128 arrivals)
+  B_K_READY = 3,   // [3] K tile rotated (a lane per warp)
   B_K_FREE = 6,    // [3] every QK^T with the stage done (commit)
   B_V_FULL = 9,    // [2] V tile landed
   B_V_FREE = 11,   // [2] every PV with the stage done (commit)
   B_S_FULL = 13,   // [2] scores written (commit; covers the buffer's PV before)
-  B_P_FULL = 15,   // [2] P in TMEM, O rescaled (128)
-  B_Q_READY = 17,  // Q tiles prepared (256)
+  B_P_FULL = 15,   // [2] P in TMEM, O rescaled (a lane per warp)
+  B_Q_READY = 17,  // Q tiles prepared (a lane per warp)
   B_FINAL = 18,    // all products done (commit)
   NBAR = 19
 };
@@ -67,7 +67,8 @@ struct Layout {
   static constexpr int FLAG_OFF = PINFO_OFF + kSlots * kPagesPerTile * 8;    // int [slot] every key visible to every row
   static constexpr int TURNS_OFF = FLAG_OFF + kSlots * 8;
   static constexpr int BAR_OFF = TURNS_OFF + (D / 2) * 8;
-  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int EXP_OFF = BAR_OFF + NBAR * 8;  // int8 [256] exponents of the rows' powers of two
+  static constexpr int MISC_OFF = EXP_OFF + 2 * kM;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
 };
 static_assert(Layout<128>::SMEM <= 227 * 1024, "shared memory budget");
@@ -83,18 +84,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = int(blockIdx.x) % a.SA, pair = int(blockIdx.x) / a.SA, kvh = blockIdx.y, grp = blockIdx.z;
   const int G = a.Hq / a.Hkv;
-  pdl_wait();
-  pdl_trigger();  // what comes behind and does not wait itself (own_kernel) touches other results
-  const int b0 = max(0, a.group_off[grp]);
-  const int nreq = min(min(a.group_off[grp + 1], a.B) - b0, a.max_group);
-  const int row0 = pair * 2 * kM, rows = min(2 * kM, nreq * G - row0);
-  const int nb = shared_blocks_of(a, grp);
-  const int ntiles_all = (nb + kPagesPerTile - 1) / kPagesPerTile, chunk = split_tiles(ntiles_all, a.SA);
-  const int t0 = split * chunk, ntiles = min(ntiles_all, t0 + chunk) - t0;
-  if (rows <= 0 || ntiles <= 0) return;  // uniform for the block
-  const bool two = rows > kM;
-  const int nsteps = two ? 2 * ntiles : ntiles;
-
   const uint32_t sQ0 = sb, sK0 = sb + L::K_OFF, sV0 = sb + L::V_OFF;
   int* pstart = reinterpret_cast<int*>(sm + L::PSTART_OFF);
   int2* pinfo = reinterpret_cast<int2*>(sm + L::PINFO_OFF);
@@ -105,10 +94,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
 
+  if (threadIdx.x == 32 * kKWarp) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i)
-      mbar_init(BAR(i), (i >= B_K_READY && i < B_K_FREE) || (i >= B_P_FULL && i < B_Q_READY) ? 128
-                        : i == B_Q_READY                                                     ? 256
+      mbar_init(BAR(i), (i >= B_K_READY && i < B_K_FREE) || (i >= B_P_FULL && i < B_Q_READY) ? 4
+                        : i == B_Q_READY                                                     ? 8
                                                                                              : 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -124,89 +117,144 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp < 8) {
+  // Up to here nothing of the call's data was touched: it ran under the kernel before.
+  pdl_wait();
+  pdl_trigger();  // what comes behind and does not wait itself (own_kernel) touches other results
+  const int b0 = max(0, a.group_off[grp]);
+  const int nreq = min(min(a.group_off[grp + 1], a.B) - b0, a.max_group);
+  const int row0 = pair * 2 * kM, rows = min(2 * kM, nreq * G - row0);
+  const int nb = shared_blocks_of(a, grp);
+  const int ntiles_all = (nb + kPagesPerTile - 1) / kPagesPerTile, chunk = split_tiles(ntiles_all, a.SA);
+  const int t0 = split * chunk, ntiles = min(ntiles_all, t0 + chunk) - t0;
+  const bool idle = rows <= 0 || ntiles <= 0;  // uniform for the block
+  const bool two = rows > kM;
+  const int nsteps = two ? 2 * ntiles : ntiles;
+
+  if (idle) {
+  } else if (warp < 8) {
     // ============================ Q preparation, softmax, epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int sl = warp >> 2, r = threadIdx.x & (kM - 1);  // score buffer; row of the tile = TMEM lane
-    const int row = row0 + (two ? sl * kM : 0) + r;
-    const int b = b0 + row / G, h = kvh * G + row % G;
-    const bool valid = row < row0 + rows;
-    const int m_row = valid ? a.seq_len[b] - 1 : -1;
-    float f = 0.f;  // scores are the products times this
+    int8_t* exps = reinterpret_cast<int8_t*>(sm + L::EXP_OFF);
     {
-      const uint32_t sQ = sQ0 + uint32_t(two ? sl * L::QTILE : 0);
-      auto qaddr = [&](int k) { return sQ + uint32_t((k >> 3) * L::BLK) + swz(r, k & 7); };
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)b * a.Hq + h) * D);
-      float top = 0.f;
+      // Q operands: NC lanes to a row (of the pair's up to 256), a run of rows to a group of lanes, so that the heads of
+      // a request share their cosines; f16, 128-byte swizzle.  A power of two per row takes it into [-1, 1], where f16
+      // keeps 11 bits of what matters.
+      constexpr int NC = POS == kRope ? D / 16 : D / 8, NG = 256 / NC, PER = 2 * kM / NG;
+      const int t = threadIdx.x, c = t % NC, n0 = t / NC * PER;
+      auto put = [&](int n, int k, const float2 (&y)[4]) {
+        st_shared_v4(sQ0 + uint32_t((n >> 7) * L::QTILE + (k >> 3) * L::BLK) + swz(n & 127, k & 7),
+                     make_uint4(f2_to_h2(y[0].x, y[0].y), f2_to_h2(y[1].x, y[1].y), f2_to_h2(y[2].x, y[2].y),
+                                f2_to_h2(y[3].x, y[3].y)));
+      };
+      auto unpack = [](uint4 u, float2 (&y)[4]) {
+        y[0] = bf2_to_f2(u.x);
+        y[1] = bf2_to_f2(u.y);
+        y[2] = bf2_to_f2(u.z);
+        y[3] = bf2_to_f2(u.w);
+      };
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const int rd = POS == kRope ? D : (POS == kRopeX ? a.pos.rotary_dim : 0), hr = rd / 2;
+      const bool inter = POS == kRopeX && a.pos.interleaved != 0;
+      // this lane's chunk, the one that it turns it against (itself: none), and its first frequency
+      const int other = POS == kRope ? c + NC : (inter || 8 * c >= rd ? c : (8 * c < hr ? c + hr / 8 : c - hr / 8));
+      const int f0 = POS == kRope ? 8 * c : (inter ? 4 * c : (8 * c < hr ? 8 * c : 8 * c - hr));
+      int req = (row0 + n0) / G, h = (row0 + n0) % G;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)(b0 + req) * a.Hq + kvh * G + h) * D);
+      constexpr int AHEAD = 4;  // rows in flight
+      uint4 raw[AHEAD][2];
+      uint32_t pos[AHEAD];
+      auto load = [&](int n, uint4 (&u)[2], uint32_t& m) {
+        const bool here = n < rows && n < n0 + PER;
+        u[0] = here ? src[c] : zero;
+        u[1] = here && other != c ? src[other] : zero;
+        m = here ? uint32_t(max(a.seq_len[b0 + req] - 1, 0)) : 0u;
+        src += ++h == G ? (size_t)(a.Hq - G + 1) * (D / 8) : D / 8;
+        if (h == G) {
+          h = 0;
+          ++req;
+        }
+      };
+      const int n1 = min(n0 + PER, two ? 2 * kM : kM);
+      if (n0 < n1)
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 u = valid ? src[k] : make_uint4(0, 0, 0, 0);
-        if (two || sl == 0) st_shared_v4(qaddr(k), u);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max3f(top, fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i])));
-      }
-      // A power of two per row takes it into [-1, 1], where f16 keeps 11 bits of what matters.
-      const int ex = q4_exponent(top, lowest_ex);
-      const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
-      f = a.pos.scale_log2 * __uint_as_float(uint32_t(127 + ex) << 23);
-      if (two || sl == 0) {
-        auto pack = [&](const float (&y)[8]) {
-          return make_uint4(f2_to_h2(y[0], y[1]), f2_to_h2(y[2], y[3]), f2_to_h2(y[4], y[5]), f2_to_h2(y[6], y[7]));
-        };
-        auto unpack = [&](uint4 u, float (&y)[8]) {
-          y[0] = bf_lo(u.x) * inv; y[1] = bf_hi(u.x) * inv; y[2] = bf_lo(u.y) * inv; y[3] = bf_hi(u.y) * inv;
-          y[4] = bf_lo(u.z) * inv; y[5] = bf_hi(u.z) * inv; y[6] = bf_lo(u.w) * inv; y[7] = bf_hi(u.w) * inv;
-        };
-        int done = 0;  // chunks [0, done) are in their final form
-        if constexpr (POS == kRope || POS == kRopeX) {
-          const uint32_t m = uint32_t(max(m_row, 0));
-          const int rd = POS == kRope ? D : a.pos.rotary_dim, hr = rd / 2;
-          if (POS == kRope || !a.pos.interleaved) {
+        for (int e = 0; e < AHEAD; ++e) load(n0 + e, raw[e], pos[e]);
+      float2 co[4], sn[4];
+      uint32_t turned = 0xFFFFFFFFu;  // position that co and sn are of
 #pragma unroll 1
-            for (int c = 0; c < hr / 8; ++c) {  // chunk c against its partner
-              float x1[8], x2[8], y1[8], y2[8];
-              unpack(ld_shared_v4(qaddr(c)), x1);
-              unpack(ld_shared_v4(qaddr(c + hr / 8)), x2);
+      for (int n2 = n0; n2 < n1; n2 += AHEAD)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float sn, co;
-                turn_sincos_fast(m, turns[c * 8 + e], sn, co);
-                y1[e] = x1[e] * co - x2[e] * sn;
-                y2[e] = x1[e] * sn + x2[e] * co;
-              }
-              st_shared_v4(qaddr(c), pack(y1));
-              st_shared_v4(qaddr(c + hr / 8), pack(y2));
-            }
-          } else {
-#pragma unroll 1
-            for (int k = 0; k < rd / 8; ++k) {  // adjacent pairs
-              float x[8], y[8];
-              unpack(ld_shared_v4(qaddr(k)), x);
+      for (int e2 = 0; e2 < AHEAD; ++e2) {
+        const int n = n2 + e2;
+        float2 x[4], z[4], y[4];
+        unpack(raw[e2][0], x);
+        unpack(raw[e2][1], z);
+        const uint32_t m = pos[e2];
+        if (n2 + AHEAD < n1) load(n + AHEAD, raw[e2], pos[e2]);
+        if ((POS == kRope || POS == kRopeX) && m != turned) {
+          turned = m;
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                float sn, co;
-                turn_sincos_fast(m, turns[k * 4 + w], sn, co);
-                y[2 * w] = x[2 * w] * co - x[2 * w + 1] * sn;
-                y[2 * w + 1] = x[2 * w] * sn + x[2 * w + 1] * co;
-              }
-              st_shared_v4(qaddr(k), pack(y));
+          for (int e = 0; e < 4; ++e) {
+            const int i0 = inter ? e : 2 * e;
+            if (8 * c < rd || POS == kRope) {
+              turn_sincos_fast(m, turns[f0 + i0], sn[e].x, co[e].x);
+              if (!inter) turn_sincos_fast(m, turns[f0 + i0 + 1], sn[e].y, co[e].y);
             }
           }
-          done = rd / 8;
         }
-#pragma unroll 1
-        for (int k = done; k < D / 8; ++k) {
-          float x[8];
-          unpack(ld_shared_v4(qaddr(k)), x);
-          st_shared_v4(qaddr(k), pack(x));
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          top = max3f(top, fabsf(x[e].x), fabsf(x[e].y));
+          if (POS == kRope) top = max3f(top, fabsf(z[e].x), fabsf(z[e].y));
         }
-        fence_async_smem();
+#pragma unroll
+        for (int o = NC / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = q4_exponent(top, lowest_ex);
+        const float inv = __uint_as_float(uint32_t(127 - ex) << 23);
+        if (c == 0) exps[n] = int8_t(ex);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = make_float2(x[e].x * inv, x[e].y * inv);
+          z[e] = make_float2(z[e].x * inv, z[e].y * inv);
+        }
+        if constexpr (POS == kRope) {
+          float2 y2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 t1 = __fmul2_rn(z[e], sn[e]);
+            y[e] = __ffma2_rn(x[e], co[e], make_float2(-t1.x, -t1.y));
+            y2[e] = __ffma2_rn(x[e], sn[e], __fmul2_rn(z[e], co[e]));
+          }
+          put(n, c, y);
+          put(n, c + NC, y2);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = x[e];
+            if (POS == kRopeX && 8 * c < rd) {
+              if (inter)
+                y[e] = make_float2(x[e].x * co[e].x - x[e].y * sn[e].x, x[e].x * sn[e].x + x[e].y * co[e].x);
+              else
+                y[e] = make_float2(x[e].x * co[e].x + (8 * c < hr ? -z[e].x : z[e].x) * sn[e].x,
+                                   x[e].y * co[e].y + (8 * c < hr ? -z[e].y : z[e].y) * sn[e].y);
+            }
+          }
+          put(n, c, y);
+        }
       }
-      mbar_arrive(BAR(B_Q_READY));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_Q_READY));
     }
+    named_sync(1, 2 * kM);  // the exponents are written
+    const int pr = (two ? sl * kM : 0) + r, row = row0 + pr;
+    const int b = b0 + row / G, hq = kvh * G + row % G;
+    const bool valid = pr < rows;
+    const int m_row = valid ? a.seq_len[b] - 1 : -1;
+    const float f = a.pos.scale_log2 * __uint_as_float(uint32_t(127 + exps[pr]) << 23);  // scores are the products times this
     float slope = 0.f;
-    if constexpr (POS == kAlibi) slope = valid ? a.pos.slopes[h] * 1.4426950408889634f : 0.f;
+    if constexpr (POS == kAlibi) slope = valid ? a.pos.slopes[hq] * 1.4426950408889634f : 0.f;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t tS = tl + uint32_t(sl * kN), tO = tl + uint32_t(2 * kN + sl * 128);
     const float2 ff = make_float2(f, f);
@@ -296,29 +344,37 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       for (int c = 0; c < kN / 64; ++c) tmem_st32(tS + uint32_t(32 * c), *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(BAR(B_P_FULL + sl));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_P_FULL + sl));
     }
     ok = ok && wait_bar(BAR(B_FINAL), 0, abort_flag, a.status);
-    if (__all_sync(0xffffffffu, ok)) {
+    // A warp whose wait gave up still meets the others at the barriers below.
+    const bool fine = __all_sync(0xffffffffu, ok);
+    {
       tc_fence_after();
       // what a row's result is relative to; -inf where it has seen no key (a NaN stays)
       float M = l_run == 0.f ? -INFINITY : (m_run == -INFINITY ? 0.f : m_run), Lt = l_run;
-      const size_t pi = ((size_t)b * a.Hq + h) * (a.SA + a.SB) + split;
-      float4* dst = reinterpret_cast<float4*>(a.part_o + pi * D);
+      // Rows go through shared memory (the K and V stages, which no copy or product uses any more; 16-byte chunks
+      // swizzled by the row), so that a warp writes whole rows: a thread's own row, 16 bytes at a time, took 8 us.
+      const uint32_t stage = sK0 + uint32_t(pr) * (D * 4);
+      const size_t pi0 = (size_t)a.SA + a.SB;
+      auto stash = [&](int col, const float (&o)[32]) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared_v4(stage + (uint32_t((col / 4 + q) ^ (r & 7)) << 4),
+                       make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]), __float_as_uint(o[4 * q + 2]),
+                                  __float_as_uint(o[4 * q + 3])));
+      };
       if (two) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + uint32_t(c * 32), o);
+        for (int c = 0; c < D / 32 && fine; ++c) {
+          float o[32];
+          tmem_ld32(tO + uint32_t(c * 32), *reinterpret_cast<uint32_t(*)[32]>(o));
           tmem_wait_ld();
-          if (valid)
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[c * 8 + q] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
-                                           __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
+          stash(c * 32, o);
         }
       } else {
-        // Even and odd tiles joined; each warpgroup writes half of the columns.  (The exchange is in the second Q tile.)
+        // even and odd tiles joined; each warpgroup takes half of the columns.  (The exchange is in the second Q tile.)
         float2* xml = reinterpret_cast<float2*>(sm + L::QTILE);
         xml[sl * kM + r] = make_float2(M, Lt);
         named_sync(1, 2 * kM);
@@ -327,7 +383,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         const float wA = hA.x == -INFINITY ? 0.f : ex2(hA.x - M), wB = hB.x == -INFINITY ? 0.f : ex2(hB.x - M);
         Lt = (wA != 0.f ? wA * hA.y : 0.f) + (wB != 0.f ? wB * hB.y : 0.f);
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+        for (int c = 0; c < D / 64 && fine; ++c) {
           const int col = sl * (D / 2) + c * 32;
           uint32_t oa[32], ob[32];
           tmem_ld32(tl + uint32_t(2 * kN + col), oa);
@@ -337,14 +393,32 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             o[e] = (wA != 0.f ? wA * __uint_as_float(oa[e]) : 0.f) + (wB != 0.f ? wB * __uint_as_float(ob[e]) : 0.f);
-          if (valid)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[col / 4 + q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          stash(col, o);
         }
       }
-      if (valid && (two || sl == 0)) {
-        a.part_ml[pi * 2] = M;
-        a.part_ml[pi * 2 + 1] = Lt;
+      if (valid && fine && (two || sl == 0)) {
+        const size_t pi = ((size_t)b * a.Hq + hq) * pi0 + split;
+        *reinterpret_cast<float2*>(a.part_ml + pi * 2) = make_float2(M, Lt);
+      }
+      if (two)
+        named_sync(1 + sl, kM);
+      else
+        named_sync(1, 2 * kM);
+      constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes to a row, rows to a warp's store
+      constexpr int kRowsPerWarp2 = kM / 4, kRowsPerWarp1 = kM / 8;
+      const int n0 = (two ? warp * kRowsPerWarp2 : warp * kRowsPerWarp1) + lane / LPR, c = lane % LPR;
+      const int n1 = fine ? min(rows, n0 - lane / LPR + (two ? kRowsPerWarp2 : kRowsPerWarp1)) : 0;
+      int req = (row0 + n0) / G, hd = (row0 + n0) % G;
+#pragma unroll 4
+      for (int q = n0; q < n1; q += RPW) {
+        const uint4 u = ld_shared_v4(sK0 + uint32_t(q) * (D * 4) + (uint32_t(c ^ (q & 7)) << 4));
+        const size_t pi = ((size_t)(b0 + req) * a.Hq + kvh * G + hd) * pi0 + split;
+        reinterpret_cast<uint4*>(a.part_o + pi * D)[c] = u;
+        hd += RPW;
+        while (hd >= G) {
+          hd -= G;
+          ++req;
+        }
       }
     }
   } else if (warp < kKWarp) {
@@ -448,7 +522,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         }
       }
       fence_async_smem();
-      mbar_arrive(BAR(B_K_READY + s));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_K_READY + s));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -465,9 +540,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     if (warp == kKWarp) {
       // ============================ block words, K copies
       int m_min = INT_MAX;  // of the block's rows
-      for (int i = row0 / G + lane; i <= (row0 + rows - 1) / G; i += 32) m_min = min(m_min, a.seq_len[b0 + i] - 1);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m_min = min(m_min, __shfl_xor_sync(0xffffffffu, m_min, o));
       uint64_t w_next = fetch(0);
       int issued = 0;
       bool ok = true;
@@ -487,18 +559,23 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           pinfo[slot * kPagesPerTile + lane] = make_int2(delta, lo);
           pstart[slot * kPagesPerTile + lane] = start - lo;
         }
-        const bool all = __all_sync(0xffffffffu, lane >= kPagesPerTile || (rows_k == kPage && start + kPage - 1 <= m_min));
         const uint32_t load = __ballot_sync(0xffffffffu, lane < kPagesPerTile && rows_k > 0);
-        if (lane == 0) {
-          flags[slot] = all;
-          mbar_arrive_expect_tx(BAR(B_K_FULL + s), uint32_t(__popc(load)) * kPage * D * 2);
-        }
-        __syncwarp();
         if ((load >> lane) & 1u)
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb)
             tma_load_page(sK0 + uint32_t(s * L::TILE + cb * L::BLK + lane * kPage * 128), &tmk, cb * 64, -lo,
                           int(word_page(w)) * a.Hkv + kvh, BAR(B_K_FULL + s));
+        if (j == 0) {
+          for (int i = row0 / G + lane; i <= (row0 + rows - 1) / G; i += 32) m_min = min(m_min, a.seq_len[b0 + i] - 1);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) m_min = min(m_min, __shfl_xor_sync(0xffffffffu, m_min, o));
+        }
+        const bool all = __all_sync(0xffffffffu, lane >= kPagesPerTile || (rows_k == kPage && start + kPage - 1 <= m_min));
+        __syncwarp();
+        if (lane == 0) {  // the phase ends with this arrival and the bytes, in either order
+          flags[slot] = all;
+          mbar_arrive_expect_tx(BAR(B_K_FULL + s), uint32_t(__popc(load)) * kPage * D * 2);
+        }
         __syncwarp();
         issued = j + 1;
       }
@@ -563,9 +640,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);
         int ks = 0, vs = 0;            // stages of the next QK^T's and PV's tiles
         uint32_t kpar = 0, vpar = 0;
+        // The next waits' barriers are asked while products queue, so that the thread goes on at once where they are done.
+        bool seen_k = false, seen_p = false, seen_v = false;
         auto qk = [&](int s) -> bool {  // step s: scores into buffer s % 2
           const bool first = !two || !(s & 1), last = !two || (s & 1);
-          if (first && !wait_bar(BAR(B_K_READY + ks), kpar, abort_flag, a.status)) return false;
+          if (first && !seen_k && !wait_bar(BAR(B_K_READY + ks), kpar, abort_flag, a.status)) return false;
           tc_fence_after();
           const uint64_t k0 = kd + uint64_t(ks * (L::TILE >> 4));
           auto go = [&](uint32_t d, uint64_t q0) {
@@ -593,8 +672,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         if (ok && nsteps > 1) ok = qk(1);
         for (int s = 0; s < nsteps && ok; ++s) {
           const bool first = !two || !(s & 1), last = !two || (s & 1);
-          ok = wait_bar(BAR(B_P_FULL + (s & 1)), uint32_t((s >> 1) & 1), abort_flag, a.status) &&
-               (!first || wait_bar(BAR(B_V_FULL + vs), vpar, abort_flag, a.status));
+          ok = (!first || seen_v || wait_bar(BAR(B_V_FULL + vs), vpar, abort_flag, a.status)) &&
+               (seen_p || wait_bar(BAR(B_P_FULL + (s & 1)), uint32_t((s >> 1) & 1), abort_flag, a.status));
           if (!ok) break;
           tc_fence_after();
           const uint64_t v0 = vd + uint64_t(vs * (L::TILE >> 4));
@@ -614,7 +693,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               vpar ^= 1u;
             }
           }
+          seen_k = mbar_peek(BAR(B_K_READY + ks), kpar);
           if (s + 2 < nsteps) ok = qk(s + 2);
+          seen_v = mbar_peek(BAR(B_V_FULL + vs), vpar);
+          seen_p = mbar_peek(BAR(B_P_FULL + ((s + 1) & 1)), uint32_t(((s + 1) >> 1) & 1));
         }
         mma_commit(BAR(B_FINAL));  // every product is done before O is read, and before TMEM goes
         WaitClock clk;
