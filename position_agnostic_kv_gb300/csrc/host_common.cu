@@ -107,7 +107,20 @@ int prepare_pos(const lazy_pos_cfg* cfg, int Hq, int D, float scale, PosParams* 
       if (bs == 0.0) bs = 1.0;
       if (!(bf > bs)) return fail(LAZY_EINVAL, "YaRN needs beta_fast > beta_slow");
     }
-    for (int i = 0; i < half; ++i) {
+    // The frequencies of the last configuration of this thread (64 powers take longer than the rest of a call): they
+    // depend on these values alone.
+    struct Last {
+      int kind, rd, ctx;
+      float theta;
+      double factor, bf, bs;
+      unsigned long long turns[kMaxHalf];
+    };
+    static thread_local Last last = {-1, 0, 0, 0.f, 0.0, 0.0, 0.0, {}};
+    const bool yarn = cfg->kind == LAZY_POS_YARN;
+    const bool same = last.kind == cfg->kind && last.rd == rd && last.theta == cfg->rope_theta &&
+                      (!yarn || (last.ctx == cfg->yarn_orig_ctx && last.factor == factor && last.bf == bf && last.bs == bs));
+    if (same) std::memcpy(out->turns, last.turns, sizeof(out->turns));
+    for (int i = 0; i < half && !same; ++i) {
       double theta = std::pow(double(cfg->rope_theta), -2.0 * i / double(rd));
       if (cfg->kind == LAZY_POS_YARN) {
         // NTK-by-parts ramp of the YaRN paper: gamma = clamp((L0/lambda - b_slow)/(b_fast - b_slow))
@@ -118,6 +131,10 @@ int prepare_pos(const lazy_pos_cfg* cfg, int Hq, int D, float scale, PosParams* 
       }
       const double turns = theta / two_pi;  // < 1 / (2 pi) since theta <= 1
       out->turns[i] = (unsigned long long)std::ldexp(turns, 64);
+    }
+    if (!same) {
+      last = {cfg->kind, rd, cfg->yarn_orig_ctx, cfg->rope_theta, factor, bf, bs, {}};
+      std::memcpy(last.turns, out->turns, sizeof(last.turns));
     }
     if (cfg->kind == LAZY_POS_YARN && factor > 1.0) {
       const double mscale = 0.1 * std::log(factor) + 1.0;

@@ -8,23 +8,23 @@ namespace lazykv {
 
 namespace {
 
-// A row's partial results joined by their maxima: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  One warp per
-// row: its lanes take the maxima and sums of up to 4 partial results each, then the columns.
+// A row's partial results joined by their maxima: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  One block of
+// kJoinWarps warps per row; every warp takes the maxima and sums (its lanes up to 4 each), then every
+// kJoinWarps-th result.
 constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SharedArgs a) {
+  constexpr int V = D / 32;  // columns per lane
+  __shared__ float part[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hq = blockIdx.x, b = blockIdx.y;
+  const size_t row = (size_t)b * a.Hq + hq, at = row * (a.SA + a.SB);
   pdl_wait();
   pdl_trigger();
-  constexpr int V = D / 32;  // columns per lane
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.Hq) return;
-  const int b = int(row / a.Hq);
   const Share sh = share_of(a, b);
   const int tiles = (sh.blocks + 7) / 8, chunk = tiles ? split_tiles(tiles, a.SA) : 1, na = (tiles + chunk - 1) / chunk;
   const int nb = visible_blocks(a.seq_len[b], a.q_start[b], a.doc_blocks[b], a.max_blocks);
   const int n = na + own_splits(max(0, nb - sh.blocks), a.SB);
-  const size_t at = (size_t)row * (a.SA + a.SB);
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
   auto index = [&](int s) { return s < na ? s : a.SA + s - na; };
   float2 mine[4];
@@ -50,31 +50,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SharedArgs 
   for (int c = 0; c < V; ++c) O[c] = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-#pragma unroll 4
-    for (int s = 32 * e; s < min(n, 32 * e + 32); ++s) {
+#pragma unroll 8
+    for (int s = 32 * e + warp; s < min(n, 32 * e + 32); s += kJoinWarps) {
       const float g = __shfl_sync(0xffffffffu, f[e], s & 31);
       const float* o = a.part_o + (at + index(s)) * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(o);
-        if (g != 0.f) {  // a split that saw no key has written nothing
-          O[0] += g * x.x;
-          O[1] += g * x.y;
-          O[2] += g * x.z;
-          O[3] += g * x.w;
-        }
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(o);
-        if (g != 0.f) {
-          O[0] += g * x.x;
-          O[1] += g * x.y;
-        }
-      }
-    }
-  const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
-  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (size_t)row * D + lane * V);
+      float x[V];
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(o);
+      else
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(o);
+      if (g != 0.f)  // a split that saw no key counts for nothing, whatever it holds
 #pragma unroll
-  for (int c = 0; c < V / 2; ++c) out[c] = f2_to_bf2(O[2 * c] * inv, O[2 * c + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+        for (int c = 0; c < V; ++c) O[c] += g * x[c];
+    }
+#pragma unroll
+  for (int c = 0; c < V; ++c) part[warp][lane * V + c] = O[c];
+  __syncthreads();
+  const int c = 2 * threadIdx.x;
+  if (c < D) {
+    float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      y0 += part[w][c];
+      y1 += part[w][c + 1];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + c) = f2_to_bf2(y0 * inv, y1 * inv);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -90,13 +93,13 @@ Sizes sizes_of(int B, int n_groups, int max_group, int max_shared, int max_block
   Sizes s;
   max_shared = std::min(max_shared, max_blocks);
   max_group = std::min(max_group, B);
-  s.SA = shared_prefix_splits(n_groups, max_group, max_shared, Hq, Hkv);
+  s.SA = shared_prefix_splits(B, n_groups, max_group, max_shared, Hq, Hkv);
   // Own blocks: enough warps for about four waves, runs of at least 32 blocks a split.
   const int own = max_blocks - (s.SA ? max_shared : 0);
   const long long units = (long long)B * Hkv * ((Hq / Hkv + 7) / 8), slots = 3ll * sm_count();
   long long sb = std::min<long long>((4 * slots + units - 1) / units, (own + 31) / 32);
   s.SB = int(std::max(1ll, std::min(64ll, sb)));
-  const size_t n = (size_t)B * Hq * (s.SA + s.SB);
+  const size_t n = s.SA + s.SB > 1 ? (size_t)B * Hq * (s.SA + s.SB) : 0;  // one result is the row's
   s.o_bytes = (n * D * 4 + 255) / 256 * 256;
   s.bytes = s.o_bytes + n * 8;
   return s;
@@ -192,10 +195,10 @@ extern "C" int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, co
   a.SB = z.SB;
   a.status = status_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.SA > 0) rc = run_shared_prefix(a, D, mk, mv, st);
-  if (!rc) rc = run_shared_own(a, D, mk, mv, a.SA > 0, st);
-  if (rc) return rc;
-  const dim3 grid(unsigned(((long long)B * Hq + kJoinWarps - 1) / kJoinWarps));
+  rc = run_shared_own(a, D, mk, mv, st);
+  if (!rc && a.SA > 0) rc = run_shared_prefix(a, D, mk, mv, st);
+  if (rc || a.SA + a.SB == 1) return rc;
+  const dim3 grid(Hq, B);
   LAZY_CUDA_TRY(D == 128 ? launch_pdl(join_kernel<128>, grid, dim3(32 * kJoinWarps), 0, st, a)
                          : launch_pdl(join_kernel<64>, grid, dim3(32 * kJoinWarps), 0, st, a));
   return LAZY_OK;

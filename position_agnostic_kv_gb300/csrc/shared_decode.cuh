@@ -67,9 +67,9 @@ __device__ __forceinline__ int split_tiles(int tiles, int S) { return (tiles + S
 __device__ __forceinline__ int own_splits(int blocks, int SB) { return min(SB, max(1, (blocks + 31) / 32)); }
 
 int cache_tensor_map(CUtensorMap* map, const void* base, int num_pages, int Hkv, int D);
-int run_shared_own(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, bool after, cudaStream_t st);
+int run_shared_own(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st);
 int run_shared_prefix(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st);
-int shared_prefix_splits(int n_groups, int max_group, int max_shared, int Hq, int Hkv);
+int shared_prefix_splits(int B, int n_groups, int max_group, int max_shared, int Hq, int Hkv);
 
 // 3-D tiled load (column x, row y inside the page, page-head z) of a box of 64 columns x 16 rows.  y may be
 // negative: the rows before row 0 are outside the tensor and arrive as zeros; the transaction counts the

@@ -59,8 +59,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 template <int D, int POS>
 __global__ void __launch_bounds__(kNW * 32) own_kernel(const __grid_constant__ CUtensorMap tmk,
-                                                       const __grid_constant__ CUtensorMap tmv, const SharedArgs a,
-                                                       const int after) {
+                                                       const __grid_constant__ CUtensorMap tmv, const SharedArgs a) {
   using L = OwnLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
@@ -70,20 +69,14 @@ __global__ void __launch_bounds__(kNW * 32) own_kernel(const __grid_constant__ C
   const int G = a.Hq / a.Hkv, per = (G + 7) / 8;             // head blocks of 8 per KV head
   const int kvh = blockIdx.y / per, h0 = kvh * G + blockIdx.y % per * 8;
   const int nh = min(8, kvh * G + G - h0);
-  // Behind the common keys' launch this one starts while that one runs: whatever came before both is done (that
-  // launch waited for it before it let this one start), and the two touch different results.  It waits at
-  // its end instead, so that the kernel behind it finds both done.
-  if (!after) pdl_wait();
+  pdl_wait();
+  pdl_trigger();  // the common keys' launch may start: it reads the same inputs and touches other results
   const Share sh = share_of(a, b);
   const int m = a.seq_len[b] - 1;
   const int nb = visible_blocks(m + 1, a.q_start[b], a.doc_blocks[b], a.max_blocks);
   if (split == 0 && blockIdx.y == 0) check_request(a, b, m);
   const int blocks = max(0, nb - sh.blocks), S = own_splits(blocks, a.SB);
-  if (split >= S) {  // uniform for the block
-    pdl_trigger();
-    if (after) pdl_wait();
-    return;
-  }
+  if (split >= S) return;  // uniform for the block
   const int chunk = (blocks + S - 1) / S;
   const int beg = sh.blocks + split * chunk, len = max(0, min(sh.blocks + blocks, beg + chunk) - beg);
   const int wb = beg + warp * len / kNW, n = beg + (warp + 1) * len / kNW - wb;
@@ -261,8 +254,6 @@ __global__ void __launch_bounds__(kNW * 32) own_kernel(const __grid_constant__ C
     __syncwarp();
     if (i + kStages < n) issue(i + kStages);
   }
-  pdl_trigger();
-
   // ---- the warps' results joined by their maxima
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
@@ -290,43 +281,46 @@ __global__ void __launch_bounds__(kNW * 32) own_kernel(const __grid_constant__ C
       O += f * mo[(w * 8 + h) * D + col];
       Ls += f * mml[(w * 8 + h) * 2 + 1];
     }
-    const size_t pi = ((size_t)b * a.Hq + h0 + h) * (a.SA + a.SB) + a.SA + split;
+    const size_t row = (size_t)b * a.Hq + h0 + h, pi = row * (a.SA + a.SB) + a.SA + split;
+    if (a.SA + a.SB == 1) {  // nothing to join
+      a.out[row * D + col] = __float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls);
+      if (a.lse && col == 0) a.lse[row] = (M + log2f(Ls)) * 0.6931471805599453f;
+      continue;
+    }
     a.part_o[pi * D + col] = O;
     if (col == 0) {
       a.part_ml[pi * 2] = M;
       a.part_ml[pi * 2 + 1] = Ls;
     }
   }
-  if (after) pdl_wait();
 }
 
 template <int D, int POS>
-int launch_own(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, bool after, cudaStream_t st) {
+int launch_own(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = own_kernel<D, POS>;
   LAZY_CUDA_TRY(smem_limit(kern, OwnLayout<D>::SMEM, done));
   const int per = (a.Hq / a.Hkv + 7) / 8;
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(a.SB, a.Hkv * per, a.B), dim3(kNW * 32), OwnLayout<D>::SMEM, st, mk, mv, a,
-                           int(after)));
+  LAZY_CUDA_TRY(launch_pdl(kern, dim3(a.SB, a.Hkv * per, a.B), dim3(kNW * 32), OwnLayout<D>::SMEM, st, mk, mv,
+                           a));
   return LAZY_OK;
 }
 
 }  // namespace
 
-int run_shared_own(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, bool after,
-                   cudaStream_t st) {
+int run_shared_own(const SharedArgs& a, int D, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
   if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
   if (D == 128) {
-    if (kind == kRope) return launch_own<128, kRope>(a, mk, mv, after, st);
-    if (kind == kRopeX) return launch_own<128, kRopeX>(a, mk, mv, after, st);
-    if (kind == kAlibi) return launch_own<128, kAlibi>(a, mk, mv, after, st);
-    return launch_own<128, kNone>(a, mk, mv, after, st);
+    if (kind == kRope) return launch_own<128, kRope>(a, mk, mv, st);
+    if (kind == kRopeX) return launch_own<128, kRopeX>(a, mk, mv, st);
+    if (kind == kAlibi) return launch_own<128, kAlibi>(a, mk, mv, st);
+    return launch_own<128, kNone>(a, mk, mv, st);
   }
-  if (kind == kRope) return launch_own<64, kRope>(a, mk, mv, after, st);
-  if (kind == kRopeX) return launch_own<64, kRopeX>(a, mk, mv, after, st);
-  if (kind == kAlibi) return launch_own<64, kAlibi>(a, mk, mv, after, st);
-  return launch_own<64, kNone>(a, mk, mv, after, st);
+  if (kind == kRope) return launch_own<64, kRope>(a, mk, mv, st);
+  if (kind == kRopeX) return launch_own<64, kRopeX>(a, mk, mv, st);
+  if (kind == kAlibi) return launch_own<64, kAlibi>(a, mk, mv, st);
+  return launch_own<64, kNone>(a, mk, mv, st);
 }
 
 }  // namespace lazykv

@@ -117,9 +117,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Up to here nothing of the call's data was touched: it ran under the kernel before.
-  pdl_wait();
-  pdl_trigger();  // what comes behind and does not wait itself (own_kernel) touches other results
+  // No wait here: own_kernel, the launch before this one, let this one start when it had waited for everything before it, and
+  // the two touch different results.  This one waits at its end, so that the launch behind it finds both done.
   const int b0 = max(0, a.group_off[grp]);
   const int nreq = min(min(a.group_off[grp + 1], a.B) - b0, a.max_group);
   const int row0 = pair * 2 * kM, rows = min(2 * kM, nreq * G - row0);
@@ -713,6 +712,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+  pdl_trigger();
+  pdl_wait();
 }
 
 template <int D, int POS>
@@ -740,17 +741,25 @@ int launch_prefix(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap&
 
 }  // namespace
 
-// Key splits of the common keys (0: too little to share, every request is decoded alone).
-int shared_prefix_splits(int n_groups, int max_group, int max_shared, int Hq, int Hkv) {
-  if (n_groups <= 0 || max_group <= 0 || max_shared <= 0) return 0;
-  const int sms = sm_count(), tiles = (max_shared + kPagesPerTile - 1) / kPagesPerTile;
-  const long long rows = (long long)max_group * (Hq / Hkv), pairs = (rows + 2 * kM - 1) / (2 * kM);
-  const long long units = (long long)n_groups * Hkv * pairs;
-  // Time of a launch in tiles: waves of blocks, each its tiles and about 4 for its start and its results.
+// Key splits of the common keys; 0: every request is decoded alone.
+int shared_prefix_splits(int B, int n_groups, int max_group, int max_shared, int Hq, int Hkv) {
+  if (B <= 0 || n_groups <= 0 || max_group <= 0 || max_shared <= 0) return 0;
+  const int sms = sm_count(), tiles = (max_shared + kPagesPerTile - 1) / kPagesPerTile, G = Hq / Hkv;
+  // Decoded alone, a page is read once per request and 8 heads, out of the L2 at about 1.8 pages of a head per ns;
+  // sharing costs two launches, about 8 us (16 requests over 130 common pages of 8 heads: 28.6 us alone, 16.9 shared;
+  // 2 requests over 5 pages of 2 heads: 14.3 and 17.0).
+  const long long alone = (long long)B * max_shared * Hkv * ((G + 7) / 8), once = (long long)n_groups * max_shared * Hkv;
+  if (alone - once < 8000) return 0;
+  const long long rows = (long long)max_group * G, pairs = (rows + 2 * kM - 1) / (2 * kM), units = n_groups * Hkv * pairs;
+  // Time of a launch in key tiles: waves of blocks, each its tiles, and its start and results, as long as 6 tiles of two
+  // Q tiles or 12 of one; then the join, with every split.  (16 requests as above, splits 4 / 6 / 9 / 17: 19.9, 17.8,
+  // 16.9, 22.2 us; 32 requests of 32 heads over 94 tiles of one KV head, splits 16 / 24 / 38: 28.2, 25.6, 30.4.)
+  const bool two = rows > kM;
+  const long long start = two ? 600 : 1200, join = two ? 15 : 30;  // hundredths of a tile
   long long best = 0;
   int S = 1;
   for (int s = 1; s <= 64 && s <= tiles; ++s) {
-    const long long t = ((units * s + sms - 1) / sms) * ((tiles + s - 1) / s + 4);
+    const long long t = ((units * s + sms - 1) / sms) * (100ll * ((tiles + s - 1) / s) + start) + join * s;
     if (s == 1 || t < best) {
       best = t;
       S = s;

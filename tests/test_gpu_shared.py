@@ -89,7 +89,16 @@ def pos_of(kind="rope", rd=128, inter=False):
     return dict(kind=kind, theta=1e4, rotary_dim=rd, interleaved=inter)
 
 
-CASES = {  # groups (requests, common documents), own documents, segments, Hq, Hkv, D, pos
+def own_and_common(n=(14, 16), outside=2):
+    """Two groups, requests outside them, and documents of some requests' own."""
+    B = sum(n) + outside
+    own = [[[], [20], [50, 3], [], [16]][i % 5] for i in range(B)]
+    return [(n[0], [33, 64]), (n[1], [128, 7])], own, [[1, 17, 2, 16, 40, 33][i % 6] for i in range(B)]
+
+
+# Few and short lists are decoded one by one; from some thousand pages on a group's common keys are taken together
+# (tests below look at which it is).
+ALONE = {  # groups (requests, common documents), own documents, segments, Hq, Hkv, D, pos
     "one_group": ([(3, [40, 200, 16])], [[]] * 3, [5, 1, 33], 8, 2, 128, pos_of()),
     "own_documents": ([(2, [33]), (3, [128, 7])], [[20], [], [50, 3], [], [16]], [1, 17, 2, 16, 40], 8, 2, 128, pos_of()),
     "outside": ([(2, [130])], [[], [], [300], [1]], [3, 3, 20, 1], 4, 4, 128, pos_of()),
@@ -112,6 +121,30 @@ CASES = {  # groups (requests, common documents), own documents, segments, Hq, H
     "long": ([(9, [1600, 900, 33])], [[]] * 9, [33] * 9, 8, 2, 128, pos_of()),
     "own_long": ([(2, [64])], [[1500, 700], [900]], [3, 3], 4, 1, 128, pos_of()),
 }
+KINDS = ([(20, [70, 233, 5])], [[9] if i % 3 == 0 else [] for i in range(20)], [1 + i for i in range(20)])
+TOGETHER = {
+    "t_one_q_tile": ([(20, [40, 200, 16])], [[]] * 20, [1 + i % 18 for i in range(20)], 64, 32, 64, pos_of(rd=64)),
+    "t_two_q_tiles": ([(40, [150, 33, 7])], [[]] * 40, [2] * 40, 64, 16, 128, pos_of()),
+    "t_two_pairs": ([(40, [130])], [[]] * 40, [2] * 40, 160, 16, 64, pos_of(rd=64)),
+    "t_one_head": ([(24, [400, 64])], [[]] * 24, [3] * 24, 16, 16, 128, pos_of()),
+    "t_ragged": ([(13, [300, 20]), (1, [50]), (9, []), (30, [16] * 9)], [[7] if i % 4 == 0 else [] for i in range(55)],
+                 [1 + i % 9 for i in range(55)], 16, 16, 128, pos_of()),
+    "t_wide": ([(12, [300, 20])], [[]] * 12, [4] * 12, 384, 16, 64, pos_of(rd=64)),
+    "t_very_wide": ([(4, [140])], [[]] * 4, [1, 2, 3, 4], 1920, 12, 64, pos_of(rd=64)),
+    "t_own": (*own_and_common(), 64, 32, 64, pos_of(rd=64)),
+    "t_short_documents": ([(30, [1, 2, 3, 16, 17, 15, 1, 40, 5, 31, 9])], [[]] * 30, [2] * 30, 32, 32, 128, pos_of()),
+    "t_long": ([(9, [1600, 900, 33])], [[]] * 9, [33] * 9, 32, 8, 128, pos_of()),
+    "t_long_small_heads": ([(9, [1600, 900, 33])], [[]] * 9, [33] * 9, 32, 8, 64, pos_of(rd=64)),
+    "t_interleaved": (*KINDS, 64, 32, 128, pos_of(inter=True)),
+    "t_partial": (*KINDS, 32, 32, 128, pos_of(rd=48)),
+    "t_partial_interleaved": (*KINDS, 64, 32, 64, pos_of(rd=16, inter=True)),
+    "t_yarn": (*KINDS, 32, 32, 128, pos_of("yarn")),
+    "t_alibi": (*KINDS, 64, 32, 128, pos_of("alibi")),
+    "t_alibi_two_q_tiles": ([(40, [150, 33, 7])], [[]] * 40, [2] * 40, 64, 16, 64, pos_of("alibi", 64)),
+    "t_none": (*KINDS, 32, 32, 64, pos_of("none", 64)),
+}
+CASES = ALONE | TOGETHER
+BOTH = pytest.mark.parametrize("name", ["own_documents", "t_own"])
 
 
 def lists(name, seed=0, **kw):
@@ -122,15 +155,19 @@ def lists(name, seed=0, **kw):
 @pytest.mark.parametrize("name", CASES)
 def test_decode_shared(lk, name):
     x = lists(name)
-    out, lse = OnGpu(lk, x).decode()
+    g = OnGpu(lk, x)
+    alone = lk.decode_shared_workspace_size(x.B, 0, 0, 0, x.max_blocks, x.Hq, x.Hkv, x.D)
+    assert (g.ws.numel() != alone) == (name in TOGETHER)  # partial results of the common keys
+    out, lse = g.decode()
     check(out, lse, ref.decode(x))
     assert lk.device_status() == 0
 
 
-def test_agrees_with_decode(lk):
+@BOTH
+def test_agrees_with_decode(lk, name):
     """attn_decode over the same lists."""
     import torch
-    x = lists("own_documents")
+    x = lists(name)
     g = OnGpu(lk, x)
     out, lse = g.decode()
     n = lk.workspace_size(lk.PHASE_DECODE, x.B, x.B, x.max_blocks, x.Hq, x.Hkv, x.D)
@@ -142,62 +179,72 @@ def test_agrees_with_decode(lk):
     check(other, ols, want)
 
 
+@BOTH
 @pytest.mark.parametrize("scale", [0.02, 2.0])
-def test_scale(lk, scale):
-    x = lists("one_group")
+def test_scale(lk, scale, name):
+    x = lists(name)
     out, lse = OnGpu(lk, x).decode(scale=scale)
     check(out, lse, ref.decode(x, scale=scale))
 
 
-def test_small_queries_under_a_large_scale(lk):
-    x = lists("one_group")
+@BOTH
+def test_small_queries_under_a_large_scale(lk, name):
+    x = lists(name)
     x.q = x.q * 2.0 ** -40
     scale = 2.0 ** 40 / np.sqrt(x.D)
     out, lse = OnGpu(lk, x).decode(scale=scale)
     check(out, lse, ref.decode(x, scale=scale))
 
 
-def test_idle_requests(lk):
+@BOTH
+def test_idle_requests(lk, name):
     """Requests of length 0 inside and outside groups: zeros, and -inf."""
-    x = lists("own_documents")
-    x.seq_len[[0, 3]] = 0
+    x = lists(name)
+    x.seq_len[[0, 3, x.B - 1]] = 0
     out, lse = OnGpu(lk, x).decode()
     want = ref.decode(x)
     check(out, lse, want)
-    assert not out[[0, 3]].any() and np.isneginf(lse[[0, 3]].cpu().numpy()).all()
+    assert not out[[0, 3, x.B - 1]].any() and np.isneginf(lse[[0, 3, x.B - 1]].cpu().numpy()).all()
     assert lk.device_status() == 0
 
 
-def test_requests_inside_their_documents(lk):
+@pytest.mark.parametrize("name", ["one_group", "t_one_q_tile", "t_two_q_tiles", "t_alibi"])
+def test_requests_inside_their_documents(lk, name):
     """A position before the end of the documents sees the keys up to itself."""
-    x = lists("one_group")
-    x.seq_len[:] = [100, 1, 250]
+    x = lists(name)
+    x.seq_len[:] = np.resize([100, 1, 250, 37, 16, 17], x.B)
+    x.seq_len = np.minimum(x.seq_len, x.q_start + np.array(x.seg))
     out, lse = OnGpu(lk, x).decode()
     check(out, lse, ref.decode(x))
 
 
-@pytest.mark.parametrize("max_group,max_shared", [(2, None), (None, 3), (1, 1), (0, 0)])
-def test_bounds_that_are_too_small(lk, max_group, max_shared):
+@pytest.mark.parametrize("name,max_group,max_shared", [
+    ("own_documents", 2, None), ("own_documents", None, 3), ("own_documents", 1, 1), ("own_documents", 0, 0),
+    ("t_own", 11, None), ("t_own", None, 8), ("t_two_q_tiles", 38, 13)])
+def test_bounds_that_are_too_small(lk, name, max_group, max_shared):
     """What the call's bounds cut off is decoded alone: the same result, and a status bit."""
-    x = lists("own_documents")
-    g = OnGpu(lk, x, max_group if max_group is not None else 3, max_shared if max_shared is not None else max(x.shared))
+    x = lists(name)
+    g = OnGpu(lk, x, max_group if max_group is not None else max(np.diff(x.off)),
+              max_shared if max_shared is not None else max(x.shared))
     out, lse = g.decode()
     check(out, lse, ref.decode(x))
     assert lk.device_status() == 8
 
 
-@pytest.mark.parametrize("max_group,max_shared", [(100, 10 ** 6), (5, 12)])
-def test_bounds_that_are_too_large(lk, max_group, max_shared):
-    x = lists("own_documents")
+@BOTH
+@pytest.mark.parametrize("max_group,max_shared", [(100, 10 ** 6), (17, 12)])
+def test_bounds_that_are_too_large(lk, name, max_group, max_shared):
+    x = lists(name)
     out, lse = OnGpu(lk, x, max_group, max_shared).decode()
     check(out, lse, ref.decode(x))
     assert lk.device_status() == 0
 
 
-def test_pages_outside_the_cache(lk):
+@BOTH
+def test_pages_outside_the_cache(lk, name):
     """Their keys are left out and the status says so; in common documents and in a request's own."""
-    x = lists("own_documents")
-    bad = [(0, 1), (1, 1), (2, 3), (3, 3), (4, 3), (2, int(x.shared[1]))]
+    x = lists(name)
+    bad = [(b, 1) for b in range(x.off[1])] + [(b, 3) for b in range(x.off[1], x.off[2])] + [(x.off[1], int(x.shared[1]))]
     want = x.meta.copy()
     for b, j in bad:
         x.meta[b, j] = int(x.meta[b, j]) & ((1 << 40) - 1) | (x.num_pages + 5) << 40
@@ -207,35 +254,41 @@ def test_pages_outside_the_cache(lk):
     assert lk.device_status() == 1
 
 
-def test_nan_stays_in_its_request(lk):
+@BOTH
+def test_nan_stays_in_its_request(lk, name):
     """A NaN in a request's own value reaches only its columns; in a common value, that column of the whole group."""
-    x = lists("own_documents")
+    x = lists(name)
     clean = ref.decode(x)
+    G, lo, hi = x.Hq // x.Hkv, x.off[1], x.off[2]
     own = ref.keys(x.meta[0], x.doc_blocks[0], x.q_start[0], x.seq_len[0])[-1]
-    com = ref.keys(x.meta[2], x.doc_blocks[2], x.q_start[2], x.seq_len[2])[5]
+    com = ref.keys(x.meta[lo], x.doc_blocks[lo], x.q_start[lo], x.seq_len[lo])[5]
     x.v[own[3], 1, own[4], 7] = np.nan
     x.v[com[3], 0, com[4], 9] = np.nan
     g = OnGpu(lk, x)
     got = g.decode()[0].float().cpu().numpy()
     hit = np.zeros(got.shape, bool)
-    hit[0, 4:, 7] = True
-    hit[2:, :4, 9] = True
+    hit[0, G:2 * G, 7] = True
+    hit[lo:hi, :G, 9] = True
     assert np.array_equal(np.isnan(got), hit)
     assert np.abs(np.where(hit, 0, got - clean[0])).max() < 0.05
 
 
-def test_nan_keys_and_queries(lk):
-    x = lists("one_group")
+@pytest.mark.parametrize("name", ["one_group", "t_one_q_tile", "t_two_q_tiles"])
+def test_nan_keys_and_queries(lk, name):
+    x = lists(name)
+    G = x.Hq // x.Hkv
     com = ref.keys(x.meta[0], x.doc_blocks[0], x.q_start[0], x.seq_len[0])[44]
     x.k[com[3], 1, com[4], 3] = np.nan
-    x.q[1, 2] = np.nan
+    x.q[1, 0] = np.nan
     got = OnGpu(lk, x).decode()[0].float().cpu().numpy()
     nan = np.isnan(got).all(-1)
-    assert nan[:, 4:].all() and nan[1, 2] and nan.sum() == 3 * 4 + 1
+    assert nan[:, G:2 * G].all() and nan[1, 0] and nan.sum() == x.B * G + 1
+    assert np.isnan(got).sum() == nan.sum() * x.D
 
 
-def test_repeats_itself(lk):
-    x = lists("many_rows")
+@pytest.mark.parametrize("name", ["many_rows", "t_two_q_tiles", "t_ragged"])
+def test_repeats_itself(lk, name):
+    x = lists(name)
     g = OnGpu(lk, x)
     a = [t.clone() for t in g.decode()]
     g.ws.fill_(0x55)
@@ -243,10 +296,11 @@ def test_repeats_itself(lk):
     assert (a[0] == b[0]).all() and (a[1] == b[1]).all()
 
 
-def test_stream_and_graph(lk):
+@BOTH
+def test_stream_and_graph(lk, name):
     """On another stream, and captured once and replayed on other queries, lengths and groups."""
     import torch
-    x, y = lists("own_documents"), lists("own_documents", 5)
+    x, y = lists(name), lists(name, 5)
     g = OnGpu(lk, x)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -257,8 +311,7 @@ def test_stream_and_graph(lk):
     with torch.cuda.graph(graph):
         g.decode()
     h = OnGpu(lk, y)
-    y.off, y.shared = [0, 1, 5], [int(y.shared[0]), int(y.shared[1])]
-    y.off = [0, 2, 4]  # the last request of the second group leaves it
+    y.off = [0, y.off[1], y.off[2] - 1]  # the last request of the second group leaves it
     for name in ("q", "k", "v", "meta", "seq_len"):
         getattr(g, name).copy_(getattr(h, name))
     g.off.copy_(dev(np.array(y.off, np.int32)))
@@ -272,7 +325,7 @@ def test_stream_and_graph(lk):
 def test_back_to_back_calls_share_a_workspace(lk):
     """Calls of different sizes one after another on one stream and one workspace."""
     import torch
-    gs = [OnGpu(lk, lists(n)) for n in ("many_rows", "one_group", "long", "no_groups")]
+    gs = [OnGpu(lk, lists(n)) for n in ("many_rows", "t_two_q_tiles", "one_group", "t_ragged", "t_alibi", "long", "no_groups")]
     ws = max((g.ws for g in gs), key=lambda t: t.numel())
     for g in gs:
         g.ws = ws
