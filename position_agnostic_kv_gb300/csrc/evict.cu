@@ -35,6 +35,7 @@ struct PlanArgs {
   float* new_weights;
   uint32_t* status;
   int first, recent, max_dst, max_blocks, num_pages;
+  int cluster;  // blocks of threads per request
 };
 
 // Where a stretch of blocks leaves the packing: whether a document starts in it, the kept keys before its
@@ -124,23 +125,47 @@ __device__ __forceinline__ void put_word(const PlanArgs& a, uint64_t* new_meta, 
   new_meta[blk] = uint64_t(bad ? 0 : rows) | uint64_t(pg) << 5 | uint64_t(delta) << 16 | uint64_t(bad ? 0 : page) << 40;
 }
 
-// Lists of up to 64 IT document blocks: one block of threads per request, the ordered weights in registers (key
-// 1024 i + t of the list is thread t's i-th).  The keep-th largest is found in digits of 11, 11 and 10 bits (the first
-// takes sign, exponent and two bits of fraction, which spreads weights over enough counters).  Kept keys are 16 bits
-// per list block; a scan over the blocks then gives each block the place of its first kept key in the new list.
+constexpr int kMaxCluster = 8;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An int of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ int peer_int(const int* p, int rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int2 peer_int2(const int* p, int rank) {
+  uint32_t at;
+  int2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// Lists of up to 64 IT C document blocks: a cluster of C blocks of threads per request, each with 64 IT list blocks and
+// their ordered weights in registers (key 1024 i + t of its part is thread t's i-th).  The keep-th largest is found in
+// digits of 11, 11 and 10 bits (the first takes sign, exponent and two bits of fraction, which spreads weights over
+// enough counters); every block adds up the cluster's counters.  Kept keys are 16 bits per list block; a scan over the
+// list blocks then gives each the place of its first kept key in the new list.
 template <int IT>
 __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const PlanArgs a) {
   constexpr int kBlocks = 64 * IT, kPer = (kBlocks + kPlanThreads - 1) / kPlanThreads;
   constexpr int kBins = 2048;
-  __shared__ int hist[kBins];
+  __shared__ __align__(8) int hists[2][kBins];
   __shared__ int buf[kWarps];
   __shared__ Packed pbuf[kWarps];
+  __shared__ __align__(8) int share[6];  // what the cluster's other blocks read: keys, equals, packing
   __shared__ int place[kBlocks];       // keys before the block; then the new place of its first kept key
   __shared__ int base[kBlocks];        // first new block of its document
   __shared__ uint16_t stays[kBlocks];  // kept keys
   __shared__ uint32_t s_prefix;
   __shared__ int s_left, s_same;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.cluster, b = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int all_t = rank * kPlanThreads + tid, all_n = C * kPlanThreads;  // of the cluster's threads
   pdl_wait();
   pdl_trigger();
   const size_t MB = a.max_blocks;
@@ -153,35 +178,63 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
   int32_t* dst = a.dst_slot + (size_t)b * a.max_dst * kPage;
   const int nd = min(max(a.doc_blocks[b], 0), a.max_blocks);
   const int want = a.keep[b];
+  const int j0 = rank * kBlocks;  // this block's first list block
   uint32_t v[IT];  // the weights, all loads in flight at once; then their ordered values, 0 where no key lies, NaN 1
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int k = i * kPlanThreads + tid;
+    const int k = j0 * kPage + i * kPlanThreads + tid;
     v[i] = k < nd * kPage ? __float_as_uint(w[k]) : 0u;
   }
   // this thread's list blocks: kPer consecutive ones, so that scans over the threads are scans over the list
   uint64_t word[kPer + 2];  // and a neighbour on either side
 #pragma unroll
   for (int e = 0; e < kPer + 2; ++e) {
-    const int j = tid * kPer + e - 1;
-    word[e] = j >= 0 && j < nd ? meta[j] : 0;
+    const int j = j0 + tid * kPer + e - 1;
+    word[e] = tid * kPer + e - 1 <= kBlocks && j >= 0 && j < nd ? meta[j] : 0;
   }
-  for (int i = tid; i < a.max_dst * kPage; i += kPlanThreads) src[i] = dst[i] = -1;
-  if (want < 0) {
-    for (int i = tid; i < a.max_blocks; i += kPlanThreads) new_meta[i] = meta[i];
-    for (int i = tid; i < a.max_blocks * kPage; i += kPlanThreads) new_w[i] = w[i];
-    if (tid == 0) a.new_doc_blocks[b] = nd;
+  for (int i = all_t; i < a.max_dst * kPage; i += all_n) src[i] = dst[i] = -1;
+  if (want < 0) {  // the same for the whole cluster
+    for (int i = all_t; i < a.max_blocks; i += all_n) new_meta[i] = meta[i];
+    for (int i = all_t; i < a.max_blocks * kPage; i += all_n) new_w[i] = w[i];
+    if (all_t == 0) a.new_doc_blocks[b] = nd;
     return;
   }
   if (tid == 0) {
     s_prefix = 0;
-    if (a.doc_blocks[b] > a.max_blocks) set_status(a.status, LAZY_STATUS_BAD_ROW);
+    if (rank == 0 && a.doc_blocks[b] > a.max_blocks) set_status(a.status, LAZY_STATUS_BAD_ROW);
   }
 
   int nv[kPer], mine = 0, total;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) mine += nv[e] = min(int(word_nvalid(word[e + 1])), kPage);
+  for (int e = 0; e < kPer; ++e) {
+    nv[e] = tid * kPer + e < kBlocks ? min(int(word_nvalid(word[e + 1])), kPage) : 0;
+    mine += nv[e];
+  }
   int before = scan_before(mine, buf, total);
+  // Sum of share[k] over the blocks before this one; `sum` gets the cluster's.
+  auto across = [&](int k, int& sum) {
+    int pre = 0;
+    sum = 0;
+    if (C == 1) {
+      sum = share[k];
+      return 0;
+    }
+    int x[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) x[r] = r < C ? peer_int(&share[k], r) : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      pre += r < rank ? x[r] : 0;
+      sum += x[r];
+    }
+    return pre;
+  };
+  auto meet = [&] {
+    if (C == 1) __syncthreads(); else cluster_sync();
+  };
+  if (tid == 0) share[0] = total;
+  meet();
+  before += across(0, total);
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     const int j = tid * kPer + e;
@@ -196,9 +249,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
 
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = (i * kPlanThreads + tid) / kPage, t = tid % kPage, rank = place[j] + t;
-    const uint32_t x = rank < a.first || rank >= total - a.recent ? kProtected : max(order_of(__uint_as_float(v[i])), 1u);
-    v[i] = j < nd && t < stays[j] ? x : 0u;
+    const int j = (i * kPlanThreads + tid) / kPage, t = tid % kPage, nth = place[j] + t;
+    const uint32_t x = nth < a.first || nth >= total - a.recent ? kProtected : max(order_of(__uint_as_float(v[i])), 1u);
+    v[i] = t < stays[j] ? x : 0u;
   }
 
   // ---- the keep-th largest value, `limit`, of which `ties` equals stay
@@ -209,15 +262,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
     for (int round = 0; round < 3; ++round) {
       const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bins = round == 2 ? 1024 : kBins;
       const uint32_t mask = round == 0 ? 0u : 0xFFFFFFFFu << (round == 1 ? 21 : 10);
+      int* hist = hists[round & 1];  // (the other blocks have read the last but one by now)
       hist[tid] = hist[tid + 1024] = 0;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < IT; ++i)
         if (v[i] != 0 && (v[i] & mask) == limit) atomicAdd(&hist[(v[i] >> shift) & (bins - 1)], 1);
-      __syncthreads();
+      meet();
       // thread t holds the digits bins - 1 - 2 t and the one below
       const int d = kBins - 1 - 2 * tid;
-      const int c0 = d < bins ? hist[d] : 0, c1 = d < bins ? hist[d - 1] : 0;
+      int c0 = 0, c1 = 0;
+      if (C == 1) {
+        c0 = d < bins ? hist[d] : 0;
+        c1 = d < bins ? hist[d - 1] : 0;
+      } else if (d < bins) {
+        int2 x[kMaxCluster];  // all loads in flight at once
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) x[r] = r < C ? peer_int2(&hist[d - 1], r) : make_int2(0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          c0 += x[r].y;
+          c1 += x[r].x;
+        }
+      }
       int all;
       const int above = scan_before(c0 + c1, buf, all);
       if (above < ties && ties <= above + c0 + c1) {
@@ -233,24 +300,28 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
   }
 
   // ---- who stays, 16 bits per list block; among equals the earlier in the list
+  int* counts = hists[1];  // (round 2 used the other)
+  int same_before = 0;
   if (keep > 0 && s_same != ties) {  // (uniform) not all of them: count the equals before each warp's keys
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const uint32_t eq = __ballot_sync(0xffffffffu, v[i] == limit);
-      if (lane == 0) hist[i * kWarps + warp] = __popc(eq);
+      if (lane == 0) counts[i * kWarps + warp] = __popc(eq);
     }
     __syncthreads();
     int sum;
-    const int c = tid < IT * kWarps ? hist[tid] : 0, c_before = scan_before(c, buf, sum);
-    if (tid < IT * kWarps) hist[tid] = c_before;
-    __syncthreads();
+    const int c = tid < IT * kWarps ? counts[tid] : 0, c_before = scan_before(c, buf, sum);
+    if (tid < IT * kWarps) counts[tid] = c_before;
+    if (tid == 0) share[1] = sum;
+    meet();
+    same_before = across(1, sum);
   }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     bool stay = keep > 0 && v[i] >= limit && v[i] != 0;
     if (keep > 0 && s_same != ties) {
       const uint32_t eq = __ballot_sync(0xffffffffu, v[i] == limit);
-      if (v[i] == limit) stay = hist[i * kWarps + warp] + __popc(eq & ((1u << lane) - 1u)) < ties;
+      if (v[i] == limit) stay = same_before + counts[i * kWarps + warp] + __popc(eq & ((1u << lane) - 1u)) < ties;
     }
     const uint32_t bits = __ballot_sync(0xffffffffu, stay);
     const int j = (i * kPlanThreads + tid) / kPage;
@@ -264,16 +335,41 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
   Packed me = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    const int j = tid * kPer + e;
+    const int jl = tid * kPer + e, j = j0 + jl;
+    const bool here = jl < kBlocks && j < nd;
     const uint32_t delta = word_delta(word[e + 1]);
-    kept[e] = j < nd ? __popc(uint32_t(stays[j])) : 0;
-    starts[e] = j < nd && (j == 0 || word_delta(word[e]) != delta);
-    ends[e] = j < nd && (j + 1 == nd || word_delta(word[e + 2]) != delta);
+    kept[e] = here ? __popc(uint32_t(stays[jl])) : 0;
+    starts[e] = here && (j == 0 || word_delta(word[e]) != delta);
+    ends[e] = here && (j + 1 == nd || word_delta(word[e + 2]) != delta);
     if (starts[e]) me = join(me, Packed{1, 0, 0, 0});
     if (me.starts) me.tail += kept[e]; else me.head += kept[e];
   }
   Packed whole;
-  const Packed pre = scan_packed(me, pbuf, whole);
+  Packed pre = scan_packed(me, pbuf, whole);
+  if (tid == 0) {
+    share[2] = whole.starts;
+    share[3] = whole.head;
+    share[4] = whole.blocks;
+    share[5] = whole.tail;
+  }
+  meet();
+  if (C > 1) {
+    Packed of[kMaxCluster], all = {0, 0, 0, 0}, lower = all;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < C) {
+        const int2 p = peer_int2(&share[2], r), q = peer_int2(&share[4], r);
+        of[r] = Packed{p.x, p.y, q.x, q.y};
+      }
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < C) {
+        if (r == rank) lower = all;
+        all = join(all, of[r]);
+      }
+    pre = join(lower, pre);
+    whole = all;
+  }
   const int nn = whole.blocks + (whole.starts ? pages_of(whole.tail) : 0);  // document blocks of the new list
   int first_block = pre.starts ? pre.blocks : 0, run = pre.starts ? pre.tail : 0;
 #pragma unroll
@@ -293,27 +389,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_short_kernel(const
   }
 
   // ---- the rest of the new list: the query segment's blocks and weights, and zeros
-  for (int i = tid; i < nn * kPage; i += kPlanThreads) new_w[i] = 0.f;
-  for (int i = tid + nn; i < a.max_blocks; i += kPlanThreads) new_meta[i] = i - nn + nd < a.max_blocks ? meta[i - nn + nd] : 0;
-  for (int i = tid + nn * kPage; i < a.max_blocks * kPage; i += kPlanThreads)
+  for (int i = all_t; i < nn * kPage; i += all_n) new_w[i] = 0.f;
+  for (int i = all_t + nn; i < a.max_blocks; i += all_n) new_meta[i] = i - nn + nd < a.max_blocks ? meta[i - nn + nd] : 0;
+  for (int i = all_t + nn * kPage; i < a.max_blocks * kPage; i += all_n)
     new_w[i] = i + (nd - nn) * kPage < a.max_blocks * kPage ? w[i + (nd - nn) * kPage] : 0.f;
-  if (tid == 0) a.new_doc_blocks[b] = nn;
-  __syncthreads();
+  if (all_t == 0) a.new_doc_blocks[b] = nn;
+  meet();  // (also: no block leaves while another reads from it)
 
   // ---- kept keys: slots, weights, and the words of full pages
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int j = (i * kPlanThreads + tid) / kPage, t = tid % kPage;
-    if (j >= nd) break;
     const uint32_t bits = stays[j];
     if (!((bits >> t) & 1u)) continue;
     const int at = place[j] + __popc(bits & ((1u << t) - 1u)), blk = at / kPage, row = at % kPage;
-    const uint64_t here = meta[j];
+    const uint64_t here = meta[j0 + j];
     const int page = blk < a.max_dst ? pages[blk] : -1;
     if (page >= 0 && page < a.num_pages) {
       src[at] = int(word_page(here)) * kPage + t;
       dst[at] = page * kPage + row;
-      new_w[at] = w[i * kPlanThreads + tid];
+      new_w[at] = w[j0 * kPage + i * kPlanThreads + tid];
     }
     if (row == kPage - 1) put_word(a, new_meta, pages, blk, blk - base[j], kPage, word_delta(here));
   }
@@ -538,10 +633,25 @@ extern "C" int lazy_evict_plan(const float* weights, const uint64_t* meta, const
   }
   int rc = check_device();
   if (rc || B == 0) return rc;
-  const PlanArgs a = {weights,  meta,     doc_blocks,  keep,          dst_pages, new_meta, new_doc_blocks, src_slot,
-                      dst_slot, new_weights, status_word(), first,    recent,    max_dst,  max_blocks,     num_pages};
-  auto kern = max_blocks <= 256 ? evict_plan_short_kernel<4> : max_blocks <= 2048 ? evict_plan_short_kernel<32> : evict_plan_kernel;
-  LAZY_CUDA_TRY(launch_pdl(kern, dim3(B), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), a));
+  PlanArgs a = {weights,  meta,     doc_blocks,  keep,          dst_pages, new_meta, new_doc_blocks, src_slot,
+                dst_slot, new_weights, status_word(), first,    recent,    max_dst,  max_blocks,     num_pages, 1};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Keys a thread and blocks of threads a list.  Few keys a thread shorten the block's chain of loops, more blocks make
+  // its meetings dearer: 16 lists of 2000 blocks take 32 us with one block of 32 keys a thread each, 26 with two of 16, 20
+  // with four of 8 and 39 with eight of 4 (clusters of eight whole SMs do not all fit at once).
+  auto clusters = [&](int per) {  // blocks of `per` list blocks each, a power of two
+    int c = 1;
+    while (c * per < max_blocks) c *= 2;
+    return c;
+  };
+  const int its = max_blocks <= 256 ? 4 : max_blocks <= 8 * 512 && (long long)B * clusters(512) <= 2 * sm_count() ? 8 : 16;
+  if (max_blocks <= 8 * 1024) {
+    auto kern = its == 4 ? evict_plan_short_kernel<4> : its == 8 ? evict_plan_short_kernel<8> : evict_plan_short_kernel<16>;
+    a.cluster = clusters(64 * its);
+    LAZY_CUDA_TRY(launch_pdl_cluster(kern, dim3((unsigned)B * a.cluster), dim3(kPlanThreads), 0, st, a.cluster, a));
+  } else {
+    LAZY_CUDA_TRY(launch_pdl(evict_plan_kernel, dim3(B), dim3(kPlanThreads), 0, st, a));
+  }
   return LAZY_OK;
 }
 

@@ -241,6 +241,13 @@ PLANS = {
     "no_documents": dict(docs=[[], [7], []], seg=[20, 1, 0], keep=[5, 3, 1]),
     "single_keys": dict(docs=[[1] * 30, [1]], seg=[1, 1], keep=[11, 1]),
     "long": dict(docs=[[1600] * 6 + [33], [17000], [100] * 90], seg=[40, 3, 1], keep=[2000, 5000, 777], first=4, recent=64),
+    "two_parts": dict(docs=[[1600] * 4, [33] * 130], seg=[40, 3], keep=[2000, 1500], first=4, recent=64),
+    "longer": dict(docs=[[20000, 33, 20000], [300]], seg=[40, 3], keep=[12345, 300], first=4, recent=64),
+    "longest": dict(docs=[[30000, 33, 30000, 30000, 30000, 12345], [300]], seg=[40, 3], keep=[33333, 20], first=4, recent=64),
+    "many": dict(docs=[[1 + 7 * i % 50, 20] for i in range(200)], seg=[1 + i % 20 for i in range(200)],
+                 keep=[i % 60 for i in range(200)], recent=5),
+    "many_longer": dict(docs=[[4500, 20] if i % 40 == 0 else [20 + i] for i in range(160)], seg=[1] * 160,
+                        keep=[5 * i for i in range(160)], first=3),
 }
 
 
@@ -251,9 +258,10 @@ def test_evict_plan(lk, name):
     assert lk.device_status() == 0
 
 
+@pytest.mark.parametrize("long", [False, True])
 @pytest.mark.parametrize("weights", ["equal", "zero", "nan", "inf", "negative", "tiny"])
-def test_evict_plan_orders_any_weights(lk, weights):
-    c = Cut(lk, [[40, 200], [70], [300, 16, 16]], [5, 1, 33], [51, 33, 100], first=1, recent=1)
+def test_evict_plan_orders_any_weights(lk, weights, long):
+    c = Cut(lk, [[40, 200], [70], [300, 16, 16] + [3000] * 4 * long], [5, 1, 33], [51, 33, 100 + 5000 * long], first=1, recent=1)
     rng = np.random.default_rng(3)
     some = rng.random(c.w.shape) < 0.4
     if weights == "equal":
