@@ -23,7 +23,7 @@ constexpr int kPrepWarp0 = 8, kPlanWarp = kPrepWarp0 + kPrepWarps, kCopyWarp0 = 
 constexpr int kMaxStages = 6, kSlots = 4, kLse = 4;
 constexpr int kRun = 32;     // pages per item
 constexpr int kFew = 32;     // up to so many rows a query value is three bf16 numbers (24 bits), else two (16)
-constexpr int kScore = 256;  // columns of a score buffer
+constexpr int kScore = 128, kBufs = 4;  // columns of a score buffer, buffers
 
 struct Args {
   const __nv_bfloat16* q;
@@ -83,9 +83,9 @@ enum : int {
   B_META = 0,                      // [kSlots] item published (1)
   B_QOK = B_META + kSlots,         // [kSlots] its Q operand is ready (a lane per warp)
   B_DONE = B_QOK + kSlots,         // [kSlots] item finished (a lane per reading warp)
-  B_SFULL = B_DONE + kSlots,       // [2] a tile's scores written (commit)
-  B_SFREE = B_SFULL + 2,           // [2] scores read (a lane per reading warp)
-  B_QFREE = B_SFREE + 2,           // [2] products with the Q buffer done (commit)
+  B_SFULL = B_DONE + kSlots,       // [kBufs] a tile's scores written (commit)
+  B_SFREE = B_SFULL + kBufs,       // [kBufs] scores read (a lane per reading warp)
+  B_QFREE = B_SFREE + kBufs,           // [2] products with the Q buffer done (commit)
   B_FINAL = B_QFREE + 2,
   B_KFULL = B_FINAL + 1,           // [stages] K tile landed (a lane per copying warp)
   NBAR_FIXED = B_KFULL             // then [stages] products with the stage done (commit)
@@ -200,18 +200,21 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       float* to = a.part + ((((size_t)(split ? 2 * it.rg + wg : it.rg) * a.Hkv + it.kvh) * a.B + it.b) * a.max_blocks +
                             it.j0) * kPage + row;
       for (int j = 0; j < np; j += kPagesPerTile, ++tile) {
-        const int buf = int(tile & 1u);
-        if (!split && buf != wg) continue;
+        const int buf = int(tile % kBufs);
+        if (!split && (buf & 1) != wg) continue;
         const int mine = j + row / kPage, start = delta + kPage * (pg0 + mine), p = start + row % kPage;
-        const float old = mine < np && start <= stored ? to[j * kPage] : 0.f;  // this thread's own, of the row block before
-        got = wait_bar(BAR(B_SFULL + buf), (tile >> 1) & 1u, abort_flag, a.status);
+        float old = 0.f;
+        if (stored >= 0 && mine < np && start <= stored) old = to[j * kPage];  // this thread's own, of the row block before
+        got = wait_bar(BAR(B_SFULL + buf), (tile / kBufs) & 1u, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(buf * kScore);
-        // rows from n0 on see the key
-        const long long see = (long long)(p - m0) * G - r0;
-        const int n0 = (flags & F_MASK) ? int(see < 0 ? 0 : (see > kRows ? kRows : see)) : 0;
+        int n0 = 0;  // rows from n0 on see the key
+        if (flags & F_MASK) {
+          const long long see = (long long)(p - m0) * G - r0;
+          n0 = int(see < 0 ? 0 : (see > kRows ? kRows : see));
+        }
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const bool masked = flags & F_MASK;
         // 16 scores, each the sum of its parts' columns: acc += 2^(s - lse)
@@ -242,18 +245,29 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         auto pair = [](const uint32_t* u, int e) {
           return make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
         };
-        if (split) {  // two parts
+        if (split) {  // the parts are in one sum
           const int cut = (n16 + 1) / 2, c1 = wg == 0 ? cut : n16;
           int c = wg == 0 ? 0 : cut;
 #pragma unroll 1
-          for (; c < c1; ++c) {
-            uint32_t u[2][16];
-            tmem_ld16(tS + uint32_t(16 * c), u[0]);
-            tmem_ld16(tS + uint32_t(rows + 16 * c), u[1]);
+          for (; c + 2 <= c1; c += 2) {
+            uint32_t u[32];
+            tmem_ld32(tS + uint32_t(16 * c), u);
             tmem_wait_ld();
             float2 x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __fadd2_rn(pair(u[0], e), pair(u[1], e));
+            for (int e = 0; e < 8; ++e) x[e] = pair(u, e);
+            weigh(x, 16 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = pair(u, 8 + e);
+            weigh(x, 16 * c + 16);
+          }
+          if (c < c1) {
+            uint32_t u[16];
+            tmem_ld16(tS + uint32_t(16 * c), u);
+            tmem_wait_ld();
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = pair(u, e);
             weigh(x, 16 * c);
           }
         } else {  // three parts
@@ -615,15 +629,19 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
       // Descriptors are built from launch constants and counters alone, and a branch chooses the Q buffer, so that
       // they stay in uniform registers.
       const uint64_t kd = sdesc(sK, 16, 1024), qd0 = sdesc(sQ, 16, 1024), qd1 = sdesc(sQ + QBUF, 16, 1024);
-      // One product for all parts of a query, side by side: it reads the keys once (a product of 16 columns costs
-      // what one of 64 does, the keys' 4 KB from shared memory).
-      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(L::parts(rows) * rows / 16 * 2 - 2) << 17);
-      const uint64_t qblk = QBLK >> 4;
+      // Blocks of few rows: one product for the three parts of a query, side by side, which reads the keys once (16
+      // columns cost what 64 do: the keys' 4 KB from shared memory).  Of many: a product per part, into one sum, so that
+      // four score buffers fit.
+      const int passes = split ? 2 : 1, cols = split ? rows : 3 * rows;
+      const uint32_t idesc = idesc_mma(kTile, 16, 0, 0) + (uint32_t(cols / 16 * 2 - 2) << 17);
+      const uint64_t qblk = QBLK >> 4, qpart = QPART >> 4;
       auto products = [&](uint32_t d, uint64_t k0, uint64_t q0) {
+#pragma unroll 1
+        for (int part = 0; part < passes; ++part, q0 += qpart)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(d, k0 + uint64_t(((kk >> 2) * L::KBLK + (kk & 3) * 32) >> 4), q0 + (kk >> 2) * qblk + (kk & 3) * 2, idesc,
-                   kk ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16(d, k0 + uint64_t(((kk >> 2) * L::KBLK + (kk & 3) * 32) >> 4), q0 + (kk >> 2) * qblk + (kk & 3) * 2, idesc,
+                     part || kk ? 1u : 0u);
       };
       int st = 0, newest = -1;
       uint32_t tile = 0, kpar = 0;
@@ -635,14 +653,21 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         const int flags = items[sl].flags, np = items[sl].np;
         if (flags & F_END) break;
         if (flags & F_NEWQ) {
+          // What a Q operand's preparation overwrites (kLse sets of log-sum-exps) must have been read: with all tiles but
+          // the last two done here, the tiles of the operand four before are.
+          if (tile >= 3) {
+            const uint32_t t = tile - 3;
+            ok = wait_bar(BAR(B_SFREE + int(t % kBufs)), (t / kBufs) & 1u, abort_flag, a.status);
+            if (!ok) break;
+          }
           if (newest >= 0) mma_commit(BAR(B_QFREE + (newest & 1)));
           ++newest;
         }
         ok = wait_bar(BAR(B_QOK + sl), uint32_t((i / kSlots) & 1), abort_flag, a.status);
         for (int j = 0; j < np && ok; j += kPagesPerTile, ++tile) {
-          const int buf = int(tile & 1u);
+          const int buf = int(tile % kBufs);
           ok = (seen_k || wait_bar(BAR(B_KFULL + st), kpar, abort_flag, a.status)) &&
-               (seen_s || wait_bar(BAR(B_SFREE + buf), (tile >> 1) & 1u ^ 1u, abort_flag, a.status));
+               (seen_s || wait_bar(BAR(B_SFREE + buf), (tile / kBufs) & 1u ^ 1u, abort_flag, a.status));
           if (!ok) break;
           tc_fence_after();
           const uint64_t k0 = kd + uint64_t(st * (L::TILE >> 4));
@@ -657,7 +682,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             kpar ^= 1u;
           }
           seen_k = mbar_peek(BAR(B_KFULL + st), kpar);
-          seen_s = mbar_peek(BAR(B_SFREE + (buf ^ 1)), ((tile + 1) >> 1) & 1u ^ 1u);
+          seen_s = mbar_peek(BAR(B_SFREE + int((tile + 1) % kBufs)), ((tile + 1) / kBufs) & 1u ^ 1u);
         }
       }
       mma_commit(BAR(B_FINAL));  // every product is done before TMEM goes
