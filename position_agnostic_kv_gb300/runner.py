@@ -13,9 +13,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (PHASE_DECODE, PHASE_DECODE_Q4, PHASE_PREFILL, PHASE_PREFILL_Q4, attn_decode,
-               attn_decode_q4, attn_prefill, attn_prefill_q4, build_doc_meta, build_rope_table, kv_write,
-               kv_write_q4, pos_cfg_from, q4_cache_shape, workspace_size)
+from . import (PHASE_DECODE, PHASE_DECODE_Q4, PHASE_KEY_WEIGHTS, PHASE_PREFILL, PHASE_PREFILL_Q4, attn_decode,
+               attn_decode_q4, attn_decode_shared, attn_key_weights, attn_prefill, attn_prefill_q4, build_doc_meta,
+               build_rope_table, decode_shared_workspace_size, evict_plan, kv_move, kv_write, kv_write_q4,
+               pos_cfg_from, q4_cache_shape, workspace_size)
 
 PAGE = 16
 
@@ -30,14 +31,34 @@ def i32(x, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(np.asarray(x, dtype=np.int32))).to(device)
 
 
+def common_prefixes(meta: np.ndarray, doc_blocks, min_blocks: int = 1):
+    """Groups of neighbouring requests whose lists begin with the same document blocks, as ``attn_decode_shared``
+    takes them: (group_off [n + 1], shared_blocks [n], int32).  A request joins the group before it while at
+    least ``min_blocks`` words stay common to all of it (the order of the requests is the caller's)."""
+    meta, nd = np.asarray(meta), np.asarray(doc_blocks)
+    off, shared = [0], []
+    for b in range(len(nd)):
+        if b > off[-1]:
+            n = min(shared[-1], int(nd[b]))
+            same = meta[b, :n] == meta[off[-1], :n]
+            n = n if same.all() else int(np.argmin(same))
+            if n >= min_blocks:
+                shared[-1] = n
+                continue
+            off.append(b)
+        shared.append(int(nd[b]))
+    return np.array(off + [len(nd)] if len(nd) else off, np.int32), np.array(shared, np.int32)
+
+
 class PagedBatch:
     """Caches, block words and per-request metadata of one batch, resident on one GPU.
 
     ``kv_bits=4`` keeps keys and values in one 4-bit cache (``kv_cache``, with the power-of-two
-    factors ``k_scale`` / ``v_scale``) instead of the bf16 ``k_cache`` and ``v_cache``."""
+    factors ``k_scale`` / ``v_scale``) instead of the bf16 ``k_cache`` and ``v_cache``.  ``spare_pages`` adds
+    free pages behind those of the workload (for ``evict``)."""
 
     def __init__(self, w, device="cuda", use_table: bool = False, pos_kind: str | None = None,
-                 kv_bits: int = 16, k_scale: float = 1.0, v_scale: float = 1.0):
+                 kv_bits: int = 16, k_scale: float = 1.0, v_scale: float = 1.0, spare_pages: int = 0):
         if kv_bits not in (4, 16):
             raise ValueError(f"kv_bits must be 16 or 4, got {kv_bits}")
         self.kv_bits, self.factors = kv_bits, dict(k_scale=k_scale, v_scale=v_scale)
@@ -56,10 +77,10 @@ class PagedBatch:
         self.cu_q = i32(w.cu_q, dev)
         self.max_q = int(np.max(w.q_len)) if len(w.q_len) else 0
         self.total_q = int(np.sum(w.q_len))
-        shape = (w.num_pages, w.Hkv, PAGE, w.D)
+        shape = (w.num_pages + spare_pages, w.Hkv, PAGE, w.D)
         self.k_cache = self.v_cache = self.kv_cache = None
         if kv_bits == 4:
-            self.kv_cache = torch.zeros(q4_cache_shape(w.num_pages, w.Hkv, w.D), dtype=torch.uint8, device=dev)
+            self.kv_cache = torch.zeros(q4_cache_shape(w.num_pages + spare_pages, w.Hkv, w.D), dtype=torch.uint8, device=dev)
         else:
             self.k_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
             self.v_cache = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
@@ -91,6 +112,7 @@ class PagedBatch:
         ws_pre = workspace_size(ph_pre, max(self.total_q, 1), self.B, self.max_blocks,
                                 self.Hq, self.Hkv, self.D)
         self.ws = torch.empty(max(ws_dec, ws_pre, 256), dtype=torch.uint8, device=dev)
+        self.groups = None  # see share_prefixes
 
     def _write(self, k, v, slot, lp):
         if self.kv_bits == 4:
@@ -151,10 +173,63 @@ class PagedBatch:
         if self.kv_bits == 4:
             attn_decode_q4(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta, self.kv_cache,
                            self.cfg, out, lse=lse, ws=self.ws, **self.factors)
+        elif self.groups is not None:
+            attn_decode_shared(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta, *self.groups,
+                               self.k_cache, self.v_cache, self.cfg, out, lse=lse, ws=self.ws)
         else:
             attn_decode(inp["q"], inp["seq_len"], self.q_start, self.doc_blocks, self.meta,
                         self.k_cache, self.v_cache, self.cfg, out, lse=lse, ws=self.ws)
         return out
+
+    def share_prefixes(self, min_blocks: int = 8):
+        """From now on decode steps read the documents that neighbouring requests list first, in the same
+        order, once per group (bf16 caches).  Returns the number of requests that share."""
+        if self.kv_bits != 16:
+            raise ValueError("share_prefixes: the calls over shared lists need a bf16 cache")
+        off, shared = common_prefixes(self.meta.cpu().numpy(), self.doc_blocks.cpu().numpy(), min_blocks)
+        size = np.diff(off)
+        biggest, longest = int(size.max(initial=0)), int(shared.max(initial=0))
+        n = decode_shared_workspace_size(self.B, len(shared), biggest, longest, self.max_blocks, self.Hq, self.Hkv, self.D)
+        if n > self.ws.numel():
+            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self.groups = (i32(off, self.device), i32(shared, self.device), biggest, longest)
+        return int(size[size > 1].sum())
+
+    # ---------------------------------------------------------------- eviction inside a context (bf16 caches)
+    def key_weights(self, q, lse, seq_len, cu_q=None, window: int = 0, weights=None):
+        """The attention weight that every key of the lists receives from the rows ``q`` (with the log-sum-exps of
+        their attention call; requests' last tokens, split by ``cu_q``, by default one row per request), in a new
+        tensor [B, 16 max_blocks], or added to ``weights``."""
+        if self.kv_bits != 16:
+            raise ValueError("key_weights: needs a bf16 cache")
+        most = q.shape[0] if cu_q is not None else 1
+        if cu_q is None:
+            cu_q = i32(np.arange(self.B + 1), self.device)
+        n = workspace_size(PHASE_KEY_WEIGHTS, q.shape[0], self.B, self.max_blocks, self.Hq, self.Hkv, self.D)
+        if n > self.ws.numel():
+            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        add = weights is not None
+        if not add:
+            weights = torch.empty((self.B, PAGE * self.max_blocks), dtype=torch.float32, device=self.device)
+        attn_key_weights(q, lse, cu_q, seq_len, self.q_start, self.doc_blocks, self.meta, self.k_cache, self.cfg, weights,
+                         most, window=window, accumulate=add, ws=self.ws)
+        return weights
+
+    def evict(self, weights, keep, pages, first: int = 0, recent: int = 0):
+        """Cut every request's documents to the ``keep`` keys of the largest ``weights`` (the ``first`` and
+        ``recent`` ones before all others): the rows move to the free ``pages`` [B, n], the lists change, and the
+        weights come back in the new order.  The old pages are the caller's to free."""
+        if self.kv_bits != 16:
+            raise ValueError("evict: needs a bf16 cache")
+        pages = i32(pages, self.device)
+        meta, nd, new_w = torch.empty_like(self.meta), torch.empty_like(self.doc_blocks), torch.empty_like(weights)
+        src = torch.empty((self.B, PAGE * pages.shape[1]), dtype=torch.int32, device=self.device)
+        dst = torch.empty_like(src)
+        evict_plan(weights, self.meta, self.doc_blocks, i32(keep, self.device), pages, self.k_cache.shape[0], self.cfg, meta,
+                   nd, src, dst, new_w, first=first, recent=recent)
+        kv_move(src, dst, self.k_cache, self.v_cache)
+        self.meta, self.doc_blocks, self.groups = meta, nd, None  # the lists differ from now on
+        return new_w
 
 
 # -------------------------------------------------------------------- cold documents

@@ -193,3 +193,16 @@ def test_reference_plan_keeps_attention(lk):
         vv = np.repeat(x.v[ks[:, 3], :, ks[:, 4]], 2, 1)
         assert np.abs(out[b] - np.einsum("ht,thd->hd", wgt, vv)).max() < 1e-12
         assert len(stay) == [30, 9][b]
+
+
+def test_common_prefixes(lk):
+    """Neighbouring requests whose lists begin alike."""
+    from position_agnostic_kv_gb300.runner import common_prefixes
+    meta = np.array([[1, 2, 3, 9], [1, 2, 4, 9], [1, 2, 3, 9], [5, 2, 3, 9], [5, 2, 3, 9], [7, 0, 0, 0]], np.uint64)
+    nd = np.array([3, 3, 2, 3, 3, 0], np.int32)
+    off, shared = common_prefixes(meta, nd)
+    assert off.tolist() == [0, 3, 5, 6] and shared.tolist() == [2, 3, 0]
+    off, shared = common_prefixes(meta, nd, min_blocks=3)
+    assert off.tolist() == [0, 1, 2, 3, 5, 6] and shared.tolist() == [3, 3, 2, 3, 0]
+    off, shared = common_prefixes(meta[:0], nd[:0])
+    assert off.tolist() == [0] and shared.tolist() == []
