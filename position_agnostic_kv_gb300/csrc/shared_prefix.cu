@@ -138,7 +138,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     {
       // Q operands: NC lanes to a row (of the pair's up to 256), a run of rows to a group of lanes, so that the heads of
       // a request share their cosines; f16, 128-byte swizzle.  A power of two per row takes it into [-1, 1], where f16
-      // keeps 11 bits of what matters.
+      // keeps 11 bits of what matters.  The raw rows come into the V stages first, by copies that are all in flight at
+      // once: loads row by row wait behind the first K and V tiles of every block (13 400 cycles until Q is ready, so
+      // 7 000).  The values' copies start when Q is ready.
       constexpr int NC = POS == kRope ? D / 16 : D / 8, NG = 256 / NC, PER = 2 * kM / NG;
       const int t = threadIdx.x, c = t % NC, n0 = t / NC * PER;
       auto put = [&](int n, int k, const float2 (&y)[4]) {
@@ -152,44 +154,50 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         y[2] = bf2_to_f2(u.z);
         y[3] = bf2_to_f2(u.w);
       };
-      const uint4 zero = make_uint4(0, 0, 0, 0);
       const int rd = POS == kRope ? D : (POS == kRopeX ? a.pos.rotary_dim : 0), hr = rd / 2;
       const bool inter = POS == kRopeX && a.pos.interleaved != 0;
       // this lane's chunk, the one that it turns it against (itself: none), and its first frequency
       const int other = POS == kRope ? c + NC : (inter || 8 * c >= rd ? c : (8 * c < hr ? c + hr / 8 : c - hr / 8));
       const int f0 = POS == kRope ? 8 * c : (inter ? 4 * c : (8 * c < hr ? 8 * c : 8 * c - hr));
-      int req = (row0 + n0) / G, h = (row0 + n0) % G;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)(b0 + req) * a.Hq + kvh * G + h) * D);
-      constexpr int AHEAD = 4;  // rows in flight
-      uint4 raw[AHEAD][2];
-      uint32_t pos[AHEAD];
-      auto load = [&](int n, uint4 (&u)[2], uint32_t& m) {
-        const bool here = n < rows && n < n0 + PER;
-        u[0] = here ? src[c] : zero;
-        u[1] = here && other != c ? src[other] : zero;
-        m = here ? uint32_t(max(a.seq_len[b0 + req] - 1, 0)) : 0u;
-        src += ++h == G ? (size_t)(a.Hq - G + 1) * (D / 8) : D / 8;
-        if (h == G) {
-          h = 0;
-          ++req;
+      const int nq = two ? 2 * kM : kM;  // rows of the operands
+      {
+        constexpr int CPR = D / 8, STEP = 256 / CPR;  // 16-byte chunks per row, rows per round of the 256 threads
+        const int k = t % CPR;
+        int n = t / CPR, rq = (row0 + n) / G, hd = (row0 + n) % G;
+        const int step_rq = STEP / G, step_hd = STEP % G;
+#pragma unroll 4
+        for (; n < nq; n += STEP) {
+          const void* src = n < rows ? a.q + ((size_t)(b0 + rq) * a.Hq + kvh * G + hd) * D + 8 * k : a.q;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sV0 + uint32_t(n) * (D * 2) + uint32_t(k) * 16),
+                       "l"(src), "r"(n < rows ? 16 : 0) : "memory");
+          rq += step_rq;
+          hd += step_hd;
+          if (hd >= G) {
+            hd -= G;
+            ++rq;
+          }
         }
-      };
-      const int n1 = min(n0 + PER, two ? 2 * kM : kM);
-      if (n0 < n1)
-#pragma unroll
-        for (int e = 0; e < AHEAD; ++e) load(n0 + e, raw[e], pos[e]);
+      }
+      // the run's rows belong to at most NC requests: lane c of the group holds the c-th's position
+      int req = (row0 + n0) / G, h = (row0 + n0) % G;
+      const int req0 = req;
+      const uint32_t pos = req0 + c < nreq ? uint32_t(max(a.seq_len[b0 + req0 + c] - 1, 0)) : 0u;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      named_sync(1, 2 * kM);
+      const int n1 = min(n0 + PER, nq);
       float2 co[4], sn[4];
       uint32_t turned = 0xFFFFFFFFu;  // position that co and sn are of
 #pragma unroll 1
-      for (int n2 = n0; n2 < n1; n2 += AHEAD)
-#pragma unroll
-      for (int e2 = 0; e2 < AHEAD; ++e2) {
-        const int n = n2 + e2;
+      for (int n = n0; n < n1; ++n) {
         float2 x[4], z[4], y[4];
-        unpack(raw[e2][0], x);
-        unpack(raw[e2][1], z);
-        const uint32_t m = pos[e2];
-        if (n2 + AHEAD < n1) load(n + AHEAD, raw[e2], pos[e2]);
+        const uint32_t raw_row = sV0 + uint32_t(n) * (D * 2);
+        unpack(ld_shared_v4(raw_row + uint32_t(c) * 16), x);
+        unpack(ld_shared_v4(raw_row + uint32_t(other) * 16), z);
+        const uint32_t m = __shfl_sync(0xffffffffu, pos, (lane & ~(NC - 1)) | (req - req0));
+        if (++h == G) {
+          h = 0;
+          ++req;
+        }
         if ((POS == kRope || POS == kRopeX) && m != turned) {
           turned = m;
 #pragma unroll
@@ -588,7 +596,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       // ============================ V copies
       uint64_t w_next = fetch(0);
       int issued = 0;
-      bool ok = true;
+      bool ok = wait_bar(BAR(B_Q_READY), 0, abort_flag, a.status);  // the raw queries have left the stages
+      ok = __all_sync(0xffffffffu, ok);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kVStages;
         const uint64_t w = w_next;
