@@ -415,17 +415,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       constexpr int kRowsPerWarp2 = kM / 4, kRowsPerWarp1 = kM / 8;
       const int n0 = (two ? warp * kRowsPerWarp2 : warp * kRowsPerWarp1) + lane / LPR, c = lane % LPR;
       const int n1 = fine ? min(rows, n0 - lane / LPR + (two ? kRowsPerWarp2 : kRowsPerWarp1)) : 0;
-      int req = (row0 + n0) / G, hd = (row0 + n0) % G;
+      int hd = (row0 + n0) % G;
+      float* to = a.part_o + (((size_t)(b0 + (row0 + n0) / G) * a.Hq + kvh * G + hd) * pi0 + split) * D + 4 * c;
+      const size_t step = pi0 * D * RPW, wrap = (size_t)(a.Hq - G) * pi0 * D;  // to the next row's; to the next request's
 #pragma unroll 4
       for (int q = n0; q < n1; q += RPW) {
-        const uint4 u = ld_shared_v4(sK0 + uint32_t(q) * (D * 4) + (uint32_t(c ^ (q & 7)) << 4));
-        const size_t pi = ((size_t)(b0 + req) * a.Hq + kvh * G + hd) * pi0 + split;
-        reinterpret_cast<uint4*>(a.part_o + pi * D)[c] = u;
-        hd += RPW;
-        while (hd >= G) {
-          hd -= G;
-          ++req;
-        }
+        *reinterpret_cast<uint4*>(to) = ld_shared_v4(sK0 + uint32_t(q) * (D * 4) + (uint32_t(c ^ (q & 7)) << 4));
+        to += step;
+        for (hd += RPW; hd >= G; hd -= G) to += wrap;
       }
     }
   } else if (warp < kKWarp) {
@@ -466,7 +463,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
 #pragma unroll
             for (int e = 0; e < 8; ++e) turn_sincos_fast(uint32_t(pi.x), turns[8 * c + e], sn[e], co[e]);
           }
-#pragma unroll
+// (unrolled by 2 and not by 8: every role's code goes through one instruction cache, 98.8 -> 92.2 us for eight groups)
+#pragma unroll 2
           for (int i = 0; i < NCP; ++i) {
             const int t = g * NCP + i;
             if (t < pi.y) continue;
