@@ -399,43 +399,65 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             }
           }
         } else {
+          // A thread owns one chunk of its rows and, with half-split pairs, reads the one that it is turned against.
           constexpr int NC = D / 8, NG = kPrep / NC;
           const int k = t % NC, per = (n16 + NG - 1) / NG, n0 = t / NC * per;
           const int rd = POS == kRopeX ? a.pos.rotary_dim : 0, hr = rd / 2;
-          const bool inter = a.pos.interleaved != 0;
+          const bool inter = a.pos.interleaved != 0, still = 8 * k >= rd, low = 8 * k < hr;
+          const int other = still || inter ? k : (low ? k + hr / 8 : k - hr / 8);
+          const int f0 = inter ? 4 * k : (low ? 8 * k : 8 * k - hr);
+          float2 co[4], sn[4];  // times the scale; sn with the sign of the partner's product
           int token = (r0 + n0) / G, h = (r0 + n0) % G;
+          int tk = token, hh = h;  // of the row that is loaded next, one ahead of the one in use
+          uint4 raw[2];
+          auto load = [&](int e) {
+            const uint4* s = e < per ? src(n0 + e, tk, hh) : nullptr;
+            raw[0] = s ? s[k] : zero;
+            raw[1] = s && other != k ? s[other] : zero;
+            if (++hh == G) {
+              hh = 0;
+              ++tk;
+            }
+          };
+          load(0);
+          bool turn = true;  // the token has changed
           ok = buffer_free();
-          for (int n = n0; ok && n < min(n0 + per, n16); ++n) {
-            const uint4* s = src(n, token, h);
-            const int dp = it.m0 + token - delta;
-            if (++h == G) {
+          const int n1 = ok ? min(n0 + per, n16) : n0;
+#pragma unroll 1
+          for (int n = n0; n < n1; ++n) {
+            float2 x[4], z[4], y[4];
+            unpack8(raw[0], x);
+            unpack8(raw[1], z);
+            load(n + 1 - n0);
+            if (turn && !still) {
+              const int dp = it.m0 + token - delta;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (inter) {  // one angle per pair of neighbours
+                  turn_sincos_signed(dp, a.pos.turns[f0 + e], sn[e].y, co[e].x);
+                  co[e].x = co[e].y = co[e].x * sc;
+                  sn[e].y *= sc;
+                  sn[e].x = -sn[e].y;
+                } else {
+                  turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e], sn[e].x, co[e].x);
+                  turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e + 1], sn[e].y, co[e].y);
+                  co[e] = make_float2(co[e].x * sc, co[e].y * sc);
+                  sn[e] = low ? make_float2(-sn[e].x * sc, -sn[e].y * sc) : make_float2(sn[e].x * sc, sn[e].y * sc);
+                }
+              }
+            }
+            turn = ++h == G;
+            if (turn) {
               h = 0;
               ++token;
             }
-            float2 x[4], y[4];
-            unpack8(s ? s[k] : zero, x);
-            if (8 * k >= rd) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].x * sc, x[e].y * sc);
-            } else if (inter) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float s1, c1;
-                turn_sincos_signed(dp, a.pos.turns[4 * k + e], s1, c1);
-                y[e] = make_float2((x[e].x * c1 - x[e].y * s1) * sc, (x[e].x * s1 + x[e].y * c1) * sc);
-              }
-            } else {
-              const bool low = 8 * k < hr;
-              const int f0 = 8 * k - (low ? 0 : hr);
-              float2 z[4];
-              unpack8(s ? s[low ? k + hr / 8 : k - hr / 8] : zero, z);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float s1, c1, s2, c2;
-                turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e], s1, c1);
-                turn_sincos_signed(dp, a.pos.turns[f0 + 2 * e + 1], s2, c2);
-                y[e] = make_float2((x[e].x * c1 + (low ? -z[e].x : z[e].x) * s1) * sc,
-                                   (x[e].y * c2 + (low ? -z[e].y : z[e].y) * s2) * sc);
+            for (int e = 0; e < 4; ++e) {
+              if (still) {
+                y[e] = make_float2(x[e].x * sc, x[e].y * sc);
+              } else {
+                const float2 p = inter ? make_float2(x[e].y, x[e].x) : z[e];  // the partners
+                y[e] = __ffma2_rn(x[e], co[e], __fmul2_rn(p, sn[e]));
               }
             }
             put(n, k, y);
