@@ -300,14 +300,16 @@ int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const int32_t* q_st
  *                  group_off[g+1]-1 form group g; requests outside every group are decoded alone
  *   shared_blocks  (device) int32 [n_groups]: the first shared_blocks[g] words of the group's lists are the
  *                  same; document blocks only (at most the doc_blocks of each of its requests).  They are
- *                  read from the list of the group's first request.
+ *                  read from the list of the group's first request (which holds them even if it is idle).
  *   max_group      upper bound (host) of the groups' sizes
  *   max_shared     upper bound (host) of shared_blocks; a larger group or value is cut to it (with
  *                  LAZY_STATUS_BAD_ROW), and what is cut off is decoded alone: the results are the same
  *   ws             lazy_decode_shared_workspace_size bytes, 256-byte aligned
  * q, seq_len, q_start, doc_blocks, meta, out and lse as in lazy_attn_decode.  seq_len[b] <= 0 marks an idle
  * request (a batch padded to a fixed size); it and one without a visible key get out = 0 and lse = -inf.
- * Common keys are rotated and taken in f16 (as in lazy_attn_prefill: magnitudes above 65504 overflow).
+ * Common keys are rotated and taken in f16 (as in lazy_attn_prefill: magnitudes above 65504 overflow); a NaN
+ * in a common value reaches that column of every request of the group.  Few and short lists are decoded one by
+ * one, where that is faster; a long list of a request alone is best given as a group of one.
  */
 int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, const int32_t* q_start,
                             const int32_t* doc_blocks, const uint64_t* meta, const int32_t* group_off,
@@ -329,13 +331,15 @@ size_t lazy_decode_shared_workspace_size(int B, int n_groups, int max_group, int
  *            request b, the last of them at position seq_len[b] - 1 (a decode step: cu_q[b] = b; a prefill:
  *            its own cu_q, and seq_len from lazy_build_doc_meta)
  *   lse      (device) float [total_q][Hq], from the attention call over the same list
- *   max_q    upper bound (host) of the rows of a request
+ *   max_q    upper bound (host) of the rows of a request; of more rows the last max_q count
+ *            (LAZY_STATUS_BAD_ROW)
  *   window   > 0: only the last `window` rows of each request count; 0: all of them
  *   accumulate  0: weights is written, 0 where no key lies; 1: added to
  *   weights  (device) float [B][16 max_blocks]
  *   ws       lazy_workspace_size(LAZY_PHASE_KEY_WEIGHTS, ...) bytes, 256-byte aligned
- * A row with lse = -inf (nothing visible) counts nothing.  Sums are in fp32, in a fixed order: two calls
- * give the same bits.
+ * A row with lse = -inf (nothing visible) counts nothing, a NaN key takes its own weight, a NaN row those of
+ * the keys that it sees.  Queries count with 24 bits (up to 32 rows per KV head) or 16, sums are in fp32 and in a
+ * fixed order: two calls give the same bits.
  */
 int lazy_attn_key_weights(const void* q, const float* lse, const int32_t* cu_q, const int32_t* seq_len,
                           const int32_t* q_start, const int32_t* doc_blocks, const uint64_t* meta, int B,

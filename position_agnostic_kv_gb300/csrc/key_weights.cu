@@ -1,5 +1,36 @@
 // The attention weight that every cached key receives: w_k = sum over query rows i and heads h of
 // 2^(s_ihk - lse_ih), s in base 2.
+//
+// One product per tile of 128 keys and block of up to 128 query rows: S = K Q^T, keys x rows, on the 5th-generation
+// tensor cores.  With the keys as its rows a score's lane is its key, so a thread adds up one key's weights and no
+// lane talks to another; keys go from the cache into the product as they are (a key's rotation is undone on the
+// query's side: Q = R_{m - Delta} q, prepared anew for every document), so a row of K that holds no key spoils
+// nothing but a sum that is not written.
+//
+// Precision: the weights are fp32 results and their sums are kept over many steps, so the scores are not rounded to
+// 16 bits: K is exact in bf16, and a query value is the sum of three bf16 numbers (24 bits) in blocks of up to 32
+// rows, of two (16 bits) in larger ones, where the rows' errors average out.  Against 64 bits: 1e-7 to 1e-6 relative.
+//
+// Work is cut into equal parts, one per SM, in the order request, KV head, group of row blocks, page; a part is a
+// sequence of items (a run of up to 32 pages of one document against one block of rows), and a tile is 8 pages of it.
+// Roles of a block (640 threads, one block per SM):
+//   warps 0-7   weights: two warpgroups, thread = key.  More than 32 rows: both read each tile, half of the columns
+//               each; fewer: every second tile each.  2^(s - lse) per row, sums in registers.
+//   warps 8-15  Q operands (two buffers): turned, scaled, split into bf16 parts, 128-byte swizzle.
+//   warp 16     the items, from the block words.
+//   warps 17-18 TMA copies of K, 64 columns x 16 rows of a page each (3 to 6 tiles in flight).
+//   warp 19     products (one thread).
+// A second launch adds the KV heads' and groups' sums in a fixed order, so results repeat bit for bit.
+//
+// What bounds it: with one row per head (a decode step) the keys' bytes: 16 requests of 32 033 keys, 8 KV heads, 182 us,
+// 5.8 TB/s, 12 of them for adding up the heads' sums.  With many rows the warps that weigh: 64 columns of a tile take a
+// warp ~1300 cycles (16 exponentials at 8 cycles, as many additions, two warps to a scheduler), a tile ~1900 in all, of
+// which the products (two passes of 16 bits) take 1024: 8 x 32 rows of 64 heads over 10 304 keys 104 us, 414 TFLOP/s.
+// Steps (this case; a decode step's in brackets): handshakes per run of pages and not per tile 123 -> 113 us [-];
+// copies, planning and preparation by warps of their own 132 [298 -> 227]; the parts of a query in one product of
+// concatenated columns [227 -> 181]; four score buffers 110 -> 104.  Left out: registers split between the roles (any
+// spill goes to the L2, as shared memory leaves no L1: 167), four warpgroups of readers (112), pages prefetched into the
+// L2 (111 [203]), 32 columns at a time (105), preparation by four warps (105, 67 instead of 60 for one long question).
 #include <algorithm>
 #include <climits>
 
@@ -249,19 +280,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
           const int cut = (n16 + 1) / 2, c1 = wg == 0 ? cut : n16;
           int c = wg == 0 ? 0 : cut;
 #pragma unroll 1
-          for (; c + 2 <= c1; c += 2) {
-            uint32_t u[32];
-            tmem_ld32(tS + uint32_t(16 * c), u);
-            tmem_wait_ld();
-            float2 x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pair(u, e);
-            weigh(x, 16 * c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pair(u, 8 + e);
-            weigh(x, 16 * c + 16);
-          }
-          if (c < c1) {
+          for (; c < c1; ++c) {
             uint32_t u[16];
             tmem_ld16(tS + uint32_t(16 * c), u);
             tmem_wait_ld();
@@ -271,6 +290,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
             weigh(x, 16 * c);
           }
         } else {  // three parts
+#pragma unroll 1
           for (int c = 0; c < n16; ++c) {
             uint32_t u[3][16];
 #pragma unroll

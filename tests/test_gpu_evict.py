@@ -142,6 +142,24 @@ def test_key_weights_of_idle_requests(lk):
     v.check(got)
 
 
+def test_key_weights_of_more_rows_than_tokens(lk):
+    """Rows before the sequence's first token see nothing; the others' positions count from the end."""
+    v = Votes(lk, "window")
+    v.x.seq_len[0] = 3
+    v.g.seq_len.copy_(dev(v.x.seq_len.astype(np.int32)))
+    v.check(v.run())
+    assert lk.device_status() == 0
+
+
+def test_key_weights_beyond_max_q(lk):
+    """Of more rows than max_q the last max_q count, and the status says so."""
+    v = Votes(lk, "all_rows")
+    got = v.run(max_q=17)
+    v.window = 17
+    v.check(got)
+    assert lk.device_status() == 8
+
+
 def test_key_weights_bad_page(lk):
     v = Votes(lk, "window")
     x = v.x

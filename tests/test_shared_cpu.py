@@ -76,7 +76,7 @@ PLAN = [
     (dict(B=-1), EINVAL, "bad sizes"), (dict(max_blocks=0), EINVAL, "bad sizes"), (dict(max_dst=0), EINVAL, "bad sizes"),
     (dict(num_pages=0), EINVAL, "bad sizes"), (dict(first=-1), EINVAL, "first"), (dict(recent=-1), EINVAL, "recent"),
     (dict(num_pages=(1 << 24) + 1), ERANGE, "num_pages"), (dict(max_dst=(1 << 26) + 1), ERANGE, "lists"),
-    (dict(cfg=None), EINVAL, "cfg"),
+    (dict(cfg=None), EINVAL, "cfg"), (dict(B=(1 << 24) + 1), ERANGE, "2^24"),
 ] + [(dict([(n, None)]), EINVAL, "NULL") for n in ("weights", "meta", "doc_blocks", "keep", "dst_pages", "new_meta",
                                                    "new_doc_blocks", "src", "dst", "new_weights")]
 MOVE = [
