@@ -22,15 +22,19 @@
 //   warp 19     products (one thread).
 // A second launch adds the KV heads' and groups' sums in a fixed order, so results repeat bit for bit.
 //
-// What bounds it: with one row per head (a decode step) the keys' bytes: 16 requests of 32 033 keys, 8 KV heads, 182 us,
-// 5.8 TB/s, 12 of them for adding up the heads' sums.  With many rows the warps that weigh: 64 columns of a tile take a
-// warp ~1300 cycles (16 exponentials at 8 cycles, as many additions, two warps to a scheduler), a tile ~1900 in all, of
-// which the products (two passes of 16 bits) take 1024: 8 x 32 rows of 64 heads over 10 304 keys 104 us, 414 TFLOP/s.
+// What bounds it: with one row per head (a decode step) the keys' bytes: 16 requests of 32 033 keys, 8 KV heads, 176 us,
+// 6.0 TB/s, some 8 of them for adding up the heads' sums.  With many rows the roles share the SM's issue slots and no one
+// of them is the limit: 8 x 32 rows of 64 heads over 10 304 keys 94.5 us, 456 TFLOP/s, a tile ~2000 cycles, of which the
+// products (two passes of 16 bits) take 1024; with a quarter of the preparation 85, without exponentials 83, with half of the
+// products 92.  One question of 800 tokens over 2400 keys 52.5, a third of it the first operand and the sums.
 // Steps (this case; a decode step's in brackets): handshakes per run of pages and not per tile 123 -> 113 us [-];
 // copies, planning and preparation by warps of their own 132 [298 -> 227]; the parts of a query in one product of
-// concatenated columns [227 -> 181]; four score buffers 110 -> 104.  Left out: registers split between the roles (any
-// spill goes to the L2, as shared memory leaves no L1: 167), four warpgroups of readers (112), pages prefetched into the
-// L2 (111 [203]), 32 columns at a time (105), preparation by four warps (105, 67 instead of 60 for one long question).
+// concatenated columns [227 -> 181]; four score buffers 110 -> 104; the share's ends found in one pass over the requests
+// without 64-bit divisions, 12 000 -> 8 000 cycles before the first tile, code for few and for many rows apart, sums that
+// read the lists before they wait 104 -> 94.5 [182 -> 176].  Left out: registers split between the roles (any spill goes to
+// the L2, as shared memory leaves no L1: 167), four warpgroups of readers (112), pages prefetched into the L2 (111 [203]), 32
+// columns at a time (105), the next 16 scores' load ahead of the exponentials (103 where 96.6), preparation by four warps
+// (105, 67 instead of 60 for the one question), the sums' launch let go early (103 where 100.7, 63.8 where 59.1).
 #include <algorithm>
 #include <climits>
 
@@ -70,7 +74,7 @@ struct Args {
   int B, max_blocks, Hq, Hkv, num_pages, window, accumulate, groups;
   int rows;             // columns of the Q buffers: query rows per block at most, a multiple of 16
   int most;             // rows per head of a request at most (the call's bound)
-  int halves;           // sums per group: 2 in blocks of many rows
+  int sums;             // per group: 2 in blocks of many rows (each warpgroup has a part of the columns)
   int stages;           // K tiles in flight
   PosParams pos;
 };
@@ -98,7 +102,16 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   return r;
 }
 // group g covers row blocks [group_start(g), group_start(g + 1))
-__device__ __forceinline__ int group_start(const Request& r, int g) { return int((long long)g * r.nrb / r.rgc); }
+__device__ __forceinline__ int group_start(const Request& r, int g) {  // up to 8 x 2^27
+  return int(uint32_t(g) * uint32_t(r.nrb) / uint32_t(r.rgc));
+}
+// x / d where the quotient is a small number: an estimate and its correction (x, d >= 0)
+__device__ __forceinline__ int small_quotient(long long x, long long d) {
+  int q = int(__fdividef(float(x), float(d)));
+  while (q * d > x) --q;
+  while ((q + 1) * d <= x) ++q;
+  return q;
+}
 
 enum : int { F_END = 1, F_NEWQ = 2, F_MASK = 4 };
 struct Item {  // a run of pages of one document against one block of query rows: tiles of 8 pages
@@ -147,6 +160,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr));
 }
 
+// Waits for the thread's loads; the values are used behind it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
 // Eight values in bf16, and what that leaves of them.
 __device__ __forceinline__ uint4 round8(const float2 (&y)[4]) {
   return make_uint4(f2_to_bf2(y[0].x, y[0].y), f2_to_bf2(y[1].x, y[1].y), f2_to_bf2(y[2].x, y[2].y),
@@ -169,7 +191,7 @@ struct Place {
   int b, kvh, rg, page;
 };
 
-template <int D, int POS>
+template <int D, int POS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   using L = WLayout<D>;
@@ -180,7 +202,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   const int NS = a.stages, rows = a.rows, G = a.Hq / a.Hkv;
   // Blocks of many rows: both warpgroups read each tile's scores, half of the columns each (their sums stay
   // apart); of few rows: every second tile each.
-  const bool split = rows > kFew;
+  constexpr bool split = SPLIT;  // rows > kFew
   const uint32_t QBUF = uint32_t(L::qbuf(rows)), QPART = uint32_t(rows) * 128, QBLK = QPART * L::parts(rows);
   const uint32_t sK = sb, sQ = sb + NS * L::TILE;
   uint8_t* const tail = sm + NS * L::TILE + 2 * QBUF;
@@ -216,12 +238,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   bool ok = *abort_flag == 0;
 
   if (warp < 8) {
-    // ============================ weights of every second item: a thread owns a key
+    // ============================ weights: a thread owns a key of a tile
     const int wg = warp >> 2, row = threadIdx.x & 127;  // TMEM lane = key of the tile
     uint32_t tile = 0;  // of this block's tiles
     for (int i = 0; ok; ++i) {
       const Item& it = items[i % kSlots];
-      // the first tile's scores say that the item is there; a warpgroup without a tile in it asks for the item itself
       bool got = wait_bar(BAR(B_META + i % kSlots), uint32_t((i / kSlots) & 1), abort_flag, a.status);
       if (!__all_sync(0xffffffffu, got)) break;
       const int flags = it.flags, np = it.np;
@@ -248,65 +269,55 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
         }
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const bool masked = flags & F_MASK;
-        // 16 scores, each the sum of its parts' columns: acc += 2^(s - lse)
-        auto weigh = [&](float2 (&x)[8], int c0) {
+        const int keys = mine < np && n0 < int(it.rows) ? int(it.page[mine] & 0xFFu) : 0;  // 0 too for a key that no row sees
+        const int cut = split ? (n16 + 1) / 2 : 0, c1 = split && wg == 0 ? cut : n16;
+        constexpr int PARTS = split ? 1 : 3;  // columns that a score is the sum of (of many rows the products add them up)
+        uint32_t u[PARTS][16];
+        auto load = [&](int c) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse + c0 + 2 * e);  // negative log-sum-exps
+          for (int e = 0; e < PARTS; ++e) tmem_ld16(tS + uint32_t(e * rows + 16 * c), u[e]);
+        };
+        int c = split && wg ? cut : 0;
+#pragma unroll 1
+        for (; c < c1; ++c) {  // 16 scores: acc += 2^(s - lse)
+          const float* l = lse + 16 * c;
+          float4 l4[4];  // negative log-sum-exps
+          auto lses = [&]() {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l4[e] = *reinterpret_cast<const float4*>(l + 4 * e);
+          };
+          load(c);
+          if constexpr (split) lses();
+#pragma unroll
+          for (int e = 0; e < PARTS; ++e) tmem_wait_ld16(u[e]);
+          if constexpr (!split) lses();
+          float2 x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            auto part = [&](int i) { return make_float2(__uint_as_float(u[i][2 * e]), __uint_as_float(u[i][2 * e + 1])); };
+            x[e] = part(0);
+            if constexpr (!split) x[e] = __fadd2_rn(x[e], __fadd2_rn(part(1), part(2)));
             if constexpr (kAl) {
-              const float *sl = lse + rows + c0 + 2 * e, *mm = sl + rows;
+              const float *sl = l + rows + 2 * e, *mm = sl + rows;
               x[e].x = fmaf(sl[0], float(p) - mm[0], x[e].x);
               x[e].y = fmaf(sl[1], float(p) - mm[1], x[e].y);
-              x[e + 1].x = fmaf(sl[2], float(p) - mm[2], x[e + 1].x);
-              x[e + 1].y = fmaf(sl[3], float(p) - mm[3], x[e + 1].y);
             }
-            x[e] = __fadd2_rn(x[e], make_float2(l4.x, l4.y));
-            x[e + 1] = __fadd2_rn(x[e + 1], make_float2(l4.z, l4.w));
+            x[e] = __fadd2_rn(x[e], e & 1 ? make_float2(l4[e / 2].z, l4[e / 2].w) : make_float2(l4[e / 2].x, l4[e / 2].y));
           }
           if (masked) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              if (c0 + 2 * e < n0) x[e].x = -INFINITY;
-              if (c0 + 2 * e + 1 < n0) x[e].y = -INFINITY;
+              if (16 * c + 2 * e < n0) x[e].x = -INFINITY;
+              if (16 * c + 2 * e + 1 < n0) x[e].y = -INFINITY;
             }
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x[e].x), ex2(x[e].y)));
-        };
-        auto pair = [](const uint32_t* u, int e) {
-          return make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
-        };
-        if (split) {  // the parts are in one sum
-          const int cut = (n16 + 1) / 2, c1 = wg == 0 ? cut : n16;
-          int c = wg == 0 ? 0 : cut;
-#pragma unroll 1
-          for (; c < c1; ++c) {
-            uint32_t u[16];
-            tmem_ld16(tS + uint32_t(16 * c), u);
-            tmem_wait_ld();
-            float2 x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pair(u, e);
-            weigh(x, 16 * c);
-          }
-        } else {  // three parts
-#pragma unroll 1
-          for (int c = 0; c < n16; ++c) {
-            uint32_t u[3][16];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) tmem_ld16(tS + uint32_t(e * rows + 16 * c), u[e]);
-            tmem_wait_ld();
-            float2 x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __fadd2_rn(pair(u[0], e), __fadd2_rn(pair(u[1], e), pair(u[2], e)));
-            weigh(x, 16 * c);
-          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_SFREE + buf));
         if (mine < np) {
-          const int keys = int(it.page[mine] & 0xFFu);
           const float w = row % kPage < keys ? ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) : 0.f;
           to[j * kPage] = old + w;
         }
@@ -492,51 +503,74 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   } else if (warp == kPlanWarp) {
     // ============================ the block's share of the work, item by item
     long long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      long long c = 0;
+    Request r = {};  // of request b0 + lane
+    long long c = 0;
+    auto count = [&](int b0) {
+      c = 0;
       if (b0 + lane < a.B) {
-        const Request r = request_of(a, b0 + lane);
+        r = request_of(a, b0 + lane);
         c = (long long)r.nb * r.nrb * a.Hkv;
       }
+    };
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      count(b0);
+      long long all = c;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-      total += c;
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      total += all;
     }
-    auto locate = [&](long long x) -> Place {  // x < total
+    // the share [total * block / blocks, total * (block + 1) / blocks)
+    const uint32_t grid = gridDim.x, bid = blockIdx.x;
+    const long long each = (total >> 32) ? total / grid : (long long)(uint32_t(total) / grid);
+    const uint32_t rest = uint32_t(total - each * grid);
+    const long long x0 = each * bid + rest * bid / grid, x1 = each * (bid + 1) + rest * (bid + 1) / grid;
+    Place at = {a.B, 0, 0, 0}, end = at;
+    int known = -1;  // request that `r` is of
+    if (x0 < x1) {
+      Request mine = {};
       long long base = 0;
-      for (int b0 = 0; b0 < a.B; b0 += 32) {
-        long long c = 0;
-        if (b0 + lane < a.B) {
-          const Request r = request_of(a, b0 + lane);
-          c = (long long)r.nb * r.nrb * a.Hkv;
-        }
+      int left = x1 < total ? 2 : 1;  // places to find
+      for (int b0 = 0; b0 < a.B && left; b0 += 32) {
+        if (a.B > 32) count(b0);
         long long up = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, up, o);
           if (lane >= o) up += y;
         }
-        const uint32_t in = __ballot_sync(0xffffffffu, x < base + up);
-        if (in) {
-          const int l = __ffs(in) - 1, b = b0 + l;
-          const Request r = request_of(a, b);
-          const long long y = x - base - __shfl_sync(0xffffffffu, up - c, l), one = (long long)r.nb * r.nrb;
-          const long long z = y % one;
-          const int kvh = int(y / one), rb = int(z / r.nb);
-          int g = int((long long)rb * r.rgc / r.nrb);
-          while (group_start(r, g + 1) <= rb) ++g;
-          const int first = group_start(r, g);
-          return {b, kvh, g, int((z - (long long)first * r.nb) / (group_start(r, g + 1) - first))};
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          const long long x = (e ? x1 : x0) - base;
+          const bool here = x >= up - c && x < up;
+          const uint32_t in = __ballot_sync(0xffffffffu, here);
+          if (!in || (e && x1 == total)) continue;
+          Place at_lane = {};
+          if (here) {
+            const long long y = x - (up - c), one = (long long)r.nb * r.nrb;
+            at_lane.kvh = small_quotient(y, one);
+            const long long z = y - at_lane.kvh * one;
+            const int rb = small_quotient(z, r.nb);
+            int g = small_quotient((long long)rb * r.rgc, r.nrb);
+            while (group_start(r, g + 1) <= rb) ++g;
+            const int first = group_start(r, g);
+            at_lane.rg = g;
+            at_lane.page = small_quotient(z - (long long)first * r.nb, group_start(r, g + 1) - first);
+          }
+          const int l = __ffs(in) - 1;
+          Place& to = e ? end : at;
+          to = {b0 + l, __shfl_sync(0xffffffffu, at_lane.kvh, l), __shfl_sync(0xffffffffu, at_lane.rg, l),
+                __shfl_sync(0xffffffffu, at_lane.page, l)};
+          if (e == 0) {
+            known = b0 + l;
+            mine = {__shfl_sync(0xffffffffu, r.nb, l),  __shfl_sync(0xffffffffu, r.docs, l),  __shfl_sync(0xffffffffu, r.n, l),
+                    __shfl_sync(0xffffffffu, r.first, l), __shfl_sync(0xffffffffu, r.m0, l),  __shfl_sync(0xffffffffu, r.R, l),
+                    __shfl_sync(0xffffffffu, r.nrb, l), __shfl_sync(0xffffffffu, r.size, l),  __shfl_sync(0xffffffffu, r.rgc, l)};
+          }
+          --left;
         }
         base += __shfl_sync(0xffffffffu, up, 31);
       }
-      return {a.B, 0, 0, 0};
-    };
-    const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
-    Place at = {a.B, 0, 0, 0}, end = at;
-    if (x0 < x1) {
-      at = locate(x0);
-      if (x1 < total) end = locate(x1);
+      r = mine;
     }
     int i = 0, qn = -1;
     auto slot_free = [&](int j) -> bool {
@@ -546,8 +580,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
     auto before = [](const Place& p, const Place& e) {
       return p.b != e.b ? p.b < e.b : p.kvh != e.kvh ? p.kvh < e.kvh : p.rg != e.rg ? p.rg < e.rg : p.page < e.page;
     };
-    Request r = {};
-    int known = -1;
     while (ok && before(at, end)) {
       if (at.b != known) r = request_of(a, known = at.b);
       if (r.R == 0) {
@@ -744,45 +776,85 @@ weights_kernel(const __grid_constant__ CUtensorMap tmk, const Args a) {
   }
 }
 
-// Adds the parts of a key: groups of row blocks, KV heads, in order.  Only what was computed is read.
-__global__ void __launch_bounds__(256) weights_sum_kernel(const Args a) {
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y, N = a.max_blocks * kPage;
+// Adds the parts of a key: groups of row blocks, KV heads, in a fixed order.  A thread owns 4 keys of a page; SL threads
+// share their parts where a launch would leave SMs idle (one request of 2400 keys with 80 parts: 62.2 us by 1, 56.1 by 2, 54.6
+// by 4, 53.6 by 8; 16 requests of 32 033 keys with 8 parts: 177, 179, 183, 187).  A page has parts of
+// the groups with a row that sees its first key; they hold 0 where a key is not there or not seen.
+constexpr int kSumThreads = 256;
+template <int SL>
+__global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const Args a) {
+  constexpr int KEYS = 4 * kSumThreads / SL;
+  __shared__ float4 share[SL][SL > 1 ? KEYS / 4 : 1];
+  // What comes before the first wait reads what was there before the weights' launch: it waited for that itself before it
+  // let this one start.
+  const int b = blockIdx.y, N = a.max_blocks * kPage, quad = threadIdx.x % (KEYS / 4), slice = threadIdx.x / (KEYS / 4);
   const size_t n = (size_t)a.B * N;
   const Request r = request_of(a, b);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    const int n = a.cu_q[b + 1] - a.cu_q[b];
-    if ((a.window > 0 ? min(n, a.window) : n) > a.most) set_status(a.status, LAZY_STATUS_BAD_ROW);
+    const int rows = a.cu_q[b + 1] - a.cu_q[b];
+    if ((a.window > 0 ? min(rows, a.window) : rows) > a.most) set_status(a.status, LAZY_STATUS_BAD_ROW);
   }
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < N; i += gridDim.x * 256) {
-    const int j = i / kPage;
+  const int per = a.sums * a.Hkv, G = a.Hq / a.Hkv, last = r.rgc * per;
+  for (int i0 = blockIdx.x * KEYS; i0 < N; i0 += gridDim.x * KEYS) {  // the same rounds for every thread
+    const int i = i0 + 4 * quad, j = i / kPage;
     const size_t at = (size_t)b * N + i;
-    float t = 0.f;
-    if (r.R > 0 && j < r.nb) {
-      const uint64_t w = a.meta[(size_t)b * a.max_blocks + j];
-      const int p = int(word_delta(w)) + kPage * int(word_pg(w)) + i % kPage;
-      if (i % kPage < int(word_nvalid(w)))
-        for (int g = 0; g < r.rgc; ++g) {
-          const int last = min(r.R, group_start(r, g + 1) * r.size) - 1;
-          if (p <= r.m0 + last / (a.Hq / a.Hkv))
-#pragma unroll 8
-            for (int h = 0; h < a.halves * a.Hkv; ++h) t += a.part[((size_t)g * a.halves * a.Hkv + h) * n + at];
-        }
+    float old[4] = {0.f, 0.f, 0.f, 0.f};
+    int g0 = r.rgc;  // the first group with a row that sees the page
+    if (i < N) {
+      if (a.accumulate && slice == 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) old[e] = a.weights[at + e];
+      if (r.R > 0 && j < r.nb) {
+        const uint64_t w = a.meta[(size_t)b * a.max_blocks + j];
+        const int p = int(word_delta(w)) + kPage * int(word_pg(w));
+        g0 = 0;
+        while (g0 < r.rgc && p > r.m0 + (min(r.R, group_start(r, g0 + 1) * r.size) - 1) / G) ++g0;
+      }
     }
-    a.weights[at] = a.accumulate ? a.weights[at] + t : t;
+    pdl_wait();
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int e = g0 * per + slice; e < last; e += SL) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part + (size_t)e * n + at);
+      t.x += x.x;
+      t.y += x.y;
+      t.z += x.z;
+      t.w += x.w;
+    }
+    if constexpr (SL > 1) {
+      share[slice][quad] = t;
+      __syncthreads();
+      if (slice == 0)
+#pragma unroll
+        for (int e = 1; e < SL; ++e) {
+          const float4 x = share[e][quad];
+          t.x += x.x;
+          t.y += x.y;
+          t.z += x.z;
+          t.w += x.w;
+        }
+      __syncthreads();
+    }
+    if (i < N && slice == 0) {
+      a.weights[at] = old[0] + t.x;
+      a.weights[at + 1] = old[1] + t.y;
+      a.weights[at + 2] = old[2] + t.z;
+      a.weights[at + 3] = old[3] + t.w;
+    }
   }
+  pdl_wait();
+  pdl_trigger();
 }
 
 int most_rows(bool alibi, long long R) {
   const long long m = alibi ? kRowsAlibi : kRows, x = (R + 15) / 16 * 16;
   return int(x < 16 ? 16 : (x < m ? x : m));
 }
-template <int D, int POS>
+template <int D, int POS, bool SPLIT>
 int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   using L = WLayout<D>;
   static std::atomic<uint64_t> done{0};
-  auto kern = weights_kernel<D, POS>;
+  auto kern = weights_kernel<D, POS, SPLIT>;
   LAZY_CUDA_TRY(smem_limit(kern, L::LIMIT, done));
   a.stages = L::stages(a.rows, POS == kAlibi);
   // A block's share is at least about a tile.
@@ -791,6 +863,10 @@ int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
   LAZY_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kThreads), L::smem(a.rows, a.stages, POS == kAlibi), st, mk,
                            a));
   return LAZY_OK;
+}
+template <int D, int POS>
+int launch_weights(Args& a, const CUtensorMap& mk, cudaStream_t st) {
+  return a.rows > kFew ? launch_weights<D, POS, true>(a, mk, st) : launch_weights<D, POS, false>(a, mk, st);
 }
 
 }  // namespace
@@ -883,7 +959,7 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   const bool alibi = a.pos.kind == kAlibi;
   a.rows = most_rows(alibi, n * (Hq / Hkv));
   a.most = int(n);
-  a.halves = a.rows <= kFew ? 1 : 2;
+  a.sums = a.rows <= kFew ? 1 : 2;
   // Row blocks in one block's share, so that it still has runs of 32 pages: a Q operand then serves four tiles, and a
   // run's pages are read from memory once for all of them.  The more groups, the more parts to add.
   const long long nrb = (n * (Hq / Hkv) + a.rows - 1) / a.rows;
@@ -905,7 +981,19 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
                             : launch_weights<64, kNone>(a, mk, st);
     if (rc) return rc;
   }
-  const int blocks = int(std::min<long long>(((long long)max_blocks * kPage + 255) / 256, 65535));
-  LAZY_CUDA_TRY(launch_pdl(weights_sum_kernel, dim3(blocks, B), dim3(256), 0, st, a));
+  int slices = 1;
+  auto sum_blocks = [&]() { return ((long long)max_blocks * kPage * slices + 4 * kSumThreads - 1) / (4 * kSumThreads); };
+  while (slices < 8 && sum_blocks() * B < sm_count() && a.groups * a.sums * Hkv >= 8 * slices) slices *= 2;
+  void (*const sum)(const Args) = slices == 1   ? weights_sum_kernel<1>
+                                  : slices == 2 ? weights_sum_kernel<2>
+                                  : slices == 4 ? weights_sum_kernel<4>
+                                                : weights_sum_kernel<8>;
+  const dim3 sums(int(std::min<long long>(sum_blocks(), 65535)), B);
+  if (total_q > 0) {
+    LAZY_CUDA_TRY(launch_pdl(sum, sums, dim3(kSumThreads), 0, st, a));
+  } else {  // what comes before has to end first
+    sum<<<sums, dim3(kSumThreads), 0, st>>>(a);
+    LAZY_CUDA_TRY(cudaGetLastError());
+  }
   return LAZY_OK;
 }
