@@ -11,7 +11,8 @@ namespace {
 // A row's partial results joined by their maxima: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  One block of
 // kJoinWarps warps per row; every warp takes the maxima and sums (its lanes up to 4 each), then every
 // kJoinWarps-th result.  Its bytes are the partial results, 20 MB for 64 requests of 32 heads with 19 each: 11 us from
-// cold caches, about 8 after the kernels that wrote them, of which half is the launch and the first loads.
+// cold caches, 7 of the call's 52 after the kernels that wrote them, half of it the launch and the first loads.  With 2
+// warps 53.5 (32 heads of one KV head: 27.1 instead of 25.5), with 8 57.5; waiting before the lists are read 53.4.
 constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SharedArgs a) {
@@ -20,12 +21,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SharedArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hq = blockIdx.x, b = blockIdx.y;
   const size_t row = (size_t)b * a.Hq + hq, at = row * (a.SA + a.SB);
-  pdl_wait();
-  pdl_trigger();
+  // The lists are as they were before the call's first launch, which waited for what came before it.
   const Share sh = share_of(a, b);
   const int tiles = (sh.blocks + 7) / 8, chunk = tiles ? split_tiles(tiles, a.SA) : 1, na = (tiles + chunk - 1) / chunk;
   const int nb = visible_blocks(a.seq_len[b], a.q_start[b], a.doc_blocks[b], a.max_blocks);
   const int n = na + own_splits(max(0, nb - sh.blocks), a.SB);
+  pdl_wait();
+  pdl_trigger();
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
   auto index = [&](int s) { return s < na ? s : a.SA + s - na; };
   float2 mine[4];
