@@ -97,10 +97,12 @@ Sizes sizes_of(int B, int n_groups, int max_group, int max_shared, int max_block
   max_shared = std::min(max_shared, max_blocks);
   max_group = std::min(max_group, B);
   s.SA = shared_prefix_splits(B, n_groups, max_group, max_shared, Hq, Hkv);
-  // Own blocks: enough warps for about four waves, runs of at least 32 blocks a split.
+  // Own blocks: three blocks of threads per SM (four fit), runs of at least 32 blocks a split.  64 requests in 8 groups, 64 /
+  // 8 heads, 2 own documents of 512 keys: 89.7 us, with four times as many splits 92.9; 16 requests with 10: 82.0 and 90.5
+  // (two per SM 86.0, the quotient rounded down 85.9); 32 requests with 20, 32 / 8 heads: 264.7, 265.7 (rounded down 302).
   const int own = max_blocks - (s.SA ? max_shared : 0);
   const long long units = (long long)B * Hkv * ((Hq / Hkv + 7) / 8), slots = 3ll * sm_count();
-  long long sb = std::min<long long>((4 * slots + units - 1) / units, (own + 31) / 32);
+  long long sb = std::min<long long>((slots + units - 1) / units, (own + 31) / 32);
   s.SB = int(std::max(1ll, std::min(64ll, sb)));
   const size_t n = s.SA + s.SB > 1 ? (size_t)B * Hq * (s.SA + s.SB) : 0;  // one result is the row's
   s.o_bytes = (n * D * 4 + 255) / 256 * 256;

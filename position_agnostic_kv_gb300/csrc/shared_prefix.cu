@@ -27,7 +27,8 @@
 // Steps (this call): mma.sync with every row in registers 569 -> this kernel 68; Q rows by lanes, results written as whole
 // rows, set-up before the launch before has ended 57; own keys before the common ones 54; raw queries by asynchronous
 // copies 52.6.  Eight groups of ragged lists: keys' rotation unrolled twice and not eight times 98 -> 92, as the roles'
-// loops together miss the instruction cache.
+// loops together miss the instruction cache.  Left out: P handed over by halves, so that the first half's products start
+// under the second's exponentials (53.1 as before, groups 94.2 instead of 92.2).
 #include <cfloat>
 #include <climits>
 
