@@ -195,6 +195,33 @@ def test_key_weights_repeat_themselves(lk):
     assert np.array_equal(a, v.run())
 
 
+def test_key_weights_of_many_requests(lk):
+    """More requests than a warp has lanes, of very different sizes, some without rows and some without keys."""
+    n = 75
+    WEIGHTS["many"] = ([[(37 * b) % 290] if b % 5 else [] for b in range(n)], [1 + b * b % 41 for b in range(n)],
+                       [min(1 + b * b % 41, b % 4 * 3) for b in range(n)], 0, 8, 2, 128, pos_of())
+    try:
+        v = Votes(lk, "many")
+    finally:
+        del WEIGHTS["many"]
+    for b in (0, 33, 63, 64, 74):
+        v.x.seq_len[b] = 0
+    v.g.seq_len.copy_(dev(v.x.seq_len.astype(np.int32)))
+    got = v.run()
+    assert not got[[0, 33, 63, 64, 74]].any()
+    v.check(got)
+    assert lk.device_status() == 0
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_key_weights_without_rows(lk, accumulate):
+    v = Votes(lk, "window", accumulate=accumulate)
+    v.q, v.lse = v.q[:0], v.lse[:0]
+    v.cu_q.zero_()
+    assert np.array_equal(v.run(max_q=0), v.base if accumulate else 0 * v.base)
+    assert lk.device_status() == 0
+
+
 def test_key_weights_stream_and_graph(lk):
     import torch
     v, u = Votes(lk, "window"), Votes(lk, "window", 9)
