@@ -34,7 +34,8 @@
 // read the lists before they wait 104 -> 94.5 [182 -> 176].  Left out: registers split between the roles (any spill goes to
 // the L2, as shared memory leaves no L1: 167), four warpgroups of readers (112), pages prefetched into the L2 (111 [203]), 32
 // columns at a time (105), the next 16 scores' load ahead of the exponentials (103 where 96.6), preparation by four warps
-// (105, 67 instead of 60 for the one question), the sums' launch let go early (103 where 100.7, 63.8 where 59.1).
+// (105, 67 instead of 60 for the one question), the sums' launch let go early (103 where 100.7, 63.8 where 59.1), an
+// operand's first row made before its buffer is free (96.6, 55.5 where 53.7).
 #include <algorithm>
 #include <climits>
 
