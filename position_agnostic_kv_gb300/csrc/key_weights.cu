@@ -23,15 +23,16 @@
 // A second launch adds the KV heads' and groups' sums in a fixed order, so results repeat bit for bit.
 //
 // What bounds it: with one row per head (a decode step) the keys' bytes: 16 requests of 32 033 keys, 8 KV heads, 176 us,
-// 6.0 TB/s, some 8 of them for adding up the heads' sums.  With many rows the roles share the SM's issue slots and no one
+// 6.0 TB/s, some 3 of them for adding up the heads' sums.  With many rows the roles share the SM's issue slots and no one
 // of them is the limit: 8 x 32 rows of 64 heads over 10 304 keys 94.5 us, 456 TFLOP/s, a tile ~2000 cycles, of which the
-// products (two passes of 16 bits) take 1024; with a quarter of the preparation 85, without exponentials 83, with half of the
-// products 92.  One question of 800 tokens over 2400 keys 52.5, a third of it the first operand and the sums.
+// products (two passes of 16 bits) take 1024; when it was 103, it was 94 with a quarter of the preparation, 92 without
+// exponentials and 101 with half of the products.  One question of 800 tokens over 2400 keys 52.5, some 7 of them before the
+// first product and 3 for the sums.
 // Steps (this case; a decode step's in brackets): handshakes per run of pages and not per tile 123 -> 113 us [-];
 // copies, planning and preparation by warps of their own 132 [298 -> 227]; the parts of a query in one product of
 // concatenated columns [227 -> 181]; four score buffers 110 -> 104; the share's ends found in one pass over the requests
-// without 64-bit divisions, 12 000 -> 8 000 cycles before the first tile, code for few and for many rows apart, sums that
-// read the lists before they wait 104 -> 94.5 [182 -> 176].  Left out: registers split between the roles (any spill goes to
+// without 64-bit divisions (2 us sooner at the first tile), code for few and for many rows apart, sums that read the lists
+// before they wait 104 -> 94.5 [182 -> 176].  Left out: registers split between the roles (any spill goes to
 // the L2, as shared memory leaves no L1: 167), four warpgroups of readers (112), pages prefetched into the L2 (111 [203]), 32
 // columns at a time (105), the next 16 scores' load ahead of the exponentials (103 where 96.6), preparation by four warps
 // (105, 67 instead of 60 for the one question), the sums' launch let go early (103 where 100.7, 63.8 where 59.1), an
