@@ -52,7 +52,7 @@ using namespace tc;
 constexpr int kTile = 128, kPagesPerTile = kTile / kPage;  // keys per tile: the rows of a product
 constexpr int kRows = 128;                                  // most query rows per block: its columns
 constexpr int kRowsAlibi = 64;                              // (ALiBi keeps two more numbers per row)
-constexpr int kGroups = 8;                                  // most partial sums of a key and KV head
+constexpr int kGroups = 8;                                  // most groups of row blocks
 constexpr int kPrepWarps = 8, kPrep = 32 * kPrepWarps;
 constexpr int kCopyWarps = 2;
 constexpr int kPrepWarp0 = 8, kPlanWarp = kPrepWarp0 + kPrepWarps, kCopyWarp0 = kPlanWarp + 1,
@@ -848,6 +848,13 @@ __global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const Args a) 
   pdl_trigger();
 }
 
+// Partial sums of a key and KV head, at most, of a call with up to R rows per KV head: one where they fit a block of few
+// rows, else two (each reading warpgroup's columns) for every group of row blocks, and blocks hold 64 (ALiBi) or 128 rows.
+// The workspace has room for so many whatever the positional kind, and a call makes no more groups than that.
+long long sums_of(long long R) {
+  return R <= kFew ? 1 : 2 * std::min<long long>(kGroups, (R + kRowsAlibi - 1) / kRowsAlibi);
+}
+
 int most_rows(bool alibi, long long R) {
   const long long m = alibi ? kRowsAlibi : kRows, x = (R + 15) / 16 * 16;
   return int(x < 16 ? 16 : (x < m ? x : m));
@@ -910,9 +917,7 @@ int check_workspace(const char* what, const void* ws, size_t got, size_t need) {
 }
 
 size_t key_weights_ws_bytes(int rows, int B, int max_blocks, int Hq, int Hkv) {
-  // sums of a key and KV head, at most: groups of row blocks of 64 (ALiBi) or twice those of 128
-  const long long R = (long long)rows * (Hq / Hkv), sums = R <= kFew ? 1 : std::min<long long>(2 * kGroups, R / 64 + 2);
-  return (size_t)sums * Hkv * B * max_blocks * kPage * 4;
+  return (size_t)sums_of((long long)rows * (Hq / Hkv)) * Hkv * B * max_blocks * kPage * 4;
 }
 
 }  // namespace lazykv
@@ -966,7 +971,7 @@ extern "C" int lazy_attn_key_weights(const void* q, const float* lse, const int3
   // run's pages are read from memory once for all of them.  The more groups, the more parts to add.
   const long long nrb = (n * (Hq / Hkv) + a.rows - 1) / a.rows;
   const long long per = std::max(1ll, nrb * max_blocks * B * Hkv / (32ll * sm_count()));
-  a.groups = int(std::min<long long>(kGroups, std::max(1ll, (nrb + per - 1) / per)));
+  a.groups = int(std::min(sums_of((long long)total_q * (Hq / Hkv)) / a.sums, std::max(1ll, (nrb + per - 1) / per)));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int kind = a.pos.kind == kYarn ? int(kRope) : a.pos.kind;
   if (kind == kRope && (a.pos.rotary_dim != D || a.pos.interleaved)) kind = kRopeX;
