@@ -113,6 +113,14 @@ class PagedBatch:
                                 self.Hq, self.Hkv, self.D)
         self.ws = torch.empty(max(ws_dec, ws_pre, 256), dtype=torch.uint8, device=dev)
         self.groups = None  # see share_prefixes
+        # What calls took before it was replaced.  Steps that were captured into graphs name it by address, so it stays.
+        self._former_ws, self._all_groups = [], []
+
+    def _workspace(self, n: int):
+        """From now on at least n bytes of workspace."""
+        if n > self.ws.numel():
+            self._former_ws.append(self.ws)
+            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def _write(self, k, v, slot, lp):
         if self.kv_bits == 4:
@@ -189,10 +197,10 @@ class PagedBatch:
         off, shared = common_prefixes(self.meta.cpu().numpy(), self.doc_blocks.cpu().numpy(), min_blocks)
         size = np.diff(off)
         biggest, longest = int(size.max(initial=0)), int(shared.max(initial=0))
-        n = decode_shared_workspace_size(self.B, len(shared), biggest, longest, self.max_blocks, self.Hq, self.Hkv, self.D)
-        if n > self.ws.numel():
-            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._workspace(decode_shared_workspace_size(self.B, len(shared), biggest, longest, self.max_blocks, self.Hq,
+                                                     self.Hkv, self.D))
         self.groups = (i32(off, self.device), i32(shared, self.device), biggest, longest)
+        self._all_groups.append(self.groups)
         return int(size[size > 1].sum())
 
     # ---------------------------------------------------------------- eviction inside a context (bf16 caches)
@@ -205,9 +213,7 @@ class PagedBatch:
         most = q.shape[0] if cu_q is not None else 1
         if cu_q is None:
             cu_q = i32(np.arange(self.B + 1), self.device)
-        n = workspace_size(PHASE_KEY_WEIGHTS, q.shape[0], self.B, self.max_blocks, self.Hq, self.Hkv, self.D)
-        if n > self.ws.numel():
-            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._workspace(workspace_size(PHASE_KEY_WEIGHTS, q.shape[0], self.B, self.max_blocks, self.Hq, self.Hkv, self.D))
         add = weights is not None
         if not add:
             weights = torch.empty((self.B, PAGE * self.max_blocks), dtype=torch.float32, device=self.device)
@@ -218,7 +224,8 @@ class PagedBatch:
     def evict(self, weights, keep, pages, first: int = 0, recent: int = 0):
         """Cut every request's documents to the ``keep`` keys of the largest ``weights`` (the ``first`` and
         ``recent`` ones before all others): the rows move to the free ``pages`` [B, n], the lists change, and the
-        weights come back in the new order.  The old pages are the caller's to free."""
+        weights come back in the new order.  The old pages are the caller's to free.  The lists change in place: a
+        step that was captured into a graph before reads the new ones, and takes nothing for common."""
         if self.kv_bits != 16:
             raise ValueError("evict: needs a bf16 cache")
         pages = i32(pages, self.device)
@@ -228,7 +235,11 @@ class PagedBatch:
         evict_plan(weights, self.meta, self.doc_blocks, i32(keep, self.device), pages, self.k_cache.shape[0], self.cfg, meta,
                    nd, src, dst, new_w, first=first, recent=recent)
         kv_move(src, dst, self.k_cache, self.v_cache)
-        self.meta, self.doc_blocks, self.groups = meta, nd, None  # the lists differ from now on
+        self.meta.copy_(meta)
+        self.doc_blocks.copy_(nd)
+        for _, shared, _, _ in self._all_groups:  # nothing is common any more
+            shared.zero_()
+        self.groups = None
         return new_w
 
 
