@@ -212,7 +212,7 @@ class PagedBatch:
             raise ValueError("key_weights: needs a bf16 cache")
         most = q.shape[0] if cu_q is not None else 1
         if cu_q is None:
-            cu_q = i32(np.arange(self.B + 1), self.device)
+            cu_q = torch.arange(self.B + 1, dtype=torch.int32, device=self.device)  # made on the device: captures take it
         self._workspace(workspace_size(PHASE_KEY_WEIGHTS, q.shape[0], self.B, self.max_blocks, self.Hq, self.Hkv, self.D))
         add = weights is not None
         if not add:

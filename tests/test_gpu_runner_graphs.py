@@ -67,3 +67,23 @@ def test_captured_steps_outlive_groups_workspaces_and_lists(lk):
         assert_close(o, now.float().cpu().numpy().astype(np.float64), "after the eviction")
     assert not torch.equal(now.float(), torch.from_numpy(want).cuda().float())
     assert lk.device_status() == 0
+
+
+def test_captured_step_with_its_weights(lk):
+    """A decode step and the weights that its rows give, summed over replays of one graph."""
+    import torch
+    _, pb = batch(lk)
+    inp = pb.upload_decode(0)
+    lse = torch.empty((pb.B, pb.Hq), device="cuda")
+    total = torch.zeros((pb.B, 16 * pb.max_blocks), device="cuda")
+
+    def step():
+        pb.decode_step(inp, lse=lse)
+        pb.key_weights(inp["q"], lse, inp["seq_len"], weights=total)
+
+    graph = captured(step)
+    once = total.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert once.any() and torch.equal(total, 2 * once)  # (a sum of two equal numbers is exact)
+    assert lk.device_status() == 0

@@ -78,3 +78,14 @@ def test_eviction_changes_the_lists_in_place(runner, monkeypatch):
     assert np.array_equal(meta.numpy().view(np.uint64), want[0]) and np.array_equal(nd.numpy(), want[1])
     assert pb.meta.data_ptr() == meta.data_ptr() and pb.doc_blocks.data_ptr() == nd.data_ptr()
     assert pb.groups is None and not any(t.any() for t in former)
+
+
+def test_key_weights_copy_nothing_from_the_host(runner, monkeypatch):
+    """A decode loop captures its weights with its step, and a capture takes no copies from pageable memory."""
+    import torch
+    seen = []
+    monkeypatch.setattr(runner, "attn_key_weights", lambda q, lse, cu_q, *a, **kw: seen.append(cu_q))
+    _, pb = batch(runner)
+    monkeypatch.setattr(runner, "i32", lambda *a: pytest.fail("a copy from the host"))
+    pb.key_weights(torch.zeros((pb.B, pb.Hq, pb.D), dtype=torch.bfloat16), torch.zeros((pb.B, pb.Hq)), pb.seq_len0)
+    assert seen[0].dtype == torch.int32 and seen[0].tolist() == list(range(pb.B + 1))
