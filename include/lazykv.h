@@ -338,8 +338,9 @@ size_t lazy_decode_shared_workspace_size(int B, int n_groups, int max_group, int
  *   weights  (device) float [B][16 max_blocks]
  *   ws       lazy_workspace_size(LAZY_PHASE_KEY_WEIGHTS, ...) bytes, 256-byte aligned
  * A row with lse = -inf (nothing visible) counts nothing, a NaN key takes its own weight, a NaN row those of
- * the keys that it sees.  Queries count with 24 bits (up to 32 rows per KV head) or 16, sums are in fp32 and in a
- * fixed order: two calls give the same bits.
+ * the keys that it sees.  Queries count with 24 bits where max_q and window leave a request up to 32 rows per KV
+ * head, else with 16: a tight max_q is worth giving.  Sums are in fp32 and in a fixed order: two calls give the
+ * same bits.
  */
 int lazy_attn_key_weights(const void* q, const float* lse, const int32_t* cu_q, const int32_t* seq_len,
                           const int32_t* q_start, const int32_t* doc_blocks, const uint64_t* meta, int B,

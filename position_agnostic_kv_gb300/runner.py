@@ -204,13 +204,18 @@ class PagedBatch:
         return int(size[size > 1].sum())
 
     # ---------------------------------------------------------------- eviction inside a context (bf16 caches)
-    def key_weights(self, q, lse, seq_len, cu_q=None, window: int = 0, weights=None):
+    def key_weights(self, q, lse, seq_len, cu_q=None, window: int = 0, weights=None, max_q: int | None = None):
         """The attention weight that every key of the lists receives from the rows ``q`` (with the log-sum-exps of
         their attention call; requests' last tokens, split by ``cu_q``, by default one row per request), in a new
-        tensor [B, 16 max_blocks], or added to ``weights``."""
+        tensor [B, 16 max_blocks], or added to ``weights``.  ``max_q`` bounds the rows of a request (by default the
+        prefill's longest segment for its own ``cu_q``, all rows for another): give it, for where it and ``window`` leave
+        up to 32 rows per KV head, queries count with 24 bits instead of 16 and the call is faster."""
         if self.kv_bits != 16:
             raise ValueError("key_weights: needs a bf16 cache")
-        most = q.shape[0] if cu_q is not None else 1
+        if max_q is None:
+            max_q = 1 if cu_q is None else self.max_q if cu_q is self.cu_q else q.shape[0]
+        if max_q < 0:
+            raise ValueError(f"key_weights: max_q must not be negative, got {max_q}")
         if cu_q is None:
             cu_q = torch.arange(self.B + 1, dtype=torch.int32, device=self.device)  # made on the device: captures take it
         self._workspace(workspace_size(PHASE_KEY_WEIGHTS, q.shape[0], self.B, self.max_blocks, self.Hq, self.Hkv, self.D))
@@ -218,7 +223,7 @@ class PagedBatch:
         if not add:
             weights = torch.empty((self.B, PAGE * self.max_blocks), dtype=torch.float32, device=self.device)
         attn_key_weights(q, lse, cu_q, seq_len, self.q_start, self.doc_blocks, self.meta, self.k_cache, self.cfg, weights,
-                         most, window=window, accumulate=add, ws=self.ws)
+                         min(max_q, q.shape[0]), window=window, accumulate=add, ws=self.ws)
         return weights
 
     def evict(self, weights, keep, pages, first: int = 0, recent: int = 0):

@@ -89,3 +89,22 @@ def test_key_weights_copy_nothing_from_the_host(runner, monkeypatch):
     monkeypatch.setattr(runner, "i32", lambda *a: pytest.fail("a copy from the host"))
     pb.key_weights(torch.zeros((pb.B, pb.Hq, pb.D), dtype=torch.bfloat16), torch.zeros((pb.B, pb.Hq)), pb.seq_len0)
     assert seen[0].dtype == torch.int32 and seen[0].tolist() == list(range(pb.B + 1))
+
+
+def test_key_weights_pass_the_rows_of_a_request(runner, monkeypatch):
+    """The bound of a request's rows decides with how many bits queries count: it is not the batch's number of rows."""
+    import torch
+    seen = []
+    monkeypatch.setattr(runner, "attn_key_weights", lambda *a, **kw: seen.append(a[10]))
+    _, pb = batch(runner)
+    n = 4 * pb.B
+    rows = lambda n: (torch.zeros((n, pb.Hq, pb.D), dtype=torch.bfloat16), torch.zeros((n, pb.Hq)), pb.seq_len0)  # noqa: E731
+    cu = torch.arange(0, n + 1, 4, dtype=torch.int32)
+    pb.key_weights(*rows(n), cu_q=cu, max_q=4)
+    pb.key_weights(*rows(n), cu_q=cu)  # unknown: all rows could be one request's
+    pb.key_weights(*rows(n), cu_q=cu, max_q=10 ** 6)
+    pb.key_weights(*rows(pb.total_q), cu_q=pb.cu_q)  # the prefill's rows
+    pb.key_weights(*rows(pb.B))
+    assert seen == [4, n, n, 20, 1]
+    with pytest.raises(ValueError, match="max_q"):
+        pb.key_weights(*rows(n), cu_q=cu, max_q=-1)
