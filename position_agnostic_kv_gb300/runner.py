@@ -31,23 +31,46 @@ def i32(x, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(np.asarray(x, dtype=np.int32))).to(device)
 
 
+# What one group more costs, in page reads (of a request's 8 heads).  Reading a page for a group takes about as long as reading
+# it twice alone, whatever the number of requests, and every group has a start, its results and their join: decode steps of
+# 64 requests, 32 / 8 heads, that begin with 8 common pages, as one group / as groups of 8 that share 30, 60, 120, 250 pages
+# more: 27.3 / 32.4, 35.5 / 34.5, 51.9 / 40.6, 88.7 / 54.9 us; of 4: 27.3 / 34.5, 37.5 / 42.7, 53.9 / 52.9, 90.8 / 81.6; of 2:
+# 29.3 / 50.8, 41.6 / 63.1, 66.2 / 83.6, 109.2 / 132.8.
+_GROUP_COST = 256
+
+
 def common_prefixes(meta: np.ndarray, doc_blocks, min_blocks: int = 1):
     """Groups of neighbouring requests whose lists begin with the same document blocks, as ``attn_decode_shared``
-    takes them: (group_off [n + 1], shared_blocks [n], int32).  A request joins the group before it while at
-    least ``min_blocks`` words stay common to all of it (the order of the requests is the caller's)."""
-    meta, nd = np.asarray(meta), np.asarray(doc_blocks)
-    off, shared = [0], []
-    for b in range(len(nd)):
-        if b > off[-1]:
-            n = min(shared[-1], int(nd[b]))
-            same = meta[b, :n] == meta[off[-1], :n]
-            n = n if same.all() else int(np.argmin(same))
-            if n >= min_blocks:
-                shared[-1] = n
-                continue
-            off.append(b)
-        shared.append(int(nd[b]))
-    return np.array(off + [len(nd)] if len(nd) else off, np.int32), np.array(shared, np.int32)
+    takes them: (group_off [n + 1], shared_blocks [n], int32).  Neighbours with fewer than ``min_blocks`` common words are
+    in different groups; others too where requests go deeper together than all share, and reading those pages once is
+    worth more than another group costs (the order of the requests is the caller's)."""
+    meta, nd = np.asarray(meta), np.asarray(doc_blocks).astype(np.int64)
+    n = len(nd)
+    if n == 0:
+        return np.zeros(1, np.int32), np.zeros(0, np.int32)
+    same = meta[1:] == meta[:-1]
+    deep = np.where(same.all(1), meta.shape[1], np.argmin(same, 1))  # words that a request shares with the one before
+    deep = np.minimum(deep, np.minimum(nd[1:], nd[:-1]))
+    # What a group shares is the least over its neighbours.  best[j]: most that the first j requests save, with a last
+    # group that begins at last[j]; low[i]: what requests i .. j - 1 share, from the first that can be in one group with j - 1.
+    best, last, low, begin = np.zeros(n + 1, np.int64), np.zeros(n + 1, np.int64), np.zeros(n, np.int64), 0
+    for j in range(1, n + 1):
+        if j > 1:
+            if deep[j - 2] < max(min_blocks, 1):
+                begin = j - 1
+            low[j - 2] = deep[j - 2]
+            np.minimum(low[begin:j - 1], deep[j - 2], out=low[begin:j - 1])
+        more = np.arange(j - 2 - begin, -2, -1)  # requests beyond two; -1 for one alone, where low is still 0
+        save = best[begin:j] + low[begin:j] * more
+        save[1:] -= _GROUP_COST  # a cut between requests that could be in one group
+        last[j] = begin + int(np.argmax(save))
+        best[j] = save[last[j] - begin]
+    off = [n]
+    while off[-1]:
+        off.append(int(last[off[-1]]))
+    off.reverse()
+    shared = [int(nd[lo]) if hi - lo == 1 else int(deep[lo:hi - 1].min()) for lo, hi in zip(off, off[1:])]
+    return np.array(off, np.int32), np.array(shared, np.int32)
 
 
 class PagedBatch:

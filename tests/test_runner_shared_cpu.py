@@ -108,3 +108,82 @@ def test_key_weights_pass_the_rows_of_a_request(runner, monkeypatch):
     assert seen == [4, n, n, 20, 1]
     with pytest.raises(ValueError, match="max_q"):
         pb.key_weights(*rows(n), cu_q=cu, max_q=-1)
+
+
+def saved(meta, nd, off, shared, least):
+    """What a grouping saves: a group's common words once instead of for every request, at the price of two readings, less
+    the price of a group for every cut between requests that could be in one.  Checks that it is a grouping."""
+    assert off[0] == 0 and off[-1] == len(nd) and (np.diff(off) > 0).all() and len(shared) == len(off) - 1
+    total = 0
+    for g, n in enumerate(shared):
+        lo, hi = off[g], off[g + 1]
+        assert all(nd[b] >= n and np.array_equal(meta[b, :n], meta[lo, :n]) for b in range(lo, hi))
+        total += max(hi - lo - 2, 0) * int(n)
+        if lo and min(nd[lo - 1], nd[lo]) >= least and np.array_equal(meta[lo, :least], meta[lo - 1, :least]):
+            total -= 256
+    return total
+
+
+def lists(*prefixes, width=300):
+    """Requests whose lists are these words, then words of their own."""
+    meta = np.zeros((len(prefixes), width), np.uint64)
+    nd = np.zeros(len(prefixes), np.int32)
+    for b, p in enumerate(prefixes):
+        nd[b] = len(p) + 3
+        meta[b, :nd[b]] = list(p) + [10 ** 6 + 3 * b + i for i in range(3)]
+    return meta, nd
+
+
+SYSTEM = list(range(8))
+LEFT, RIGHT = SYSTEM + list(range(100, 200)), SYSTEM + list(range(200, 300))
+
+
+@pytest.mark.parametrize("name,requests,min_blocks,off,shared", [
+    ("system_prompt", [LEFT] * 4 + [RIGHT] * 4, 8, [0, 4, 8], [108, 108]),
+    ("outsider", [LEFT] * 13 + [SYSTEM] + [LEFT] * 14, 8, [0, 13, 14, 28], [108, 11, 108]),
+    ("outsider_at_the_end", [LEFT] * 5 + [SYSTEM], 1, [0, 5, 6], [108, 11]),
+    ("only_the_prompt", [SYSTEM + [1000 + b] * 50 for b in range(6)], 8, [0, 6], [8]),
+    ("pairs", [SYSTEM + [1000 + b // 2] * 250 for b in range(6)], 8, [0, 6], [8]),  # (slower as pairs)
+    ("shallow", [SYSTEM + [1000 + b // 8] * 30 for b in range(64)], 8, [0, 64], [8]),
+    ("deep", [SYSTEM + [1000 + b // 8] * 120 for b in range(64)], 8, list(range(0, 72, 8)), [128] * 8),
+    ("below_the_least", [LEFT] * 2 + [SYSTEM[:7]] * 2, 8, [0, 2, 3, 4], [108, 10, 10]),
+])
+def test_common_prefixes_keep_deep_sharing(runner, name, requests, min_blocks, off, shared):
+    """What requests share beyond a prompt that all of them begin with is not given away for it."""
+    meta, nd = lists(*requests)
+    got = runner.common_prefixes(meta, nd, min_blocks)
+    assert got[0].tolist() == off and got[1].tolist() == shared
+    assert got[0].dtype == np.int32 and got[1].dtype == np.int32
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_common_prefixes_save_the_most(runner, seed):
+    """Against every way to cut a batch of up to nine requests."""
+    rng = np.random.default_rng(seed)
+    n, least, width = int(rng.integers(1, 10)), int(rng.integers(1, 40)), 600
+    deep = np.exp(rng.uniform(0, np.log(width), n)).astype(int)  # with the request before
+    meta, nd = np.zeros((n, width), np.uint64), rng.integers(300, width, n).astype(np.int32)
+    meta[0] = rng.integers(1, 1 << 40, width)
+    for b in range(1, n):
+        meta[b] = rng.integers(1, 1 << 40, width)
+        meta[b, :deep[b]] = meta[b - 1, :deep[b]]
+    off, shared = runner.common_prefixes(meta, nd, least)
+    best = None
+    for cuts in range(1 << (n - 1)):
+        ends = [0] + [b for b in range(1, n) if cuts >> (b - 1) & 1] + [n]
+        common = []
+        for lo, hi in zip(ends, ends[1:]):
+            same = (meta[lo:hi] == meta[lo]).all(0)
+            k = int(min(nd[lo:hi].min(), width if same.all() else np.argmin(same)))
+            common.append(int(nd[lo]) if hi - lo == 1 else k)
+        if all(k >= least or hi - lo == 1 for k, lo, hi in zip(common, ends, ends[1:])):
+            one = saved(meta, nd, np.array(ends), common, least)
+            best = one if best is None else max(best, one)
+    assert saved(meta, nd, off, shared, least) == best
+
+
+def test_common_prefixes_of_a_large_batch(runner):
+    """Thousands of requests: groups of unequal depth under one prompt."""
+    meta, nd = lists(*[SYSTEM + [1000 + b // 37] * 60 for b in range(4000)], width=80)
+    off, shared = runner.common_prefixes(meta, nd, 8)
+    assert off.tolist() == list(range(0, 4000, 37)) + [4000] and (shared == 68).all()
