@@ -308,7 +308,7 @@ int lazy_attn_prefill_q4(const void* q, const int32_t* cu_q, const int32_t* q_st
  * q, seq_len, q_start, doc_blocks, meta, out and lse as in lazy_attn_decode.  seq_len[b] <= 0 marks an idle
  * request (a batch padded to a fixed size); it and one without a visible key get out = 0 and lse = -inf.
  * Common keys are rotated and taken in f16 (as in lazy_attn_prefill: magnitudes above 65504 overflow); a NaN
- * in a common value reaches that column of every request of the group.  Few and short lists are decoded one by
+ * or an infinity in a common value reaches that column of every request of the group.  Few and short lists are decoded one by
  * one, where that is faster; a long list of a request alone is best given as a group of one.
  */
 int lazy_attn_decode_shared(const void* q, const int32_t* seq_len, const int32_t* q_start,
