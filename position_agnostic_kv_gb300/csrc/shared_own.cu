@@ -12,8 +12,9 @@
 // instruction's first operand.
 //
 // What bounds it: latency on short lists, then bytes.  64 requests of 33 own keys each, 8 KV heads: 8 to 10 us of a call
-// (block words, first pages, one rotation, merge, a chain of dependent loads); 64 requests of 532: 43.6 us for 135 MB from
-// cold caches, 3.1 TB/s, most warps waiting for their next page with 53 KB a block and two pages a warp in flight.
+// (block words, first pages, one rotation, merge, a chain of dependent loads); 64 requests of up to 1064 keys,
+// 515 on average: 38.3 us for 135 MB from cold caches, 3.5 TB/s.  They are 512 blocks, all resident, with one list
+// each, so the launch lasts as long as its longest list, twice the average.
 #include <cfloat>
 
 #include "shared_decode.cuh"

@@ -214,7 +214,9 @@ class PagedBatch:
 
     def share_prefixes(self, min_blocks: int = 8):
         """From now on decode steps read the documents that neighbouring requests list first, in the same
-        order, once per group (bf16 caches).  Returns the number of requests that share."""
+        order, once per group (bf16 caches).  Returns the number of requests that share.  Keys that a group shares meet
+        its queries in f16 and their weights are rounded to bf16, where a request's own keys and ``attn_decode`` keep more:
+        relative to 64 bits 0.0024 instead of 0.0017, which is the result's rounding to bf16."""
         if self.kv_bits != 16:
             raise ValueError("share_prefixes: the calls over shared lists need a bf16 cache")
         off, shared = common_prefixes(self.meta.cpu().numpy(), self.doc_blocks.cpu().numpy(), min_blocks)
