@@ -798,7 +798,9 @@ __global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const Args a) 
   const Request r = request_of(a, b);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     const int rows = a.cu_q[b + 1] - a.cu_q[b];
-    if ((a.window > 0 ? min(rows, a.window) : rows) > a.most) set_status(a.status, LAZY_STATUS_BAD_ROW);
+    if ((a.window > 0 ? min(rows, a.window) : rows) > a.most ||
+        (r.R > 0 && list_too_long(a.seq_len[b] - 1, a.q_start[b], a.doc_blocks[b], a.max_blocks)))
+      set_status(a.status, LAZY_STATUS_BAD_ROW);
   }
   const int per = a.sums * a.Hkv, G = a.Hq / a.Hkv, last = r.rgc * per;
   for (int i0 = blockIdx.x * KEYS; i0 < N; i0 += gridDim.x * KEYS) {  // the same rounds for every thread

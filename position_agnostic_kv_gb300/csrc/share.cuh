@@ -49,5 +49,9 @@ __device__ __forceinline__ int visible_blocks(int seq_len, int q_start, int doc_
   const long long nb = (long long)max(doc_blocks, 0) + (own > 0 ? (own + kPage - 1) / kPage : 0);
   return int(nb < max_blocks ? nb : max_blocks);
 }
+// A token at position m of the query segment sees more blocks than a list has words.
+__device__ __forceinline__ bool list_too_long(int m, int q_start, int doc_blocks, int max_blocks) {
+  return m >= q_start && (long long)doc_blocks + (m - q_start) / kPage + 1 > max_blocks;
+}
 
 }  // namespace lazykv

@@ -55,8 +55,7 @@ __device__ __forceinline__ Share share_of(const SharedArgs& a, int b) {
 // Reports a list that is longer than max_blocks, and a group or its common blocks above the call's bounds (a block of
 // threads per request).
 __device__ __forceinline__ void check_request(const SharedArgs& a, int b, int m) {
-  bool bad = threadIdx.x == 0 && m >= a.q_start[b] &&
-             (long long)a.doc_blocks[b] + (m - a.q_start[b]) / kPage + 1 > a.max_blocks;
+  bool bad = threadIdx.x == 0 && m >= 0 && list_too_long(m, a.q_start[b], a.doc_blocks[b], a.max_blocks);
   for (int g = threadIdx.x; b == 0 && g < a.n_groups; g += blockDim.x)
     bad |= a.group_off[g + 1] - a.group_off[g] > a.max_group || a.shared_blocks[g] > a.max_shared;
   if (bad) set_status(a.status, LAZY_STATUS_BAD_ROW);

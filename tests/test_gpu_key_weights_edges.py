@@ -61,3 +61,29 @@ def test_runner_bounds_the_rows_of_a_request(lk):
     lk.attn_key_weights(q, lse, cu, pb.seq_len0, pb.q_start, pb.doc_blocks, pb.meta, pb.k_cache, pb.cfg, want, 4, ws=pb.ws)
     assert torch.equal(got, want) and got.any()
     assert lk.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["window", "odd_heads", "alibi"])
+def test_a_list_longer_than_the_row_of_words(lk, name):
+    """A position behind the last word of the list: the status says so, as it does for attention."""
+    v = Votes(lk, name)
+    x = v.x
+    x.seq_len[0] += 16 * 40
+    v.g.seq_len.copy_(dev(x.seq_len.astype(np.int32)))
+    got = v.run()
+    x.meta = np.pad(x.meta, ((0, 0), (0, 40)))  # words without keys
+    want = ref.key_weights(x, v.qh, v.lse_h, v.cu, v.window)
+    nan = np.isnan(want)  # the rest of the segment's last page, visible now, was never written
+    assert nan[0].any() and np.array_equal(np.isnan(got), nan)
+    x.k = np.nan_to_num(x.k)
+    v.check(np.where(nan, ref.key_weights(x, v.qh, v.lse_h, v.cu, v.window), got))
+    assert lk.device_status() == 8
+
+
+def test_idle_requests_and_requests_without_rows_report_nothing(lk):
+    v = Votes(lk, "no_rows")
+    v.x.seq_len[0] = 10 ** 6  # no rows
+    v.x.seq_len[1] = 0
+    v.g.seq_len.copy_(dev(v.x.seq_len.astype(np.int32)))
+    assert not v.run().any()
+    assert lk.device_status() == 0
