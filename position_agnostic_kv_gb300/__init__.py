@@ -578,8 +578,10 @@ def kv_move(src_slot, dst_slot, k_cache, v_cache, stream=None):
     shape; entries with a negative slot are skipped).  Destinations are distinct and none is a source."""
     if _torch is None:
         _bind_torch()
-    cache, slots = k_cache.shape, src_slot.shape
+    cache, slots, rows = k_cache.shape, src_slot.shape, src_slot.numel()
     dev = k_cache.get_device()
+    if rows > 2 ** 31 - 8:
+        raise ValueError(f"kv_move: src_slot must have fewer than 2^31 - 7 entries, got {rows}")
     if not (dev >= 0 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and src_slot.dtype is _I32
             and dst_slot.dtype is _I32 and len(cache) == 4 and cache[2] == 16 and v_cache.shape == cache
             and dst_slot.shape == slots and k_cache.is_contiguous() and v_cache.is_contiguous()
@@ -589,7 +591,7 @@ def kv_move(src_slot, dst_slot, k_cache, v_cache, stream=None):
             raise ValueError(f"kv_move: k_cache must be [num_pages, Hkv, 16, D], got {tuple(cache)}")
         _q4_refuse("kv_move", (("k_cache", k_cache, _BF16, cache), ("v_cache", v_cache, _BF16, cache),
                                ("src_slot", src_slot, _I32, slots), ("dst_slot", dst_slot, _I32, slots)))
-    _q4_run(lib.lazy_kv_move, "kv_move", dev, stream, src_slot.data_ptr(), dst_slot.data_ptr(), src_slot.numel(),
+    _q4_run(lib.lazy_kv_move, "kv_move", dev, stream, src_slot.data_ptr(), dst_slot.data_ptr(), rows,
             cache[1], cache[3], k_cache.data_ptr(), v_cache.data_ptr(), cache[0])
 
 

@@ -667,6 +667,7 @@ extern "C" int lazy_kv_move(const int32_t* src_slot, const int32_t* dst_slot, in
     return fail(LAZY_EINVAL, "%s: bad sizes (T=%d Hkv=%d num_pages=%d)", what, T, Hkv, num_pages);
   if (D != 64 && D != 128) return fail(LAZY_EINVAL, "%s: head_dim must be 64 or 128, got %d", what, D);
   if (num_pages > (1 << 24)) return fail(LAZY_ERANGE, "%s: num_pages above 2^24", what);
+  if (T > 0x7fffffff - 7) return fail(LAZY_ERANGE, "%s: T must be below 2^31 - 7", what);  // (8 rows to a block of threads)
   if (T > 0) {
     if (!src_slot || !dst_slot || !k_cache || !v_cache) return fail(LAZY_EINVAL, "%s: NULL pointer", what);
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(LAZY_EINVAL, "%s: caches must be 16-byte aligned", what);

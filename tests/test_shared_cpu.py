@@ -206,3 +206,14 @@ def test_common_prefixes(lk):
     assert off.tolist() == [0, 1, 2, 3, 5, 6] and shared.tolist() == [3, 3, 2, 3, 0]
     off, shared = common_prefixes(meta[:0], nd[:0])
     assert off.tolist() == [0] and shared.tolist() == []
+
+
+def test_kv_move_of_more_rows_than_an_int_counts(lk):
+    """Refused before anything is launched, by the call and by its Python form."""
+    import torch
+    a = _Args(lk)
+    for T in (2 ** 31 - 7, 2 ** 31 - 1):
+        assert a.call("kv_move", T=T) == ERANGE and "2^31" in lk.lib.lazy_last_error().decode()
+    slots, k = (torch.empty(s, dtype=d, device="meta") for s, d in (((2 ** 32 + 5,), torch.int32), ((8, 2, 16, 64), torch.bfloat16)))
+    with pytest.raises(ValueError, match="2\\^31"):
+        lk.kv_move(slots, slots, k, k)
