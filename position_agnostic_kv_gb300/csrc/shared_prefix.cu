@@ -773,6 +773,12 @@ int shared_prefix_splits(int B, int n_groups, int max_group, int max_shared, int
   const long long alone = (long long)B * max_shared * Hkv * ((G + 7) / 8), once = (long long)n_groups * max_shared * Hkv;
   if (alone - once < 8000) return 0;
   const long long rows = (long long)max_group * G, pairs = (rows + 2 * kM - 1) / (2 * kM), units = n_groups * Hkv * pairs;
+  // A shared page takes a block as long as two pages alone, and its start and results as long as 120: groups of two or of few
+  // common pages are faster alone, where the requests alone are one wave of blocks.  (32 / 8 heads, 32 groups of 2 requests
+  // over 260 common pages: alone 109.2 us, shared 134.8; 16 of 4 over 30: 25.2, 34.4; over 260: 92.8, 81.5.  More waves: 32 / 32
+  // heads, 6 groups of 2 over 600: 249.5, 186.0.)
+  const long long lists = (long long)B * Hkv * ((G + 7) / 8), splits = (3ll * sms + lists - 1) / lists;
+  if (lists * splits <= 4ll * sms && alone < 2 * once + 120 * units) return 0;
   // Time of a launch in key tiles: waves of blocks, each its tiles, and its start and results, as long as 6 tiles of two
   // Q tiles or 12 of one; then the join, with every split.  (16 requests as above, splits 4 / 6 / 9 / 17: 19.9, 17.8,
   // 16.9, 22.2 us; 32 requests of 32 heads over 94 tiles of one KV head, splits 16 / 24 / 38: 28.2, 25.6, 30.4.)

@@ -217,3 +217,13 @@ def test_kv_move_of_more_rows_than_an_int_counts(lk):
     slots, k = (torch.empty(s, dtype=d, device="meta") for s, d in (((2 ** 32 + 5,), torch.int32), ((8, 2, 16, 64), torch.bfloat16)))
     with pytest.raises(ValueError, match="2\\^31"):
         lk.kv_move(slots, slots, k, k)
+
+
+@pytest.mark.parametrize("B,groups,deep,Hq,Hkv,alone", [
+    (64, 32, 260, 32, 8, True), (64, 32, 60, 64, 8, True), (64, 16, 30, 32, 8, True), (12, 6, 600, 64, 8, True),
+    (64, 16, 260, 32, 8, False), (64, 8, 130, 32, 8, False), (64, 1, 2000, 32, 8, False), (12, 6, 600, 32, 32, False)])
+def test_groups_too_small_to_gain_are_decoded_alone(lk, B, groups, deep, Hq, Hkv, alone):
+    """Such a call needs the workspace of one without groups."""
+    size = lk.decode_shared_workspace_size
+    got = size(B, groups, B // groups, deep, deep + 3, Hq, Hkv, 128)
+    assert (got == size(B, 0, 0, 0, deep + 3, Hq, Hkv, 128)) == alone
