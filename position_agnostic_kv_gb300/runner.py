@@ -34,8 +34,8 @@ def i32(x, device) -> torch.Tensor:
 # What one group more costs, in page reads (of a request's 8 heads).  Reading a page for a group takes about as long as reading
 # it twice alone, whatever the number of requests, and every group has a start, its results and their join: decode steps of
 # 64 requests, 32 / 8 heads, that begin with 8 common pages, as one group / as groups of 8 that share 30, 60, 120, 250 pages
-# more: 27.3 / 32.4, 35.5 / 34.5, 51.9 / 40.6, 88.7 / 54.9 us; of 4: 27.3 / 34.5, 37.5 / 42.7, 53.9 / 52.9, 90.8 / 81.6; of 2:
-# 29.3 / 50.8, 41.6 / 63.1, 66.2 / 83.6, 109.2 / 132.8.
+# more: 27.3 / 32.4, 35.5 / 34.5, 51.9 / 40.6, 88.7 / 54.9 us; of 4 with 60, 120, 250: 37.5 / 42.7, 53.9 / 54.9, 90.9 / 81.6.
+# (Groups of 2, and of 4 with 30, the call decodes alone either way.)
 _GROUP_COST = 256
 
 

@@ -143,7 +143,7 @@ LEFT, RIGHT = SYSTEM + list(range(100, 200)), SYSTEM + list(range(200, 300))
     ("outsider", [LEFT] * 13 + [SYSTEM] + [LEFT] * 14, 8, [0, 13, 14, 28], [108, 11, 108]),
     ("outsider_at_the_end", [LEFT] * 5 + [SYSTEM], 1, [0, 5, 6], [108, 11]),
     ("only_the_prompt", [SYSTEM + [1000 + b] * 50 for b in range(6)], 8, [0, 6], [8]),
-    ("pairs", [SYSTEM + [1000 + b // 2] * 250 for b in range(6)], 8, [0, 6], [8]),  # (slower as pairs)
+    ("pairs", [SYSTEM + [1000 + b // 2] * 250 for b in range(6)], 8, [0, 6], [8]),  # (pairs gain nothing)
     ("shallow", [SYSTEM + [1000 + b // 8] * 30 for b in range(64)], 8, [0, 64], [8]),
     ("deep", [SYSTEM + [1000 + b // 8] * 120 for b in range(64)], 8, list(range(0, 72, 8)), [128] * 8),
     ("below_the_least", [LEFT] * 2 + [SYSTEM[:7]] * 2, 8, [0, 2, 3, 4], [108, 10, 10]),
