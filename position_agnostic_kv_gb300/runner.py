@@ -224,8 +224,9 @@ class PagedBatch:
         biggest, longest = int(size.max(initial=0)), int(shared.max(initial=0))
         self._workspace(decode_shared_workspace_size(self.B, len(shared), biggest, longest, self.max_blocks, self.Hq,
                                                      self.Hkv, self.D))
-        self.groups = (i32(off, self.device), i32(shared, self.device), biggest, longest)
-        self._all_groups.append(self.groups)
+        if self.groups is None or not all(map(np.array_equal, self._grouping, (off, shared))):
+            self.groups, self._grouping = (i32(off, self.device), i32(shared, self.device), biggest, longest), (off, shared)
+            self._all_groups.append(self.groups)
         return int(size[size > 1].sum())
 
     # ---------------------------------------------------------------- eviction inside a context (bf16 caches)

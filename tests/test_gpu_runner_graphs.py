@@ -34,7 +34,7 @@ def test_captured_steps_outlive_groups_workspaces_and_lists(lk):
     pb.share_prefixes(min_blocks=4)
     graphs.append(captured(lambda: pb.decode_step(inp, out=outs[1])))
     sizes.append(pb.ws.numel())
-    pb.share_prefixes(min_blocks=1)
+    pb.share_prefixes(min_blocks=1000)  # every request a group of its own
     graphs.append(captured(lambda: pb.decode_step(inp, out=outs[2], lse=lse)))
     sizes.append(pb.ws.numel())
     weights = pb.key_weights(torch.cat([inp["q"]] * 9), torch.cat([lse] * 9), inp["seq_len"],

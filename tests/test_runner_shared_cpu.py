@@ -49,7 +49,7 @@ def test_former_groups_stay(runner):
     _, pb = batch(runner)
     pb.share_prefixes(min_blocks=4)
     former = [weakref.ref(t) for t in pb.groups[:2]]
-    pb.share_prefixes(min_blocks=1)
+    pb.share_prefixes(min_blocks=1000)
     gc.collect()
     assert all(r() is not None for r in former)
 
@@ -61,7 +61,7 @@ def test_eviction_changes_the_lists_in_place(runner, monkeypatch):
     monkeypatch.setattr(runner, "evict_plan", fake_plan)
     monkeypatch.setattr(runner, "kv_move", lambda *a: None)
     w, pb = batch(runner, spare_pages=34 * 10)
-    pb.share_prefixes(min_blocks=1)
+    pb.share_prefixes(min_blocks=1000)
     former = [pb.groups[1]]
     pb.share_prefixes(min_blocks=4)
     former.append(pb.groups[1])
@@ -187,3 +187,15 @@ def test_common_prefixes_of_a_large_batch(runner):
     meta, nd = lists(*[SYSTEM + [1000 + b // 37] * 60 for b in range(4000)], width=80)
     off, shared = runner.common_prefixes(meta, nd, 8)
     assert off.tolist() == list(range(0, 4000, 37)) + [4000] and (shared == 68).all()
+
+
+def test_sharing_again_takes_no_more_memory(runner):
+    """A loop that calls it before every step: groups that have not changed are the same tensors."""
+    _, pb = batch(runner)
+    n = pb.share_prefixes(min_blocks=4)
+    groups = pb.groups
+    for _ in range(3):
+        assert pb.share_prefixes(min_blocks=4) == n
+    assert pb.groups is groups and len(pb._all_groups) == 1
+    pb.share_prefixes(min_blocks=1000)
+    assert pb.groups is not groups and len(pb._all_groups) == 2
